@@ -45,6 +45,8 @@
 #ifndef VLA_H
 #define VLA_H
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -77,6 +79,7 @@ typedef enum {
 /* Status flags, ORed over all pairs since the last vla_status() call. */
 #define VLA_STATUS_NONFINITE 1u  /* a NaN/Inf reached delta, the readout or ||S|| ("Mathematical Primitives" §1, finite state enforcement) */
 #define VLA_STATUS_TIMEOUT   2u  /* a bounded wait on an input copy expired; that pair stopped early */
+#define VLA_STATUS_INDEX     4u  /* an offset or slot outside its range; that sequence was skipped */
 
 typedef struct {
   unsigned int flags;                 /* VLA_STATUS_* */
@@ -309,6 +312,101 @@ vla_err_t vla_scan_fwd_noalloc(const void* q, const void* k, const void* v, cons
                                int P, float eps_n, float tau, long long t0,
                                vla_dtype_t io_dtype, vla_pair_status_t* pair_status,
                                void* stream);
+
+/* ------------------------------------------------------------------------
+ * Operators of a state space layer, for prompts and for single tokens: the short
+ * causal convolution, the selective scan behind it, and the norm before each
+ * projection.  All are asynchronous on `stream`, allocate nothing, read the
+ * host's arguments before they return, give the same bits every time, and can be
+ * captured in a CUDA graph.  The pages have no counterpart to them.
+ *
+ * Sequences.  `offsets` NULL: a dense batch of n_seq sequences of T tokens; token t
+ * of sequence s starts at x + s * (sequence stride) + t * (token stride).  `offsets`
+ * (device, n_seq + 1 int32): a packed buffer of T token rows in which sequence s is
+ * the rows [offsets[s], offsets[s+1]) and the sequence strides are not used; max_len
+ * is a bound on the sequences' lengths that sizes the launch (T is always valid).
+ * Rows that no sequence covers are neither read nor written.
+ *
+ * States.  `state` is a pool of n_slots states; sequence s continues from slot
+ * slots[s] (device int32; NULL: slot s) and leaves its new state there.  A negative
+ * slot skips its sequence: nothing of it is read or written, as for the padding of
+ * a batch of fixed size.  No two sequences of a call may name one slot.  state NULL: every sequence starts
+ * from zeros and its state is not kept.  A sequence without tokens leaves its state
+ * as it is.
+ *
+ * Offsets that decrease, leave [0, T] or span more than max_len, and slots >=
+ * n_slots, set VLA_STATUS_INDEX in the handle's status, and their sequence is
+ * skipped like one with a negative slot.
+ *
+ * Strides count elements and are >= 0; within a token the values are adjacent.  No
+ * alignment is required of x, y, dt, B, C, z and w beyond their type's; rows that
+ * start on 16-byte boundaries are faster.  Outputs must not overlap any input
+ * (the norm's residual is both). */
+
+/* y[t, c] = act(bias[c] + sum_{j<K} w[c, j] x[t - K + 1 + j, c]); act(v) = v * sigmoid(v)
+ * if silu, else v.  Inputs before a sequence's first token come from its state.
+ *
+ *   x, y      token rows of C channels, io dtype.
+ *   w         [C, K] float32; K in {2, 3, 4}.   bias  [C] float32 or NULL.
+ *   state     [n_slots, K-1, C] io dtype, row K-2 the latest input; or NULL.
+ *   strides   host array {x sequence, x token, y sequence, y token}.
+ * Sums are taken in float32.  Errors (before any launch): INVALID_ARG for NULL
+ * pointers, sizes or strides out of range, slots without a state, fewer states than
+ * sequences without slots; UNSUPPORTED for other K; CUDA if the launch fails. */
+vla_err_t vla_short_conv(vla_handle_t h, const void* x, const float* w, const float* bias, void* state, void* y,
+                         long long n_seq, long long T, long long max_len, const int* offsets, const int* slots,
+                         long long n_slots, long long C, int K, const long long* strides, int silu,
+                         vla_dtype_t io_dtype, void* stream);
+
+/* The selective scan of H heads, t in order:
+ *   s = softplus(dt_t + dt_bias)  (s = dt_t + dt_bias without softplus)
+ *   h = exp(A s) h + s x_t B_t^T;   y_t = (h C_t + D x_t) * z_t * sigmoid(z_t)
+ *
+ *   x, z, y   token rows of H * P values, io dtype (z NULL: no gate).
+ *   dt        token rows of H values, io dtype.
+ *   B, C      token rows of G * N values, io dtype; head i reads group i / (H / G).
+ *   A, D, dt_bias   [H] float32 (D and dt_bias may be NULL: 0).  A s <= 0 is expected
+ *             (a decay): with a growing state the chunked form can overflow earlier
+ *             than the recurrence.
+ *   state     [n_slots, H, P, N] float32, 16-byte aligned, or NULL.
+ *   N         1..256.
+ *   strides   host array {x, dt, B, C, z, y} x {sequence, token}.
+ *   workspace device memory of vla_ssm_workspace bytes, 16-byte aligned, that nothing
+ *             else uses until the call's work is done; NULL where that is 0.
+ * State and sums are float32.  Errors (before any launch): as for vla_short_conv;
+ * INVALID_ARG also for H no multiple of G, a misaligned state, a workspace that is
+ * too small; UNSUPPORTED for N > 256. */
+vla_err_t vla_ssm_scan(vla_handle_t h, const void* x, const void* dt, const float* A, const void* B, const void* C,
+                       const float* D, const void* z, const float* dt_bias, float* state, void* y,
+                       long long n_seq, long long T, long long max_len, const int* offsets, const int* slots,
+                       long long n_slots, long long H, long long P, long long G, long long N,
+                       const long long* strides, int softplus, vla_dtype_t io_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that vla_ssm_scan needs for these arguments (packed: whether it
+ * gets offsets).  Errors: INVALID_ARG for a NULL argument or a negative size. */
+vla_err_t vla_ssm_workspace(vla_handle_t h, long long n_seq, long long T, long long max_len, int packed, long long H,
+                            long long P, long long N, vla_dtype_t io_dtype, size_t* bytes);
+
+typedef enum { VLA_OUT_IO = 0, VLA_OUT_E4M3 = 1, VLA_OUT_INT8 = 2 } vla_out_t;
+
+/* Root-mean-square norm of rows of D values (1..32768):
+ *   r = x + residual (residual <- r in its own type),  v = r / sqrt(mean(r^2) + eps) * w
+ * y is v in the io dtype (VLA_OUT_IO), or codes of 8 bits (VLA_OUT_E4M3: e4m3 floats,
+ * VLA_OUT_INT8: integers in [-127, 127]) with float32 scales such that v ~ code * scale:
+ * scale = max|v| / 448 or / 127 over the row (group 0, scale [rows]) or over each 128
+ * values (group 128, scale [rows, ceil(D / 128)]), 1 where that is below the smallest
+ * normal float32, and code = v * (1 / scale) to nearest even.  A row with a NaN has NaN scales.
+ *
+ *   x, y, residual   rows at x_row, y_row, res_row elements; residual NULL, or
+ *                    res_dtype, updated in place.   w  [D] float32.
+ * v is formed in float32 from r before r is rounded to the residual's type.
+ * Errors (before any launch): INVALID_ARG for NULL pointers, sizes or strides out of
+ * range, unknown types, group not 0 or 128, eps < 0 or NaN; UNSUPPORTED for D > 32768;
+ * CUDA if the launch fails. */
+vla_err_t vla_rms_norm(vla_handle_t h, const void* x, const float* w, void* residual, void* y, float* scale,
+                       long long rows, long long D, long long x_row, long long res_row, long long y_row, float eps,
+                       int group, vla_out_t out, vla_dtype_t io_dtype, vla_dtype_t res_dtype, void* stream);
 
 #ifdef __cplusplus
 }

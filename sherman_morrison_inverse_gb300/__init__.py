@@ -16,6 +16,10 @@ are float32 CUDA tensors updated in place; o [B, H, T, d_v] is returned.
 
 takes the same tensors in (page-locked) host memory and pipelines the copies in
 and out with the scan, window by window of the sequence.
+
+``short_conv``, ``ssm_scan``, their single-token forms ``short_conv_step`` and
+``ssm_step``, and ``rms_norm`` are the operators of a state space layer (see
+``layer.py``).
 """
 from __future__ import annotations
 
@@ -25,8 +29,12 @@ import threading
 
 import torch
 
-__all__ = ["scan_fwd", "scan_fwd_host", "project_u", "Handle", "VlaError", "library_path", "load_library",
-           "STATUS_NONFINITE", "STATUS_TIMEOUT", "SEQUENTIAL", "CHUNKED", "DELTA"]
+from . import layer as _layer
+from .layer import STATUS_INDEX
+
+__all__ = ["scan_fwd", "scan_fwd_host", "project_u", "short_conv", "short_conv_step", "ssm_scan", "ssm_step",
+           "rms_norm", "Handle", "VlaError", "library_path", "load_library",
+           "STATUS_NONFINITE", "STATUS_TIMEOUT", "STATUS_INDEX", "SEQUENTIAL", "CHUNKED", "DELTA"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 SEQUENTIAL, CHUNKED, DELTA = 0, 1, 2
@@ -97,6 +105,7 @@ def load_library():
         lib.vla_host_path_info.restype = ci
         lib.vla_project_u.argtypes = [vp, vp, vp, vp, cll, ci, ci, ci, vp]
         lib.vla_project_u.restype = ci
+        _layer.declare(lib)
         _lib = lib
         return lib
 
@@ -113,7 +122,7 @@ def _stream_ptr(stream, device) -> int:
     return int(stream.cuda_stream)
 
 
-class Handle:
+class Handle(_layer.LayerOps):
     """A library handle bound to one CUDA device (owns the device status block)."""
 
     def __init__(self, device: int | torch.device | None = None):
@@ -146,7 +155,7 @@ class Handle:
         _check(self.lib, self._h, self.lib.vla_status(self._h, _stream_ptr(stream, self.device),
                                                       ctypes.byref(st)))
         return dict(flags=st.flags, nonfinite=bool(st.flags & STATUS_NONFINITE),
-                    timeout=bool(st.flags & STATUS_TIMEOUT), guard_count=st.guard_count,
+                    timeout=bool(st.flags & STATUS_TIMEOUT), index=bool(st.flags & STATUS_INDEX), guard_count=st.guard_count,
                     renorm_count=st.renorm_count, chunk_fallbacks=st.chunk_fallbacks)
 
     def project_u(self, k_raw, W_u, u=None, stream=None):
@@ -291,3 +300,28 @@ def scan_fwd_host(q, k, v, u, A, S, n, o=None, *, P: int, eps_n: float, tau: flo
     h = handle if handle is not None else default_handle(device)
     return h.scan_fwd_host(q, k, v, u, A, S, n, o, P=P, eps_n=eps_n, tau=tau, t0=t0, mode=mode,
                            chunk=chunk, seg=seg, stream=stream, wait=wait)
+
+
+def short_conv(x, *args, handle: Handle | None = None, **kw):
+    """Short causal convolution on x's device (see Handle.short_conv)."""
+    return (handle or default_handle(x.device)).short_conv(x, *args, **kw)
+
+
+def short_conv_step(x, *args, handle: Handle | None = None, **kw):
+    """The convolution of one token a sequence (see Handle.short_conv_step)."""
+    return (handle or default_handle(x.device)).short_conv_step(x, *args, **kw)
+
+
+def ssm_scan(x, *args, handle: Handle | None = None, **kw):
+    """Selective state space scan on x's device (see Handle.ssm_scan)."""
+    return (handle or default_handle(x.device)).ssm_scan(x, *args, **kw)
+
+
+def ssm_step(x, *args, handle: Handle | None = None, **kw):
+    """The scan of one token a sequence (see Handle.ssm_step)."""
+    return (handle or default_handle(x.device)).ssm_step(x, *args, **kw)
+
+
+def rms_norm(x, *args, handle: Handle | None = None, **kw):
+    """Root-mean-square norm with residual and 8-bit output on x's device (see Handle.rms_norm)."""
+    return (handle or default_handle(x.device)).rms_norm(x, *args, **kw)

@@ -1,5 +1,6 @@
 // C ABI of the VLA scan: argument checks, handle, status block, dispatch.
 #include "vla.h"
+#include "vla_handle.cuh"
 #include "vla_internal.cuh"
 
 #include <cuda.h>   // driver types for the pointer-attribute query (resolved at run time)
@@ -38,57 +39,14 @@ thread_local std::string g_create_error;
 
 void vla::set_thread_error(const char* msg) { g_create_error = msg ? msg : ""; }
 
-namespace {
-constexpr int kHostSlots = 3;   // staging slots of the host-buffer path (copy in / scan / copy out)
-}
-
-struct vla_handle_s {
-  int device = 0;
-  int sm_count = 0;
-  vla::DevStatus* status = nullptr;
-  std::string last_error;
-  // Host-buffer path (vla_scan_fwd_host), made on its first use: a device workspace with
-  // the state and kHostSlots staging slots, a copy-in and a copy-out stream, and events.
-  bool host_ready = false;
-  int last_gathered = -1;       // copy-in path and window of the last vla_scan_fwd_host call
-  long long last_seg = 0;
-  void* ws = nullptr;
-  size_t ws_bytes = 0;
-  cudaStream_t s_in = nullptr, s_out = nullptr;
-  cudaEvent_t ev_start = nullptr, ev_end = nullptr;
-  cudaEvent_t ev_in[kHostSlots] = {}, ev_run[kHostSlots] = {}, ev_out[kHostSlots] = {};
-};
-
-namespace {
-
-vla_err_t fail(vla_handle_t h, vla_err_t code, const std::string& msg) {
+vla_err_t vla::api::fail(vla_handle_t h, vla_err_t code, const std::string& msg) {
   if (h) h->last_error = msg; else g_create_error = msg;
   return code;
 }
 
-std::string cuda_msg(const char* what, cudaError_t e) {
-  return std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
-}
+using namespace vla::api;
 
-// Runs `fn` with `device` current and restores the caller's device.
-template <typename F>
-cudaError_t on_device(int device, F fn) {
-  int prev = -1;
-  cudaError_t e = cudaGetDevice(&prev);
-  if (e != cudaSuccess) return e;
-  if (prev != device) {
-    e = cudaSetDevice(device);
-    if (e != cudaSuccess) return e;
-  }
-  cudaError_t r = fn();
-  if (prev != device) {
-    cudaError_t e2 = cudaSetDevice(prev);
-    if (r == cudaSuccess) r = e2;
-  }
-  return r;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
