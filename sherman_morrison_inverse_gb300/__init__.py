@@ -133,6 +133,7 @@ class Handle(_layer.LayerOps):
         h = ctypes.c_void_p()
         _check(self.lib, None, self.lib.vla_create(ctypes.byref(h), self.device.index))
         self._h = h
+        self._ptr_value, self._device_index = h.value, self.device.index
 
     @property
     def ptr(self):
@@ -142,6 +143,7 @@ class Handle(_layer.LayerOps):
         if self._h:
             _check(self.lib, None, self.lib.vla_destroy(self._h))
             self._h = None
+            self._ptr_value = 0
 
     def __del__(self):
         try:

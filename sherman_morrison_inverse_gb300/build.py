@@ -2,7 +2,8 @@
 
 Each .cu file compiles to an object in parallel; the objects link into
 ``sherman_morrison_inverse_gb300/libvla.so`` with the CUDA runtime linked
-statically.  Usage: ``python -m sherman_morrison_inverse_gb300.build`` or
+statically.  ``csrc/layer_binding.c`` becomes the Python module ``_layer_binding.so``
+beside it.  Usage: ``python -m sherman_morrison_inverse_gb300.build`` or
 ``build()`` from Python.
 """
 from __future__ import annotations
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvla.so")
+BINDING = os.path.join(PKG, "_layer_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -34,6 +37,21 @@ def _nvcc() -> str:
 
 def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+
+
+def build_binding() -> str:
+    """The layer operators' argument checks (CPython API; no CUDA and no torch headers)."""
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler")
+    tmp = BINDING + ".tmp"
+    cmd = [cc, "-O2", "-std=c11", "-Wall", "-Wextra", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+           "-I", INCLUDE, os.path.join(CSRC, "layer_binding.c"), "-o", tmp]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"{cc} failed on layer_binding.c:\n{p.stdout}\n{p.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -60,6 +78,7 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, LIB)
+    build_binding()
     return LIB
 
 

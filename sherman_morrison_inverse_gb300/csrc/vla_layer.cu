@@ -116,6 +116,8 @@ vla_err_t vla_ssm_scan(vla_handle_t h, const void* x, const void* dt, const floa
   cudaError_t e = on_device(h->device, [&]() {
     bool used = false;
     cudaError_t r = cudaSuccess;
+    r = vla::launch_ssm_token(a, bf16, h->sm_count, static_cast<cudaStream_t>(stream), &used);
+    if (r != cudaSuccess || used) return r;
     if (plan.fits) r = vla::launch_ssm_prompt(a, plan, static_cast<cudaStream_t>(stream), &used);
     if (r != cudaSuccess || used) return r;
     return vla::launch_ssm_steps(a, bf16, h->sm_count, static_cast<cudaStream_t>(stream));
@@ -163,6 +165,7 @@ vla_err_t vla_rms_norm(vla_handle_t h, const void* x, const float* w, void* resi
   a.x = x; a.w = w; a.residual = residual; a.y = y; a.scale = scale;
   a.rows = rows; a.D = D; a.x_row = x_row; a.res_row = res_row; a.y_row = y_row;
   a.eps = eps; a.group = out == VLA_OUT_IO ? 0 : group; a.out = out; a.res_bf16 = res_dtype == VLA_BF16;
+  a.sm_count = h->sm_count;
   cudaError_t e = on_device(h->device, [&]() {
     return vla::launch_rms_norm(a, io_dtype == VLA_BF16, static_cast<cudaStream_t>(stream));
   });

@@ -73,6 +73,58 @@ __device__ __forceinline__ void st_vec(T* p, const Vec<T, VEC>& x) {
   *reinterpret_cast<decltype(x.raw)*>(p) = x.raw;
 }
 
+// Pairs of float32 in one 64-bit register, and their packed arithmetic (one instruction a pair).
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Two bfloat16 of one 32-bit word (a in the low half), and back.
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float hi_f(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+
+// x * sigmoid(x) of a pair with approximate exponential and reciprocal (a few ulp of float32).
+// e^-x overflows to infinity below -88: the reciprocal is then 0 and the result -0.
+__device__ __forceinline__ uint64_t silu2(uint64_t x) {
+  const float l = -1.44269504088896341f;
+  float a, b;
+  unpair(mul2(x, pair(l, l)), a, b);
+  unpair(add2(pair(ex2(a), ex2(b)), pair(1.f, 1.f)), a, b);
+  return mul2(x, pair(rcp(a), rcp(b)));
+}
+
 // x * sigmoid(x).  float32 results keep expf and the rounded division; a result that is rounded to
 // bfloat16 takes the approximate ones (a few ulp of float32).
 template <bool FAST>
@@ -113,6 +165,9 @@ struct SsmArgs {
   float* ws;              // segments' states (see vla_ssm_prompt.cu)
   DevStatus* status;
 };
+// One token a sequence; *used = false: not this form's call, nothing was launched.
+cudaError_t launch_ssm_token(const SsmArgs& a, bool bf16, int sm_count, cudaStream_t s, bool* used);
+// Token by token, any sizes.
 cudaError_t launch_ssm_steps(const SsmArgs& a, bool bf16, int sm_count, cudaStream_t s);
 
 struct NormArgs {
@@ -126,6 +181,7 @@ struct NormArgs {
   int group;        // 0 or 128
   int out;          // vla_out_t
   bool res_bf16;
+  int sm_count;
 };
 cudaError_t launch_rms_norm(const NormArgs& a, bool bf16, cudaStream_t s);
 

@@ -6,9 +6,12 @@
 //
 // One pass: a row stays in the registers of its threads between the sum of squares, the maximum and
 // the rounding, so x and the residual are read once and every output written once (7 bytes a value
-// for bfloat16 with a residual and e4m3); memory bound.  A row has TPR threads (a warp at least),
-// each with NV vectors of VEC adjacent values (16 bytes where alignment allows); short rows share
-// a block.  Sums run in float32 in a fixed order: the same bits every time.
+// for bfloat16 with a residual and e4m3); memory bound.  v is taken as (r w) / sqrt(..): the
+// largest |v| of a row is then the largest |r w| times the same factor, and the sum and the
+// maximum are reduced together, one barrier a row.  Blocks are persistent: w stays in registers
+// and the next row is loaded before the present one is reduced.  A row has `tpr` threads (whole
+// warps), each with NV vectors of VEC adjacent values (16 bytes where alignment allows); short rows
+// share a block.  Sums run in float32 in a fixed order: the same bits every time.
 #include "vla.h"
 #include "vla_layer.cuh"
 
@@ -22,166 +25,213 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-template <bool MAX>
-__device__ __forceinline__ float join(float a, float b) { return MAX ? max_nan(a, b) : a + b; }
-
-// Sum or maximum over the threads of a row (warps [w0, w0 + wn) of the block; `part` has a place
-// for each warp of the block).  Every thread of the block calls it.
-template <bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* part, int w0, int wn) {
+// N values to N codes: e4m3 saturated to 448, or integers to nearest even.  A NaN keeps e4m3's
+// code for it and gives the integer 0 (its scale is NaN).
+template <int OUT, int N>
+__device__ __forceinline__ void codes(const float (&v)[N], unsigned char* o) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = join<MAX>(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if (wn == 1) return v;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __syncthreads();   // `part` may still be read from the previous call
-  if (lane == 0) part[warp] = v;
-  __syncthreads();
-  v = lane < wn ? part[w0 + lane] : 0.f;   // 0 is neutral: sums of squares and magnitudes
+  for (int i = 0; i + 1 < N; i += 2) {
+    if (OUT == VLA_OUT_E4M3) {
+      unsigned short r;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v[i + 1]), "f"(v[i]));
+      o[i] = (unsigned char)(r & 0xff);
+      o[i + 1] = (unsigned char)(r >> 8);
+    } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = join<MAX>(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
-template <int OUT>
-__device__ __forceinline__ unsigned char code(float v) {
-  if (OUT == VLA_OUT_E4M3) return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
-  const int q = __float2int_rn(v);   // NaN gives 0 (its scale is NaN)
-  return (unsigned char)(signed char)(q > 127 ? 127 : q < -127 ? -127 : q);
+      for (int j = 0; j < 2; ++j) {
+        int r;
+        asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(r) : "f"(v[i + j]));
+        o[i + j] = (unsigned char)r;
+      }
+    }
+  }
+  if (N == 1) {
+    if (OUT == VLA_OUT_E4M3) {
+      o[0] = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+    } else {
+      int r;
+      asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(r) : "f"(v[0]));
+      o[0] = (unsigned char)r;
+    }
+  }
 }
 
 // RES: 0 none, 1 bfloat16, 2 float32
 template <typename T, int RES, int OUT, int VEC, int NV>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormArgs a, int tpr, int rows_per_cta) {
+__global__ void __launch_bounds__(NV == 1 ? 256 : NV == 2 ? 512 : 1024) rms_norm_kernel(const NormArgs a, int tpr, int rows_per_cta, float inv_d) {
   using R = typename std::conditional<RES == 1, __nv_bfloat16, float>::type;
-  __shared__ float part[32];
-  __shared__ float gmax[VEC == 1 && OUT != VLA_OUT_IO ? NV * 32 : 1];
+  constexpr int RV = sizeof(R) * VEC > 16 ? 16 / (int)sizeof(R) : VEC;   // 16 bytes an access
+  constexpr bool QUANT = OUT != VLA_OUT_IO;
+  __shared__ float part_ss[2][32], part_top[2][32];
+  __shared__ float gmax[2][VEC == 1 && QUANT ? NV * 32 : 1];
   const int slot = threadIdx.x / tpr, tid = threadIdx.x - slot * tpr;
-  const long long row = (long long)blockIdx.x * rows_per_cta + slot;
-  const bool live = row < a.rows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w0 = slot * (tpr >> 5), wn = tpr >> 5;
-  const T* x = static_cast<const T*>(a.x) + row * a.x_row;
-  R* res = static_cast<R*>(a.residual) + row * a.res_row;
+  const int D = (int)a.D;
 
-  float r[NV][VEC];
-  float ss = 0.f;
+  float w[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const long long e = ((long long)i * tpr + tid) * VEC;
-    if (live && e < a.D) {
-      const Vec<T, VEC> in = ld_vec<T, VEC>(x + e);
-      if (RES != 0) {
-        constexpr int RV = sizeof(R) * VEC > 16 ? 16 / (int)sizeof(R) : VEC;   // 16 bytes an access
+    const int e = (i * tpr + tid) * VEC;
 #pragma unroll
-        for (int j = 0; j < VEC; j += RV) {
-          Vec<R, RV> p = ld_vec<R, RV>(res + e + j);
+    for (int v = 0; v < VEC; ++v) w[i][v] = e < D ? a.w[e + v] : 0.f;
+  }
+  Vec<T, VEC> in[NV];
+  Vec<R, RV> res[NV][VEC / RV];
+  auto load = [&](long long row) {
+    if (row >= a.rows) return;
+    const T* x = static_cast<const T*>(a.x) + row * a.x_row;
+    const R* r = static_cast<const R*>(a.residual) + row * a.res_row;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + tid) * VEC;
+      if (e >= D) continue;
+      in[i] = ld_vec<T, VEC>(x + e);
+      if (RES != 0) {
+#pragma unroll
+        for (int j = 0; j < VEC / RV; ++j) res[i][j] = ld_vec<R, RV>(r + e + j * RV);
+      }
+    }
+  };
+  const long long step = (long long)gridDim.x * rows_per_cta;
+  long long row = (long long)blockIdx.x * rows_per_cta + slot;
+  load(row);
+  int par = 0;
+  for (long long first = (long long)blockIdx.x * rows_per_cta; first < a.rows; first += step, row += step, par ^= 1) {
+    const bool live = row < a.rows;
+    float r[NV][VEC];
+    float ss = 0.f, all = 0.f, top[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = (i * tpr + tid) * VEC;
+      top[i] = 0.f;
+      if (live && e < D) {
+#pragma unroll
+        for (int j = 0; j < VEC / RV; ++j) {
 #pragma unroll
           for (int v = 0; v < RV; ++v) {
-            r[i][j + v] = to_f32<T>(in.v[j + v]) + to_f32<R>(p.v[v]);
-            p.v[v] = from_f32<R>(r[i][j + v]);
+            float now = to_f32<T>(in[i].v[j * RV + v]);
+            if (RES != 0) {
+              now += to_f32<R>(res[i][j].v[v]);
+              res[i][j].v[v] = from_f32<R>(now);
+            }
+            ss = fmaf(now, now, ss);
+            now *= w[i][j * RV + v];
+            r[i][j * RV + v] = now;
+            if (QUANT) top[i] = max_nan(top[i], fabsf(now));
           }
-          st_vec<R, RV>(res + e + j, p);
+          if (RES != 0) st_vec<R, RV>(static_cast<R*>(a.residual) + row * a.res_row + e + j * RV, res[i][j]);
         }
+        if (QUANT) all = max_nan(all, top[i]);
       } else {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) r[i][v] = to_f32<T>(in.v[v]);
-      }
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) ss = fmaf(r[i][v], r[i][v], ss);
-    } else {
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) r[i][v] = 0.f;
-    }
-  }
-  ss = row_reduce<false>(ss, part, w0, wn);
-  const float rstd = rsqrtf(ss / (float)a.D + a.eps);
-  float top[NV], all = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const long long e = ((long long)i * tpr + tid) * VEC;
-    top[i] = 0.f;
-    if (live && e < a.D) {
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        r[i][v] = r[i][v] * rstd * a.w[e + v];
-        if (OUT != VLA_OUT_IO) top[i] = max_nan(top[i], fabsf(r[i][v]));
+        for (int v = 0; v < VEC; ++v) r[i][v] = 0.f;
       }
     }
-    all = max_nan(all, top[i]);
-  }
-  if (OUT == VLA_OUT_IO) {
-    T* y = static_cast<T*>(a.y) + row * a.y_row;
+    load(row + step);
+    // sum of squares and maximum over the row
+    const bool row_top = QUANT && a.group == 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const long long e = ((long long)i * tpr + tid) * VEC;
-      if (!live || e >= a.D) continue;
-      Vec<T, VEC> o;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) o.v[v] = from_f32<T>(r[i][v]);
-      st_vec<T, VEC>(y + e, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (row_top) all = max_nan(all, __shfl_xor_sync(0xffffffffu, all, o));
     }
-    return;
-  }
-  // the maximum over a row, or over the 128 / VEC adjacent threads of a group
-  if (a.group == 0) {
-    all = row_reduce<true>(all, part, w0, wn);
-  } else if (VEC > 1) {
+    if (QUANT && VEC == 1 && a.group) {   // a group is 4 warps (tpr is a multiple of 128 here)
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
 #pragma unroll
-      for (int o = 64 / VEC; o > 0; o >>= 1) top[i] = max_nan(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-  } else {
-    const int warp = threadIdx.x >> 5;   // a group is 4 warps (tpr is a multiple of 128 here)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top[i] = max_nan(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-      if ((threadIdx.x & 31) == 0) gmax[i * 32 + warp] = top[i];
+        for (int o = 16; o > 0; o >>= 1) top[i] = max_nan(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+        if (lane == 0) gmax[par][i * 32 + warp] = top[i];
+      }
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const float* g = gmax + i * 32 + (warp & ~3);
-      top[i] = max_nan(max_nan(g[0], g[1]), max_nan(g[2], g[3]));
+    if (wn > 1) {
+      // the other half of `part` is still read by warps that are a row behind
+      if (lane == 0) {
+        part_ss[par][warp] = ss;
+        if (row_top) part_top[par][warp] = all;
+      }
+      __syncthreads();
+      ss = lane < wn ? part_ss[par][w0 + lane] : 0.f;
+      if (row_top) all = lane < wn ? part_top[par][w0 + lane] : 0.f;
+      for (int o = wn > 16 ? 16 : wn > 8 ? 8 : wn > 4 ? 4 : 2; o > 0; o >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (row_top) all = max_nan(all, __shfl_xor_sync(0xffffffffu, all, o));
+      }
+      ss = __shfl_sync(0xffffffffu, ss, 0);
+      if (row_top) all = __shfl_sync(0xffffffffu, all, 0);
     }
-  }
-  unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.y_row;
-  const float full = OUT == VLA_OUT_E4M3 ? 448.f : 127.f;
-  const long long groups = (a.D + 127) / 128;
+    const float rstd = rsqrtf(fmaf(ss, inv_d, a.eps));
+    if (!QUANT) {
+      T* y = static_cast<T*>(a.y) + row * a.y_row;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const long long e = ((long long)i * tpr + tid) * VEC;
-    if (!live || e >= a.D) continue;
-    float scale = (a.group ? top[i] : all) / full;
+      for (int i = 0; i < NV; ++i) {
+        const int e = (i * tpr + tid) * VEC;
+        if (!live || e >= D) continue;
+        Vec<T, VEC> o;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) o.v[v] = from_f32<T>(r[i][v] * rstd);
+        st_vec<T, VEC>(y + e, o);
+      }
+      continue;
+    }
+    unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.y_row;
+    const float full = OUT == VLA_OUT_E4M3 ? 448.f : 127.f;
+    const int groups = (D + 127) / 128;
+    float scale = all * rstd / full, inv;
     if (scale < 1.17549435e-38f) scale = 1.f;   // false for a NaN
-    const float inv = 1.f / scale;
-    Vec<unsigned char, VEC == 1 ? 2 : VEC> o;   // VEC == 1 stores its byte alone
+    inv = 1.f / scale;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) o.v[v] = code<OUT>(r[i][v] * inv);
-    if constexpr (VEC == 1) y[e] = o.v[0];
-    else st_vec<unsigned char, VEC>(y + e, o);
-    if (a.group) {
-      if (e % 128 == 0) a.scale[row * groups + e / 128] = scale;
-    } else if (e == 0) {
-      a.scale[row] = scale;
+    for (int i = 0; i < NV; ++i) {
+      if (a.group) {
+        if (VEC > 1) {
+#pragma unroll
+          for (int o = 64 / VEC; o > 0; o >>= 1) top[i] = max_nan(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+        } else {
+          const float* g = gmax[par] + i * 32 + (warp & ~3);
+          top[i] = max_nan(max_nan(g[0], g[1]), max_nan(g[2], g[3]));
+        }
+        scale = top[i] * rstd / full;
+        if (scale < 1.17549435e-38f) scale = 1.f;
+        inv = 1.f / scale;
+      }
+      const int e = (i * tpr + tid) * VEC;
+      if (!live || e >= D) continue;
+      float v[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[j] = r[i][j] * rstd * inv;
+      Vec<unsigned char, VEC == 1 ? 2 : VEC> o;   // VEC == 1 stores its byte alone
+      codes<OUT, VEC>(v, o.v);
+      if constexpr (VEC == 1) y[e] = o.v[0];
+      else st_vec<unsigned char, VEC>(y + e, o);
+      if (a.group) {
+        if (e % 128 == 0) a.scale[row * groups + e / 128] = scale;
+      } else if (e == 0) {
+        a.scale[row] = scale;
+      }
     }
   }
 }
 
 template <typename T, int RES, int OUT, int VEC, int NV>
 cudaError_t launch(const NormArgs& a, cudaStream_t s) {
+  auto kern = rms_norm_kernel<T, RES, OUT, VEC, NV>;
   const int unit = VEC == 1 && a.group ? 128 : 32;
   const long long need = (a.D + (long long)VEC * NV - 1) / ((long long)VEC * NV);
   const int tpr = (int)((need + unit - 1) / unit * unit);
   const int rows = tpr >= 256 ? 1 : 256 / tpr;
-  const long long ctas = (a.rows + rows - 1) / rows;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  rms_norm_kernel<T, RES, OUT, VEC, NV><<<(unsigned int)ctas, tpr * rows, 0, s>>>(a, tpr, rows);
+  int per_sm = 0;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, tpr * rows, 0);
+  if (e != cudaSuccess) return e;
+  const long long all = (a.rows + rows - 1) / rows, most = (long long)(per_sm > 0 ? per_sm : 1) * a.sm_count;
+  kern<<<(unsigned int)(all < most ? all : most), tpr * rows, 0, s>>>(a, tpr, rows, 1.f / (float)a.D);
   return cudaGetLastError();
 }
 
+// Values a thread: few enough that the row after this one fits in registers too.
 template <typename T, int RES, int OUT, int VEC>
 cudaError_t by_width(const NormArgs& a, cudaStream_t s) {
-  if (a.D <= 1024LL * VEC) return launch<T, RES, OUT, VEC, 1>(a, s);
+  if (VEC > 1 && a.D <= 256LL * VEC) return launch<T, RES, OUT, VEC, VEC == 1 ? 2 : 1>(a, s);
+  if (a.D <= 1024LL * VEC) return launch<T, RES, OUT, VEC, 2>(a, s);
   if (a.D <= 4096LL * VEC) return launch<T, RES, OUT, VEC, 4>(a, s);
   return launch<T, RES, OUT, VEC, 32 / VEC>(a, s);   // up to 32768 values (the entry point's limit)
 }

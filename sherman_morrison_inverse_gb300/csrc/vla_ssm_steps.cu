@@ -4,11 +4,10 @@
 //
 // Rows of h never meet, so a CTA takes ROWS = 32 R of the P rows of one (sequence, head) and keeps
 // them in registers for the whole call: 8 lanes a row, lane j holding the states 32 i + 4 j .. + 3
-// (i < NI), so that a row of the state moves as 128-byte pieces.  This is the form for single
-// tokens, where reading and writing the float32 state (8 P N bytes a head) is all the time there
-// is, and for what the tensor-core form (vla_ssm_prompt.cu) does not take: float32 input and
-// output, short prompts, odd sizes and alignments.  On long prompts it is bound by the 3 float32
-// operations a state element and token.
+// (i < NI), so that a row of the state moves as 128-byte pieces.  This is the form for what the
+// single-token form (vla_ssm_token.cu) and the tensor-core form (vla_ssm_prompt.cu) do not take:
+// float32 input and output, short prompts, odd sizes and alignments.  On long prompts it is bound
+// by the 3 float32 operations a state element and token.
 // Everything is float32 and every sum has a fixed order: the same bits every time.
 #include "vla_layer.cuh"
 
