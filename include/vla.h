@@ -329,8 +329,8 @@ vla_err_t vla_scan_fwd_noalloc(const void* q, const void* k, const void* v, cons
  *
  * States.  `state` is a pool of n_slots states; sequence s continues from slot
  * slots[s] (device int32; NULL: slot s) and leaves its new state there.  A negative
- * slot skips its sequence: nothing of it is read or written, as for the padding of
- * a batch of fixed size.  No two sequences of a call may name one slot.  state NULL: every sequence starts
+ * slot skips its sequence: nothing of it is written and its inputs do not matter, as
+ * for the padding of a batch of fixed size.  No two sequences of a call may name one slot.  state NULL: every sequence starts
  * from zeros and its state is not kept.  A sequence without tokens leaves its state
  * as it is.
  *

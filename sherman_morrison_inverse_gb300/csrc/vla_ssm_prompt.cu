@@ -14,13 +14,21 @@
 // once (2^-9 relative, as the output itself is).  The suffix sums c_L - c_s are summed from
 // the end, so that what is left of the last tokens does not suffer from a large c_L.
 //
-// exp(c_t - c_s) takes no exponential a pair outside the four diagonal 32 x 32 blocks: with e_j the
-// sum at the end of block j of s, exp(c_t - e_j) exp(e_j - c_s) is one factor a row and one a column,
-// both at most 1.
+// exp(c_t - c_s) takes no exponential a pair: with e_j the sum at the end of block j of 32 tokens s,
+// exp(c_t - e_j) exp(e_j - c_s) is one factor a row and one a column, both at most 1, for the rows
+// behind the block.  In a diagonal block e_j is the sum before the block; the column's factor is
+// then at least 1, so this holds while the block's sums stay below 2^100, and beyond that (nothing
+// is left of a token a few tokens later) the exponentials are taken pair by pair.
+//
+// Roles.  Eight warps compute (thread = a row of the chunk, or a state n, and 32 of 64 columns);
+// the ninth issues the loads and the products and, while the tensor cores work, forms the decays of
+// the next chunk.  They meet on mbarriers.  In the order of a chunk:
+//   ninth: S, C h^T | computing: X~ | ninth: B^T X~ | computing: M, scaling of C h^T | ninth: M X,
+//   loads of the next B and C | computing: state, Y | ninth: Y's store, load of the next X.
 //
 // Operands.  B, C [128 tokens][N] and X [128][64] arrive by TMA as 128-byte-swizzled tiles of 64
 // columns; the same B tile is the K-major operand of S and the transposed (MN-major) one of the
-// state's product.  M goes back to tensor memory as the A operand of M X.  Shared memory is reused
+// state's product.  M replaces S in tensor memory as the A operand of M X.  Shared memory is reused
 // within a chunk (X~ overwrites C and the bfloat16 state once S and C h^T are done; Y overwrites X), which
 // keeps a CTA below half an SM's: two CTAs an SM hide each other's latencies.
 //
@@ -39,10 +47,13 @@ namespace vla {
 namespace {
 
 constexpr int kL = 128;            // tokens a chunk
-constexpr int kThreads = 256;
+constexpr int kCompute = 256;      // threads of the computing warps
+constexpr int kThreads = 288;
 constexpr uint32_t kTile = 16384;  // bytes of a [128][64] bfloat16 tile
-constexpr uint32_t kCols = 256;    // tensor memory columns a CTA: S | M | Y, the state's product over S
-constexpr uint32_t kColS = 0, kColU = 0, kColM = 128, kColY = 192;
+constexpr uint32_t kCols = 256;    // tensor memory columns a CTA: S (M) | Y | the state's product U
+constexpr uint32_t kColS = 0, kColY = 128, kColU = 192;
+constexpr int kVec = 5 * kL + 16;  // floats of a chunk's decays (two buffers)
+constexpr int kBars = 10;
 
 // Shared memory: B | C | X | state (bfloat16, [n][64 p]) | more X~ | vectors | barriers
 template <int NN>
@@ -55,7 +66,7 @@ struct Cfg {
   static constexpr uint32_t term1 = NN == 128 ? oC + kTile : oMore;
   static constexpr uint32_t term2 = NN == 128 ? oH : oMore + kTile;
   static constexpr uint32_t oVec = NN == 128 ? oMore : oMore + 2 * kTile;
-  static constexpr uint32_t bytes = oVec + 4 * (4 * kL + 16) + 8 * 4 + 16;
+  static constexpr uint32_t bytes = oVec + 4 * 2 * kVec + 8 * kBars + 16;
 };
 
 // Matrix descriptor of a 128-byte-swizzled operand: `lbo` bytes between blocks of 64 in the
@@ -155,45 +166,39 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
 
-  float* cum = reinterpret_cast<float*>(smem + Cf::oVec);   // [128] log2 decay up to a token, from the chunk's start
-  float* wcol = cum + kL;                                   // [128] s exp(e_j - c), j the token's block
-  float* wx = wcol + kL;                                    // [128] s exp(c_L - c)
-  float* step = wx + kL;                                    // [128] s
-  float* blk = step + kL;                                   // [4] block sums, [4..8) sums to the block's end, [8] total
-  uint64_t* bar = reinterpret_cast<uint64_t*>(blk + 16);    // full, S, Y, U
-  uint64_t *b_full = bar, *b_s = bar + 1, *b_y = bar + 2, *b_u = bar + 3;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + 4);
+  // decays of chunk c at vec + (c & 1) kVec: cum [128] log2 decay from the chunk's start up to a token;
+  // wcol [128] s exp(e_j - c), j the token's block; wdg [128] the same with the sum before the
+  // block; wx [128] s exp(c_L - c); step [128] s; then [4] sums before the blocks, [4] to their ends,
+  // [8] the total, [12..16) whether wdg holds
+  float* vec = reinterpret_cast<float*>(smem + Cf::oVec);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(vec + 2 * kVec);
+  uint64_t *b_bc = bar, *b_x = bar + 1, *b_dec = bar + 2;           // B and C, X loaded; decays written
+  uint64_t *b_s = bar + 3, *b_u = bar + 4, *b_y = bar + 5;          // products done: S and C h^T, U, M X
+  uint64_t *b_xt = bar + 6, *b_m = bar + 7;                         // X~, M written
+  uint64_t *b_next = bar + 8, *b_out = bar + 9;                     // tensor memory and h free; Y staged
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + kBars);
+  volatile int* fail = reinterpret_cast<volatile int*>(tslot + 1);
 
   const bool packed = a.seqs.offsets != nullptr;
   const int row0 = packed ? (int)q.start : 0, batch = packed ? 0 : (int)seq;   // tensor map coordinates
   const __nv_bfloat16* dt = a.dt + (packed ? q.start * a.dt_tok : seq * a.dt_seq) + head;
   const float A2 = a.A[head] * 1.44269504088896341f, bias = a.dt_bias ? a.dt_bias[head] : 0.f;
   const float Dh = a.D ? a.D[head] : 0.f;
-  constexpr uint32_t kLoad = (FULL ? 2 : 1) * Cf::NT * kTile + kTile;
-
-  auto issue_loads = [&](long long c) {   // one thread
-    const int t = row0 + (int)(c * kL);
-    mbar_arrive_expect_tx(b_full, kLoad);
-    for (uint32_t i = 0; i < Cf::NT; ++i) {
-      load_4d(sbase + Cf::oB + i * kTile, &map_B, 64 * (int)i, group, t, batch, b_full);
-      if (FULL) load_4d(sbase + Cf::oC + i * kTile, &map_C, 64 * (int)i, group, t, batch, b_full);
-    }
-    load_4d(sbase + Cf::oX, &map_x, p0, head, t, batch, b_full);
-  };
 
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(bar + i, 1);
+    for (int i = 0; i < 6; ++i) mbar_init(bar + i, 1);
+    for (int i = 6; i < kBars; ++i) mbar_init(bar + i, kCompute / 32);
+    *fail = 0;
     fence_mbar_init();
-    issue_loads(c_begin);
   }
   if (warp == 1) tc::tmem_alloc(tslot, kCols);
 
   // this thread's part of the state: n = row, 32 columns p from 32 half
-  const int row = tid & (kL - 1), half = tid >> 7;
+  const int row = tid & (kL - 1), half = (tid >> 7) & 1;
   const int n = row;
   const bool n_ok = n < a.N;
   float h[32];
-  {
+  if (tid < kCompute) {
     const int pc = a.P - p0 - 32 * half;   // columns of this thread that exist
     const bool from_ws = a.nseg > 1 && FULL && chunks > a.seg_chunks;
     float* wsq = from_ws || !FULL ? a.ws + (seq * slices + slice) * ws_floats(a.nseg, NN) : nullptr;
@@ -232,83 +237,125 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   };
-  if (FULL) put_state();
+  if (FULL && tid < kCompute) put_state();
   fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tslot;
-  const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);   // this warp's lanes
-  const int qd = warp & 3;                                            // its block of rows
-  if (FULL) {   // M's blocks above the diagonal stay zero
-    const uint32_t zero[16] = {};
-    for (int j = qd + 1; j < 4; ++j)
-      if ((j >> 1) == half) tmem_st16(tlane + kColM + 16 * j, zero);
-    tmem_wait_st();
-  }
   constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
   constexpr uint32_t kId64 = (1u << 4) | (1u << 7) | (1u << 10) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
-  const bool issuer = tid == 0;
-
-  float log_total = 0.f;
-  bool failed = false;
-  auto dt_at = [&](long long c) {
-    const long long t = c * kL + tid;
-    return tid < kL && t < q.len ? __bfloat162float(dt[t * a.dt_tok]) : 0.f;
-  };
-  float dt_next = dt_at(c_begin);
-  uint32_t phase = 0;
-  bool loads_pending = true;
-  for (long long c = c_begin; c < c_end; ++c, phase ^= 1u) {
-    const long long t0 = c * kL;
-    const int valid = (int)(q.len - t0 < kL ? q.len - t0 : kL);
-    // ---- decays
-    float s = 0.f, inc = 0.f, suf = 0.f, ex = 0.f;
-    if (tid < kL) {
-      s = tid < valid ? time_step(dt_next, bias, a.softplus) : 0.f;
-      const float l = tid < valid ? A2 * s : 0.f;
-      inc = suf = l;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, inc, o), d = __shfl_down_sync(0xffffffffu, suf, o);
-        if (lane >= o) inc += u;
-        if (lane + o < 32) suf += d;
-      }
-      ex = __shfl_down_sync(0xffffffffu, suf, 1);
-      if (lane == 31) { ex = 0.f; blk[warp] = inc; }
+  // Bounded wait of a whole warp; gives up early when another one has.
+  auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
+    bool ok = mbar_try_wait(b, parity);
+    if (!ok) {
+      const unsigned long long t_start = globaltimer_ns();
+      while (!(ok = mbar_try_wait(b, parity)))
+        if (*fail || globaltimer_ns() - t_start > kWaitLimitNs) break;
     }
-    if (__syncthreads_or(failed)) break;
-    if (tid < kL) {
-      float before = 0.f, after = 0.f;
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) *fail = 1;
+    return ok;
+  };
+  // One arrival a warp, after everything its lanes have written to shared or tensor memory.
+  auto arrive = [&](uint64_t* b) {
+    fence_proxy_async_smem();
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+  };
+
+  if (warp == kCompute / 32) {
+    // ------------------------------------------------ loads, products, decays
+    const bool one = lane == 0;
+    auto load_bc = [&](long long c) {
+      const int t = row0 + (int)(c * kL);
+      mbar_arrive_expect_tx(b_bc, (FULL ? 2 : 1) * Cf::NT * kTile);
+      for (uint32_t i = 0; i < Cf::NT; ++i) {
+        load_4d(sbase + Cf::oB + i * kTile, &map_B, 64 * (int)i, group, t, batch, b_bc);
+        if (FULL) load_4d(sbase + Cf::oC + i * kTile, &map_C, 64 * (int)i, group, t, batch, b_bc);
+      }
+    };
+    auto load_x = [&](long long c) {
+      mbar_arrive_expect_tx(b_x, kTile);
+      load_4d(sbase + Cf::oX, &map_x, p0, head, row0 + (int)(c * kL), batch, b_x);
+    };
+    float raw[4];   // dt of the chunk whose decays come next: tokens lane, 32 + lane, ..
+    auto load_dt = [&](long long c) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j < warp) before += blk[j];
-        if (j > warp) after += blk[j];
+        const long long t = c * kL + 32 * j + lane;
+        raw[j] = t < q.len ? __bfloat162float(dt[t * a.dt_tok]) : 0.f;
       }
-      cum[tid] = before + inc;
-      step[tid] = s;
-      wcol[tid] = s * ex2(ex);
-      wx[tid] = s * ex2(ex + after);
-      if (lane == 31) blk[4 + warp] = before + inc;
-    }
-    const float total = blk[0] + blk[1] + blk[2] + blk[3];
-    if (c + 1 < c_end) dt_next = dt_at(c + 1);
-    const bool tail = packed && valid < kL;   // rows of the next sequence lie behind this one's
-    if (tail) {
-      failed |= !mbar_wait_bounded(b_full, phase);
-      for (int e = tid; e < (kL - valid) * 8; e += kThreads) {
-        const uint32_t at = (uint32_t)(valid + (e >> 3)) * 128 + ((e & 7) << 4);
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(smem + Cf::oX + at) = zero;
-        for (uint32_t i = 0; i < Cf::NT; ++i) *reinterpret_cast<uint4*>(smem + Cf::oB + i * kTile + at) = zero;
+    };
+    auto decays = [&](long long c) {
+      float* v = vec + (c & 1) * kVec;
+      float s[4], inc[4], ex[4], end[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = c * kL + 32 * j + lane < q.len;
+        s[j] = in ? time_step(raw[j], bias, a.softplus) : 0.f;
+        inc[j] = in ? A2 * s[j] : 0.f;
+        ex[j] = inc[j];
       }
-      fence_proxy_async_smem();
-      if (__syncthreads_or(failed)) break;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float u = __shfl_up_sync(0xffffffffu, inc[j], o), d = __shfl_down_sync(0xffffffffu, ex[j], o);
+          if (lane >= o) inc[j] += u;
+          if (lane + o < 32) ex[j] += d;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        end[j] = __shfl_sync(0xffffffffu, inc[j], 31);
+        ex[j] = __shfl_down_sync(0xffffffffu, ex[j], 1);
+        if (lane == 31) ex[j] = 0.f;
+      }
+      float before = 0.f, after[4];
+      after[3] = 0.f;
+#pragma unroll
+      for (int j = 2; j >= 0; --j) after[j] = after[j + 1] + end[j + 1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = 32 * j + lane;
+        v[t] = before + inc[j];
+        v[kL + t] = s[j] * ex2(ex[j]);
+        v[2 * kL + t] = s[j] * ex2(-inc[j]);
+        v[3 * kL + t] = s[j] * ex2(ex[j] + after[j]);
+        v[4 * kL + t] = s[j];
+        const bool small = __all_sync(0xffffffffu, fabsf(inc[j]) < 100.f);
+        if (lane == 0) {
+          v[5 * kL + j] = before;
+          v[5 * kL + 4 + j] = before + end[j];
+          v[5 * kL + 12 + j] = small ? 1.f : 0.f;
+        }
+        before += end[j];
+      }
+      if (lane == 0) v[5 * kL + 8] = before;
+    };
+    auto publish = [&]() {
+      __syncwarp();
+      if (one) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b_dec)) : "memory");
+    };
+    if (one) {
+      load_bc(c_begin);
+      load_x(c_begin);
     }
-    if (FULL && issuer) {
-      failed |= !mbar_wait_bounded(b_full, phase);
-      if (!failed) {
-        tc::fence_after_sync();
+    load_dt(c_begin);
+    decays(c_begin);
+    publish();
+    if (c_begin + 1 < c_end) load_dt(c_begin + 1);
+    uint32_t ph = 0, bc_ph = 0, x_ph = 0;   // phases of the loads in flight
+    bool bc_pending = true, x_pending = true;
+    for (long long c = c_begin; c < c_end; ++c, ph ^= 1u) {
+      const bool more = c + 1 < c_end;
+      if (c > c_begin && !wait(b_next, ph ^ 1u)) break;
+      if (!wait(b_bc, ph)) break;
+      bc_pending = false;
+      tc::fence_after_sync();
+      if (FULL && one) {
 #pragma unroll
         for (int k = 0; k < NN / 16; ++k) {
           const uint32_t at = (uint32_t)(k >> 2) * kTile + (uint32_t)(k & 3) * 32;
@@ -322,105 +369,194 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         tc::mma_commit(b_s);
       }
-    }
-    if (__syncthreads_or(failed)) break;   // the vectors are written
-    const float my_cum = cum[row];
-    if (FULL) {
-      // ---- M from S, and the state's part of Y scaled by the row's decay
-      failed |= !mbar_wait_bounded(b_s, phase);
+      __syncwarp();
+      if (more) {
+        decays(c + 1);
+        if (c + 2 < c_end) load_dt(c + 2);
+      }
+      if (!wait(b_xt, ph)) break;
+      x_pending = false;   // the computing warps have seen X, and this chunk's decays
+      if (more) publish();
       tc::fence_after_sync();
-#pragma unroll 1
-      for (int jj = 0; jj < 2; ++jj) {
-        const int j = 2 * half + jj;
-        if (j > qd) break;
-        float v[32];
-        tc::tmem_ld32(tlane + kColS + 32 * j, v);
-        uint32_t m[16];
-        if (j < qd) {
-          const float r = ex2(my_cum - blk[4 + j]);
+      if (one) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(wcol + 32 * j + i);
-            m[i / 2] = pack2(v[i] * r * w.x, v[i + 1] * r * w.y);
-            m[i / 2 + 1] = pack2(v[i + 2] * r * w.z, v[i + 3] * r * w.w);
-          }
-        } else {
+        for (int t = 0; t < 3; ++t) {
+          const uint32_t term = t == 0 ? Cf::term2 : t == 1 ? Cf::term1 : Cf::term0;   // small terms first
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 cs = *reinterpret_cast<const float4*>(cum + 32 * j + i);
-            const float4 ss = *reinterpret_cast<const float4*>(step + 32 * j + i);
-            const float e0 = i <= lane ? v[i] * ex2(my_cum - cs.x) * ss.x : 0.f;
-            const float e1 = i + 1 <= lane ? v[i + 1] * ex2(my_cum - cs.y) * ss.y : 0.f;
-            const float e2 = i + 2 <= lane ? v[i + 2] * ex2(my_cum - cs.z) * ss.z : 0.f;
-            const float e3 = i + 3 <= lane ? v[i + 3] * ex2(my_cum - cs.w) * ss.w : 0.f;
-            m[i / 2] = pack2(e0, e1);
-            m[i / 2 + 1] = pack2(e2, e3);
-          }
+          for (int k = 0; k < kL / 16; ++k)
+            tc::mma_f16(tmem + kColU, desc128(sbase + Cf::oB + 2048u * k, kTile),
+                        desc128(sbase + term + 2048u * k, 16), kId64 | kTransA | kTransB, t > 0 || k > 0);
         }
-        tmem_st16(tlane + kColM + 16 * j, m);
+        tc::mma_commit(b_u);
       }
-      {
-        float v[32];
-        tc::tmem_ld32(tlane + kColY + 32 * half, v);
-        const float r = ex2(my_cum);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= r;
-        tc::tmem_st32(tlane + kColY + 32 * half, v);
-      }
-      tmem_wait_st();
-      tc::fence_before_sync();
-      if (__syncthreads_or(failed)) break;
-      if (issuer) {
+      __syncwarp();
+      if (FULL) {
+        if (!wait(b_m, ph)) break;
         tc::fence_after_sync();
+        if (one) {
 #pragma unroll
-        for (int k = 0; k < kL / 16; ++k)
-          mma_f16_tx(tmem + kColY, tmem + kColM + 8 * k, desc128(sbase + Cf::oX + 2048u * k, 16), kId64 | kTransB, true);
-        tc::mma_commit(b_y);
-      }
-    }
-    // ---- X~ in three terms: this thread's token `row`, 32 columns
-    loads_pending = !mbar_wait_bounded(b_full, phase);
-    failed |= loads_pending;
-    uint4 xr[4];
-    {
-      const float w = wx[row];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t at = (uint32_t)row * 128 + (((4 * half + i) ^ (row & 7)) << 4);
-        xr[i] = *reinterpret_cast<const uint4*>(smem + Cf::oX + at);
-        const uint32_t in[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
-        uint32_t t1[4], t2[4], t3[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float u = lo_f(in[j]) * w, v = hi_f(in[j]) * w;
-          t1[j] = pack2(u, v);
-          u -= lo_f(t1[j]);   // exact
-          v -= hi_f(t1[j]);
-          t2[j] = pack2(u, v);
-          t3[j] = pack2(u - lo_f(t2[j]), v - hi_f(t2[j]));
+          for (int k = 0; k < kL / 16; ++k)
+            mma_f16_tx(tmem + kColY, tmem + kColS + 64 * (k >> 2) + 8 * (k & 3), desc128(sbase + Cf::oX + 2048u * k, 16),
+                       kId64 | kTransB, true);
+          tc::mma_commit(b_y);
         }
-        *reinterpret_cast<uint4*>(smem + Cf::term0 + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-        *reinterpret_cast<uint4*>(smem + Cf::term1 + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-        *reinterpret_cast<uint4*>(smem + Cf::term2 + at) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+        __syncwarp();
+      }
+      if (more) {
+        if (!wait(b_u, ph)) break;
+        if (one) {
+          load_bc(c + 1);
+          if (!FULL) load_x(c + 1);
+        }
+        bc_pending = true;
+        bc_ph = ph ^ 1u;
+        if (!FULL) x_pending = true, x_ph = ph ^ 1u;
+        __syncwarp();
+      }
+      if (FULL) {
+        if (!wait(b_out, ph)) break;
+        const bool tail = packed && q.len - c * kL < kL;
+        if (one) {
+          if (!tail) store_4d(&map_y, p0, head, row0 + (int)(c * kL), batch, sbase + Cf::oX);
+          if (more) {
+            store_read_done();
+            load_x(c + 1);
+          }
+        }
+        if (more) x_pending = true, x_ph = ph ^ 1u;
+        __syncwarp();
       }
     }
-    fence_proxy_async_smem();
-    if (__syncthreads_or(failed)) break;
-    if (issuer) {
+    // nothing lands after the CTA has gone
+    if (*fail) {
+      if (bc_pending) mbar_wait_bounded(b_bc, bc_ph);
+      if (x_pending) mbar_wait_bounded(b_x, x_ph);
+    }
+    if (FULL && one) store_done();
+  } else {
+    // ------------------------------------------------ arithmetic
+    const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);   // this warp's lanes
+    const int qd = warp & 3;                                            // its block of rows
+    const uint32_t rsw = (uint32_t)(row & 7);
+    float log_total = 0.f;
+    uint32_t ph = 0;
+    for (long long c = c_begin; c < c_end; ++c, ph ^= 1u) {
+      const long long t0 = c * kL;
+      const bool tail = packed && q.len - t0 < kL;   // rows of the next sequence lie behind this one's
+      const bool in = t0 + row < q.len;
+      const float* v = vec + (c & 1) * kVec;
+      if (!wait(b_dec, ph) || !wait(b_x, ph)) break;
+      if (FULL ? !wait(b_s, ph) : !wait(b_bc, ph)) break;
       tc::fence_after_sync();
+      // ---- X~ in three terms: token `row`, 32 columns
+      {
+        const float w = v[3 * kL + row];
+        const uint64_t w2 = pair(w, w), minus = pair(-1.f, -1.f);
+        const bool clear = tail && !in;
 #pragma unroll
-      for (int t = 0; t < 3; ++t) {
-        const uint32_t term = t == 0 ? Cf::term2 : t == 1 ? Cf::term1 : Cf::term0;   // small terms first
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at = (uint32_t)row * 128 + (((4 * half + i) ^ rsw) << 4);
+          uint4 xv = *reinterpret_cast<const uint4*>(smem + Cf::oX + at);
+          if (clear) {
+            xv = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + Cf::oX + at) = xv;
+            for (uint32_t k = 0; k < Cf::NT; ++k) *reinterpret_cast<uint4*>(smem + Cf::oB + k * kTile + at) = xv;
+          }
+          const uint32_t xi[4] = {xv.x, xv.y, xv.z, xv.w};
+          uint32_t t1[4], t2[4], t3[4];
 #pragma unroll
-        for (int k = 0; k < kL / 16; ++k)
-          tc::mma_f16(tmem + kColU, desc128(sbase + Cf::oB + 2048u * k, kTile), desc128(sbase + term + 2048u * k, 16),
-                      kId64 | kTransA | kTransB, t > 0 || k > 0);
+          for (int j = 0; j < 4; ++j) {
+            float e, f;
+            uint64_t u = mul2(pair(lo_f(xi[j]), hi_f(xi[j])), w2);
+            unpair(u, e, f);
+            t1[j] = pack2(e, f);
+            u = fma2(pair(lo_f(t1[j]), hi_f(t1[j])), minus, u);   // exact
+            unpair(u, e, f);
+            t2[j] = pack2(e, f);
+            u = fma2(pair(lo_f(t2[j]), hi_f(t2[j])), minus, u);
+            unpair(u, e, f);
+            t3[j] = pack2(e, f);
+          }
+          *reinterpret_cast<uint4*>(smem + Cf::term0 + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+          *reinterpret_cast<uint4*>(smem + Cf::term1 + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+          *reinterpret_cast<uint4*>(smem + Cf::term2 + at) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+        }
       }
-      tc::mma_commit(b_u);
-    }
-    if (FULL) {
-      // ---- output rows: Y + D x, gated
-      const bool out = t0 + row < q.len;
+      arrive(b_xt);
+      if (FULL) {
+        // ---- M from S in place, and the state's part of Y scaled by the row's decay
+        const float my_cum = v[row];
+#pragma unroll 1
+        for (int jj = 0; jj < 2; ++jj) {
+          const int j = 2 * half + jj;
+          uint32_t m[16];
+          if (j > qd) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m[i] = 0;
+          } else {
+            float s[32];
+            tc::tmem_ld32(tlane + kColS + 32 * j, s);
+            const bool diag = j == qd;
+            if (!diag || v[5 * kL + 12 + j] != 0.f) {
+              const float r = ex2(my_cum - v[5 * kL + (diag ? 0 : 4) + j]);
+              const float* wv = v + (diag ? 2 : 1) * kL + 32 * j;
+              const uint64_t r2 = pair(r, r);
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(wv + i);
+                float e0, e1, e2, e3;
+                unpair(mul2(mul2(pair(s[i], s[i + 1]), pair(w.x, w.y)), r2), e0, e1);
+                unpair(mul2(mul2(pair(s[i + 2], s[i + 3]), pair(w.z, w.w)), r2), e2, e3);
+                if (diag) {
+                  e0 = i <= lane ? e0 : 0.f;
+                  e1 = i + 1 <= lane ? e1 : 0.f;
+                  e2 = i + 2 <= lane ? e2 : 0.f;
+                  e3 = i + 3 <= lane ? e3 : 0.f;
+                }
+                m[i / 2] = pack2(e0, e1);
+                m[i / 2 + 1] = pack2(e2, e3);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 cs = *reinterpret_cast<const float2*>(v + 32 * j + i);
+                const float2 ss = *reinterpret_cast<const float2*>(v + 4 * kL + 32 * j + i);
+                m[i / 2] = pack2(i <= lane ? s[i] * ex2(my_cum - cs.x) * ss.x : 0.f,
+                                 i + 1 <= lane ? s[i + 1] * ex2(my_cum - cs.y) * ss.y : 0.f);
+              }
+            }
+          }
+          tmem_st16(tlane + kColS + 64 * half + 16 * jj, m);
+        }
+        {
+          float y[32];
+          tc::tmem_ld32(tlane + kColY + 32 * half, y);
+          const float r = ex2(my_cum);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] *= r;
+          tc::tmem_st32(tlane + kColY + 32 * half, y);
+        }
+        tmem_wait_st();
+        arrive(b_m);
+      }
+      // ---- the state after the chunk
+      const float total = v[5 * kL + 8];
+      if (!wait(b_u, ph)) break;
+      tc::fence_after_sync();
+      {
+        float u[32];
+        tc::tmem_ld32(tlane + kColU + 32 * half, u);
+        const float d = ex2(total);
+        const uint64_t d2 = pair(d, d);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) unpair(fma2(d2, pair(h[i], h[i + 1]), pair(u[i], u[i + 1])), h[i], h[i + 1]);
+        log_total += total;
+      }
+      if (!FULL) {
+        arrive(b_next);
+        continue;
+      }
+      if (c + 1 < c_end) put_state();
       uint4 zr[4];
       if (a.z) {
         const __nv_bfloat16* z = a.z + (packed ? (q.start + t0 + row) * a.z_tok : seq * a.z_seq + (t0 + row) * a.z_tok) +
@@ -429,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           zr[i] = make_uint4(0, 0, 0, 0);
-          if (!out || 8 * i >= pc) continue;
+          if (!in || 8 * i >= pc) continue;
           if (a.z_vec) {
             zr[i] = *reinterpret_cast<const uint4*>(z + 8 * i);
           } else {
@@ -439,65 +575,38 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
-      failed |= !mbar_wait_bounded(b_y, phase);
+      if (!wait(b_y, ph)) break;
       tc::fence_after_sync();
-      float v[32];
-      tc::tmem_ld32(tlane + kColY + 32 * half, v);
-      __nv_bfloat16* y = a.y + (packed ? (q.start + t0 + row) * a.y_tok : 0) + (long long)head * a.P + p0 + 32 * half;
+      float y[32];
+      tc::tmem_ld32(tlane + kColY + 32 * half, y);
+      arrive(b_next);   // the next chunk's S and C h^T may start
+      // ---- output rows: Y + D x, gated
+      __nv_bfloat16* yp = a.y + (packed ? (q.start + t0 + row) * a.y_tok : 0) + (long long)head * a.P + p0 + 32 * half;
+      const uint64_t D2 = pair(Dh, Dh);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t in[4] = {xr[i].x, xr[i].y, xr[i].z, xr[i].w};
+        const uint32_t at = (uint32_t)row * 128 + (((4 * half + i) ^ rsw) << 4);
+        const uint4 xv = *reinterpret_cast<const uint4*>(smem + Cf::oX + at);
+        const uint32_t xi[4] = {xv.x, xv.y, xv.z, xv.w};
         const uint32_t zi[4] = {zr[i].x, zr[i].y, zr[i].z, zr[i].w};
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float u = fmaf(Dh, lo_f(in[j]), v[8 * i + 2 * j]), w = fmaf(Dh, hi_f(in[j]), v[8 * i + 2 * j + 1]);
-          if (a.z) {
-            u *= silu<true>(lo_f(zi[j]));
-            w *= silu<true>(hi_f(zi[j]));
-          }
-          o[j] = pack2(u, w);
+          uint64_t u = fma2(D2, pair(lo_f(xi[j]), hi_f(xi[j])), pair(y[8 * i + 2 * j], y[8 * i + 2 * j + 1]));
+          if (a.z) u = mul2(u, silu2(pair(lo_f(zi[j]), hi_f(zi[j]))));
+          float e, f;
+          unpair(u, e, f);
+          o[j] = pack2(e, f);
         }
         const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
-        if (!tail) {
-          *reinterpret_cast<uint4*>(smem + Cf::oX + (uint32_t)row * 128 + (((4 * half + i) ^ (row & 7)) << 4)) = ov;
-        } else if (out && p0 + 32 * half + 8 * i < a.P) {
-          *reinterpret_cast<uint4*>(y + 8 * i) = ov;
-        }
+        if (!tail) *reinterpret_cast<uint4*>(smem + Cf::oX + at) = ov;
+        else if (in && p0 + 32 * half + 8 * i < a.P) *reinterpret_cast<uint4*>(yp + 8 * i) = ov;
       }
-      fence_proxy_async_smem();
-      tc::fence_before_sync();
-      if (__syncthreads_or(failed)) break;
-      if (issuer && !tail) store_4d(&map_y, p0, head, row0 + (int)t0, batch, sbase + Cf::oX);
+      arrive(b_out);
     }
-    // ---- the state after the chunk
-    failed |= !mbar_wait_bounded(b_u, phase);
-    tc::fence_after_sync();
-    {
-      float v[32];
-      tc::tmem_ld32(tlane + kColU + 32 * half, v);
-      const float d = ex2(total);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) h[i] = fmaf(d, h[i], v[i]);
-      log_total += total;
-    }
-    if (FULL && c + 1 < c_end) put_state();
-    fence_proxy_async_smem();
-    tc::fence_before_sync();
-    if (__syncthreads_or(failed)) break;   // every tile of this chunk is free
-    if (c + 1 < c_end) {
-      if (issuer) {
-        store_read_done();
-        issue_loads(c + 1);
-      }
-      loads_pending = true;
-    }
-  }
-  if (failed) {
-    if (tid == 0) atomicOr(&a.status->flags, kStatusTimeout);
-    if (loads_pending && tid == 0) mbar_wait_bounded(b_full, phase);   // nothing lands after the CTA has gone
-  } else if (!FULL || last) {
-    if (!FULL) {
+    if (*fail) {
+      if (tid == 0) atomicOr(&a.status->flags, kStatusTimeout);
+    } else if (!FULL) {
       if (n < NN) {
         float* wsq = a.ws + (seq * slices + slice) * ws_floats(a.nseg, NN);
         float* e = wsq + ((long long)seg * 64 + 32 * half) * NN;
@@ -505,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < 32; ++i) e[i * NN + n] = h[i];
         if (tid == 0) wsq[(long long)a.nseg * 64 * NN + seg] = ex2(log_total);
       }
-    } else if (a.state && n_ok) {
+    } else if (last && a.state && n_ok) {
       float* dst = a.state + ((q.slot * a.H + head) * a.P + p0 + 32 * half) * a.N + n;
       const int pc = a.P - p0 - 32 * half;
 #pragma unroll
@@ -513,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (i < pc) dst[(long long)i * a.N] = h[i];
     }
   }
-  if (FULL && issuer) store_done();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
