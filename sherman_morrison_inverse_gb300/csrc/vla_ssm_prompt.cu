@@ -21,8 +21,8 @@
 // is left of a token a few tokens later) the exponentials are taken pair by pair.
 //
 // Roles.  Eight warps compute (thread = a row of the chunk, or a state n, and 32 of 64 columns);
-// the ninth issues the loads and the products and, while the tensor cores work, forms the decays of
-// the next chunk.  They meet on mbarriers.  In the order of a chunk:
+// the ninth issues the loads and the products, and the tenth forms the decays, up to two chunks
+// ahead.  They meet on mbarriers.  In the order of a chunk:
 //   ninth: S, C h^T | computing: X~ | ninth: B^T X~ | computing: M, scaling of C h^T | ninth: M X,
 //   loads of the next B and C | computing: state, Y | ninth: Y's store, load of the next X.
 //
@@ -48,12 +48,12 @@ namespace {
 
 constexpr int kL = 128;            // tokens a chunk
 constexpr int kCompute = 256;      // threads of the computing warps
-constexpr int kThreads = 288;
+constexpr int kThreads = 320;
 constexpr uint32_t kTile = 16384;  // bytes of a [128][64] bfloat16 tile
 constexpr uint32_t kCols = 256;    // tensor memory columns a CTA: S (M) | Y | the state's product U
 constexpr uint32_t kColS = 0, kColY = 128, kColU = 192;
 constexpr int kVec = 5 * kL + 16;  // floats of a chunk's decays (two buffers)
-constexpr int kBars = 10;
+constexpr int kBars = 13;
 
 // Shared memory: B | C | X | state (bfloat16, [n][64 p]) | more X~ | vectors | barriers
 template <int NN>
@@ -105,6 +105,13 @@ __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, in
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
+}
+// the tile of a later load, from memory into L2
+__device__ __forceinline__ void prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 __device__ __forceinline__ void store_4d(const CUtensorMap* map, int x, int y, int z, int w, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];\n\t"
@@ -172,10 +179,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   // [8] the total, [12..16) whether wdg holds
   float* vec = reinterpret_cast<float*>(smem + Cf::oVec);
   uint64_t* bar = reinterpret_cast<uint64_t*>(vec + 2 * kVec);
-  uint64_t *b_bc = bar, *b_x = bar + 1, *b_dec = bar + 2;           // B and C, X loaded; decays written
-  uint64_t *b_s = bar + 3, *b_u = bar + 4, *b_y = bar + 5;          // products done: S and C h^T, U, M X
-  uint64_t *b_xt = bar + 6, *b_m = bar + 7;                         // X~, M written
-  uint64_t *b_next = bar + 8, *b_out = bar + 9;                     // tensor memory and h free; Y staged
+  uint64_t *b_bc = bar, *b_x = bar + 1, *b_dec = bar + 2;           // B and C, X loaded; decays written [2]
+  uint64_t *b_s = bar + 4, *b_u = bar + 5, *b_y = bar + 6;          // products done: S and C h^T, U, M X
+  uint64_t *b_xt = bar + 7, *b_m = bar + 8, *b_free = bar + 9;      // X~, M written; decays read [2]
+  uint64_t *b_next = bar + 11, *b_out = bar + 12;                   // tensor memory and h free; Y staged
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + kBars);
   volatile int* fail = reinterpret_cast<volatile int*>(tslot + 1);
 
@@ -186,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float Dh = a.D ? a.D[head] : 0.f;
 
   if (tid == 0) {
-    for (int i = 0; i < 6; ++i) mbar_init(bar + i, 1);
-    for (int i = 6; i < kBars; ++i) mbar_init(bar + i, kCompute / 32);
+    for (int i = 0; i < 7; ++i) mbar_init(bar + i, 1);
+    for (int i = 7; i < kBars; ++i) mbar_init(bar + i, kCompute / 32);
     *fail = 0;
     fence_mbar_init();
   }
@@ -245,13 +252,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t tmem = *tslot;
   constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
   constexpr uint32_t kId64 = (1u << 4) | (1u << 7) | (1u << 10) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
-  // Bounded wait of a whole warp; gives up early when another one has.
+  // Bounded wait of a whole warp; gives up early when another one has.  The timer is read once in
+  // many polls: it takes longer than a poll, and a wait ends when the poll after it is made.
   auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
-    bool ok = mbar_try_wait(b, parity);
-    if (!ok) {
-      const unsigned long long t_start = globaltimer_ns();
-      while (!(ok = mbar_try_wait(b, parity)))
-        if (*fail || globaltimer_ns() - t_start > kWaitLimitNs) break;
+    bool ok = false;
+    unsigned long long t_start = 0;
+    while (true) {
+#pragma unroll 1
+      for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(b, parity);
+      if (ok || *fail) break;
+      const unsigned long long now = globaltimer_ns();
+      if (t_start == 0) t_start = now;
+      if (now - t_start > kWaitLimitNs) break;
     }
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) *fail = 1;
@@ -280,73 +292,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       mbar_arrive_expect_tx(b_x, kTile);
       load_4d(sbase + Cf::oX, &map_x, p0, head, row0 + (int)(c * kL), batch, b_x);
     };
-    float raw[4];   // dt of the chunk whose decays come next: tokens lane, 32 + lane, ..
-    auto load_dt = [&](long long c) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const long long t = c * kL + 32 * j + lane;
-        raw[j] = t < q.len ? __bfloat162float(dt[t * a.dt_tok]) : 0.f;
+    // a chunk's tiles are asked for when their places are free, which is late: their rows are fetched
+    // into L2 two chunks ahead
+    auto prefetch = [&](long long c) {
+      const int t = row0 + (int)(c * kL);
+      prefetch_4d(&map_x, p0, head, t, batch);
+      for (uint32_t i = 0; i < Cf::NT; ++i) {
+        prefetch_4d(&map_B, 64 * (int)i, group, t, batch);
+        if (FULL) prefetch_4d(&map_C, 64 * (int)i, group, t, batch);
       }
-    };
-    auto decays = [&](long long c) {
-      float* v = vec + (c & 1) * kVec;
-      float s[4], inc[4], ex[4], end[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = c * kL + 32 * j + lane < q.len;
-        s[j] = in ? time_step(raw[j], bias, a.softplus) : 0.f;
-        inc[j] = in ? A2 * s[j] : 0.f;
-        ex[j] = inc[j];
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float u = __shfl_up_sync(0xffffffffu, inc[j], o), d = __shfl_down_sync(0xffffffffu, ex[j], o);
-          if (lane >= o) inc[j] += u;
-          if (lane + o < 32) ex[j] += d;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        end[j] = __shfl_sync(0xffffffffu, inc[j], 31);
-        ex[j] = __shfl_down_sync(0xffffffffu, ex[j], 1);
-        if (lane == 31) ex[j] = 0.f;
-      }
-      float before = 0.f, after[4];
-      after[3] = 0.f;
-#pragma unroll
-      for (int j = 2; j >= 0; --j) after[j] = after[j + 1] + end[j + 1];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = 32 * j + lane;
-        v[t] = before + inc[j];
-        v[kL + t] = s[j] * ex2(ex[j]);
-        v[2 * kL + t] = s[j] * ex2(-inc[j]);
-        v[3 * kL + t] = s[j] * ex2(ex[j] + after[j]);
-        v[4 * kL + t] = s[j];
-        const bool small = __all_sync(0xffffffffu, fabsf(inc[j]) < 100.f);
-        if (lane == 0) {
-          v[5 * kL + j] = before;
-          v[5 * kL + 4 + j] = before + end[j];
-          v[5 * kL + 12 + j] = small ? 1.f : 0.f;
-        }
-        before += end[j];
-      }
-      if (lane == 0) v[5 * kL + 8] = before;
-    };
-    auto publish = [&]() {
-      __syncwarp();
-      if (one) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b_dec)) : "memory");
     };
     if (one) {
       load_bc(c_begin);
       load_x(c_begin);
+      if (c_begin + 1 < c_end) prefetch(c_begin + 1);
     }
-    load_dt(c_begin);
-    decays(c_begin);
-    publish();
-    if (c_begin + 1 < c_end) load_dt(c_begin + 1);
     uint32_t ph = 0, bc_ph = 0, x_ph = 0;   // phases of the loads in flight
     bool bc_pending = true, x_pending = true;
     for (long long c = c_begin; c < c_end; ++c, ph ^= 1u) {
@@ -370,13 +330,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc::mma_commit(b_s);
       }
       __syncwarp();
-      if (more) {
-        decays(c + 1);
-        if (c + 2 < c_end) load_dt(c + 2);
-      }
+      if (one && c + 2 < c_end) prefetch(c + 2);
       if (!wait(b_xt, ph)) break;
-      x_pending = false;   // the computing warps have seen X, and this chunk's decays
-      if (more) publish();
+      x_pending = false;   // the computing warps have seen X
       tc::fence_after_sync();
       if (one) {
 #pragma unroll
@@ -433,11 +389,78 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (x_pending) mbar_wait_bounded(b_x, x_ph);
     }
     if (FULL && one) store_done();
+  } else if (warp == kCompute / 32 + 1) {
+    // ------------------------------------------------ decays, up to two chunks ahead
+    float raw[4];   // dt of the chunk whose decays come next: tokens lane, 32 + lane, ..
+    auto load_dt = [&](long long c) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const long long t = c * kL + 32 * j + lane;
+        raw[j] = t < q.len ? __bfloat162float(dt[t * a.dt_tok]) : 0.f;
+      }
+    };
+    auto decays = [&](long long c) {
+      float* v = vec + (c & 1) * kVec;
+      float s[4], inc[4], ex[4], end[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = c * kL + 32 * j + lane < q.len;
+        s[j] = in ? time_step(raw[j], bias, a.softplus) : 0.f;
+        inc[j] = in ? A2 * s[j] : 0.f;
+        ex[j] = inc[j];
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float u = __shfl_up_sync(0xffffffffu, inc[j], o), d = __shfl_down_sync(0xffffffffu, ex[j], o);
+          if (lane >= o) inc[j] += u;
+          if (lane + o < 32) ex[j] += d;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        end[j] = __shfl_sync(0xffffffffu, inc[j], 31);
+        ex[j] = __shfl_down_sync(0xffffffffu, ex[j], 1);
+        if (lane == 31) ex[j] = 0.f;
+      }
+      float before = 0.f, after[4];
+      after[3] = 0.f;
+#pragma unroll
+      for (int j = 2; j >= 0; --j) after[j] = after[j + 1] + end[j + 1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = 32 * j + lane;
+        v[t] = before + inc[j];
+        v[kL + t] = s[j] * ex2(ex[j]);
+        v[2 * kL + t] = s[j] * ex2(-inc[j]);
+        v[3 * kL + t] = s[j] * ex2(ex[j] + after[j]);
+        v[4 * kL + t] = s[j];
+        const bool small = __all_sync(0xffffffffu, fabsf(inc[j]) < 100.f);
+        if (lane == 0) {
+          v[5 * kL + j] = before;
+          v[5 * kL + 4 + j] = before + end[j];
+          v[5 * kL + 12 + j] = small ? 1.f : 0.f;
+        }
+        before += end[j];
+      }
+      if (lane == 0) v[5 * kL + 8] = before;
+    };
+    load_dt(c_begin);
+    for (long long c = c_begin; c < c_end; ++c) {
+      const uint32_t use = (uint32_t)((c - c_begin) >> 1), buf = (uint32_t)(c & 1);
+      if (use > 0 && !wait(b_free + buf, (use - 1) & 1u)) break;
+      decays(c);
+      __syncwarp();
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b_dec + buf)) : "memory");
+      if (c + 1 < c_end) load_dt(c + 1);
+    }
   } else {
     // ------------------------------------------------ arithmetic
     const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);   // this warp's lanes
     const int qd = warp & 3;                                            // its block of rows
     const uint32_t rsw = (uint32_t)(row & 7);
+    const uint64_t D2 = pair(Dh, Dh);
     float log_total = 0.f;
     uint32_t ph = 0;
     for (long long c = c_begin; c < c_end; ++c, ph ^= 1u) {
@@ -445,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const bool tail = packed && q.len - t0 < kL;   // rows of the next sequence lie behind this one's
       const bool in = t0 + row < q.len;
       const float* v = vec + (c & 1) * kVec;
-      if (!wait(b_dec, ph) || !wait(b_x, ph)) break;
+      if (!wait(b_dec + (c & 1), (uint32_t)((c - c_begin) >> 1) & 1u) || !wait(b_x, ph)) break;
       if (FULL ? !wait(b_s, ph) : !wait(b_bc, ph)) break;
       tc::fence_after_sync();
       // ---- X~ in three terms: token `row`, 32 columns
@@ -453,16 +476,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float w = v[3 * kL + row];
         const uint64_t w2 = pair(w, w), minus = pair(-1.f, -1.f);
         const bool clear = tail && !in;
+        uint4 xv[4];   // read ahead of the first store
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          xv[i] = *reinterpret_cast<const uint4*>(smem + Cf::oX + (uint32_t)row * 128 + (((4 * half + i) ^ rsw) << 4));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t at = (uint32_t)row * 128 + (((4 * half + i) ^ rsw) << 4);
-          uint4 xv = *reinterpret_cast<const uint4*>(smem + Cf::oX + at);
           if (clear) {
-            xv = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(smem + Cf::oX + at) = xv;
-            for (uint32_t k = 0; k < Cf::NT; ++k) *reinterpret_cast<uint4*>(smem + Cf::oB + k * kTile + at) = xv;
+            xv[i] = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(smem + Cf::oX + at) = xv[i];
+            for (uint32_t k = 0; k < Cf::NT; ++k) *reinterpret_cast<uint4*>(smem + Cf::oB + k * kTile + at) = xv[i];
           }
-          const uint32_t xi[4] = {xv.x, xv.y, xv.z, xv.w};
+          const uint32_t xi[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
           uint32_t t1[4], t2[4], t3[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -484,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       arrive(b_xt);
       if (FULL) {
-        // ---- M from S in place, and the state's part of Y scaled by the row's decay
+        // ---- M from S in place; Y = D x + the state's part scaled by the row's decay
         const float my_cum = v[row];
 #pragma unroll 1
         for (int jj = 0; jj < 2; ++jj) {
@@ -532,8 +558,17 @@ __global__ void __launch_bounds__(kThreads, 2)
           float y[32];
           tc::tmem_ld32(tlane + kColY + 32 * half, y);
           const float r = ex2(my_cum);
+          const uint64_t r2 = pair(r, r);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] *= r;
+          for (int i = 0; i < 4; ++i) {
+            const uint4 xv = *reinterpret_cast<const uint4*>(smem + Cf::oX + (uint32_t)row * 128 + (((4 * half + i) ^ rsw) << 4));
+            const uint32_t xi[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int e = 8 * i + 2 * j;
+              unpair(fma2(pair(y[e], y[e + 1]), r2, mul2(D2, pair(lo_f(xi[j]), hi_f(xi[j])))), y[e], y[e + 1]);
+            }
+          }
           tc::tmem_st32(tlane + kColY + 32 * half, y);
         }
         tmem_wait_st();
@@ -541,6 +576,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // ---- the state after the chunk
       const float total = v[5 * kL + 8];
+      __syncwarp();   // the last that this chunk needs of its decays
+      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b_free + (c & 1))) : "memory");
       if (!wait(b_u, ph)) break;
       tc::fence_after_sync();
       {
@@ -580,22 +617,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       float y[32];
       tc::tmem_ld32(tlane + kColY + 32 * half, y);
       arrive(b_next);   // the next chunk's S and C h^T may start
-      // ---- output rows: Y + D x, gated
+      // ---- output rows: Y, gated, over X (every product that reads X is done)
       __nv_bfloat16* yp = a.y + (packed ? (q.start + t0 + row) * a.y_tok : 0) + (long long)head * a.P + p0 + 32 * half;
-      const uint64_t D2 = pair(Dh, Dh);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t at = (uint32_t)row * 128 + (((4 * half + i) ^ rsw) << 4);
-        const uint4 xv = *reinterpret_cast<const uint4*>(smem + Cf::oX + at);
-        const uint32_t xi[4] = {xv.x, xv.y, xv.z, xv.w};
         const uint32_t zi[4] = {zr[i].x, zr[i].y, zr[i].z, zr[i].w};
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint64_t u = fma2(D2, pair(lo_f(xi[j]), hi_f(xi[j])), pair(y[8 * i + 2 * j], y[8 * i + 2 * j + 1]));
-          if (a.z) u = mul2(u, silu2(pair(lo_f(zi[j]), hi_f(zi[j]))));
-          float e, f;
-          unpair(u, e, f);
+          float e = y[8 * i + 2 * j], f = y[8 * i + 2 * j + 1];
+          if (a.z) unpair(mul2(pair(e, f), silu2(pair(lo_f(zi[j]), hi_f(zi[j])))), e, f);
           o[j] = pack2(e, f);
         }
         const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
