@@ -30,6 +30,11 @@ vla_err_t check_seqs(vla_handle_t h, const std::string& f, long long n_seq, long
   return VLA_OK;
 }
 
+// Which form runs can hang on the operands' alignment: the workspace serves either.
+size_t ws_need(const vla::PromptPlan& prompt, const vla::StepsPlan& steps) {
+  return prompt.fits && prompt.ws_bytes > steps.ws_bytes ? prompt.ws_bytes : steps.ws_bytes;
+}
+
 bool stride_ok(long long v) { return v >= 0 && v < (1LL << 40); }
 
 // Rows of an output must not overlap: a stride that the call uses is at least a row's width.
@@ -110,7 +115,9 @@ vla_err_t vla_ssm_scan(vla_handle_t h, const void* x, const void* dt, const floa
   a.status = h->status;
   const bool bf16 = io_dtype == VLA_BF16;
   const vla::PromptPlan plan = vla::ssm_prompt_plan(n_seq, a.seqs.max_len, H, P, N, bf16, h->sm_count);
-  if (plan.ws_bytes > 0 && (!workspace || workspace_bytes < plan.ws_bytes || !aligned16(workspace)))
+  const vla::StepsPlan steps = vla::ssm_steps_plan(n_seq, a.seqs.max_len, H, P, N, h->sm_count);
+  const size_t need = ws_need(plan, steps);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return fail(h, VLA_ERR_INVALID_ARG, f + ": workspace missing, misaligned or smaller than vla_ssm_workspace says");
   a.ws = static_cast<float*>(workspace);
   cudaError_t e = on_device(h->device, [&]() {
@@ -120,7 +127,7 @@ vla_err_t vla_ssm_scan(vla_handle_t h, const void* x, const void* dt, const floa
     if (r != cudaSuccess || used) return r;
     if (plan.fits) r = vla::launch_ssm_prompt(a, plan, static_cast<cudaStream_t>(stream), &used);
     if (r != cudaSuccess || used) return r;
-    return vla::launch_ssm_steps(a, bf16, h->sm_count, static_cast<cudaStream_t>(stream));
+    return vla::launch_ssm_steps(a, steps, bf16, static_cast<cudaStream_t>(stream));
   });
   if (e != cudaSuccess) return fail(h, VLA_ERR_CUDA, cuda_msg("vla_ssm_scan: launch", e));
   return VLA_OK;
@@ -136,7 +143,9 @@ vla_err_t vla_ssm_workspace(vla_handle_t h, long long n_seq, long long T, long l
     return fail(h, VLA_ERR_INVALID_ARG, f + ": negative size");
   if (io_dtype != VLA_F32 && io_dtype != VLA_BF16) return fail(h, VLA_ERR_INVALID_ARG, f + ": unknown io_dtype");
   if (packed && max_len > T) max_len = T;
-  *bytes = vla::ssm_prompt_plan(n_seq, packed ? max_len : T, H, P, N, io_dtype == VLA_BF16, h->sm_count).ws_bytes;
+  const long long len = packed ? max_len : T;
+  *bytes = ws_need(vla::ssm_prompt_plan(n_seq, len, H, P, N, io_dtype == VLA_BF16, h->sm_count),
+                   vla::ssm_steps_plan(n_seq, len, H, P, N, h->sm_count));
   return VLA_OK;
 }
 

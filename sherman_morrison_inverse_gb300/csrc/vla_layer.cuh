@@ -162,13 +162,22 @@ struct SsmArgs {
   long long H, P, G, N;
   long long x_seq, x_tok, dt_seq, dt_tok, B_seq, B_tok, C_seq, C_tok, z_seq, z_tok, y_seq, y_tok;
   bool softplus;
-  float* ws;              // segments' states (see vla_ssm_prompt.cu)
+  float* ws;              // segments' states
   DevStatus* status;
 };
 // One token a sequence; *used = false: not this form's call, nothing was launched.
 cudaError_t launch_ssm_token(const SsmArgs& a, bool bf16, int sm_count, cudaStream_t s, bool* used);
 // Token by token, any sizes.
-cudaError_t launch_ssm_steps(const SsmArgs& a, bool bf16, int sm_count, cudaStream_t s);
+struct StepsPlan {
+  int ni;                         // 32 ni >= N states a row
+  int rows;                       // rows of the state a CTA: 32 or 64
+  long long row_blocks;
+  int nseg;                       // segments a sequence is cut into
+  long long seg_len;              // tokens a segment
+  size_t ws_bytes;
+};
+StepsPlan ssm_steps_plan(long long n_seq, long long max_len, long long H, long long P, long long N, int sm_count);
+cudaError_t launch_ssm_steps(const SsmArgs& a, const StepsPlan& plan, bool bf16, cudaStream_t s);
 
 struct NormArgs {
   const void* x;
