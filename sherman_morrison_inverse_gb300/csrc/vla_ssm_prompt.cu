@@ -20,17 +20,25 @@
 // then at least 1, so this holds while the block's sums stay below 2^100, and beyond that (nothing
 // is left of a token a few tokens later) the exponentials are taken pair by pair.
 //
-// Roles.  Eight warps compute (thread = a row of the chunk, or a state n, and 32 of 64 columns);
-// the ninth issues the loads and the products, and the tenth forms the decays, up to two chunks
-// ahead.  They meet on mbarriers.  In the order of a chunk:
-//   ninth: S, C h^T | computing: X~ | ninth: B^T X~ | computing: M, scaling of C h^T | ninth: M X,
-//   loads of the next B and C | computing: state, Y | ninth: Y's store, load of the next X.
+// Roles (24 warps, one CTA an SM; they meet on mbarriers and every operand has two places, so the two
+// sides of a chunk run side by side and ahead of each other):
+//   0-7   output: M from S, then Y = D x + exp(c) C h^T, later y from Y
+//   8-15  state: X~, then h' from its product U
+//   16    issues C h^T and M X               17  issues B^T X~ and then S of the next chunk
+//   18    issues the loads                    19  stores y
+//   22-23 decays, 64 tokens of a chunk each
+// In order: S of the next chunk is formed while M of this one is, M of the next one while M X of
+// this one runs.  The longest chain is X~, U, h, X~ ..: so U comes before S, and h's copy is written
+// after the next X~.
+// All of this code runs once a chunk: what does not fit the instruction caches is fetched again
+// every time (written out, 122 KB of it took three times as long), so loops stay rolled, a body
+// takes 16 columns, and a wait that does not succeed at once goes through one shared function.
 //
 // Operands.  B, C [128 tokens][N] and X [128][64] arrive by TMA as 128-byte-swizzled tiles of 64
 // columns; the same B tile is the K-major operand of S and the transposed (MN-major) one of the
-// state's product.  M replaces S in tensor memory as the A operand of M X.  Shared memory is reused
-// within a chunk (X~ overwrites C and the bfloat16 state once S and C h^T are done; Y overwrites X), which
-// keeps a CTA below half an SM's: two CTAs an SM hide each other's latencies.
+// state's product.  M replaces S in tensor memory as the A operand of M X.  The terms t1, t2, t3 of X~ make
+// two operands of 128 columns, [t1 | t2 / 2] and [t2 / 2 | t3], that share the tile of t2 / 2 and an
+// accumulator (a product of 64 columns takes as long as one of 128: 16 of these, not 24).
 //
 // Few slices: the sequence is cut into segments, one CTA each.  A first launch forms what every
 // segment but a sequence's last adds to the state (B^T X~ alone), the second starts each segment from
@@ -47,26 +55,46 @@ namespace vla {
 namespace {
 
 constexpr int kL = 128;            // tokens a chunk
-constexpr int kCompute = 256;      // threads of the computing warps
-constexpr int kThreads = 320;
+constexpr int kSide = 256;         // threads of the output's and of the state's warps
+constexpr int kThreads = 768;
 constexpr uint32_t kTile = 16384;  // bytes of a [128][64] bfloat16 tile
-constexpr uint32_t kCols = 256;    // tensor memory columns a CTA: S (M) | Y | the state's product U
-constexpr uint32_t kColS = 0, kColY = 128, kColU = 192;
-constexpr int kVec = 5 * kL + 16;  // floats of a chunk's decays (two buffers)
-constexpr int kBars = 13;
+constexpr uint32_t kCols = 512;    // tensor memory columns: S (M) [2] | Y [2] | U
+constexpr uint32_t kColS = 0, kColY = 256, kColU = 384;
+constexpr int kVec = 5 * kL + 24;  // floats of a chunk's decays
+constexpr int kDec = 4;            // chunks of decays
+constexpr int kUnits = 16;         // pieces of 32 tokens and 16 columns of X~
 
-// Shared memory: B | C | X | state (bfloat16, [n][64 p]) | more X~ | vectors | barriers
+// mbarriers (where there are two or more, chunk i uses i mod their number)
+enum : int {
+  kFullB = 0,      // [2] B has landed
+  kFullC = 2,      //     C
+  kFullX = 3,      // [2] X
+  kEmptyB = 5,     // [2] S and U have read B
+  kEmptyC = 7,     //     S and C h^T have read C
+  kEmptyX = 8,     // [2] X~, D x and M X have read X
+  kFullS = 10,     // [2] S is formed
+  kEmptyS = 12,    // [2] M X is formed: S's place is free
+  kFullYi = 14,    // [2] C h^T is formed (and h's copy read)
+  kM = 16,         //     M, and D x + exp(c) C h^T, are written
+  kFullY = 17,     // [2] M X is added
+  kH = 19,         //     h's copy is written
+  kEmptyY = 20,    // [2] Y is read
+  kXt = 22,        //     X~ is written, the U before it read
+  kFullU = 23,     //     U is formed
+  kFullDec = 24,   // [4] decays are written
+  kEmptyDec = 28,  // [4] and read
+  kStage = 32,     //     y is staged
+  kStaged = 33,    //     and its store has read it
+  kBars = 34
+};
+
+// Shared memory: B [2] | C | X [2] | X~ (three terms) | state (bfloat16, [n][64 p]) | y | decays | barriers
 template <int NN>
 struct Cfg {
   static constexpr uint32_t NT = NN / 64;
-  static constexpr uint32_t oB = 0, oC = NT * kTile, oX = 2 * NT * kTile, oH = oX + kTile;
-  static constexpr uint32_t HB = NN * 128;
-  static constexpr uint32_t oMore = oH + HB;
-  static constexpr uint32_t term0 = oC;
-  static constexpr uint32_t term1 = NN == 128 ? oC + kTile : oMore;
-  static constexpr uint32_t term2 = NN == 128 ? oH : oMore + kTile;
-  static constexpr uint32_t oVec = NN == 128 ? oMore : oMore + 2 * kTile;
-  static constexpr uint32_t bytes = oVec + 4 * 2 * kVec + 8 * kBars + 16;
+  static constexpr uint32_t oB = 0, oC = 2 * NT * kTile, oX = oC + NT * kTile, oT = oX + 2 * kTile;
+  static constexpr uint32_t oH = oT + 3 * kTile, oY = oH + NN * 128, oVec = oY + kTile;
+  static constexpr uint32_t bytes = oVec + 4 * kDec * kVec + 8 * kBars + 16;
 };
 
 // Matrix descriptor of a 128-byte-swizzled operand: `lbo` bytes between blocks of 64 in the
@@ -77,14 +105,24 @@ __device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo) {
 }
 constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;   // instruction descriptor: MN-major operands
 
-// D (+)= X Y with X in tensor memory (bfloat16, two K elements a column)
-__device__ __forceinline__ void mma_f16_tx(uint32_t d_tmem, uint32_t x_tmem, uint64_t ydesc, uint32_t idesc,
-                                           bool accumulate) {
-  const uint32_t acc = accumulate ? 1u : 0u;
+// One MMA, D (+)= X Y for a K step of 16, issued by the lane whose `one` is set.  The whole warp runs the
+// loop around it, predicated and not branched, so that descriptors and addresses stay in uniform
+// registers: from a divergent branch each MMA takes over a hundred cycles to issue.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t xdesc, uint64_t ydesc, uint32_t idesc, bool accumulate,
+                                       uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(x_tmem), "l"(ydesc), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(xdesc), "l"(ydesc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(one)
+      : "memory");
+}
+// The same with X in tensor memory (bfloat16, two K elements a column).
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t x_tmem, uint64_t ydesc, uint32_t idesc, bool accumulate,
+                                       uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(x_tmem), "l"(ydesc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(one)
       : "memory");
 }
 
@@ -98,6 +136,39 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Bounded wait of a whole warp whose first poll has failed; gives up early when another warp has.
+// One lane polls: two dozen warps that poll with all their lanes slow every access to shared memory.
+__device__ __noinline__ bool wait_on(uint64_t* b, uint32_t parity, volatile int* fail) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) {
+    unsigned long long t_start = 0;
+    while (true) {
+#pragma unroll 1
+      for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(b, parity);
+      if (ok || *fail) break;
+      const unsigned long long now = globaltimer_ns();
+      if (t_start == 0) t_start = now;
+      if (now - t_start > kWaitLimitNs) {
+        *fail = 1;
+        break;
+      }
+    }
+  }
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// Named barrier over n threads that also ORs a flag across them.
+__device__ __forceinline__ bool named_or(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
 
 __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
   asm volatile(
@@ -122,6 +193,13 @@ __device__ __forceinline__ void store_4d(const CUtensorMap* map, int x, int y, i
 __device__ __forceinline__ void store_read_done() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// The n lowest bits set, n < 0: none, n > 32: all.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  uint32_t r;
+  asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(r) : "r"(n < 0 ? 0 : n));
+  return r;
+}
+
 struct PromptArgs {
   const __nv_bfloat16* dt;
   const float* A;
@@ -144,8 +222,8 @@ struct PromptArgs {
 __host__ __device__ constexpr long long ws_floats(int nseg, int NN) { return (long long)nseg * 64 * NN + (nseg + 63) / 64 * 64; }
 
 // FULL: the outputs and the final state; else what the segment adds to the state.
-template <int NN, bool FULL>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int NN, bool FULL, bool GATE>
+__global__ void __launch_bounds__(kThreads, 1)
     ssm_prompt_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_B,
                       const __grid_constant__ CUtensorMap map_C, const __grid_constant__ CUtensorMap map_y,
                       const __grid_constant__ PromptArgs a) {
@@ -173,47 +251,56 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
 
-  // decays of chunk c at vec + (c & 1) kVec: cum [128] log2 decay from the chunk's start up to a token;
+  // decays of chunk i at vec + (i mod 4) kVec: cum [128] log2 decay from the chunk's start up to a token;
   // wcol [128] s exp(e_j - c), j the token's block; wdg [128] the same with the sum before the
   // block; wx [128] s exp(c_L - c); step [128] s; then [4] sums before the blocks, [4] to their ends,
-  // [8] the total, [12..16) whether wdg holds
+  // [8] the total, [12..16) the blocks' own sums, [16..20) whether wdg holds
   float* vec = reinterpret_cast<float*>(smem + Cf::oVec);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(vec + 2 * kVec);
-  uint64_t *b_bc = bar, *b_x = bar + 1, *b_dec = bar + 2;           // B and C, X loaded; decays written [2]
-  uint64_t *b_s = bar + 4, *b_u = bar + 5, *b_y = bar + 6;          // products done: S and C h^T, U, M X
-  uint64_t *b_xt = bar + 7, *b_m = bar + 8, *b_free = bar + 9;      // X~, M written; decays read [2]
-  uint64_t *b_next = bar + 11, *b_out = bar + 12;                   // tensor memory and h free; Y staged
+  uint64_t* bar = reinterpret_cast<uint64_t*>(vec + kDec * kVec);
   uint32_t* tslot = reinterpret_cast<uint32_t*>(bar + kBars);
   volatile int* fail = reinterpret_cast<volatile int*>(tslot + 1);
 
   const bool packed = a.seqs.offsets != nullptr;
   const int row0 = packed ? (int)q.start : 0, batch = packed ? 0 : (int)seq;   // tensor map coordinates
-  const __nv_bfloat16* dt = a.dt + (packed ? q.start * a.dt_tok : seq * a.dt_seq) + head;
-  const float A2 = a.A[head] * 1.44269504088896341f, bias = a.dt_bias ? a.dt_bias[head] : 0.f;
-  const float Dh = a.D ? a.D[head] : 0.f;
+  const int n_chunks = (int)(c_end - c_begin);
+  const long long t_first = c_begin * kL;
 
   if (tid == 0) {
-    for (int i = 0; i < 7; ++i) mbar_init(bar + i, 1);
-    for (int i = 7; i < kBars; ++i) mbar_init(bar + i, kCompute / 32);
+    constexpr int W = kSide / 32;
+    for (int i = 0; i < kBars; ++i) {
+      int count = 1;
+      if (i == kEmptyB || i == kEmptyB + 1 || i == kEmptyC) count = FULL ? 2 : 1;
+      if (i == kEmptyX || i == kEmptyX + 1) count = FULL ? 2 * W + 1 : W;
+      if (i >= kEmptyDec && i < kEmptyDec + kDec) count = FULL ? 2 * W : W;
+      if (i >= kFullDec && i < kFullDec + kDec) count = 2;
+      if (i == kM || i == kH || i == kEmptyY || i == kEmptyY + 1 || i == kXt || i == kStage) count = W;
+      mbar_init(bar + i, count);
+    }
     *fail = 0;
     fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc(tslot, kCols);
 
-  // this thread's part of the state: n = row, 32 columns p from 32 half
-  const int row = tid & (kL - 1), half = (tid >> 7) & 1;
+  const int row = tid & (kL - 1), half = (tid >> 7) & 1;   // token or state n; columns 32 half ..
+  const uint32_t rsw = (uint32_t)(row & 7);
+  const uint32_t row_at = (uint32_t)row * 128;
+  const int pc = a.P - p0 - 32 * half;   // columns of this thread that exist
+  float* wsq = a.nseg > 1 ? a.ws + (seq * slices + slice) * ws_floats(a.nseg, NN) : nullptr;
   const int n = row;
-  const bool n_ok = n < a.N;
-  float h[32];
-  if (tid < kCompute) {
-    const int pc = a.P - p0 - 32 * half;   // columns of this thread that exist
-    const bool from_ws = a.nseg > 1 && FULL && chunks > a.seg_chunks;
-    float* wsq = from_ws || !FULL ? a.ws + (seq * slices + slice) * ws_floats(a.nseg, NN) : nullptr;
+  float h[32];   // of the state's warps: state n, columns p
+  if (warp >= kSide / 32 && warp < 2 * kSide / 32) {
+    const bool from_ws = FULL && chunks > a.seg_chunks;
     const float* src = nullptr;
     long long pitch = 0;
-    if (from_ws && seg == 0) { src = wsq + ((long long)(a.nseg - 1) * 64 + 32 * half) * NN; pitch = NN; }
-    else if (!from_ws && a.state && seg == 0) { src = a.state + ((q.slot * a.H + head) * a.P + p0 + 32 * half) * a.N; pitch = a.N; }
-    const bool mine = from_ws ? n < NN : n_ok;
+    bool mine = n < a.N;
+    if (from_ws && seg == 0) {
+      src = wsq + ((long long)(a.nseg - 1) * 64 + 32 * half) * NN;
+      pitch = NN;
+      mine = n < NN;
+    } else if (!from_ws && a.state && seg == 0) {
+      src = a.state + ((q.slot * a.H + head) * a.P + p0 + 32 * half) * a.N;
+      pitch = a.N;
+    }
 #pragma unroll
     for (int i = 0; i < 32; ++i) h[i] = src && mine && (from_ws || i < pc) ? src[i * pitch + n] : 0.f;
     if (!FULL && seg == 0 && n < NN) {   // the copy that the second launch starts from
@@ -240,418 +327,480 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < 4; ++i) {
         const uint4 v = make_uint4(pack2(h[8 * i], h[8 * i + 1]), pack2(h[8 * i + 2], h[8 * i + 3]),
                                    pack2(h[8 * i + 4], h[8 * i + 5]), pack2(h[8 * i + 6], h[8 * i + 7]));
-        *reinterpret_cast<uint4*>(smem + Cf::oH + n * 128 + (((4 * half + i) ^ (n & 7)) << 4)) = v;
+        *reinterpret_cast<uint4*>(smem + Cf::oH + row_at + (((uint32_t)(4 * half + i) ^ rsw) << 4)) = v;
       }
     }
   };
-  if (FULL && tid < kCompute) put_state();
+  if (FULL && warp >= kSide / 32 && warp < 2 * kSide / 32) put_state();
   fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tslot;
-  constexpr uint32_t kIdS = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-  constexpr uint32_t kId64 = (1u << 4) | (1u << 7) | (1u << 10) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
-  // Bounded wait of a whole warp; gives up early when another one has.  The timer is read once in
-  // many polls: it takes longer than a poll, and a wait ends when the poll after it is made.
-  auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
-    bool ok = false;
-    unsigned long long t_start = 0;
-    while (true) {
-#pragma unroll 1
-      for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(b, parity);
-      if (ok || *fail) break;
-      const unsigned long long now = globaltimer_ns();
-      if (t_start == 0) t_start = now;
-      if (now - t_start > kWaitLimitNs) break;
-    }
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) *fail = 1;
-    return ok;
-  };
-  // One arrival a warp, after everything its lanes have written to shared or tensor memory.
-  auto arrive = [&](uint64_t* b) {
-    fence_proxy_async_smem();
-    tc::fence_before_sync();
-    __syncwarp();
-    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
-  };
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tslot, 0);   // the same in every lane
+  constexpr uint32_t kId = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);   // bf16, 128 rows
+  constexpr uint32_t kN64 = (64u >> 3) << 17, kN128 = (128u >> 3) << 17;
 
-  if (warp == kCompute / 32) {
-    // ------------------------------------------------ loads, products, decays
-    const bool one = lane == 0;
-    auto load_bc = [&](long long c) {
-      const int t = row0 + (int)(c * kL);
-      mbar_arrive_expect_tx(b_bc, (FULL ? 2 : 1) * Cf::NT * kTile);
-      for (uint32_t i = 0; i < Cf::NT; ++i) {
-        load_4d(sbase + Cf::oB + i * kTile, &map_B, 64 * (int)i, group, t, batch, b_bc);
-        if (FULL) load_4d(sbase + Cf::oC + i * kTile, &map_C, 64 * (int)i, group, t, batch, b_bc);
-      }
-    };
-    auto load_x = [&](long long c) {
-      mbar_arrive_expect_tx(b_x, kTile);
-      load_4d(sbase + Cf::oX, &map_x, p0, head, row0 + (int)(c * kL), batch, b_x);
-    };
-    // a chunk's tiles are asked for when their places are free, which is late: their rows are fetched
-    // into L2 two chunks ahead
-    auto prefetch = [&](long long c) {
-      const int t = row0 + (int)(c * kL);
-      prefetch_4d(&map_x, p0, head, t, batch);
-      for (uint32_t i = 0; i < Cf::NT; ++i) {
-        prefetch_4d(&map_B, 64 * (int)i, group, t, batch);
-        if (FULL) prefetch_4d(&map_C, 64 * (int)i, group, t, batch);
-      }
-    };
-    if (one) {
-      load_bc(c_begin);
-      load_x(c_begin);
-      if (c_begin + 1 < c_end) prefetch(c_begin + 1);
-    }
-    uint32_t ph = 0, bc_ph = 0, x_ph = 0;   // phases of the loads in flight
-    bool bc_pending = true, x_pending = true;
-    for (long long c = c_begin; c < c_end; ++c, ph ^= 1u) {
-      const bool more = c + 1 < c_end;
-      if (c > c_begin && !wait(b_next, ph ^ 1u)) break;
-      if (!wait(b_bc, ph)) break;
-      bc_pending = false;
-      tc::fence_after_sync();
-      if (FULL && one) {
-#pragma unroll
-        for (int k = 0; k < NN / 16; ++k) {
-          const uint32_t at = (uint32_t)(k >> 2) * kTile + (uint32_t)(k & 3) * 32;
-          tc::mma_f16(tmem + kColS, desc128(sbase + Cf::oC + at, 16), desc128(sbase + Cf::oB + at, 16), kIdS, k > 0);
-        }
-#pragma unroll
-        for (int k = 0; k < NN / 16; ++k) {
-          const uint32_t at = (uint32_t)(k >> 2) * kTile + (uint32_t)(k & 3) * 32;
-          tc::mma_f16(tmem + kColY, desc128(sbase + Cf::oC + at, 16), desc128(sbase + Cf::oH + 2048u * k, 16),
-                      kId64 | kTransB, k > 0);
-        }
-        tc::mma_commit(b_s);
-      }
-      __syncwarp();
-      if (one && c + 2 < c_end) prefetch(c + 2);
-      if (!wait(b_xt, ph)) break;
-      x_pending = false;   // the computing warps have seen X
-      tc::fence_after_sync();
-      if (one) {
-#pragma unroll
-        for (int t = 0; t < 3; ++t) {
-          const uint32_t term = t == 0 ? Cf::term2 : t == 1 ? Cf::term1 : Cf::term0;   // small terms first
-#pragma unroll
-          for (int k = 0; k < kL / 16; ++k)
-            tc::mma_f16(tmem + kColU, desc128(sbase + Cf::oB + 2048u * k, kTile),
-                        desc128(sbase + term + 2048u * k, 16), kId64 | kTransA | kTransB, t > 0 || k > 0);
-        }
-        tc::mma_commit(b_u);
-      }
-      __syncwarp();
-      if (FULL) {
-        if (!wait(b_m, ph)) break;
+  // Wait of a whole warp for completion `use` (0, 1, ..) of a barrier.
+  auto wait = [&](int b, int use) -> bool {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar + b, (uint32_t)use & 1u))) return true;
+    return wait_on(bar + b, (uint32_t)use & 1u, fail);
+  };
+  // One arrival a warp.
+  auto arrive = [&](int b) {
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar + b)) : "memory");
+  };
+  const bool one = lane == 0;
+  auto arrive_one = [&](int b) {   // by one lane, after a __syncwarp
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar + b)) : "memory");
+  };
+  const int last_i = n_chunks - 1;
+  // whether rows of the next sequence lie behind this one's in the last chunk
+  const bool ragged = packed && c_end == chunks && q.len % kL != 0;
+
+  if (warp < kSide / 32) {
+    if constexpr (FULL) {
+      // ------------------------------------------------ output
+      const int qd = warp & 3;   // block of rows
+      const uint32_t tlane = tmem + ((uint32_t)(32 * qd) << 16);
+      const float Dh = a.D ? a.D[head] : 0.f;
+      const uint64_t D2 = pair(Dh, Dh);
+      // y of chunk i: Y, gated
+      auto finish = [&](int i) -> bool {
+        const long long t = t_first + (long long)i * kL + row;
+        const bool in = t < q.len, tail = ragged && i == last_i;
+        const __nv_bfloat16* z = GATE ? a.z + (packed ? (q.start + t) * a.z_tok : seq * a.z_seq + t * a.z_tok) +
+                                            (long long)head * a.P + p0 + 32 * half
+                                      : nullptr;
+        if (!wait(kFullY + (i & 1), i >> 1) || (i > 0 && !wait(kStaged, i - 1))) return false;
         tc::fence_after_sync();
-        if (one) {
-#pragma unroll
-          for (int k = 0; k < kL / 16; ++k)
-            mma_f16_tx(tmem + kColY, tmem + kColS + 64 * (k >> 2) + 8 * (k & 3), desc128(sbase + Cf::oX + 2048u * k, 16),
-                       kId64 | kTransB, true);
-          tc::mma_commit(b_y);
-        }
-        __syncwarp();
-      }
-      if (more) {
-        if (!wait(b_u, ph)) break;
-        if (one) {
-          load_bc(c + 1);
-          if (!FULL) load_x(c + 1);
-        }
-        bc_pending = true;
-        bc_ph = ph ^ 1u;
-        if (!FULL) x_pending = true, x_ph = ph ^ 1u;
-        __syncwarp();
-      }
-      if (FULL) {
-        if (!wait(b_out, ph)) break;
-        const bool tail = packed && q.len - c * kL < kL;
-        if (one) {
-          if (!tail) store_4d(&map_y, p0, head, row0 + (int)(c * kL), batch, sbase + Cf::oX);
-          if (more) {
-            store_read_done();
-            load_x(c + 1);
-          }
-        }
-        if (more) x_pending = true, x_ph = ph ^ 1u;
-        __syncwarp();
-      }
-    }
-    // nothing lands after the CTA has gone
-    if (*fail) {
-      if (bc_pending) mbar_wait_bounded(b_bc, bc_ph);
-      if (x_pending) mbar_wait_bounded(b_x, x_ph);
-    }
-    if (FULL && one) store_done();
-  } else if (warp == kCompute / 32 + 1) {
-    // ------------------------------------------------ decays, up to two chunks ahead
-    float raw[4];   // dt of the chunk whose decays come next: tokens lane, 32 + lane, ..
-    auto load_dt = [&](long long c) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const long long t = c * kL + 32 * j + lane;
-        raw[j] = t < q.len ? __bfloat162float(dt[t * a.dt_tok]) : 0.f;
-      }
-    };
-    auto decays = [&](long long c) {
-      float* v = vec + (c & 1) * kVec;
-      float s[4], inc[4], ex[4], end[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = c * kL + 32 * j + lane < q.len;
-        s[j] = in ? time_step(raw[j], bias, a.softplus) : 0.f;
-        inc[j] = in ? A2 * s[j] : 0.f;
-        ex[j] = inc[j];
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float u = __shfl_up_sync(0xffffffffu, inc[j], o), d = __shfl_down_sync(0xffffffffu, ex[j], o);
-          if (lane >= o) inc[j] += u;
-          if (lane + o < 32) ex[j] += d;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        end[j] = __shfl_sync(0xffffffffu, inc[j], 31);
-        ex[j] = __shfl_down_sync(0xffffffffu, ex[j], 1);
-        if (lane == 31) ex[j] = 0.f;
-      }
-      float before = 0.f, after[4];
-      after[3] = 0.f;
-#pragma unroll
-      for (int j = 2; j >= 0; --j) after[j] = after[j + 1] + end[j + 1];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = 32 * j + lane;
-        v[t] = before + inc[j];
-        v[kL + t] = s[j] * ex2(ex[j]);
-        v[2 * kL + t] = s[j] * ex2(-inc[j]);
-        v[3 * kL + t] = s[j] * ex2(ex[j] + after[j]);
-        v[4 * kL + t] = s[j];
-        const bool small = __all_sync(0xffffffffu, fabsf(inc[j]) < 100.f);
-        if (lane == 0) {
-          v[5 * kL + j] = before;
-          v[5 * kL + 4 + j] = before + end[j];
-          v[5 * kL + 12 + j] = small ? 1.f : 0.f;
-        }
-        before += end[j];
-      }
-      if (lane == 0) v[5 * kL + 8] = before;
-    };
-    load_dt(c_begin);
-    for (long long c = c_begin; c < c_end; ++c) {
-      const uint32_t use = (uint32_t)((c - c_begin) >> 1), buf = (uint32_t)(c & 1);
-      if (use > 0 && !wait(b_free + buf, (use - 1) & 1u)) break;
-      decays(c);
-      __syncwarp();
-      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b_dec + buf)) : "memory");
-      if (c + 1 < c_end) load_dt(c + 1);
-    }
-  } else {
-    // ------------------------------------------------ arithmetic
-    const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);   // this warp's lanes
-    const int qd = warp & 3;                                            // its block of rows
-    const uint32_t rsw = (uint32_t)(row & 7);
-    const uint64_t D2 = pair(Dh, Dh);
-    float log_total = 0.f;
-    uint32_t ph = 0;
-    for (long long c = c_begin; c < c_end; ++c, ph ^= 1u) {
-      const long long t0 = c * kL;
-      const bool tail = packed && q.len - t0 < kL;   // rows of the next sequence lie behind this one's
-      const bool in = t0 + row < q.len;
-      const float* v = vec + (c & 1) * kVec;
-      if (!wait(b_dec + (c & 1), (uint32_t)((c - c_begin) >> 1) & 1u) || !wait(b_x, ph)) break;
-      if (FULL ? !wait(b_s, ph) : !wait(b_bc, ph)) break;
-      tc::fence_after_sync();
-      // ---- X~ in three terms: token `row`, 32 columns
-      {
-        const float w = v[3 * kL + row];
-        const uint64_t w2 = pair(w, w), minus = pair(-1.f, -1.f);
-        const bool clear = tail && !in;
-        uint4 xv[4];   // read ahead of the first store
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          xv[i] = *reinterpret_cast<const uint4*>(smem + Cf::oX + (uint32_t)row * 128 + (((4 * half + i) ^ rsw) << 4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t at = (uint32_t)row * 128 + (((4 * half + i) ^ rsw) << 4);
-          if (clear) {
-            xv[i] = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(smem + Cf::oX + at) = xv[i];
-            for (uint32_t k = 0; k < Cf::NT; ++k) *reinterpret_cast<uint4*>(smem + Cf::oB + k * kTile + at) = xv[i];
-          }
-          const uint32_t xi[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
-          uint32_t t1[4], t2[4], t3[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float e, f;
-            uint64_t u = mul2(pair(lo_f(xi[j]), hi_f(xi[j])), w2);
-            unpair(u, e, f);
-            t1[j] = pack2(e, f);
-            u = fma2(pair(lo_f(t1[j]), hi_f(t1[j])), minus, u);   // exact
-            unpair(u, e, f);
-            t2[j] = pack2(e, f);
-            u = fma2(pair(lo_f(t2[j]), hi_f(t2[j])), minus, u);
-            unpair(u, e, f);
-            t3[j] = pack2(e, f);
-          }
-          *reinterpret_cast<uint4*>(smem + Cf::term0 + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-          *reinterpret_cast<uint4*>(smem + Cf::term1 + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-          *reinterpret_cast<uint4*>(smem + Cf::term2 + at) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
-        }
-      }
-      arrive(b_xt);
-      if (FULL) {
-        // ---- M from S in place; Y = D x + the state's part scaled by the row's decay
-        const float my_cum = v[row];
 #pragma unroll 1
-        for (int jj = 0; jj < 2; ++jj) {
-          const int j = 2 * half + jj;
-          uint32_t m[16];
-          if (j > qd) {
+        for (int k = 0; k < 32; k += 16) {
+          uint4 zr[2];
+          if (GATE) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) m[i] = 0;
-          } else {
-            float s[32];
-            tc::tmem_ld32(tlane + kColS + 32 * j, s);
-            const bool diag = j == qd;
-            if (!diag || v[5 * kL + 12 + j] != 0.f) {
-              const float r = ex2(my_cum - v[5 * kL + (diag ? 0 : 4) + j]);
-              const float* wv = v + (diag ? 2 : 1) * kL + 32 * j;
-              const uint64_t r2 = pair(r, r);
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 w = *reinterpret_cast<const float4*>(wv + i);
-                float e0, e1, e2, e3;
-                unpair(mul2(mul2(pair(s[i], s[i + 1]), pair(w.x, w.y)), r2), e0, e1);
-                unpair(mul2(mul2(pair(s[i + 2], s[i + 3]), pair(w.z, w.w)), r2), e2, e3);
-                if (diag) {
-                  e0 = i <= lane ? e0 : 0.f;
-                  e1 = i + 1 <= lane ? e1 : 0.f;
-                  e2 = i + 2 <= lane ? e2 : 0.f;
-                  e3 = i + 3 <= lane ? e3 : 0.f;
-                }
-                m[i / 2] = pack2(e0, e1);
-                m[i / 2 + 1] = pack2(e2, e3);
+            for (int j = 0; j < 2; ++j) {
+              zr[j] = make_uint4(0, 0, 0, 0);
+              const int c = k + 8 * j;
+              if (!in || c >= pc) continue;
+              if (a.z_vec) {
+                zr[j] = *reinterpret_cast<const uint4*>(z + c);
+              } else {
+                const unsigned short* zs = reinterpret_cast<const unsigned short*>(z + c);
+                zr[j] = make_uint4(zs[0] | (uint32_t)zs[1] << 16, zs[2] | (uint32_t)zs[3] << 16,
+                                   zs[4] | (uint32_t)zs[5] << 16, zs[6] | (uint32_t)zs[7] << 16);
               }
+            }
+          }
+          float y[16];
+          tc::tmem_ld16(tlane + kColY + 64 * (i & 1) + 32 * half + k, y);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t zi[4] = {zr[j].x, zr[j].y, zr[j].z, zr[j].w};
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float f = y[8 * j + 2 * e], g = y[8 * j + 2 * e + 1];
+              if (GATE) unpair(mul2(pair(f, g), silu2(pair(lo_f(zi[e]), hi_f(zi[e])))), f, g);
+              w[e] = pack2(f, g);
+            }
+            const uint4 o = make_uint4(w[0], w[1], w[2], w[3]);
+            const int c = k + 8 * j;
+            if (!tail) {
+              *reinterpret_cast<uint4*>(smem + Cf::oY + row_at + (((uint32_t)(4 * half + (c >> 3)) ^ rsw) << 4)) = o;
+            } else if (in && c < pc) {
+              *reinterpret_cast<uint4*>(a.y + (q.start + t) * a.y_tok + (long long)head * a.P + p0 + 32 * half + c) = o;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc::fence_before_sync();
+        arrive(kEmptyY + (i & 1));
+        if (one) arrive_one(kStage);
+        return true;
+      };
+      for (int i = 0; i <= n_chunks; ++i) {   // the last turn finishes the last chunk only
+        const int r = i & 1, u = i >> 1;
+        const float* v = vec + (i % kDec) * kVec;
+        float row_decay = 0.f;
+        if (i < n_chunks) {
+          if (!wait(kFullDec + i % kDec, i / kDec) || !wait(kFullS + r, u)) break;
+          tc::fence_after_sync();
+          const float my_cum = v[row];
+          row_decay = ex2(my_cum);
+          // M from S in place: blocks 2 half and 2 half + 1 of s end up at S's columns 64 half + 0 and + 16
+          const uint32_t ts = tlane + kColS + 128 * r + 64 * half;
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {
+            const int j = 2 * half + g;
+            uint32_t m[16];
+            if (j > qd) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) m[k] = 0;
             } else {
+              float s[32];
+              tc::tmem_ld32(ts + 32 * g, s);
+              const bool diag = j == qd;
+              if (!diag || v[5 * kL + 16 + j] != 0.f) {
+                const float f = ex2(my_cum - v[5 * kL + (diag ? 0 : 4) + j]);
+                const float* wv = v + (diag ? 2 : 1) * kL + 32 * j;
+                const uint64_t f2 = pair(f, f);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 cs = *reinterpret_cast<const float2*>(v + 32 * j + i);
-                const float2 ss = *reinterpret_cast<const float2*>(v + 4 * kL + 32 * j + i);
-                m[i / 2] = pack2(i <= lane ? s[i] * ex2(my_cum - cs.x) * ss.x : 0.f,
-                                 i + 1 <= lane ? s[i + 1] * ex2(my_cum - cs.y) * ss.y : 0.f);
+                for (int k = 0; k < 32; k += 4) {
+                  const float4 w = *reinterpret_cast<const float4*>(wv + k);
+                  float e0, e1, e2, e3;
+                  unpair(mul2(mul2(pair(s[k], s[k + 1]), pair(w.x, w.y)), f2), e0, e1);
+                  unpair(mul2(mul2(pair(s[k + 2], s[k + 3]), pair(w.z, w.w)), f2), e2, e3);
+                  m[k / 2] = pack2(e0, e1);
+                  m[k / 2 + 1] = pack2(e2, e3);
+                }
+                if (diag) {   // columns behind the row's own are zero
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) m[k] &= low_bits(16 * (lane + 1 - 2 * k));
+                }
+              } else {
+                const float* cv = v + 32 * j;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const float e = 2 * k <= lane ? s[2 * k] * ex2(my_cum - cv[2 * k]) * cv[4 * kL + 2 * k] : 0.f;
+                  const float f = 2 * k + 1 <= lane ? s[2 * k + 1] * ex2(my_cum - cv[2 * k + 1]) * cv[4 * kL + 2 * k + 1] : 0.f;
+                  m[k] = pack2(e, f);
+                }
               }
             }
+            tmem_st16(ts + 16 * g, m);
           }
-          tmem_st16(tlane + kColS + 64 * half + 16 * jj, m);
+          arrive(kEmptyDec + i % kDec);
         }
-        {
-          float y[32];
-          tc::tmem_ld32(tlane + kColY + 32 * half, y);
-          const float r = ex2(my_cum);
-          const uint64_t r2 = pair(r, r);
+        if (i > 0 && !finish(i - 1)) break;
+        if (i == n_chunks) break;
+        // Y = D x + the state's part scaled by the row's decay
+        if (!wait(kFullX + r, u) || !wait(kFullYi + r, u)) break;
+        tc::fence_after_sync();
+        const bool clear = ragged && i == last_i && t_first + (long long)i * kL + row >= q.len;
+        const uint32_t ty = tlane + kColY + 64 * r + 32 * half;
+        const uint64_t f2 = pair(row_decay, row_decay);
+#pragma unroll 1
+        for (int k = 0; k < 32; k += 16) {
+          float y[16];
+          uint32_t bits[16];
+          uint4* at = reinterpret_cast<uint4*>(smem + Cf::oX + r * kTile + row_at + (((uint32_t)(4 * half + (k >> 3)) ^ rsw) << 4));
+          uint4* at2 = reinterpret_cast<uint4*>(smem + Cf::oX + r * kTile + row_at + (((uint32_t)(4 * half + (k >> 3) + 1) ^ rsw) << 4));
+          const uint4 xa = *at, xb = *at2;
+          tc::tmem_ld16(ty + k, y);
+          if (clear) *at = *at2 = make_uint4(0, 0, 0, 0);   // M X multiplies these rows by zeros: no NaN may be there
+          const uint32_t xi[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 xv = *reinterpret_cast<const uint4*>(smem + Cf::oX + (uint32_t)row * 128 + (((4 * half + i) ^ rsw) << 4));
-            const uint32_t xi[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int e = 8 * i + 2 * j;
-              unpair(fma2(pair(y[e], y[e + 1]), r2, mul2(D2, pair(lo_f(xi[j]), hi_f(xi[j])))), y[e], y[e + 1]);
-            }
+          for (int j = 0; j < 8; ++j) {
+            unpair(fma2(pair(y[2 * j], y[2 * j + 1]), f2, mul2(D2, pair(lo_f(xi[j]), hi_f(xi[j])))), y[2 * j], y[2 * j + 1]);
+            bits[2 * j] = __float_as_uint(y[2 * j]);
+            bits[2 * j + 1] = __float_as_uint(y[2 * j + 1]);
           }
-          tc::tmem_st32(tlane + kColY + 32 * half, y);
+          tmem_st16(ty + k, bits);
         }
+        if (clear) fence_proxy_async_smem();
         tmem_wait_st();
-        arrive(b_m);
+        tc::fence_before_sync();
+        arrive(kM);
+        if (one) arrive_one(kEmptyX + r);
       }
-      // ---- the state after the chunk
-      const float total = v[5 * kL + 8];
-      __syncwarp();   // the last that this chunk needs of its decays
-      if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b_free + (c & 1))) : "memory");
-      if (!wait(b_u, ph)) break;
+    }
+  } else if (warp < 2 * kSide / 32) {
+    // ------------------------------------------------ state
+    const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColU + 32 * half;
+    float log_total = 0.f;
+    // h <- exp(c_L) h + U
+    auto update = [&](float total) {
+      const float d = ex2(total);
+      const uint64_t d2 = pair(d, d);
+      log_total += total;
       tc::fence_after_sync();
-      {
-        float u[32];
-        tc::tmem_ld32(tlane + kColU + 32 * half, u);
-        const float d = ex2(total);
-        const uint64_t d2 = pair(d, d);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) unpair(fma2(d2, pair(h[i], h[i + 1]), pair(u[i], u[i + 1])), h[i], h[i + 1]);
-        log_total += total;
-      }
-      if (!FULL) {
-        arrive(b_next);
-        continue;
-      }
-      if (c + 1 < c_end) put_state();
-      uint4 zr[4];
-      if (a.z) {
-        const __nv_bfloat16* z = a.z + (packed ? (q.start + t0 + row) * a.z_tok : seq * a.z_seq + (t0 + row) * a.z_tok) +
-                                 (long long)head * a.P + p0 + 32 * half;
-        const int pc = a.P - p0 - 32 * half;
+      for (int k = 0; k < 32; k += 16) {
+        float e[16], f[16];
+        tc::tmem_ld16(tlane + k, e);        // B^T (t1 + t2 / 2)
+        tc::tmem_ld16(tlane + 64 + k, f);   // B^T (t2 / 2 + t3)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          zr[i] = make_uint4(0, 0, 0, 0);
-          if (!in || 8 * i >= pc) continue;
-          if (a.z_vec) {
-            zr[i] = *reinterpret_cast<const uint4*>(z + 8 * i);
-          } else {
-            const unsigned short* zs = reinterpret_cast<const unsigned short*>(z + 8 * i);
-            zr[i] = make_uint4(zs[0] | (uint32_t)zs[1] << 16, zs[2] | (uint32_t)zs[3] << 16,
-                               zs[4] | (uint32_t)zs[5] << 16, zs[6] | (uint32_t)zs[7] << 16);
-          }
-        }
+        for (int j = 0; j < 16; j += 2)
+          unpair(fma2(d2, pair(h[k + j], h[k + j + 1]), add2(pair(e[j], e[j + 1]), pair(f[j], f[j + 1]))), h[k + j],
+                 h[k + j + 1]);
       }
-      if (!wait(b_y, ph)) break;
-      tc::fence_after_sync();
-      float y[32];
-      tc::tmem_ld32(tlane + kColY + 32 * half, y);
-      arrive(b_next);   // the next chunk's S and C h^T may start
-      // ---- output rows: Y, gated, over X (every product that reads X is done)
-      __nv_bfloat16* yp = a.y + (packed ? (q.start + t0 + row) * a.y_tok : 0) + (long long)head * a.P + p0 + 32 * half;
+    };
+    const uint64_t minus = pair(-1.f, -1.f), minus_two = pair(-2.f, -2.f), one_half = pair(0.5f, 0.5f);
+    // One piece of X~ of chunk i in three terms: 32 tokens and 16 columns
+    auto make_piece = [&](int i, int piece) {
+      const int token = 32 * (piece & 3) + lane, r = i & 1;
+      const uint32_t c = 2 * ((uint32_t)piece >> 2), sw = (uint32_t)(token & 7);
+      const uint32_t at0 = (uint32_t)token * 128 + ((c ^ sw) << 4), at1 = (uint32_t)token * 128 + (((c + 1) ^ sw) << 4);
+      const float w = vec[(i % kDec) * kVec + 3 * kL + token];
+      const uint64_t w2 = pair(w, w);
+      uint4 xa = *reinterpret_cast<const uint4*>(smem + Cf::oX + r * kTile + at0);
+      uint4 xb = *reinterpret_cast<const uint4*>(smem + Cf::oX + r * kTile + at1);
+      // rows of the next sequence: none of them may reach the product
+      if (ragged && i == last_i && t_first + (long long)i * kL + token >= q.len) xa = xb = make_uint4(0, 0, 0, 0);
+      const uint32_t xi[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+      uint32_t t1[8], t2[8], t3[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t at = (uint32_t)row * 128 + (((4 * half + i) ^ rsw) << 4);
-        const uint32_t zi[4] = {zr[i].x, zr[i].y, zr[i].z, zr[i].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float e = y[8 * i + 2 * j], f = y[8 * i + 2 * j + 1];
-          if (a.z) unpair(mul2(pair(e, f), silu2(pair(lo_f(zi[j]), hi_f(zi[j])))), e, f);
-          o[j] = pack2(e, f);
-        }
-        const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
-        if (!tail) *reinterpret_cast<uint4*>(smem + Cf::oX + at) = ov;
-        else if (in && p0 + 32 * half + 8 * i < a.P) *reinterpret_cast<uint4*>(yp + 8 * i) = ov;
+      for (int j = 0; j < 8; ++j) {
+        float e, f;
+        uint64_t z = mul2(pair(lo_f(xi[j]), hi_f(xi[j])), w2);
+        unpair(z, e, f);
+        t1[j] = pack2(e, f);
+        z = fma2(pair(lo_f(t1[j]), hi_f(t1[j])), minus, z);   // exact
+        unpair(mul2(z, one_half), e, f);
+        t2[j] = pack2(e, f);   // half of the second term
+        z = fma2(pair(lo_f(t2[j]), hi_f(t2[j])), minus_two, z);
+        unpair(z, e, f);
+        t3[j] = pack2(e, f);
       }
-      arrive(b_out);
+      unsigned char* to = smem + Cf::oT;
+      *reinterpret_cast<uint4*>(to + at0) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+      *reinterpret_cast<uint4*>(to + at1) = make_uint4(t1[4], t1[5], t1[6], t1[7]);
+      *reinterpret_cast<uint4*>(to + kTile + at0) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+      *reinterpret_cast<uint4*>(to + kTile + at1) = make_uint4(t2[4], t2[5], t2[6], t2[7]);
+      *reinterpret_cast<uint4*>(to + 2 * kTile + at0) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+      *reinterpret_cast<uint4*>(to + 2 * kTile + at1) = make_uint4(t3[4], t3[5], t3[6], t3[7]);
+      fence_proxy_async_smem();
+    };
+    float total = 0.f;   // of the chunk whose U comes next
+    for (int i = 0; i <= n_chunks; ++i) {
+      const int r = i & 1, u = i >> 1;
+      if (i > 0) {
+        if (!wait(kFullU, i - 1)) break;
+        update(total);
+        if (i == n_chunks) break;
+      }
+      if (ragged && i == last_i) {   // rows of the next sequence: none of B's may reach the product
+        if (!wait(kFullB + r, u)) break;
+        if (half == 0 && t_first + (long long)i * kL + row >= q.len)
+          for (uint32_t k = 0; k < 8 * Cf::NT; ++k)
+            *reinterpret_cast<uint4*>(smem + Cf::oB + (r * Cf::NT + (k >> 3)) * kTile + row_at + ((k & 7) << 4)) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      if (!wait(kFullDec + i % kDec, i / kDec) || !wait(kFullX + r, u)) break;
+#pragma unroll 1
+      for (int piece = warp - kSide / 32; piece < kUnits; piece += kSide / 32) make_piece(i, piece);
+      tc::fence_before_sync();
+      arrive(kXt);
+      total = vec[(i % kDec) * kVec + 5 * kL + 8];
+      __syncwarp();
+      if (one) {
+        arrive_one(kEmptyX + r);
+        arrive_one(kEmptyDec + i % kDec);
+      }
+      // the copy of the state before this chunk, once the one before it has been read
+      if (FULL && i > 0) {
+        if (!wait(kFullYi + (r ^ 1), (i - 1) >> 1)) break;
+        put_state();
+        fence_proxy_async_smem();
+        arrive(kH);
+      }
     }
     if (*fail) {
-      if (tid == 0) atomicOr(&a.status->flags, kStatusTimeout);
+      if (tid == kSide) atomicOr(&a.status->flags, kStatusTimeout);
     } else if (!FULL) {
       if (n < NN) {
-        float* wsq = a.ws + (seq * slices + slice) * ws_floats(a.nseg, NN);
         float* e = wsq + ((long long)seg * 64 + 32 * half) * NN;
 #pragma unroll
         for (int i = 0; i < 32; ++i) e[i * NN + n] = h[i];
-        if (tid == 0) wsq[(long long)a.nseg * 64 * NN + seg] = ex2(log_total);
+        if (tid == kSide) wsq[(long long)a.nseg * 64 * NN + seg] = ex2(log_total);
       }
-    } else if (last && a.state && n_ok) {
+    } else if (last && a.state && n < a.N) {
       float* dst = a.state + ((q.slot * a.H + head) * a.P + p0 + 32 * half) * a.N + n;
-      const int pc = a.P - p0 - 32 * half;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
         if (i < pc) dst[(long long)i * a.N] = h[i];
+    }
+  } else if (warp == 16) {
+    if constexpr (FULL) {
+      // ------------------------------------------------ C h^T, M X
+      const uint64_t c0 = desc128(sbase + Cf::oC, 16), h0 = desc128(sbase + Cf::oH, 16);
+      for (int i = 0; i < n_chunks; ++i) {
+        const int r = i & 1, u = i >> 1;
+        const uint32_t ty = tmem + kColY + 64 * r, ts = tmem + kColS + 128 * r;
+        const uint64_t x0 = desc128(sbase + Cf::oX + r * kTile, 16);
+        if (!wait(kFullC, i) || (i > 0 && !wait(kH, i - 1)) || (u > 0 && !wait(kEmptyY + r, u - 1))) break;
+        tc::fence_after_sync();
+#pragma unroll 4
+        for (int k = 0; k < NN / 16; ++k)
+          mma_ss(ty, c0 + (k >> 2) * (kTile >> 4) + (k & 3) * 2, h0 + k * 128, kId | kN64 | kTransB, k > 0, one);
+        if (one) {
+          tc::mma_commit(bar + kFullYi + r);
+          tc::mma_commit(bar + kEmptyC);
+        }
+        __syncwarp();
+        if (!wait(kM, i) || !wait(kFullX + r, u)) break;
+        tc::fence_after_sync();
+#pragma unroll 4
+        for (int k = 0; k < kL / 16; ++k)
+          mma_ts(ty, ts + 64 * (k >> 2) + 8 * (k & 3), x0 + k * 128, kId | kN64 | kTransB, true, one);
+        if (one) {
+          tc::mma_commit(bar + kFullY + r);
+          tc::mma_commit(bar + kEmptyS + r);
+          tc::mma_commit(bar + kEmptyX + r);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 17) {
+    // ------------------------------------------------ B^T X~, then S of the next chunk
+    const uint64_t c0 = desc128(sbase + Cf::oC, 16), t0 = desc128(sbase + Cf::oT, kTile);
+    for (int i = FULL ? -1 : 0; i < n_chunks; ++i) {   // turn -1 forms the first S
+      if (i >= 0) {
+        const int r = i & 1;
+        const uint64_t b0 = desc128(sbase + Cf::oB + r * Cf::NT * kTile, kTile);
+        if (!wait(kXt, i) || !wait(kFullB + r, i >> 1)) break;
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass)
+#pragma unroll 4
+          for (int k = 0; k < kL / 16; ++k)
+            mma_ss(tmem + kColU, b0 + k * 128, t0 + pass * (kTile >> 4) + k * 128, kId | kN128 | kTransA | kTransB,
+                   pass > 0 || k > 0, one);
+        if (one) {
+          tc::mma_commit(bar + kFullU);
+          tc::mma_commit(bar + kEmptyB + r);
+        }
+        __syncwarp();
+      }
+      if (!FULL || i == last_i) continue;
+      const int r = (i + 1) & 1, u = (i + 1) >> 1;
+      if (!wait(kFullB + r, u) || !wait(kFullC, i + 1) || (u > 0 && !wait(kEmptyS + r, u - 1))) break;
+      tc::fence_after_sync();
+      const uint64_t b0 = desc128(sbase + Cf::oB + r * Cf::NT * kTile, 16);
+#pragma unroll 4
+      for (int k = 0; k < NN / 16; ++k) {
+        const uint32_t at = (k >> 2) * (kTile >> 4) + (k & 3) * 2;
+        mma_ss(tmem + kColS + 128 * r, c0 + at, b0 + at, kId | kN128, k > 0, one);
+      }
+      if (one) {
+        tc::mma_commit(bar + kFullS + r);
+        tc::mma_commit(bar + kEmptyB + r);
+        tc::mma_commit(bar + kEmptyC);
+      }
+      __syncwarp();
+    }
+  } else if (FULL && warp == 19) {
+    // ------------------------------------------------ stores of y
+    for (int i = 1; i <= n_chunks; ++i) {
+      if (!wait(kStage, i - 1)) break;
+      if (one) {
+        if (!(ragged && i - 1 == last_i))
+          store_4d(&map_y, p0, head, row0 + (int)(t_first + (long long)(i - 1) * kL), batch, sbase + Cf::oY);
+        store_read_done();
+        arrive_one(kStaged);
+      }
+      __syncwarp();
+    }
+    if (one) store_done();
+  } else if (warp == 18) {
+    // ------------------------------------------------ loads
+    int i = 0;
+    for (; i < n_chunks; ++i) {
+      const int r = i & 1, u = i >> 1;
+      const int t = row0 + (int)(t_first + (long long)i * kL);
+      if (u > 0 && !wait(kEmptyB + r, u - 1)) break;
+      if (one) {
+        mbar_arrive_expect_tx(bar + kFullB + r, Cf::NT * kTile);
+#pragma unroll 1
+        for (uint32_t k = 0; k < Cf::NT; ++k)
+          load_4d(sbase + Cf::oB + (r * Cf::NT + k) * kTile, &map_B, 64 * (int)k, group, t, batch, bar + kFullB + r);
+      }
+      __syncwarp();
+      if (u > 0 && !wait(kEmptyX + r, u - 1)) break;
+      if (one) {
+        mbar_arrive_expect_tx(bar + kFullX + r, kTile);
+        load_4d(sbase + Cf::oX + r * kTile, &map_x, p0, head, t, batch, bar + kFullX + r);
+        // C has one place and is asked for late: its rows are fetched into L2 now
+        if (FULL && i > 0)
+#pragma unroll 1
+          for (uint32_t k = 0; k < Cf::NT; ++k) prefetch_4d(&map_C, 64 * (int)k, group, t, batch);
+      }
+      __syncwarp();
+      if (FULL) {
+        if (i > 0 && !wait(kEmptyC, i - 1)) break;
+        if (one) {
+          mbar_arrive_expect_tx(bar + kFullC, Cf::NT * kTile);
+#pragma unroll 1
+          for (uint32_t k = 0; k < Cf::NT; ++k)
+            load_4d(sbase + Cf::oC + k * kTile, &map_C, 64 * (int)k, group, t, batch, bar + kFullC);
+        }
+        __syncwarp();
+      }
+    }
+    if (*fail || i < n_chunks) {   // nothing lands after the CTA has gone
+      for (int j = i > 2 ? i - 2 : 0; j <= i && j < n_chunks; ++j) {
+        if (!mbar_wait_bounded(bar + kFullB + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitLimitNs / 8)) continue;
+        mbar_wait_bounded(bar + kFullX + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitLimitNs / 8);
+        if (FULL) mbar_wait_bounded(bar + kFullC, (uint32_t)j & 1u, kWaitLimitNs / 8);
+      }
+    }
+  } else if (warp >= 22) {
+    // ------------------------------------------------ decays: blocks j0 and j0 + 1 of 32 tokens of every chunk
+    const int j0 = 2 * (warp - 22);
+    const __nv_bfloat16* dt = a.dt + (packed ? q.start * a.dt_tok : seq * a.dt_seq) + head;
+    const float A2 = a.A[head] * 1.44269504088896341f, bias = a.dt_bias ? a.dt_bias[head] : 0.f;
+    long long t = t_first + 32 * j0 + lane;
+    float raw[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) raw[j] = t + 32 * j < q.len ? __bfloat162float(dt[(t + 32 * j) * a.dt_tok]) : 0.f;
+#pragma unroll 1
+    for (int i = 0; i < n_chunks; ++i) {
+      float s[2], inc[2], ex[2], end[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool in = t + 32 * j < q.len;
+        s[j] = in ? time_step(raw[j], bias, a.softplus) : 0.f;
+        inc[j] = ex[j] = in ? A2 * s[j] : 0.f;
+      }
+      t += kL;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (t + 32 * j < q.len && i < last_i) raw[j] = __bfloat162float(dt[(t + 32 * j) * a.dt_tok]);
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float up = __shfl_up_sync(0xffffffffu, inc[j], o), down = __shfl_down_sync(0xffffffffu, ex[j], o);
+          if (lane >= o) inc[j] += up;
+          if (lane + o < 32) ex[j] += down;
+        }
+      }
+      float* v = vec + (i % kDec) * kVec;
+      // the two warps leave together: each reads the other's sums
+      const bool ok = i < kDec || wait(kEmptyDec + i % kDec, i / kDec - 1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        end[j] = __shfl_sync(0xffffffffu, inc[j], 31);
+        ex[j] = __shfl_down_sync(0xffffffffu, ex[j], 1);
+        if (lane == 31) ex[j] = 0.f;
+        if (ok && one) v[5 * kL + 12 + j0 + j] = end[j];
+      }
+      if (named_or(1, 64, !ok)) break;
+      float sum[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = v[5 * kL + 12 + j];
+      float before = j0 == 0 ? 0.f : sum[0] + sum[1];
+      const float after = j0 == 0 ? sum[2] + sum[3] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int at = 32 * (j0 + j) + lane;
+        const float behind = j == 0 ? end[1] + after : after;
+        v[at] = before + inc[j];
+        v[kL + at] = s[j] * ex2(ex[j]);
+        v[2 * kL + at] = s[j] * ex2(-inc[j]);
+        v[3 * kL + at] = s[j] * ex2(ex[j] + behind);
+        v[4 * kL + at] = s[j];
+        const bool small = __all_sync(0xffffffffu, fabsf(inc[j]) < 100.f);
+        if (one) {
+          v[5 * kL + j0 + j] = before;
+          v[5 * kL + 4 + j0 + j] = before + end[j];
+          v[5 * kL + 16 + j0 + j] = small ? 1.f : 0.f;
+        }
+        before += end[j];
+      }
+      if (one && j0 == 0) v[5 * kL + 8] = sum[0] + sum[1] + sum[2] + sum[3];
+      arrive(kFullDec + i % kDec);
     }
   }
   tc::fence_before_sync();
@@ -704,17 +853,17 @@ cudaError_t launch(const SsmArgs& s, const PromptArgs& a, const PromptPlan& plan
   const long long ctas = s.seqs.n_seq * a.H * a.pslices * plan.nseg;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   constexpr int bytes = (int)Cfg<NN>::bytes;
-  cudaError_t e = cudaFuncSetAttribute(ssm_prompt_kernel<NN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  if (plan.nseg > 1) {
-    e = cudaFuncSetAttribute(ssm_prompt_kernel<NN, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  auto run = [&](auto kern) -> cudaError_t {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    ssm_prompt_kernel<NN, false><<<(unsigned int)ctas, kThreads, bytes, st>>>(maps[0], maps[1], maps[2], maps[3], a);
-    e = cudaGetLastError();
+    kern<<<(unsigned int)ctas, kThreads, bytes, st>>>(maps[0], maps[1], maps[2], maps[3], a);
+    return cudaGetLastError();
+  };
+  if (plan.nseg > 1) {
+    const cudaError_t e = run(ssm_prompt_kernel<NN, false, false>);
     if (e != cudaSuccess) return e;
   }
-  ssm_prompt_kernel<NN, true><<<(unsigned int)ctas, kThreads, bytes, st>>>(maps[0], maps[1], maps[2], maps[3], a);
-  return cudaGetLastError();
+  return a.z ? run(ssm_prompt_kernel<NN, true, true>) : run(ssm_prompt_kernel<NN, true, false>);
 }
 
 }  // namespace
@@ -724,12 +873,12 @@ PromptPlan ssm_prompt_plan(long long n_seq, long long max_len, long long H, long
   PromptPlan p{};
   p.fits = bf16 && P % 8 == 0 && N % 8 == 0 && N <= 128 && max_len >= kPromptMin && H < (1 << 20) && P < (1 << 20);
   if (!p.fits) return p;
-  const long long slices = H * ((P + 63) / 64), chunks = (max_len + kL - 1) / kL, slots = 2LL * sm_count;
+  const long long slices = H * ((P + 63) / 64), chunks = (max_len + kL - 1) / kL, slots = sm_count;
   p.nn = N <= 64 ? 64 : 128;
   p.nseg = 1;
   p.seg_chunks = chunks;
-  // Two CTAs an SM.  While the slices leave most of them idle, segments shorten the longest run of
-  // chunks; a chunk of the first launch costs about half of one of the second.
+  // One CTA an SM.  While the slices leave SMs idle, segments shorten the longest run of chunks; a
+  // chunk of the first launch costs about half of one of the second.
   double best = (double)((n_seq * slices + slots - 1) / slots) * chunks;
   for (long long k = 2; k <= chunks && k <= 64 && n_seq * slices * k <= 2 * slots; ++k) {
     const long long per = (chunks + k - 1) / k, nseg = (chunks + per - 1) / per;
