@@ -26,7 +26,8 @@
 //   8-15  state: X~, then h' from its product U
 //   16    issues C h^T and M X               17  issues B^T X~ and then S of the next chunk
 //   18    issues the loads                    19  stores y
-//   22-23 decays, 64 tokens of a chunk each
+//   20-21 decays, 64 tokens of a chunk each
+// (the first launch of a cut sequence has no output: warps 0-7 form half of X~ there)
 // In order: S of the next chunk is formed while M of this one is, M of the next one while M X of
 // this one runs.  The longest chain is X~, U, h, X~ ..: so U comes before S, and h's copy is written
 // after the next X~.
@@ -85,7 +86,8 @@ enum : int {
   kEmptyDec = 28,  // [4] and read
   kStage = 32,     //     y is staged
   kStaged = 33,    //     and its store has read it
-  kBars = 34
+  kFullZ = 34,     //     z has landed where y will be staged
+  kBars = 35
 };
 
 // Shared memory: B [2] | C | X [2] | X~ (three terms) | state (bfloat16, [n][64 p]) | y | decays | barriers
@@ -213,7 +215,7 @@ struct PromptArgs {
   int H, P, G, N, pslices;
   int nseg, seg_chunks;
   long long dt_seq, dt_tok, z_seq, z_tok, y_seq, y_tok;
-  bool softplus, z_vec;
+  bool softplus;
   DevStatus* status;
 };
 
@@ -222,10 +224,12 @@ struct PromptArgs {
 __host__ __device__ constexpr long long ws_floats(int nseg, int NN) { return (long long)nseg * 64 * NN + (nseg + 63) / 64 * 64; }
 
 // FULL: the outputs and the final state; else what the segment adds to the state.
-template <int NN, bool FULL, bool GATE>
+// GATE: 0 no z, 1 z by TMA through y's staging tile, 2 z read directly (rows not on 16-byte boundaries).
+template <int NN, bool FULL, int GATE>
 __global__ void __launch_bounds__(kThreads, 1)
     ssm_prompt_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_B,
                       const __grid_constant__ CUtensorMap map_C, const __grid_constant__ CUtensorMap map_y,
+                      const __grid_constant__ CUtensorMap map_z,
                       const __grid_constant__ PromptArgs a) {
   using Cf = Cfg<NN>;
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -270,10 +274,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kBars; ++i) {
       int count = 1;
       if (i == kEmptyB || i == kEmptyB + 1 || i == kEmptyC) count = FULL ? 2 : 1;
-      if (i == kEmptyX || i == kEmptyX + 1) count = FULL ? 2 * W + 1 : W;
-      if (i >= kEmptyDec && i < kEmptyDec + kDec) count = FULL ? 2 * W : W;
+      if (i == kEmptyX || i == kEmptyX + 1) count = FULL ? 2 * W + 1 : 2 * W;
+      if (i >= kEmptyDec && i < kEmptyDec + kDec) count = 2 * W;
       if (i >= kFullDec && i < kFullDec + kDec) count = 2;
-      if (i == kM || i == kH || i == kEmptyY || i == kEmptyY + 1 || i == kXt || i == kStage) count = W;
+      if (i == kM || i == kH || i == kEmptyY || i == kEmptyY + 1 || i == kStage) count = W;
+      if (i == kXt) count = FULL ? W : 2 * W;
       mbar_init(bar + i, count);
     }
     *fail = 0;
@@ -358,8 +363,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   // whether rows of the next sequence lie behind this one's in the last chunk
   const bool ragged = packed && c_end == chunks && q.len % kL != 0;
 
+  const uint64_t minus = pair(-1.f, -1.f), minus_two = pair(-2.f, -2.f), one_half = pair(0.5f, 0.5f);
+  // One piece of X~ of chunk i in three terms: 32 tokens and 16 columns
+  auto make_piece = [&](int i, int piece) {
+    const int token = 32 * (piece & 3) + lane, r = i & 1;
+    const uint32_t c = 2 * ((uint32_t)piece >> 2), sw = (uint32_t)(token & 7);
+    const uint32_t at0 = (uint32_t)token * 128 + ((c ^ sw) << 4), at1 = (uint32_t)token * 128 + (((c + 1) ^ sw) << 4);
+    const float w = vec[(i % kDec) * kVec + 3 * kL + token];
+    const uint64_t w2 = pair(w, w);
+    uint4 xa = *reinterpret_cast<const uint4*>(smem + Cf::oX + r * kTile + at0);
+    uint4 xb = *reinterpret_cast<const uint4*>(smem + Cf::oX + r * kTile + at1);
+    // rows of the next sequence: none of them may reach the product
+    if (ragged && i == last_i && t_first + (long long)i * kL + token >= q.len) xa = xb = make_uint4(0, 0, 0, 0);
+    const uint32_t xi[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+    uint32_t t1[8], t2[8], t3[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float e, f;
+      uint64_t z = mul2(pair(lo_f(xi[j]), hi_f(xi[j])), w2);
+      unpair(z, e, f);
+      t1[j] = pack2(e, f);
+      z = fma2(pair(lo_f(t1[j]), hi_f(t1[j])), minus, z);   // exact
+      unpair(mul2(z, one_half), e, f);
+      t2[j] = pack2(e, f);   // half of the second term
+      z = fma2(pair(lo_f(t2[j]), hi_f(t2[j])), minus_two, z);
+      unpair(z, e, f);
+      t3[j] = pack2(e, f);
+    }
+    unsigned char* to = smem + Cf::oT;
+    *reinterpret_cast<uint4*>(to + at0) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+    *reinterpret_cast<uint4*>(to + at1) = make_uint4(t1[4], t1[5], t1[6], t1[7]);
+    *reinterpret_cast<uint4*>(to + kTile + at0) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+    *reinterpret_cast<uint4*>(to + kTile + at1) = make_uint4(t2[4], t2[5], t2[6], t2[7]);
+    *reinterpret_cast<uint4*>(to + 2 * kTile + at0) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+    *reinterpret_cast<uint4*>(to + 2 * kTile + at1) = make_uint4(t3[4], t3[5], t3[6], t3[7]);
+    fence_proxy_async_smem();
+  };
+
   if (warp < kSide / 32) {
-    if constexpr (FULL) {
+    if constexpr (!FULL) {
+      // ------------------------------------------------ the other half of X~
+      for (int i = 0; i < n_chunks; ++i) {
+        if (!wait(kFullDec + i % kDec, i / kDec) || !wait(kFullX + (i & 1), i >> 1) || (i > 0 && !wait(kFullU, i - 1))) break;
+        make_piece(i, kSide / 32 + warp);
+        arrive(kXt);
+        if (one) {
+          arrive_one(kEmptyX + (i & 1));
+          arrive_one(kEmptyDec + i % kDec);
+        }
+      }
+    } else {
       // ------------------------------------------------ output
       const int qd = warp & 3;   // block of rows
       const uint32_t tlane = tmem + ((uint32_t)(32 * qd) << 16);
@@ -369,33 +422,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto finish = [&](int i) -> bool {
         const long long t = t_first + (long long)i * kL + row;
         const bool in = t < q.len, tail = ragged && i == last_i;
-        const __nv_bfloat16* z = GATE ? a.z + (packed ? (q.start + t) * a.z_tok : seq * a.z_seq + t * a.z_tok) +
-                                            (long long)head * a.P + p0 + 32 * half
-                                      : nullptr;
-        if (!wait(kFullY + (i & 1), i >> 1) || (i > 0 && !wait(kStaged, i - 1))) return false;
+        const __nv_bfloat16* z = GATE == 2 ? a.z + (packed ? (q.start + t) * a.z_tok : seq * a.z_seq + t * a.z_tok) +
+                                                 (long long)head * a.P + p0 + 32 * half
+                                           : nullptr;
+        if (!wait(kFullY + (i & 1), i >> 1)) return false;
+        if (GATE == 1 ? !wait(kFullZ, i) : (i > 0 && !wait(kStaged, i - 1))) return false;
         tc::fence_after_sync();
 #pragma unroll 1
         for (int k = 0; k < 32; k += 16) {
           uint4 zr[2];
-          if (GATE) {
+          if (GATE == 2) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               zr[j] = make_uint4(0, 0, 0, 0);
               const int c = k + 8 * j;
               if (!in || c >= pc) continue;
-              if (a.z_vec) {
-                zr[j] = *reinterpret_cast<const uint4*>(z + c);
-              } else {
-                const unsigned short* zs = reinterpret_cast<const unsigned short*>(z + c);
-                zr[j] = make_uint4(zs[0] | (uint32_t)zs[1] << 16, zs[2] | (uint32_t)zs[3] << 16,
-                                   zs[4] | (uint32_t)zs[5] << 16, zs[6] | (uint32_t)zs[7] << 16);
-              }
+              const unsigned short* zs = reinterpret_cast<const unsigned short*>(z + c);
+              zr[j] = make_uint4(zs[0] | (uint32_t)zs[1] << 16, zs[2] | (uint32_t)zs[3] << 16,
+                                 zs[4] | (uint32_t)zs[5] << 16, zs[6] | (uint32_t)zs[7] << 16);
             }
           }
           float y[16];
           tc::tmem_ld16(tlane + kColY + 64 * (i & 1) + 32 * half + k, y);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
+            const int c = k + 8 * j;
+            uint4* at = reinterpret_cast<uint4*>(smem + Cf::oY + row_at + (((uint32_t)(4 * half + (c >> 3)) ^ rsw) << 4));
+            if (GATE == 1) zr[j] = *at;
             const uint32_t zi[4] = {zr[j].x, zr[j].y, zr[j].z, zr[j].w};
             uint32_t w[4];
 #pragma unroll
@@ -405,9 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               w[e] = pack2(f, g);
             }
             const uint4 o = make_uint4(w[0], w[1], w[2], w[3]);
-            const int c = k + 8 * j;
             if (!tail) {
-              *reinterpret_cast<uint4*>(smem + Cf::oY + row_at + (((uint32_t)(4 * half + (c >> 3)) ^ rsw) << 4)) = o;
+              *at = o;
             } else if (in && c < pc) {
               *reinterpret_cast<uint4*>(a.y + (q.start + t) * a.y_tok + (long long)head * a.P + p0 + 32 * half + c) = o;
             }
@@ -526,42 +578,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                  h[k + j + 1]);
       }
     };
-    const uint64_t minus = pair(-1.f, -1.f), minus_two = pair(-2.f, -2.f), one_half = pair(0.5f, 0.5f);
-    // One piece of X~ of chunk i in three terms: 32 tokens and 16 columns
-    auto make_piece = [&](int i, int piece) {
-      const int token = 32 * (piece & 3) + lane, r = i & 1;
-      const uint32_t c = 2 * ((uint32_t)piece >> 2), sw = (uint32_t)(token & 7);
-      const uint32_t at0 = (uint32_t)token * 128 + ((c ^ sw) << 4), at1 = (uint32_t)token * 128 + (((c + 1) ^ sw) << 4);
-      const float w = vec[(i % kDec) * kVec + 3 * kL + token];
-      const uint64_t w2 = pair(w, w);
-      uint4 xa = *reinterpret_cast<const uint4*>(smem + Cf::oX + r * kTile + at0);
-      uint4 xb = *reinterpret_cast<const uint4*>(smem + Cf::oX + r * kTile + at1);
-      // rows of the next sequence: none of them may reach the product
-      if (ragged && i == last_i && t_first + (long long)i * kL + token >= q.len) xa = xb = make_uint4(0, 0, 0, 0);
-      const uint32_t xi[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
-      uint32_t t1[8], t2[8], t3[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float e, f;
-        uint64_t z = mul2(pair(lo_f(xi[j]), hi_f(xi[j])), w2);
-        unpair(z, e, f);
-        t1[j] = pack2(e, f);
-        z = fma2(pair(lo_f(t1[j]), hi_f(t1[j])), minus, z);   // exact
-        unpair(mul2(z, one_half), e, f);
-        t2[j] = pack2(e, f);   // half of the second term
-        z = fma2(pair(lo_f(t2[j]), hi_f(t2[j])), minus_two, z);
-        unpair(z, e, f);
-        t3[j] = pack2(e, f);
-      }
-      unsigned char* to = smem + Cf::oT;
-      *reinterpret_cast<uint4*>(to + at0) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-      *reinterpret_cast<uint4*>(to + at1) = make_uint4(t1[4], t1[5], t1[6], t1[7]);
-      *reinterpret_cast<uint4*>(to + kTile + at0) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-      *reinterpret_cast<uint4*>(to + kTile + at1) = make_uint4(t2[4], t2[5], t2[6], t2[7]);
-      *reinterpret_cast<uint4*>(to + 2 * kTile + at0) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
-      *reinterpret_cast<uint4*>(to + 2 * kTile + at1) = make_uint4(t3[4], t3[5], t3[6], t3[7]);
-      fence_proxy_async_smem();
-    };
     float total = 0.f;   // of the chunk whose U comes next
     for (int i = 0; i <= n_chunks; ++i) {
       const int r = i & 1, u = i >> 1;
@@ -579,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!wait(kFullDec + i % kDec, i / kDec) || !wait(kFullX + r, u)) break;
 #pragma unroll 1
-      for (int piece = warp - kSide / 32; piece < kUnits; piece += kSide / 32) make_piece(i, piece);
+      for (int piece = warp - kSide / 32; piece < (FULL ? kUnits : kUnits / 2); piece += kSide / 32) make_piece(i, piece);
       tc::fence_before_sync();
       arrive(kXt);
       total = vec[(i % kDec) * kVec + 5 * kL + 8];
@@ -681,18 +697,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else if (FULL && warp == 19) {
-    // ------------------------------------------------ stores of y
-    for (int i = 1; i <= n_chunks; ++i) {
-      if (!wait(kStage, i - 1)) break;
+    // ------------------------------------------------ stores of y, and z of the next chunk into the same tile
+    for (int i = 0; i <= n_chunks; ++i) {
+      if (i > 0 && !wait(kStage, i - 1)) break;
       if (one) {
-        if (!(ragged && i - 1 == last_i))
-          store_4d(&map_y, p0, head, row0 + (int)(t_first + (long long)(i - 1) * kL), batch, sbase + Cf::oY);
-        store_read_done();
-        arrive_one(kStaged);
+        const int t = row0 + (int)(t_first + (long long)i * kL);
+        if (i > 0) {
+          if (!(ragged && i - 1 == last_i)) store_4d(&map_y, p0, head, t - kL, batch, sbase + Cf::oY);
+          store_read_done();
+          arrive_one(kStaged);
+        }
+        if (GATE == 1 && i < n_chunks) {
+          mbar_arrive_expect_tx(bar + kFullZ, kTile);
+          load_4d(sbase + Cf::oY, &map_z, p0, head, t, batch, bar + kFullZ);
+        }
       }
       __syncwarp();
     }
     if (one) store_done();
+    if (GATE == 1 && *fail)   // nothing lands after the CTA has gone
+      for (int j = 0; j < 2; ++j) mbar_wait_bounded(bar + kFullZ, (uint32_t)j, kWaitLimitNs / 8);
   } else if (warp == 18) {
     // ------------------------------------------------ loads
     int i = 0;
@@ -735,9 +759,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (FULL) mbar_wait_bounded(bar + kFullC, (uint32_t)j & 1u, kWaitLimitNs / 8);
       }
     }
-  } else if (warp >= 22) {
+  } else if (warp == 20 || warp == 21) {
     // ------------------------------------------------ decays: blocks j0 and j0 + 1 of 32 tokens of every chunk
-    const int j0 = 2 * (warp - 22);
+    const int j0 = 2 * (warp - 20);
     const __nv_bfloat16* dt = a.dt + (packed ? q.start * a.dt_tok : seq * a.dt_seq) + head;
     const float A2 = a.A[head] * 1.44269504088896341f, bias = a.dt_bias ? a.dt_bias[head] : 0.f;
     long long t = t_first + 32 * j0 + lane;
@@ -849,21 +873,25 @@ bool encode(CUtensorMap* m, const void* base, long long width, long long heads, 
 
 template <int NN>
 cudaError_t launch(const SsmArgs& s, const PromptArgs& a, const PromptPlan& plan, const CUtensorMap* maps,
-                   cudaStream_t st) {
+                   int gate, cudaStream_t st) {
   const long long ctas = s.seqs.n_seq * a.H * a.pslices * plan.nseg;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   constexpr int bytes = (int)Cfg<NN>::bytes;
   auto run = [&](auto kern) -> cudaError_t {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned int)ctas, kThreads, bytes, st>>>(maps[0], maps[1], maps[2], maps[3], a);
+    kern<<<(unsigned int)ctas, kThreads, bytes, st>>>(maps[0], maps[1], maps[2], maps[3], maps[4], a);
     return cudaGetLastError();
   };
   if (plan.nseg > 1) {
-    const cudaError_t e = run(ssm_prompt_kernel<NN, false, false>);
+    const cudaError_t e = run(ssm_prompt_kernel<NN, false, 0>);
     if (e != cudaSuccess) return e;
   }
-  return a.z ? run(ssm_prompt_kernel<NN, true, true>) : run(ssm_prompt_kernel<NN, true, false>);
+  switch (gate) {
+    case 0: return run(ssm_prompt_kernel<NN, true, 0>);
+    case 1: return run(ssm_prompt_kernel<NN, true, 1>);
+    default: return run(ssm_prompt_kernel<NN, true, 2>);
+  }
 }
 
 }  // namespace
@@ -877,13 +905,16 @@ PromptPlan ssm_prompt_plan(long long n_seq, long long max_len, long long H, long
   p.nn = N <= 64 ? 64 : 128;
   p.nseg = 1;
   p.seg_chunks = chunks;
-  // One CTA an SM.  While the slices leave SMs idle, segments shorten the longest run of chunks; a
-  // chunk of the first launch costs about half of one of the second.
-  double best = (double)((n_seq * slices + slots - 1) / slots) * chunks;
-  for (long long k = 2; k <= chunks && k <= 64 && n_seq * slices * k <= 2 * slots; ++k) {
-    const long long per = (chunks + k - 1) / k, nseg = (chunks + per - 1) / per;
-    if (nseg != k) continue;
-    const double cost = 1.5 * (double)((n_seq * slices * k + slots - 1) / slots) * per + 2.0 + 0.1 * k;
+  // One CTA an SM.  While the slices leave SMs idle, segments shorten the longest run of chunks.  In
+  // microseconds, measured: a chunk 2.3, a chunk of the first launch 1.2, a CTA's start 3, and 0.7 for
+  // each segment that a start joins.  (One sequence of 16384 tokens, 16 heads: 9 segments; 19, which
+  // fill the SMs twice, take a third longer.)
+  const auto waves = [&](long long k) { return (double)((n_seq * slices * k + slots - 1) / slots); };
+  double best = waves(1) * (2.3 * chunks + 3.0);
+  for (long long k = 2; k <= chunks && k <= 64; ++k) {
+    const long long per = (chunks + k - 1) / k;
+    if ((chunks + per - 1) / per != k) continue;
+    const double cost = waves(k) * (3.5 * per + 6.0 + 0.7 * k);
     if (cost < best) {
       best = cost;
       p.nseg = (int)k;
@@ -898,12 +929,14 @@ cudaError_t launch_ssm_prompt(const SsmArgs& s, const PromptPlan& plan, cudaStre
   *used = false;
   const bool packed = s.seqs.offsets != nullptr;
   const long long tokens = s.seqs.T, batch = packed ? 1 : s.seqs.n_seq;
-  CUtensorMap maps[4];
+  CUtensorMap maps[5];
   if (!encode(&maps[0], s.x, s.P, s.H, tokens, batch, s.x_tok, s.x_seq) ||
       !encode(&maps[1], s.B, s.N, s.G, tokens, batch, s.B_tok, s.B_seq) ||
       !encode(&maps[2], s.C, s.N, s.G, tokens, batch, s.C_tok, s.C_seq) ||
       !encode(&maps[3], s.y, s.P, s.H, tokens, batch, s.y_tok, s.y_seq))
     return cudaSuccess;
+  maps[4] = maps[3];
+  const int gate = !s.z ? 0 : encode(&maps[4], s.z, s.P, s.H, tokens, batch, s.z_tok, s.z_seq) ? 1 : 2;
   PromptArgs a{};
   a.dt = static_cast<const __nv_bfloat16*>(s.dt);
   a.A = s.A; a.D = s.D; a.dt_bias = s.dt_bias; a.state = s.state; a.ws = s.ws;
@@ -916,11 +949,9 @@ cudaError_t launch_ssm_prompt(const SsmArgs& s, const PromptPlan& plan, cudaStre
   a.seg_chunks = (int)plan.seg_chunks;
   a.dt_seq = s.dt_seq; a.dt_tok = s.dt_tok; a.z_seq = s.z_seq; a.z_tok = s.z_tok; a.y_seq = s.y_seq; a.y_tok = s.y_tok;
   a.softplus = s.softplus;
-  a.z_vec = ((reinterpret_cast<uintptr_t>(s.z) & 15u) | (unsigned long long)(s.z_tok % 8) |
-             (unsigned long long)(packed ? 0 : s.z_seq % 8)) == 0;
   a.status = s.status;
   *used = true;
-  return plan.nn == 64 ? launch<64>(s, a, plan, maps, st) : launch<128>(s, a, plan, maps, st);
+  return plan.nn == 64 ? launch<64>(s, a, plan, maps, gate, st) : launch<128>(s, a, plan, maps, gate, st);
 }
 
 }  // namespace vla
