@@ -29,8 +29,8 @@ static scan_fn f_scan;
 static ws_fn f_ws;
 static norm_fn f_norm;
 static PyObject *t_f32, *t_bf16, *t_i32, *t_e4m3, *t_i8;          /* torch dtypes */
-static PyObject *c_like, *c_empty, *c_bytes, *c_stream;           /* allocators and the current stream */
-static PyObject *s_shape, *s_dtype, *s_get_device, *s_stride, *s_data_ptr, *s_ptr, *s_index, *s_fail;
+static PyObject *c_like, *c_dense, *c_empty, *c_bytes, *c_stream; /* allocators and the current stream */
+static PyObject *s_shape, *s_dtype, *s_get_device, *s_stride, *s_data_ptr, *s_ptr, *s_index, *s_fail, *k_dtype;
 
 enum { MAXD = 8 };
 typedef struct {
@@ -252,9 +252,23 @@ static PyObject* failed(PyObject* self, vla_err_t code, PyObject* y) {
   return r;
 }
 
+/* A new contiguous tensor of x's shape; dtype NULL: x's.  torch.empty_like keeps the strides of a
+ * contiguous x, and costs a fifth of the call that asks for a layout. */
+static PyObject* like(const Tensor* x, PyObject* dtype) {
+  long long step = 1;
+  int dense = 1;
+  for (int i = x->nd - 1; i >= 0; --i) {
+    if (x->shape[i] != 1 && x->stride[i] != step) dense = 0;
+    step *= x->shape[i];
+  }
+  PyObject* args[2] = {x->obj, dtype};
+  if (!dense) return PyObject_Vectorcall(c_dense, args, dtype ? 2 : 1, NULL);
+  return PyObject_Vectorcall(c_like, args, 1, dtype ? k_dtype : NULL);
+}
+
 /* y as given, or a new contiguous tensor like x. */
-static PyObject* output(PyObject* y, PyObject* x) {
-  if (y == Py_None) return PyObject_CallOneArg(c_like, x);
+static PyObject* output(PyObject* y, const Tensor* x) {
+  if (y == Py_None) return like(x, NULL);
   Py_INCREF(y);
   return y;
 }
@@ -292,7 +306,7 @@ static PyObject* py_conv(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
   if (dense(a[3], "bias", shape, 1, t_f32, c.device, &bias)) return NULL;
   shape[0] = b.n_slots; shape[1] = K - 1; shape[2] = C;
   if (dense(a[4], "state", shape, 3, dtype, c.device, &sp)) return NULL;
-  if (!(y = output(a[5], a[1]))) return NULL;
+  if (!(y = output(a[5], &x))) return NULL;
   if (rows(&yt, y, "y", x.shape, x.nd, dtype, c.device, b.form, strides + 2)) {
     Py_DECREF(y);
     return NULL;
@@ -346,7 +360,7 @@ static PyObject* py_scan(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
   size_t need = 0;
   vla_err_t code = f_ws(c.h, b.n_seq, b.T, b.max_len, b.form == PACKED, H, P, N, io, &need);
   if (code) return failed(self, code, NULL);
-  if (!(y = output(a[7], a[1]))) return NULL;
+  if (!(y = output(a[7], &x))) return NULL;
   if (rows(&yt, y, "y", x.shape, x.nd, dtype, c.device, b.form, strides + 10)) {
     Py_DECREF(y);
     return NULL;
@@ -432,11 +446,8 @@ static PyObject* py_norm(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
   if (a[4] != Py_None) {
     y = a[4];
     Py_INCREF(y);
-  } else if (out == 0) {
-    y = PyObject_CallOneArg(c_like, a[1]);
   } else {
-    PyObject* args[2] = {a[1], odtype};
-    y = PyObject_Vectorcall(c_like, args, 2, NULL);
+    y = like(&x, out == 0 ? NULL : odtype);
   }
   if (!y) return NULL;
   if (read_tensor(&yt, y, "y") || check(&yt, x.shape, x.nd, odtype, c.device) || even(&yt, &ignored, &y_row)) goto bad;
@@ -475,20 +486,20 @@ bad:
   return NULL;
 }
 
-/* setup(addresses of the four entry points, dtypes f32 bf16 i32 e4m3 i8, like, empty, bytes, stream) */
+/* setup(addresses of the four entry points, dtypes f32 bf16 i32 e4m3 i8, like, dense, empty, bytes, stream) */
 static PyObject* py_setup(PyObject* mod, PyObject* args) {
   (void)mod;
   unsigned long long p[4];
-  PyObject* o[9];
-  if (!PyArg_ParseTuple(args, "KKKKOOOOOOOOO", p, p + 1, p + 2, p + 3, o, o + 1, o + 2, o + 3, o + 4, o + 5, o + 6,
-                        o + 7, o + 8))
+  PyObject* o[10];
+  if (!PyArg_ParseTuple(args, "KKKKOOOOOOOOOO", p, p + 1, p + 2, p + 3, o, o + 1, o + 2, o + 3, o + 4, o + 5, o + 6,
+                        o + 7, o + 8, o + 9))
     return NULL;
   f_conv = (conv_fn)(uintptr_t)p[0];
   f_scan = (scan_fn)(uintptr_t)p[1];
   f_ws = (ws_fn)(uintptr_t)p[2];
   f_norm = (norm_fn)(uintptr_t)p[3];
-  PyObject** slot[9] = {&t_f32, &t_bf16, &t_i32, &t_e4m3, &t_i8, &c_like, &c_empty, &c_bytes, &c_stream};
-  for (int i = 0; i < 9; ++i) {
+  PyObject** slot[10] = {&t_f32, &t_bf16, &t_i32, &t_e4m3, &t_i8, &c_like, &c_dense, &c_empty, &c_bytes, &c_stream};
+  for (int i = 0; i < 10; ++i) {
     Py_INCREF(o[i]);
     Py_XDECREF(*slot[i]);
     *slot[i] = o[i];
@@ -514,5 +525,6 @@ PyMODINIT_FUNC PyInit__layer_binding(void) {
   s_ptr = PyUnicode_InternFromString("_ptr_value");
   s_index = PyUnicode_InternFromString("_device_index");
   s_fail = PyUnicode_InternFromString("_layer_fail");
+  k_dtype = PyTuple_Pack(1, s_dtype);
   return PyModule_Create(&module);
 }

@@ -40,7 +40,7 @@ struct Row {
 
 template <typename T, int K, int VEC>
 __global__ void __launch_bounds__(kThreads, VEC <= 4 ? 8 : 4)
-    short_conv_kernel(const ConvArgs a, int tiles, int cblocks, int tile_len) {
+    short_conv_kernel(const ConvArgs a, int tiles, int cblocks, int tile_len, bool w_vec) {
   using R = Row<T, VEC>;
   constexpr int PAIRS = R::PAIRS;
   const int cb = (int)(blockIdx.x % cblocks);
@@ -58,13 +58,37 @@ __global__ void __launch_bounds__(kThreads, VEC <= 4 ? 8 : 4)
   T* y = static_cast<T*>(a.y) + (a.seqs.offsets ? q.start * a.y_tok : s * a.y_seq) + c;
   T* state = a.state ? static_cast<T*>(a.state) + q.slot * (K - 1) * a.C + c : nullptr;
 
+  // the VEC filters, one after another in memory: as VEC values an access where aligned (a call for
+  // single tokens reads little else)
+  float f[VEC * K], fb[VEC];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    if (w_vec) {
+      const Vec<float, VEC> v = ld_vec<float, VEC>(a.w + c * K + i * VEC);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[i * VEC + j] = v.v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[i * VEC + j] = a.w[c * K + i * VEC + j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) fb[j] = 0.f;
+  if (a.bias && w_vec) {
+    const Vec<float, VEC> v = ld_vec<float, VEC>(a.bias + c);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) fb[j] = v.v[j];
+  } else if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) fb[j] = a.bias[c + j];
+  }
   uint64_t w[K][PAIRS], b[PAIRS];
 #pragma unroll
   for (int i = 0; i < PAIRS; ++i) {
     const int second = VEC == 1 ? 0 : 1;
-    b[i] = a.bias ? pair(a.bias[c + 2 * i], a.bias[c + 2 * i + second]) : pair(0.f, 0.f);
+    b[i] = pair(fb[2 * i], fb[2 * i + second]);
 #pragma unroll
-    for (int j = 0; j < K; ++j) w[j][i] = pair(a.w[(c + 2 * i) * K + j], a.w[(c + 2 * i + second) * K + j]);
+    for (int j = 0; j < K; ++j) w[j][i] = pair(f[2 * i * K + j], f[(2 * i + second) * K + j]);
   }
   // the K - 1 inputs before the tile; row i is input t0 - (K - 1) + i
   R h[K - 1];
@@ -149,7 +173,8 @@ cudaError_t launch(const ConvArgs& a, cudaStream_t s) {
   if (tiles > 0x7fffffffLL || cblocks > 0x7fffffffLL || tiles * cblocks > 0x7fffffffLL / a.seqs.n_seq)
     return cudaErrorInvalidConfiguration;
   const long long ctas = tiles * cblocks * a.seqs.n_seq;
-  short_conv_kernel<T, K, VEC><<<(unsigned int)ctas, kThreads, 0, s>>>(a, (int)tiles, (int)cblocks, (int)tile);
+  const bool w_vec = (reinterpret_cast<uintptr_t>(a.w) | reinterpret_cast<uintptr_t>(a.bias)) % (4 * VEC) == 0;
+  short_conv_kernel<T, K, VEC><<<(unsigned int)ctas, kThreads, 0, s>>>(a, (int)tiles, (int)cblocks, (int)tile, w_vec);
   return cudaGetLastError();
 }
 

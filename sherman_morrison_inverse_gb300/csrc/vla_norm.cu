@@ -15,6 +15,8 @@
 #include "vla.h"
 #include "vla_layer.cuh"
 
+#include <atomic>
+
 namespace vla {
 namespace {
 
@@ -58,7 +60,7 @@ __device__ __forceinline__ void codes(const float (&v)[N], unsigned char* o) {
 
 // RES: 0 none, 1 bfloat16, 2 float32
 template <typename T, int RES, int OUT, int VEC, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 256 : NV == 2 ? 512 : 1024) rms_norm_kernel(const NormArgs a, int tpr, int rows_per_cta, float inv_d) {
+__global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) rms_norm_kernel(const NormArgs a, int tpr, int rows_per_cta, float inv_d) {
   using R = typename std::conditional<RES == 1, __nv_bfloat16, float>::type;
   constexpr int RV = sizeof(R) * VEC > 16 ? 16 / (int)sizeof(R) : VEC;   // 16 bytes an access
   constexpr bool QUANT = OUT != VLA_OUT_IO;
@@ -86,10 +88,10 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : NV == 2 ? 512 : 1024) rms_norm
     for (int i = 0; i < NV; ++i) {
       const int e = (i * tpr + tid) * VEC;
       if (e >= D) continue;
-      in[i] = ld_vec<T, VEC>(x + e);
+      in[i].raw = __ldcs(reinterpret_cast<const decltype(in[i].raw)*>(x + e));   // read once
       if (RES != 0) {
 #pragma unroll
-        for (int j = 0; j < VEC / RV; ++j) res[i][j] = ld_vec<R, RV>(r + e + j * RV);
+        for (int j = 0; j < VEC / RV; ++j) res[i][j].raw = __ldcs(reinterpret_cast<const decltype(res[i][j].raw)*>(r + e + j * RV));
       }
     }
   };
@@ -219,18 +221,28 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
   const long long need = (a.D + (long long)VEC * NV - 1) / ((long long)VEC * NV);
   const int tpr = (int)((need + unit - 1) / unit * unit);
   const int rows = tpr >= 256 ? 1 : 256 / tpr;
-  int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, tpr * rows, 0);
-  if (e != cudaSuccess) return e;
+  // blocks an SM for this kernel and block size: asked for once, packed as size | blocks
+  static std::atomic<unsigned int> known{0};
+  const unsigned int threads = (unsigned int)(tpr * rows);
+  unsigned int k = known.load(std::memory_order_relaxed);
+  if (k >> 16 != threads) {
+    int blocks = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kern, (int)threads, 0);
+    if (e != cudaSuccess) return e;
+    k = threads << 16 | (unsigned int)blocks;
+    known.store(k, std::memory_order_relaxed);
+  }
+  const int per_sm = (int)(k & 0xffffu);
   const long long all = (a.rows + rows - 1) / rows, most = (long long)(per_sm > 0 ? per_sm : 1) * a.sm_count;
   kern<<<(unsigned int)(all < most ? all : most), tpr * rows, 0, s>>>(a, tpr, rows, 1.f / (float)a.D);
   return cudaGetLastError();
 }
 
-// Values a thread: few enough that the row after this one fits in registers too.
+// Values a thread: few, so that many threads have a load in flight (16384 x 4096 bfloat16 with residual
+// and e4m3: 8 values 87 us, 16 values 94 us, 32 values 195 us).
 template <typename T, int RES, int OUT, int VEC>
 cudaError_t by_width(const NormArgs& a, cudaStream_t s) {
-  if (VEC > 1 && a.D <= 256LL * VEC) return launch<T, RES, OUT, VEC, VEC == 1 ? 2 : 1>(a, s);
+  if (VEC > 1 && a.D <= 512LL * VEC) return launch<T, RES, OUT, VEC, VEC == 1 ? 2 : 1>(a, s);
   if (a.D <= 1024LL * VEC) return launch<T, RES, OUT, VEC, 2>(a, s);
   if (a.D <= 4096LL * VEC) return launch<T, RES, OUT, VEC, 4>(a, s);
   return launch<T, RES, OUT, VEC, 32 / VEC>(a, s);   // up to 32768 values (the entry point's limit)

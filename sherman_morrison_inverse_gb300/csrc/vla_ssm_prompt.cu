@@ -46,7 +46,7 @@
 // those, joined in a fixed order.
 #include <cuda.h>   // CUtensorMap and the encode entry point's types (resolved at run time)
 
-#include <algorithm>
+#include <atomic>
 
 #include "vla_layer.cuh"
 #include "vla_ssm_prompt.cuh"
@@ -877,20 +877,28 @@ cudaError_t launch(const SsmArgs& s, const PromptArgs& a, const PromptPlan& plan
   const long long ctas = s.seqs.n_seq * a.H * a.pslices * plan.nseg;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   constexpr int bytes = (int)Cfg<NN>::bytes;
-  auto run = [&](auto kern) -> cudaError_t {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
+  if (err != cudaSuccess) return err;
+  auto run = [&](auto kern, std::atomic<unsigned long long>& ready) -> cudaError_t {
+    // more than 48 KB of shared memory: allowed once a kernel and device (the first 64)
+    if (device >= 64 || !(ready.load(std::memory_order_relaxed) >> device & 1)) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e != cudaSuccess) return e;
+      if (device < 64) ready.fetch_or(1ull << device, std::memory_order_relaxed);
+    }
     kern<<<(unsigned int)ctas, kThreads, bytes, st>>>(maps[0], maps[1], maps[2], maps[3], maps[4], a);
     return cudaGetLastError();
   };
+  static std::atomic<unsigned long long> ready[4];
   if (plan.nseg > 1) {
-    const cudaError_t e = run(ssm_prompt_kernel<NN, false, 0>);
+    const cudaError_t e = run(ssm_prompt_kernel<NN, false, 0>, ready[0]);
     if (e != cudaSuccess) return e;
   }
   switch (gate) {
-    case 0: return run(ssm_prompt_kernel<NN, true, 0>);
-    case 1: return run(ssm_prompt_kernel<NN, true, 1>);
-    default: return run(ssm_prompt_kernel<NN, true, 2>);
+    case 0: return run(ssm_prompt_kernel<NN, true, 0>, ready[1]);
+    case 1: return run(ssm_prompt_kernel<NN, true, 1>, ready[2]);
+    default: return run(ssm_prompt_kernel<NN, true, 2>, ready[3]);
   }
 }
 

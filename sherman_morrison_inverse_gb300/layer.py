@@ -24,7 +24,7 @@ STATUS_INDEX = 4
 _OUT = {"io": 0, "e4m3": 1, "int8": 2}
 
 
-def _like(x, dtype=None):
+def _dense(x, dtype=None):
     return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
 
 
@@ -55,7 +55,7 @@ def declare(lib):
     # the current stream's handle without a Stream object around it, where torch has that
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
     native.setup(*at, torch.float32, torch.bfloat16, torch.int32, torch.float8_e4m3fn, torch.int8,
-                 _like, _empty, _bytes, stream)
+                 torch.empty_like, _dense, _empty, _bytes, stream)
     _native = native
 
 
