@@ -44,8 +44,15 @@ _native = None
 
 
 def declare(lib):
-    """Hand the layer's entry points of the loaded library to the argument checks in C."""
+    """Declare the layer's C signatures, and hand the entry points to the argument checks in C."""
     global _native
+    vp, ci, cll, cf = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
+    lib.vla_short_conv.argtypes = [vp] * 6 + [cll] * 3 + [vp] * 2 + [cll] * 2 + [ci, vp, ci, ci, vp]
+    lib.vla_ssm_scan.argtypes = [vp] * 11 + [cll] * 3 + [vp] * 2 + [cll] * 5 + [vp, ci, ci, vp, ctypes.c_size_t, vp]
+    lib.vla_ssm_workspace.argtypes = [vp, cll, cll, cll, ci, cll, cll, cll, ci, ctypes.POINTER(ctypes.c_size_t)]
+    lib.vla_rms_norm.argtypes = [vp] * 6 + [cll] * 5 + [cf, ci, ci, ci, ci, vp]
+    for fn in (lib.vla_short_conv, lib.vla_ssm_scan, lib.vla_ssm_workspace, lib.vla_rms_norm):
+        fn.restype = ci
     try:
         native = importlib.import_module("._layer_binding", __package__)
     except ImportError as e:

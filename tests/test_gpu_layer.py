@@ -423,3 +423,118 @@ def test_a_layer_decodes_what_it_would_prefill(vla):
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     assert m.demo(width=256, heads=4, n_layers=2, n_tokens=5, lens=(3, 140, 29, 1)) <= 0.05
+
+
+# ---------------------------------------------------------------------------------------------
+# layouts and sizes away from the ordinary
+
+@pytest.mark.parametrize("form", ["token-major", "odd start", "shared B and C"])
+def test_ssm_scan_with_other_strides(vla, form):
+    """Sequences interleaved token by token; rows off every 16-byte boundary (another kernel); B and C
+    broadcast over the sequences.  The values are those of contiguous copies."""
+    gen = generator(31)
+    v = scan_inputs(gen, (3, 150), 4, 64, 2, 64, torch.bfloat16, True, False)
+    if form == "token-major":
+        v = {k: t.transpose(0, 1).contiguous().transpose(0, 1) if k in ("x", "dt", "B", "C", "z") else t for k, t in v.items()}
+        out = torch.empty(150, 3, 4, 64, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    elif form == "odd start":
+        def shift(t):
+            flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:]
+            return flat.copy_(t.flatten()).view(t.shape)
+        v = {k: shift(t) if k in ("x", "dt", "B", "C", "z") else t for k, t in v.items()}
+        out = shift(torch.zeros(3, 150, 4, 64, dtype=torch.bfloat16, device="cuda"))
+    else:
+        v["B"], v["C"] = v["B"][:1].expand(3, -1, -1, -1), v["C"][:1].expand(3, -1, -1, -1)
+        out = None
+    state = torch.zeros(3, 4, 64, 64, device="cuda")
+    y = vla.ssm_scan(state=state, y=out, **v)
+    if out is not None:
+        assert y.data_ptr() == out.data_ptr()
+    for s in range(3):
+        one = lambda k: f64(v[k][s])   # noqa: E731
+        yr, ya, hr, ha = ref.ssm_scan(one("x"), one("dt"), f64(v["A"]), one("B"), one("C"), np.zeros((4, 64, 64)),
+                                      f64(v["D"]), one("z"), f64(v["dt_bias"]))
+        c = (8 * 150 + 4 + 6 * 256) * U32
+        close(f64(state[s]), hr, c * ha + 1e-30, "state")
+        close(f64(y[s]), yr, (U16 + 2.0 ** -20 * (1 + np.abs(one("z")))) * np.abs(yr) + (c + U16) * ya + 1e-30, "y")
+
+
+def test_short_conv_with_interleaved_sequences(vla):
+    gen = generator(32)
+    x = rand(gen, 70, 3, 96, dtype=torch.bfloat16).transpose(0, 1)
+    w = rand(gen, 96, 4)
+    assert torch.equal(vla.short_conv(x, w), vla.short_conv(x.contiguous(), w))
+
+
+@pytest.mark.parametrize("T", [1, 40, 200])
+def test_states_and_rows_past_two_to_the_31(vla, T):
+    """A pool and a token buffer whose last elements lie past 2^31: 64-bit offsets everywhere."""
+    if torch.cuda.get_device_properties(0).total_memory < 60 * 2 ** 30:
+        pytest.skip("needs 60 GB of device memory")
+    gen = generator(T)
+    H, P, G, N, width = 64, 64, 1, 128, 64 * 64 + 2 * 128
+    slots = torch.tensor([4200, 3], dtype=torch.int32, device="cuda")
+    state = torch.empty(4201, H, P, N, device="cuda")           # 2.2e9 floats
+    state[3], state[4200] = 0.5, 0.25
+    rows = 2 ** 31 // width + 2 * T + 1
+    buf = torch.empty(rows, width, dtype=torch.bfloat16, device="cuda")
+    tail = buf[rows - 2 * T:]
+    tail.copy_(rand(gen, 2 * T, width))
+    dt = torch.empty(rows, H, dtype=torch.bfloat16, device="cuda")
+    dt[rows - 2 * T:] = rand(gen, 2 * T, H).to(torch.bfloat16)
+    A = -torch.rand(H, generator=gen, device="cuda")
+    split = lambda t: (t[..., :4096].unflatten(-1, (H, P)), t[..., 4096:4224].unflatten(-1, (G, N)),   # noqa: E731
+                       t[..., 4224:].unflatten(-1, (G, N)))
+    off = torch.tensor([rows - 2 * T, rows - T, rows], dtype=torch.int32, device="cuda")
+    x, B, C = split(buf)
+    y = torch.empty(rows, H, P, dtype=torch.bfloat16, device="cuda")
+    vla.ssm_scan(x, dt, A, B, C, state, y, offsets=off, slots=slots, max_len=T)
+    small = torch.empty(2, H, P, N, device="cuda")
+    small[0], small[1] = 0.25, 0.5
+    xs, Bs, Cs = split(tail.clone())
+    ys = vla.ssm_scan(xs, dt[rows - 2 * T:].clone(), A, Bs, Cs, small, offsets=off - (rows - 2 * T), max_len=T)
+    assert torch.equal(y[rows - 2 * T:], ys) and torch.equal(state[4200], small[0]) and torch.equal(state[3], small[1])
+    w = rand(gen, width, 4)
+    out = torch.empty_like(buf)
+    vla.short_conv(buf, w, None, None, out, offsets=off, max_len=T)
+    assert torch.equal(out[rows - 2 * T:], vla.short_conv(tail.clone(), w, offsets=off - (rows - 2 * T), max_len=T))
+
+
+def test_many_sequences(vla):
+    """More sequences than a grid's second dimension holds."""
+    gen = generator(33)
+    S, H, P, N = 70001, 1, 8, 4
+    x, dt, B, C = (rand(gen, S, *s) for s in ((H, P), (H,), (1, N), (1, N)))
+    A, state = -torch.ones(H, device="cuda"), rand(gen, S, H, P, N)
+    before = state.clone()
+    y = vla.ssm_step(x, dt, A, B, C, state)
+    step = torch.nn.functional.softplus(dt.double())
+    h = torch.exp(-step)[..., None, None] * before.double() + step[..., None, None] * x.double()[..., None] * B.double()[:, :, None]
+    assert (state - h).abs().max() <= 64 * U32 * h.abs().max()
+    want = (h * C.double()[:, :, None]).sum(-1)
+    assert (y - want).abs().max() <= 64 * U32 * (h * C.double()[:, :, None]).abs().sum(-1).max()
+    cs, xs, w = torch.zeros(S, 1, 8, device="cuda"), rand(gen, S, 8), rand(gen, 8, 2)
+    assert torch.equal(vla.short_conv_step(xs, w, None, cs, silu=False), xs * w[:, 1]) and torch.equal(cs[:, 0], xs)
+
+
+def test_no_wait_runs_out_and_scratch_is_checked(vla):
+    """Every form leaves the status clean, and a workspace that is too small is refused."""
+    import ctypes
+    h = vla.Handle()
+    gen = generator(34)
+    for lead, N in (((1, 3000), 128), ((2, 900), 64), ((40, 300), 128), ((3, 1), 64), ((2, 500), 20)):
+        v = scan_inputs(gen, lead, 8, 64, 1, N, torch.bfloat16, True, False)
+        h.ssm_scan(**v)
+        assert h.status()["flags"] == 0
+    need = ctypes.c_size_t()
+    args = (h.ptr, 1, 3000, 3000, 0, 8, 64, 128, 1, ctypes.byref(need))
+    assert h.lib.vla_ssm_workspace(*args) == 0 and need.value > 0
+    x = torch.zeros(1, 3000, 8, 128, dtype=torch.bfloat16, device="cuda")
+    f = torch.zeros(8, device="cuda")
+    p, q = x.data_ptr(), f.data_ptr()
+    strides = (ctypes.c_longlong * 12)(*[v for _ in range(6) for v in (3000 * 1024, 1024)])
+    for ws, size in ((None, 0), (p, need.value - 1)):
+        code = h.lib.vla_ssm_scan(h.ptr, p, p, q, p, p, None, None, None, None, p, 1, 3000, 3000, None, None, 0, 8, 64,
+                                  1, 128, strides, 1, 1, ws, size, None)
+        assert code == 1 and b"workspace" in h.lib.vla_last_error(h.ptr)
+    h.close()
