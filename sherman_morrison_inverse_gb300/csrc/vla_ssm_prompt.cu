@@ -26,7 +26,7 @@
 //   8-15  state: X~, then h' from its product U
 //   16    issues C h^T and M X               17  issues B^T X~ and then S of the next chunk
 //   18    issues the loads                    19  stores y
-//   20-21 decays, 64 tokens of a chunk each
+//   20-23 decays, 32 tokens of a chunk each
 // (the first launch of a cut sequence has no output: warps 0-7 form half of X~ there)
 // In order: S of the next chunk is formed while M of this one is, M of the next one while M X of
 // this one runs.  The longest chain is X~, U, h, X~ ..: so U comes before S, and h's copy is written
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i == kEmptyB || i == kEmptyB + 1 || i == kEmptyC) count = FULL ? 2 : 1;
       if (i == kEmptyX || i == kEmptyX + 1) count = FULL ? 2 * W + 1 : 2 * W;
       if (i >= kEmptyDec && i < kEmptyDec + kDec) count = 2 * W;
-      if (i >= kFullDec && i < kFullDec + kDec) count = 2;
+      if (i >= kFullDec && i < kFullDec + kDec) count = 4;
       if (i == kM || i == kH || i == kEmptyY || i == kEmptyY + 1 || i == kStage) count = W;
       if (i == kXt) count = FULL ? W : 2 * W;
       mbar_init(bar + i, count);
@@ -718,112 +718,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (GATE == 1 && *fail)   // nothing lands after the CTA has gone
       for (int j = 0; j < 2; ++j) mbar_wait_bounded(bar + kFullZ, (uint32_t)j, kWaitLimitNs / 8);
   } else if (warp == 18) {
-    // ------------------------------------------------ loads
-    int i = 0;
-    for (; i < n_chunks; ++i) {
-      const int r = i & 1, u = i >> 1;
-      const int t = row0 + (int)(t_first + (long long)i * kL);
-      if (u > 0 && !wait(kEmptyB + r, u - 1)) break;
+    // ------------------------------------------------ loads: B, X, C of a chunk in turn
+    const int kinds = FULL ? 3 : 2;
+    int i = 0, kind = 0;
+    while (i < n_chunks) {
+      const int r = i & 1;
+      // the place is free: its use before has been read (C has one place, the others two)
+      const int empty = kind == 0 ? kEmptyB + r : kind == 1 ? kEmptyX + r : kEmptyC;
+      const int use = kind == 2 ? i : i >> 1;
+      if (use > 0 && !wait(empty, use - 1)) break;
       if (one) {
-        mbar_arrive_expect_tx(bar + kFullB + r, Cf::NT * kTile);
+        const int t = row0 + (int)(t_first + (long long)i * kL);
+        const CUtensorMap* map = kind == 0 ? &map_B : kind == 1 ? &map_x : &map_C;
+        uint64_t* full = bar + (kind == 0 ? kFullB + r : kind == 1 ? kFullX + r : kFullC);
+        const uint32_t to = sbase + (kind == 0 ? Cf::oB + r * Cf::NT * kTile : kind == 1 ? Cf::oX + r * kTile : Cf::oC);
+        const uint32_t tiles = kind == 1 ? 1u : Cf::NT;
+        mbar_arrive_expect_tx(full, tiles * kTile);
 #pragma unroll 1
-        for (uint32_t k = 0; k < Cf::NT; ++k)
-          load_4d(sbase + Cf::oB + (r * Cf::NT + k) * kTile, &map_B, 64 * (int)k, group, t, batch, bar + kFullB + r);
-      }
-      __syncwarp();
-      if (u > 0 && !wait(kEmptyX + r, u - 1)) break;
-      if (one) {
-        mbar_arrive_expect_tx(bar + kFullX + r, kTile);
-        load_4d(sbase + Cf::oX + r * kTile, &map_x, p0, head, t, batch, bar + kFullX + r);
-        // C has one place and is asked for late: its rows are fetched into L2 now
-        if (FULL && i > 0)
-#pragma unroll 1
-          for (uint32_t k = 0; k < Cf::NT; ++k) prefetch_4d(&map_C, 64 * (int)k, group, t, batch);
-      }
-      __syncwarp();
-      if (FULL) {
-        if (i > 0 && !wait(kEmptyC, i - 1)) break;
-        if (one) {
-          mbar_arrive_expect_tx(bar + kFullC, Cf::NT * kTile);
-#pragma unroll 1
-          for (uint32_t k = 0; k < Cf::NT; ++k)
-            load_4d(sbase + Cf::oC + k * kTile, &map_C, 64 * (int)k, group, t, batch, bar + kFullC);
+        for (uint32_t k = 0; k < tiles; ++k) {
+          load_4d(to + k * kTile, map, kind == 1 ? p0 : 64 * (int)k, kind == 1 ? head : group, t, batch, full);
+          // C is asked for late: its rows are fetched into L2 beside B's
+          if (FULL && kind == 0) prefetch_4d(&map_C, 64 * (int)k, group, t, batch);
         }
-        __syncwarp();
+      }
+      __syncwarp();
+      if (++kind == kinds) {
+        kind = 0;
+        ++i;
       }
     }
-    if (*fail || i < n_chunks) {   // nothing lands after the CTA has gone
-      for (int j = i > 2 ? i - 2 : 0; j <= i && j < n_chunks; ++j) {
-        if (!mbar_wait_bounded(bar + kFullB + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitLimitNs / 8)) continue;
-        mbar_wait_bounded(bar + kFullX + (j & 1), (uint32_t)(j >> 1) & 1u, kWaitLimitNs / 8);
-        if (FULL) mbar_wait_bounded(bar + kFullC, (uint32_t)j & 1u, kWaitLimitNs / 8);
-      }
-    }
-  } else if (warp == 20 || warp == 21) {
-    // ------------------------------------------------ decays: blocks j0 and j0 + 1 of 32 tokens of every chunk
-    const int j0 = 2 * (warp - 20);
+    if (*fail)   // nothing lands after the CTA has gone
+#pragma unroll 1
+      for (int k = 0; k < 10; ++k) mbar_wait_bounded(bar + kFullB + (k >> 1), (uint32_t)k & 1u, kWaitLimitNs / 8);
+  } else if (warp >= 20) {
+    // ------------------------------------------------ decays: tokens 32 j + lane of every chunk
+    const int j = warp - 20;
     const __nv_bfloat16* dt = a.dt + (packed ? q.start * a.dt_tok : seq * a.dt_seq) + head;
     const float A2 = a.A[head] * 1.44269504088896341f, bias = a.dt_bias ? a.dt_bias[head] : 0.f;
-    long long t = t_first + 32 * j0 + lane;
-    float raw[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) raw[j] = t + 32 * j < q.len ? __bfloat162float(dt[(t + 32 * j) * a.dt_tok]) : 0.f;
+    long long t = t_first + 32 * j + lane;
+    float raw = t < q.len ? __bfloat162float(dt[t * a.dt_tok]) : 0.f;
 #pragma unroll 1
     for (int i = 0; i < n_chunks; ++i) {
-      float s[2], inc[2], ex[2], end[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bool in = t + 32 * j < q.len;
-        s[j] = in ? time_step(raw[j], bias, a.softplus) : 0.f;
-        inc[j] = ex[j] = in ? A2 * s[j] : 0.f;
-      }
+      const bool in = t < q.len;
+      const float s = in ? time_step(raw, bias, a.softplus) : 0.f;
       t += kL;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (t + 32 * j < q.len && i < last_i) raw[j] = __bfloat162float(dt[(t + 32 * j) * a.dt_tok]);
+      if (t < q.len && i < last_i) raw = __bfloat162float(dt[t * a.dt_tok]);
+      float inc = in ? A2 * s : 0.f, ex = inc;
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float up = __shfl_up_sync(0xffffffffu, inc[j], o), down = __shfl_down_sync(0xffffffffu, ex[j], o);
-          if (lane >= o) inc[j] += up;
-          if (lane + o < 32) ex[j] += down;
-        }
+        const float up = __shfl_up_sync(0xffffffffu, inc, o), down = __shfl_down_sync(0xffffffffu, ex, o);
+        if (lane >= o) inc += up;
+        if (lane + o < 32) ex += down;
       }
+      ex = __shfl_down_sync(0xffffffffu, ex, 1);
+      if (lane == 31) ex = 0.f;
+      const bool small = __all_sync(0xffffffffu, fabsf(inc) < 100.f);
       float* v = vec + (i % kDec) * kVec;
-      // the two warps leave together: each reads the other's sums
+      float* sums = v + 5 * kL;
+      // the four warps leave together: each reads the others' sums
       const bool ok = i < kDec || wait(kEmptyDec + i % kDec, i / kDec - 1);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        end[j] = __shfl_sync(0xffffffffu, inc[j], 31);
-        ex[j] = __shfl_down_sync(0xffffffffu, ex[j], 1);
-        if (lane == 31) ex[j] = 0.f;
-        if (ok && one) v[5 * kL + 12 + j0 + j] = end[j];
+      if (lane == 31) sums[12 + j] = inc;
+      if (named_or(1, 128, !ok)) break;
+      float before = 0.f, behind = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const float e = sums[12 + k];
+        if (k < j) before += e;
+        if (k > j) behind += e;
       }
-      if (named_or(1, 64, !ok)) break;
-      float sum[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] = v[5 * kL + 12 + j];
-      float before = j0 == 0 ? 0.f : sum[0] + sum[1];
-      const float after = j0 == 0 ? sum[2] + sum[3] : 0.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int at = 32 * (j0 + j) + lane;
-        const float behind = j == 0 ? end[1] + after : after;
-        v[at] = before + inc[j];
-        v[kL + at] = s[j] * ex2(ex[j]);
-        v[2 * kL + at] = s[j] * ex2(-inc[j]);
-        v[3 * kL + at] = s[j] * ex2(ex[j] + behind);
-        v[4 * kL + at] = s[j];
-        const bool small = __all_sync(0xffffffffu, fabsf(inc[j]) < 100.f);
-        if (one) {
-          v[5 * kL + j0 + j] = before;
-          v[5 * kL + 4 + j0 + j] = before + end[j];
-          v[5 * kL + 16 + j0 + j] = small ? 1.f : 0.f;
-        }
-        before += end[j];
+      v += 32 * j + lane;
+      v[0] = before + inc;
+      v[kL] = s * ex2(ex);
+      v[2 * kL] = s * ex2(-inc);
+      v[3 * kL] = s * ex2(ex + behind);
+      v[4 * kL] = s;
+      if (lane == 31) {
+        sums[j] = before;
+        sums[4 + j] = before + inc;
+        sums[16 + j] = small ? 1.f : 0.f;
+        if (j == 3) sums[8] = before + inc;
       }
-      if (one && j0 == 0) v[5 * kL + 8] = sum[0] + sum[1] + sum[2] + sum[3];
       arrive(kFullDec + i % kDec);
     }
   }
