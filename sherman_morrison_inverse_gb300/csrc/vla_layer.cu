@@ -114,7 +114,7 @@ vla_err_t vla_ssm_scan(vla_handle_t h, const void* x, const void* dt, const floa
   a.softplus = softplus != 0;
   a.status = h->status;
   const bool bf16 = io_dtype == VLA_BF16;
-  const vla::PromptPlan plan = vla::ssm_prompt_plan(n_seq, a.seqs.max_len, H, P, N, bf16, h->sm_count);
+  const vla::PromptPlan plan = vla::ssm_prompt_plan(n_seq, offsets ? T : n_seq * T, a.seqs.max_len, H, P, N, bf16, h->sm_count);
   const vla::StepsPlan steps = vla::ssm_steps_plan(n_seq, a.seqs.max_len, H, P, N, h->sm_count);
   const size_t need = ws_need(plan, steps);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
@@ -144,7 +144,7 @@ vla_err_t vla_ssm_workspace(vla_handle_t h, long long n_seq, long long T, long l
   if (io_dtype != VLA_F32 && io_dtype != VLA_BF16) return fail(h, VLA_ERR_INVALID_ARG, f + ": unknown io_dtype");
   if (packed && max_len > T) max_len = T;
   const long long len = packed ? max_len : T;
-  *bytes = ws_need(vla::ssm_prompt_plan(n_seq, len, H, P, N, io_dtype == VLA_BF16, h->sm_count),
+  *bytes = ws_need(vla::ssm_prompt_plan(n_seq, packed ? T : n_seq * T, len, H, P, N, io_dtype == VLA_BF16, h->sm_count),
                    vla::ssm_steps_plan(n_seq, len, H, P, N, h->sm_count));
   return VLA_OK;
 }

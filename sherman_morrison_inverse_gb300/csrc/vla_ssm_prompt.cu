@@ -46,6 +46,7 @@
 // those, joined in a fixed order.
 #include <cuda.h>   // CUtensorMap and the encode entry point's types (resolved at run time)
 
+#include <algorithm>
 #include <atomic>
 
 #include "vla_layer.cuh"
@@ -78,7 +79,7 @@ enum : int {
   kFullYi = 14,    // [2] C h^T is formed (and h's copy read)
   kM = 16,         //     M, and D x + exp(c) C h^T, are written
   kFullY = 17,     // [2] M X is added
-  kH = 19,         //     h's copy is written
+  kH = 19,         //     the copy of h before chunk i is written
   kEmptyY = 20,    // [2] Y is read
   kXt = 22,        //     X~ is written, the U before it read
   kFullU = 23,     //     U is formed
@@ -178,6 +179,9 @@ __device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, in
           dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 // the tile of a later load, from memory into L2
 __device__ __forceinline__ void prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
@@ -285,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc(tslot, kCols);
+  if (warp == 18 && lane < 4) prefetch_map(lane == 0 ? &map_B : lane == 1 ? &map_x : lane == 2 ? &map_C : &map_y);
 
   const int row = tid & (kL - 1), half = (tid >> 7) & 1;   // token or state n; columns 32 half ..
   const uint32_t rsw = (uint32_t)(row & 7);
@@ -292,52 +297,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pc = a.P - p0 - 32 * half;   // columns of this thread that exist
   float* wsq = a.nseg > 1 ? a.ws + (seq * slices + slice) * ws_floats(a.nseg, NN) : nullptr;
   const int n = row;
-  float h[32];   // of the state's warps: state n, columns p
-  if (warp >= kSide / 32 && warp < 2 * kSide / 32) {
-    const bool from_ws = FULL && chunks > a.seg_chunks;
-    const float* src = nullptr;
-    long long pitch = 0;
-    bool mine = n < a.N;
-    if (from_ws && seg == 0) {
-      src = wsq + ((long long)(a.nseg - 1) * 64 + 32 * half) * NN;
-      pitch = NN;
-      mine = n < NN;
-    } else if (!from_ws && a.state && seg == 0) {
-      src = a.state + ((q.slot * a.H + head) * a.P + p0 + 32 * half) * a.N;
-      pitch = a.N;
-    }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) h[i] = src && mine && (from_ws || i < pc) ? src[i * pitch + n] : 0.f;
-    if (!FULL && seg == 0 && n < NN) {   // the copy that the second launch starts from
-      float* keep = wsq + ((long long)(a.nseg - 1) * 64 + 32 * half) * NN;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) keep[i * NN + n] = h[i];
-    }
-    if (from_ws) {
-      const float* dec = wsq + (long long)a.nseg * 64 * NN;
-      for (int j = 0; j < seg; ++j) {
-        const float d = j == 0 ? 0.f : dec[j];   // segment 0's result holds the state before the sequence
-        const float* e = wsq + ((long long)j * 64 + 32 * half) * NN;
-        if (n < NN) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) h[i] = fmaf(d, j == 0 ? 0.f : h[i], e[i * NN + n]);
-        }
-      }
-    }
-  }
-  // the bfloat16 copy of the state, [n][64 p]: this thread's 64 bytes of row n
-  auto put_state = [&]() {
-    if (n < NN) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = make_uint4(pack2(h[8 * i], h[8 * i + 1]), pack2(h[8 * i + 2], h[8 * i + 3]),
-                                   pack2(h[8 * i + 4], h[8 * i + 5]), pack2(h[8 * i + 6], h[8 * i + 7]));
-        *reinterpret_cast<uint4*>(smem + Cf::oH + row_at + (((uint32_t)(4 * half + i) ^ rsw) << 4)) = v;
-      }
-    }
-  };
-  if (FULL && warp >= kSide / 32 && warp < 2 * kSide / 32) put_state();
-  fence_proxy_async_smem();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -559,6 +518,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < 2 * kSide / 32) {
     // ------------------------------------------------ state
+    // the state before the segment: state n, columns p (the first tiles and decays are on their way)
+    float h[32];
+    {
+      const bool from_ws = FULL && chunks > a.seg_chunks;
+      const float* src = nullptr;
+      long long pitch = 0;
+      bool mine = n < a.N;
+      if (from_ws && seg == 0) {
+        src = wsq + ((long long)(a.nseg - 1) * 64 + 32 * half) * NN;
+        pitch = NN;
+        mine = n < NN;
+      } else if (!from_ws && a.state && seg == 0) {
+        src = a.state + ((q.slot * a.H + head) * a.P + p0 + 32 * half) * a.N;
+        pitch = a.N;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) h[i] = src && mine && (from_ws || i < pc) ? src[i * pitch + n] : 0.f;
+      if (!FULL && seg == 0 && n < NN) {   // the copy that the second launch starts from
+        float* keep = wsq + ((long long)(a.nseg - 1) * 64 + 32 * half) * NN;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) keep[i * NN + n] = h[i];
+      }
+      if (from_ws) {
+        const float* dec = wsq + (long long)a.nseg * 64 * NN;
+        for (int j = 0; j < seg; ++j) {
+          const float d = j == 0 ? 0.f : dec[j];   // segment 0's result holds the state before the sequence
+          const float* e = wsq + ((long long)j * 64 + 32 * half) * NN;
+          if (n < NN) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) h[i] = fmaf(d, j == 0 ? 0.f : h[i], e[i * NN + n]);
+          }
+        }
+      }
+    }
+    // the bfloat16 copy of the state, [n][64 p]: this thread's 64 bytes of row n
+    auto put_state = [&]() {
+      if (n < NN) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = make_uint4(pack2(h[8 * i], h[8 * i + 1]), pack2(h[8 * i + 2], h[8 * i + 3]),
+                                     pack2(h[8 * i + 4], h[8 * i + 5]), pack2(h[8 * i + 6], h[8 * i + 7]));
+          *reinterpret_cast<uint4*>(smem + Cf::oH + row_at + (((uint32_t)(4 * half + i) ^ rsw) << 4)) = v;
+        }
+      }
+    };
+    if (FULL) {
+      put_state();
+      fence_proxy_async_smem();
+      arrive(kH);
+    }
     const uint32_t tlane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kColU + 32 * half;
     float log_total = 0.f;
     // h <- exp(c_L) h + U
@@ -635,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = i & 1, u = i >> 1;
         const uint32_t ty = tmem + kColY + 64 * r, ts = tmem + kColS + 128 * r;
         const uint64_t x0 = desc128(sbase + Cf::oX + r * kTile, 16);
-        if (!wait(kFullC, i) || (i > 0 && !wait(kH, i - 1)) || (u > 0 && !wait(kEmptyY + r, u - 1))) break;
+        if (!wait(kFullC, i) || !wait(kH, i) || (u > 0 && !wait(kEmptyY + r, u - 1))) break;
         tc::fence_after_sync();
 #pragma unroll 4
         for (int k = 0; k < NN / 16; ++k)
@@ -878,31 +887,40 @@ cudaError_t launch(const SsmArgs& s, const PromptArgs& a, const PromptPlan& plan
 
 }  // namespace
 
-PromptPlan ssm_prompt_plan(long long n_seq, long long max_len, long long H, long long P, long long N, bool bf16,
-                           int sm_count) {
+PromptPlan ssm_prompt_plan(long long n_seq, long long tokens, long long max_len, long long H, long long P, long long N,
+                           bool bf16, int sm_count) {
   PromptPlan p{};
-  p.fits = bf16 && P % 8 == 0 && N % 8 == 0 && N <= 128 && max_len >= kPromptMin && H < (1 << 20) && P < (1 << 20);
+  p.fits = bf16 && P % 8 == 0 && N % 8 == 0 && N <= 128 && max_len > 8 && H < (1 << 20) && P < (1 << 20);
   if (!p.fits) return p;
   const long long slices = H * ((P + 63) / 64), chunks = (max_len + kL - 1) / kL, slots = sm_count;
   p.nn = N <= 64 ? 64 : 128;
   p.nseg = 1;
   p.seg_chunks = chunks;
   // One CTA an SM.  While the slices leave SMs idle, segments shorten the longest run of chunks.  In
-  // microseconds, measured: a chunk 2.3, a chunk of the first launch 1.2, a CTA's start 3, and 0.7 for
+  // microseconds, measured: a chunk 2.3, a chunk of the first launch 1.2, a CTA's start 4.5, and 0.7 for
   // each segment that a start joins.  (One sequence of 16384 tokens, 16 heads: 9 segments; 19, which
   // fill the SMs twice, take a third longer.)
+  constexpr double kStart = 4.5;
   const auto waves = [&](long long k) { return (double)((n_seq * slices * k + slots - 1) / slots); };
-  double best = waves(1) * (2.3 * chunks + 3.0);
+  double best = waves(1) * (2.3 * chunks + kStart);
   for (long long k = 2; k <= chunks && k <= 64; ++k) {
     const long long per = (chunks + k - 1) / k;
     if ((chunks + per - 1) / per != k) continue;
-    const double cost = waves(k) * (3.5 * per + 6.0 + 0.7 * k);
+    const double cost = waves(k) * (3.5 * per + 2 * kStart + 0.7 * k);
     if (cost < best) {
       best = cost;
       p.nseg = (int)k;
       p.seg_chunks = per;
     }
   }
+  // The token-by-token form takes, measured: a launch and the states' traffic, then 0.2 us a token or
+  // what its arithmetic needs.  (8 sequences of 64 heads of 64, 128 states: 24 tokens 39 us against
+  // 34 us here, 16 tokens 30 against 34; one sequence: 24 tokens 9.0 against 9.8, 32 tokens 10.5 against 9.4.)
+  const double units = (double)(n_seq * slices) * (double)N / 128.0;
+  const double steps = 3.5 + 0.04 * units +
+                       std::max(0.2 * (double)max_len, 0.0017 * (double)tokens * (double)slices * (double)N / 128.0);
+  p.fits = best + 2.5 < steps;
+  if (!p.fits) return p;
   if (p.nseg > 1) p.ws_bytes = (size_t)(n_seq * slices) * ws_floats(p.nseg, p.nn) * sizeof(float);
   return p;
 }

@@ -5,19 +5,18 @@
 
 namespace vla {
 
-// Below this length the token-by-token form is faster.
-constexpr long long kPromptMin = 24;
-
 struct PromptPlan {
-  bool fits;              // sizes and type that the form takes (alignment is seen at the launch)
+  bool fits;              // the form takes these sizes and type, and is the faster one (alignment is seen
+                          // at the launch)
   int nn;                 // states rounded up: 64 or 128
   int nseg;               // segments a sequence is cut into
   long long seg_chunks;   // chunks of 128 tokens a segment
   size_t ws_bytes;
 };
 
-PromptPlan ssm_prompt_plan(long long n_seq, long long max_len, long long H, long long P, long long N, bool bf16,
-                           int sm_count);
+// tokens: of all sequences together
+PromptPlan ssm_prompt_plan(long long n_seq, long long tokens, long long max_len, long long H, long long P, long long N,
+                           bool bf16, int sm_count);
 
 // *used = false: some operand's alignment or strides do not fit, nothing was launched.
 cudaError_t launch_ssm_prompt(const SsmArgs& a, const PromptPlan& plan, cudaStream_t s, bool* used);
