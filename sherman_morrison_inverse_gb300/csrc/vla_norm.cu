@@ -20,11 +20,52 @@
 namespace vla {
 namespace {
 
-// max that keeps a NaN
+// The larger of two, a NaN if either is one (then without a sign: 0x7fffffff).
 __device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+// The largest of a warp's magnitudes, in every lane: they compare like their bits, and a NaN lies
+// above them all.
+__device__ __forceinline__ float warp_max(float v) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
+// The 16 (sizeof 2) or fewer values of a vector as float32 pairs, and back with one rounding.
+template <typename T, int N>
+__device__ __forceinline__ void widen(const Vec<T, N>& x, uint64_t (&p)[(N + 1) / 2]) {
+  if constexpr (N == 1) {
+    p[0] = pair(to_f32<T>(x.v[0]), 0.f);
+  } else if constexpr (sizeof(T) == 2) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x.raw);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) p[i] = pair(lo_f(w[i]), hi_f(w[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) p[i] = pair(to_f32<T>(x.v[2 * i]), to_f32<T>(x.v[2 * i + 1]));
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> narrow(const uint64_t (&p)[(N + 1) / 2]) {
+  Vec<T, N> x;
+  float a, b;
+  if constexpr (N == 1) {
+    unpair(p[0], a, b);
+    x.v[0] = from_f32<T>(a);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      unpair(p[i], a, b);
+      if constexpr (sizeof(T) == 2) {
+        reinterpret_cast<uint32_t*>(&x.raw)[i] = pack2(a, b);
+      } else {
+        x.v[2 * i] = from_f32<T>(a);
+        x.v[2 * i + 1] = from_f32<T>(b);
+      }
+    }
+  }
+  return x;
 }
 
 // N values to N codes: e4m3 saturated to 448, or integers to nearest even.  A NaN keeps e4m3's
@@ -71,12 +112,16 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) rms_norm_kernel(const No
   const int w0 = slot * (tpr >> 5), wn = tpr >> 5;
   const int D = (int)a.D;
 
-  float w[NV][VEC];
+  constexpr int PAIRS = (VEC + 1) / 2, RP = (RV + 1) / 2;
+  uint64_t w[NV][PAIRS];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = (i * tpr + tid) * VEC;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) w[i][v] = e < D ? a.w[e + v] : 0.f;
+    for (int v = 0; v < PAIRS; ++v) {
+      const float w0_ = e < D ? a.w[e + 2 * v] : 0.f, w1_ = VEC > 1 && e < D ? a.w[e + 2 * v + 1] : 0.f;
+      w[i][v] = pair(w0_, w1_);
+    }
   }
   Vec<T, VEC> in[NV];
   Vec<R, RV> res[NV][VEC / RV];
@@ -98,51 +143,56 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) rms_norm_kernel(const No
   const long long step = (long long)gridDim.x * rows_per_cta;
   long long row = (long long)blockIdx.x * rows_per_cta + slot;
   load(row);
+  int span = 2;   // the power of two from wn on
+  while (span < wn) span *= 2;
   int par = 0;
   for (long long first = (long long)blockIdx.x * rows_per_cta; first < a.rows; first += step, row += step, par ^= 1) {
     const bool live = row < a.rows;
-    float r[NV][VEC];
-    float ss = 0.f, all = 0.f, top[NV];
+    uint64_t r[NV][PAIRS], sum = 0;   // r w; the squares' sums (two zeros)
+    float all = 0.f, top[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = (i * tpr + tid) * VEC;
       top[i] = 0.f;
       if (live && e < D) {
+        widen<T, VEC>(in[i], r[i]);
+        if (RES != 0) {
 #pragma unroll
-        for (int j = 0; j < VEC / RV; ++j) {
+          for (int j = 0; j < VEC / RV; ++j) {
+            uint64_t p[RP];
+            widen<R, RV>(res[i][j], p);
 #pragma unroll
-          for (int v = 0; v < RV; ++v) {
-            float now = to_f32<T>(in[i].v[j * RV + v]);
-            if (RES != 0) {
-              now += to_f32<R>(res[i][j].v[v]);
-              res[i][j].v[v] = from_f32<R>(now);
-            }
-            ss = fmaf(now, now, ss);
-            now *= w[i][j * RV + v];
-            r[i][j * RV + v] = now;
-            if (QUANT) top[i] = max_nan(top[i], fabsf(now));
+            for (int v = 0; v < RP; ++v) p[v] = r[i][j * RP + v] = add2(r[i][j * RP + v], p[v]);
+            st_vec<R, RV>(static_cast<R*>(a.residual) + row * a.res_row + e + j * RV, narrow<R, RV>(p));
           }
-          if (RES != 0) st_vec<R, RV>(static_cast<R*>(a.residual) + row * a.res_row + e + j * RV, res[i][j]);
+        }
+#pragma unroll
+        for (int v = 0; v < PAIRS; ++v) {
+          sum = fma2(r[i][v], r[i][v], sum);
+          r[i][v] = mul2(r[i][v], w[i][v]);
+          float p, q;
+          unpair(r[i][v], p, q);
+          if (QUANT) top[i] = max_nan(max_nan(top[i], fabsf(p)), fabsf(q));
         }
         if (QUANT) all = max_nan(all, top[i]);
       } else {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) r[i][v] = 0.f;
+        for (int v = 0; v < PAIRS; ++v) r[i][v] = 0;
       }
     }
     load(row + step);
     // sum of squares and maximum over the row
+    float s0, s1;
+    unpair(sum, s0, s1);
+    float ss = s0 + s1;
     const bool row_top = QUANT && a.group == 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (row_top) all = max_nan(all, __shfl_xor_sync(0xffffffffu, all, o));
-    }
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (row_top) all = warp_max(all);
     if (QUANT && VEC == 1 && a.group) {   // a group is 4 warps (tpr is a multiple of 128 here)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top[i] = max_nan(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+        top[i] = warp_max(top[i]);
         if (lane == 0) gmax[par][i * 32 + warp] = top[i];
       }
     }
@@ -153,35 +203,31 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) rms_norm_kernel(const No
         if (row_top) part_top[par][warp] = all;
       }
       __syncthreads();
-      ss = lane < wn ? part_ss[par][w0 + lane] : 0.f;
-      if (row_top) all = lane < wn ? part_top[par][w0 + lane] : 0.f;
-      for (int o = wn > 16 ? 16 : wn > 8 ? 8 : wn > 4 ? 4 : 2; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (row_top) all = max_nan(all, __shfl_xor_sync(0xffffffffu, all, o));
-      }
-      ss = __shfl_sync(0xffffffffu, ss, 0);
-      if (row_top) all = __shfl_sync(0xffffffffu, all, 0);
+      const int at = lane & (span - 1);   // every lane ends up with the row's sum
+      ss = at < wn ? part_ss[par][w0 + at] : 0.f;
+      for (int o = span >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (row_top) all = warp_max(at < wn ? part_top[par][w0 + at] : 0.f);
     }
     const float rstd = rsqrtf(fmaf(ss, inv_d, a.eps));
     if (!QUANT) {
       T* y = static_cast<T*>(a.y) + row * a.y_row;
+      const uint64_t f2 = pair(rstd, rstd);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int e = (i * tpr + tid) * VEC;
         if (!live || e >= D) continue;
-        Vec<T, VEC> o;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) o.v[v] = from_f32<T>(r[i][v] * rstd);
-        st_vec<T, VEC>(y + e, o);
+        for (int v = 0; v < PAIRS; ++v) r[i][v] = mul2(r[i][v], f2);
+        st_vec<T, VEC>(y + e, narrow<T, VEC>(r[i]));
       }
       continue;
     }
     unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.y_row;
     const float full = OUT == VLA_OUT_E4M3 ? 448.f : 127.f;
     const int groups = (D + 127) / 128;
-    float scale = all * rstd / full, inv;
+    float scale = all * rstd / full;
     if (scale < 1.17549435e-38f) scale = 1.f;   // false for a NaN
-    inv = 1.f / scale;
+    float f = rstd * (1.f / scale);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (a.group) {
@@ -194,17 +240,22 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) rms_norm_kernel(const No
         }
         scale = top[i] * rstd / full;
         if (scale < 1.17549435e-38f) scale = 1.f;
-        inv = 1.f / scale;
+        f = rstd * (1.f / scale);
       }
       const int e = (i * tpr + tid) * VEC;
       if (!live || e >= D) continue;
-      float v[VEC];
+      const uint64_t f2 = pair(f, f);
+      float v[2 * PAIRS];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = r[i][j] * rstd * inv;
-      Vec<unsigned char, VEC == 1 ? 2 : VEC> o;   // VEC == 1 stores its byte alone
-      codes<OUT, VEC>(v, o.v);
-      if constexpr (VEC == 1) y[e] = o.v[0];
-      else st_vec<unsigned char, VEC>(y + e, o);
+      for (int j = 0; j < PAIRS; ++j) unpair(mul2(r[i][j], f2), v[2 * j], v[2 * j + 1]);
+      if constexpr (VEC == 1) {
+        const float one[1] = {v[0]};
+        codes<OUT, 1>(one, y + e);
+      } else {
+        Vec<unsigned char, VEC> o;
+        codes<OUT, VEC>(v, o.v);
+        st_vec<unsigned char, VEC>(y + e, o);
+      }
       if (a.group) {
         if (e % 128 == 0) a.scale[row * groups + e / 128] = scale;
       } else if (e == 0) {

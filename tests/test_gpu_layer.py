@@ -362,6 +362,14 @@ def test_rms_norm_of_zeros_and_of_nan(vla):
         q, s = vla.rms_norm(x, w, out=out, group=128)
         assert s.shape == (3, 2) and s[0].tolist() == [1, 1] and s[1].isnan().all() and s[2, 0] == 1
     assert vla.rms_norm(x, w)[0].float().abs().max() == 0
+    w[100] = float("nan")   # of the filter: every row's scale, or its group's
+    for D in (256, 255):
+        xs, ws = x[:, :D].contiguous(), w[:D].contiguous()
+        assert vla.rms_norm(xs, ws, out="int8")[1].isnan().all()
+        s = vla.rms_norm(xs, ws, out="e4m3", group=128)[1]
+        assert s[:, 0].isnan().all() and not s[2, 1].isnan()
+        ws[100] = float("inf")   # times x's zero
+        assert vla.rms_norm(xs, ws, out="e4m3")[1].isnan().all()
 
 
 # ---------------------------------------------------------------------------------------------
