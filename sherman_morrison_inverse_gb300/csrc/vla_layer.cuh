@@ -170,7 +170,7 @@ cudaError_t launch_ssm_token(const SsmArgs& a, bool bf16, int sm_count, cudaStre
 // Token by token, any sizes.
 struct StepsPlan {
   int ni;                         // 32 ni >= N states a row
-  int rows;                       // rows of the state a CTA: 32 or 64
+  int rows;                       // rows of the state a CTA
   long long row_blocks;
   int nseg;                       // segments a sequence is cut into
   long long seg_len;              // tokens a segment

@@ -1,7 +1,7 @@
 // Root-mean-square norm with the residual's addition and an output in 8 bits:
 //   r = x + residual (float32; residual <- r in its own type),  v = r / sqrt(mean(r^2) + eps) * w,
 //   and either v in x's type, or codes q with scale = max|v| / 448 (e4m3) or / 127 (integers) over a
-//   row or over every 128 values, q = v * (1 / scale) rounded to nearest even.
+//   row or over every 128 values, q = v / scale rounded to nearest even.
 // A scale below the smallest normal float32 (a row of zeros) is 1; a NaN makes its scale NaN.
 //
 // One pass: a row stays in the registers of its threads between the sum of squares, the maximum and
@@ -225,9 +225,17 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) rms_norm_kernel(const No
     unsigned char* y = static_cast<unsigned char*>(a.y) + row * a.y_row;
     const float full = OUT == VLA_OUT_E4M3 ? 448.f : 127.f;
     const int groups = (D + 127) / 128;
-    float scale = all * rstd / full;
-    if (scale < 1.17549435e-38f) scale = 1.f;   // false for a NaN
-    float f = rstd * (1.f / scale);
+    float scale, f;
+    // v / scale = r w (full / max|r w|): rstd cancels, and with it its error
+    auto factors = [&](float m) {
+      scale = m * rstd / full;
+      f = full / m;
+      if (scale < 1.17549435e-38f) {   // false for a NaN
+        scale = 1.f;
+        f = rstd;
+      }
+    };
+    if (!a.group) factors(all);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (a.group) {
@@ -238,9 +246,7 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) rms_norm_kernel(const No
           const float* g = gmax[par] + i * 32 + (warp & ~3);
           top[i] = max_nan(max_nan(g[0], g[1]), max_nan(g[2], g[3]));
         }
-        scale = top[i] * rstd / full;
-        if (scale < 1.17549435e-38f) scale = 1.f;
-        f = rstd * (1.f / scale);
+        factors(top[i]);
       }
       const int e = (i * tpr + tid) * VEC;
       if (!live || e >= D) continue;

@@ -914,10 +914,10 @@ PromptPlan ssm_prompt_plan(long long n_seq, long long tokens, long long max_len,
     }
   }
   // The token-by-token form takes, measured: a launch and the states' traffic, then 0.2 us a token or
-  // what its arithmetic needs.  (8 sequences of 64 heads of 64, 128 states: 24 tokens 39 us against
-  // 34 us here, 16 tokens 30 against 34; one sequence: 24 tokens 9.0 against 9.8, 32 tokens 10.5 against 9.4.)
+  // what its arithmetic needs.  (8 sequences of 64 heads of 64, 128 states: 16 tokens 29 us against
+  // 21.5 us here; one sequence: 24 tokens 8.8 against 9.8, 32 tokens about 10.3 against 8.3.)
   const double units = (double)(n_seq * slices) * (double)N / 128.0;
-  const double steps = 3.5 + 0.04 * units +
+  const double steps = 2.9 + 0.025 * units +
                        std::max(0.2 * (double)max_len, 0.0017 * (double)tokens * (double)slices * (double)N / 128.0);
   p.fits = best + 2.5 < steps;
   if (!p.fits) return p;
