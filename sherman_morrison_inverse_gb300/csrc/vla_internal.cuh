@@ -26,7 +26,6 @@ struct PairStatus {
 
 constexpr unsigned int kStatusNonfinite = 1u;
 constexpr unsigned int kStatusTimeout = 2u;
-constexpr unsigned int kStatusIndex = 4u;
 
 // Arguments of one scan launch (plain pointers; the pair index p = b*H + h is
 // blockIdx.x).

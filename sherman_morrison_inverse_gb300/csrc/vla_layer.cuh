@@ -8,6 +8,8 @@
 
 namespace vla {
 
+constexpr unsigned int kStatusIndex = 4u;   // VLA_STATUS_INDEX
+
 // A batch of sequences over token rows.  Dense (offsets == NULL): n_seq sequences of T tokens.
 // Packed: sequence s is the rows [offsets[s], offsets[s + 1]) of a buffer of T rows.
 struct Seqs {
