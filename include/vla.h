@@ -340,8 +340,8 @@ vla_err_t vla_scan_fwd_noalloc(const void* q, const void* k, const void* v, cons
  *
  * Strides count elements and are >= 0; within a token the values are adjacent.  No
  * alignment is required of x, y, dt, B, C, z and w beyond their type's; rows that
- * start on 16-byte boundaries are faster.  Outputs must not overlap any input
- * (the norm's residual is both). */
+ * start on 16-byte boundaries are faster.  A pointer that is not aligned to its type
+ * is INVALID_ARG.  Outputs must not overlap any input (the norm's residual is both). */
 
 /* y[t, c] = act(bias[c] + sum_{j<K} w[c, j] x[t - K + 1 + j, c]); act(v) = v * sigmoid(v)
  * if silu, else v.  Inputs before a sequence's first token come from its state.
@@ -396,7 +396,7 @@ typedef enum { VLA_OUT_IO = 0, VLA_OUT_E4M3 = 1, VLA_OUT_INT8 = 2 } vla_out_t;
  * VLA_OUT_INT8: integers in [-127, 127]) with float32 scales such that v ~ code * scale:
  * scale = max|v| / 448 or / 127 over the row (group 0, scale [rows]) or over each 128
  * values (group 128, scale [rows, ceil(D / 128)]), 1 where that is below the smallest
- * normal float32, and code = v * (1 / scale) to nearest even.  A row with a NaN has NaN scales.
+ * normal float32, and code = v / scale to nearest even.  A row with a NaN has NaN scales.
  *
  *   x, y, residual   rows at x_row, y_row, res_row elements; residual NULL, or
  *                    res_dtype, updated in place.   w  [D] float32.

@@ -4,6 +4,8 @@
 #include "vla_layer.cuh"
 #include "vla_ssm_prompt.cuh"
 
+#include <exception>
+
 using namespace vla::api;
 
 namespace {
@@ -35,6 +37,11 @@ size_t ws_need(const vla::PromptPlan& prompt, const vla::StepsPlan& steps) {
   return prompt.fits && prompt.ws_bytes > steps.ws_bytes ? prompt.ws_bytes : steps.ws_bytes;
 }
 
+// Whether pointers (NULL among them) are aligned to values of `size` bytes.
+template <typename... P>
+bool to_values(size_t size, P... p) { return ((reinterpret_cast<uintptr_t>(p) | ...) & (size - 1)) == 0; }
+size_t size_of(vla_dtype_t t) { return t == VLA_BF16 ? 2 : 4; }
+
 bool stride_ok(long long v) { return v >= 0 && v < (1LL << 40); }
 
 // Rows of an output must not overlap: a stride that the call uses is at least a row's width.
@@ -51,7 +58,7 @@ extern "C" {
 vla_err_t vla_short_conv(vla_handle_t h, const void* x, const float* w, const float* bias, void* state, void* y,
                          long long n_seq, long long T, long long max_len, const int* offsets, const int* slots,
                          long long n_slots, long long C, int K, const long long* strides, int silu,
-                         vla_dtype_t io_dtype, void* stream) {
+                         vla_dtype_t io_dtype, void* stream) try {
   const std::string f = "vla_short_conv";
   if (!h) return fail(nullptr, VLA_ERR_INVALID_ARG, f + ": handle is NULL");
   h->last_error.clear();
@@ -63,6 +70,8 @@ vla_err_t vla_short_conv(vla_handle_t h, const void* x, const float* w, const fl
   if (err != VLA_OK) return err;
   if (n_seq == 0 || T == 0 || C == 0 || a.seqs.max_len == 0) return VLA_OK;
   if (!x || !w || !y || !strides) return fail(h, VLA_ERR_INVALID_ARG, f + ": NULL pointer");
+  if (!to_values(size_of(io_dtype), x, state, y) || !to_values(4, w, bias, offsets, slots))
+    return fail(h, VLA_ERR_INVALID_ARG, f + ": misaligned pointer");
   for (int i = 0; i < 4; ++i)
     if (!stride_ok(strides[i])) return fail(h, VLA_ERR_INVALID_ARG, f + ": stride out of range");
   if (!out_ok(a.seqs, strides[2], strides[3], C))
@@ -79,6 +88,8 @@ vla_err_t vla_short_conv(vla_handle_t h, const void* x, const float* w, const fl
   });
   if (e != cudaSuccess) return fail(h, VLA_ERR_CUDA, cuda_msg("vla_short_conv: launch", e));
   return VLA_OK;
+} catch (const std::exception&) {   // no memory for a message
+  return VLA_ERR_NOMEM;
 }
 
 vla_err_t vla_ssm_scan(vla_handle_t h, const void* x, const void* dt, const float* A, const void* B, const void* C,
@@ -86,7 +97,7 @@ vla_err_t vla_ssm_scan(vla_handle_t h, const void* x, const void* dt, const floa
                        long long n_seq, long long T, long long max_len, const int* offsets, const int* slots,
                        long long n_slots, long long H, long long P, long long G, long long N,
                        const long long* strides, int softplus, vla_dtype_t io_dtype, void* workspace,
-                       size_t workspace_bytes, void* stream) {
+                       size_t workspace_bytes, void* stream) try {
   const std::string f = "vla_ssm_scan";
   if (!h) return fail(nullptr, VLA_ERR_INVALID_ARG, f + ": handle is NULL");
   h->last_error.clear();
@@ -101,6 +112,8 @@ vla_err_t vla_ssm_scan(vla_handle_t h, const void* x, const void* dt, const floa
   if (N == 0) return fail(h, VLA_ERR_INVALID_ARG, f + ": N must be positive");
   if (N > kMaxStates) return fail(h, VLA_ERR_UNSUPPORTED, f + ": built for N up to 256");
   if (!x || !dt || !A || !B || !C || !y || !strides) return fail(h, VLA_ERR_INVALID_ARG, f + ": NULL pointer");
+  if (!to_values(size_of(io_dtype), x, dt, B, C, z, y) || !to_values(4, A, D, dt_bias, offsets, slots))
+    return fail(h, VLA_ERR_INVALID_ARG, f + ": misaligned pointer");
   if (state && !aligned16(state)) return fail(h, VLA_ERR_INVALID_ARG, f + ": state must be 16-byte aligned");
   for (int i = 0; i < 12; ++i)
     if (!stride_ok(strides[i])) return fail(h, VLA_ERR_INVALID_ARG, f + ": stride out of range");
@@ -131,10 +144,12 @@ vla_err_t vla_ssm_scan(vla_handle_t h, const void* x, const void* dt, const floa
   });
   if (e != cudaSuccess) return fail(h, VLA_ERR_CUDA, cuda_msg("vla_ssm_scan: launch", e));
   return VLA_OK;
+} catch (const std::exception&) {   // no memory for a message
+  return VLA_ERR_NOMEM;
 }
 
 vla_err_t vla_ssm_workspace(vla_handle_t h, long long n_seq, long long T, long long max_len, int packed, long long H,
-                            long long P, long long N, vla_dtype_t io_dtype, size_t* bytes) {
+                            long long P, long long N, vla_dtype_t io_dtype, size_t* bytes) try {
   const std::string f = "vla_ssm_workspace";
   if (!h) return fail(nullptr, VLA_ERR_INVALID_ARG, f + ": handle is NULL");
   h->last_error.clear();
@@ -147,11 +162,13 @@ vla_err_t vla_ssm_workspace(vla_handle_t h, long long n_seq, long long T, long l
   *bytes = ws_need(vla::ssm_prompt_plan(n_seq, packed ? T : n_seq * T, len, H, P, N, io_dtype == VLA_BF16, h->sm_count),
                    vla::ssm_steps_plan(n_seq, len, H, P, N, h->sm_count));
   return VLA_OK;
+} catch (const std::exception&) {   // no memory for a message
+  return VLA_ERR_NOMEM;
 }
 
 vla_err_t vla_rms_norm(vla_handle_t h, const void* x, const float* w, void* residual, void* y, float* scale,
                        long long rows, long long D, long long x_row, long long res_row, long long y_row, float eps,
-                       int group, vla_out_t out, vla_dtype_t io_dtype, vla_dtype_t res_dtype, void* stream) {
+                       int group, vla_out_t out, vla_dtype_t io_dtype, vla_dtype_t res_dtype, void* stream) try {
   const std::string f = "vla_rms_norm";
   if (!h) return fail(nullptr, VLA_ERR_INVALID_ARG, f + ": handle is NULL");
   h->last_error.clear();
@@ -168,6 +185,9 @@ vla_err_t vla_rms_norm(vla_handle_t h, const void* x, const float* w, void* resi
   if (rows == 0 || D == 0) return VLA_OK;
   if (D > kMaxWidth) return fail(h, VLA_ERR_UNSUPPORTED, f + ": built for D up to 32768");
   if (!x || !w || !y || (out != VLA_OUT_IO && !scale)) return fail(h, VLA_ERR_INVALID_ARG, f + ": NULL pointer");
+  if (!to_values(size_of(io_dtype), x) || !to_values(out == VLA_OUT_IO ? size_of(io_dtype) : 1, y) ||
+      !to_values(size_of(res_dtype), residual) || !to_values(4, w, scale))
+    return fail(h, VLA_ERR_INVALID_ARG, f + ": misaligned pointer");
   if (rows > 1 && (y_row < D || (residual && res_row < D)))
     return fail(h, VLA_ERR_INVALID_ARG, f + ": rows of y or the residual overlap");
   vla::NormArgs a{};
@@ -180,6 +200,8 @@ vla_err_t vla_rms_norm(vla_handle_t h, const void* x, const float* w, void* resi
   });
   if (e != cudaSuccess) return fail(h, VLA_ERR_CUDA, cuda_msg("vla_rms_norm: launch", e));
   return VLA_OK;
+} catch (const std::exception&) {   // no memory for a message
+  return VLA_ERR_NOMEM;
 }
 
 }  // extern "C"

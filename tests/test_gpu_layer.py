@@ -546,3 +546,22 @@ def test_no_wait_runs_out_and_scratch_is_checked(vla):
                                   1, 128, strides, 1, 1, ws, size, None)
         assert code == 1 and b"workspace" in h.lib.vla_last_error(h.ptr)
     h.close()
+
+
+def test_misaligned_pointers_are_refused(vla):
+    """Before any launch: each pointer in turn a byte off its type's alignment."""
+    import ctypes
+    h, p = vla.Handle(), torch.zeros(1 << 16, device="cuda").data_ptr()
+    ones = lambda n: (ctypes.c_longlong * n)(*[64] * n)   # noqa: E731
+
+    def refused(call, n):
+        for i in range(n):
+            assert call([p + (i == j) for j in range(n)]) == 1, i
+            assert b"aligned" in h.lib.vla_last_error(h.ptr)
+
+    refused(lambda q: h.lib.vla_short_conv(h.ptr, *q, 1, 4, 4, None, None, 1, 8, 4, ones(4), 0, 0, None), 5)
+    refused(lambda q: h.lib.vla_ssm_scan(h.ptr, *q[:10], 1, 4, 4, None, None, 1, 2, 8, 1, 8, ones(12), 1, 0, None, 0,
+                                         None), 10)
+    refused(lambda q: h.lib.vla_rms_norm(h.ptr, *q, None, 1, 8, 8, 8, 8, 1e-6, 0, 0, 0, 0, None), 4)
+    assert h.lib.vla_rms_norm(h.ptr, p, p, None, p, p + 1, 1, 8, 8, 8, 8, 1e-6, 0, 1, 0, 0, None) == 1
+    h.close()
