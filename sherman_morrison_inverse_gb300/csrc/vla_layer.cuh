@@ -177,6 +177,7 @@ struct StepsPlan {
   int nseg;                       // segments a sequence is cut into
   long long seg_len;              // tokens a segment
   size_t ws_bytes;
+  bool overlap;                   // the second launch starts beside the first
 };
 StepsPlan ssm_steps_plan(long long n_seq, long long max_len, long long H, long long P, long long N, int sm_count);
 cudaError_t launch_ssm_steps(const SsmArgs& a, const StepsPlan& plan, bool bf16, cudaStream_t s);
@@ -201,6 +202,26 @@ cudaError_t launch_rms_norm(const NormArgs& a, bool bf16, cudaStream_t s);
 __device__ __forceinline__ float time_step(float x, float bias, bool softplus) {
   x += bias;
   return softplus && x <= 20.f ? log1pf(expf(x)) : x;
+}
+
+// A launch in two parts: the second's CTAs start as SMs become free, once every CTA of the first is
+// running (all_started there), and wait for the first's results where they read them.
+__device__ __forceinline__ void all_started() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_first() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_second(void (*kern)(P...), unsigned int ctas, int threads, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(ctas);
+  c.blockDim = dim3((unsigned int)threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, static_cast<A&&>(args)...);
 }
 
 }  // namespace vla

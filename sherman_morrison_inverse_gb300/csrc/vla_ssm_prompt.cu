@@ -43,17 +43,19 @@
 //
 // Few slices: the sequence is cut into segments, one CTA each.  A first launch forms what every
 // segment but a sequence's last adds to the state (B^T X~ alone), the second starts each segment from
-// those, joined in a fixed order.
+// those, joined in a fixed order.  The second launch's CTAs start beside the first's and wait where they
+// read what it leaves.  Many slices, but the last wave of CTAs far from full: only what is left for that
+// wave is cut, its first launch and the whole slices share the SMs.
 //
-// What bounds it.  8 sequences of 4096 tokens, 64 heads of 64, 128 states: 316 us, about 4450 cycles a
-// chunk and SM.  The 40 products of a chunk take 65 to 75 cycles each, whatever their width up to
+// What bounds it.  8 sequences of 4096 tokens, 64 heads of 64, 128 states: 297 us (315 uncut), about
+// 4450 cycles a chunk and SM.  The 40 products of a chunk take 65 to 75 cycles each, whatever their width up to
 // 128 columns: at least 2800 cycles (the tensor pipe is 43 % busy by the counters, memory 22 %).
 // The chain of the state takes the whole period: X~ 1370, its product 1900 (it shares the pipe with
 // the output's), h 540, hand-overs 700; the output's side needs about 4400.  Side by side in one CTA
-// with everything double-buffered, not as two CTAs an SM that hide each other (328 us) nor with 16
+// with everything double-buffered, not as two CTAs an SM that hide each other (328 us, uncut) nor with 16
 // warps a side; dropping a term of X~ would save 4 % and lose the float32 state.
-// One sequence of 16384 tokens, 16 heads, gated: 82 us in 9 segments.  Nine packed prompts of 1 to 2047
-// tokens, 16 heads of 128, 64 states, gated: 54 us.
+// One sequence of 16384 tokens, 16 heads, gated: 78.5 us in 9 segments (82 without the overlap of the
+// launches).  Nine packed prompts of 1 to 2047 tokens, 16 heads of 128, 64 states, gated: 53 us.
 #include <cuda.h>   // CUtensorMap and the encode entry point's types (resolved at run time)
 
 #include <algorithm>
@@ -228,6 +230,7 @@ struct PromptArgs {
   Seqs seqs;
   int H, P, G, N, pslices;
   int nseg, seg_chunks;
+  int whole;         // (sequence, slice) pairs that are not cut, the first ones
   long long dt_seq, dt_tok, z_seq, z_tok, y_seq, y_tok;
   bool softplus;
   DevStatus* status;
@@ -249,20 +252,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slices = a.H * a.pslices;
-  const int slice = (int)(blockIdx.x % slices);
-  const long long rest = blockIdx.x / slices;
-  const int seg = (int)(rest % a.nseg);
-  const long long seq = rest / a.nseg;
+  if (!FULL) all_started();
+  // the whole pairs' CTAs come first, then the segments
+  const int pairs = (int)a.seqs.n_seq * slices, block = (int)blockIdx.x + (FULL ? 0 : a.whole);
+  const bool is_whole = FULL && block < a.whole;
+  const int seg = is_whole ? 0 : (block - a.whole) / (pairs - a.whole);
+  const int at = block - seg * (pairs - a.whole);
+  const int seq = at / slices, slice = at - seq * slices;
   const int head = slice / a.pslices, p0 = (slice - head * a.pslices) * 64, group = head / (a.H / a.G);
 
   unsigned int bad = 0;
   const SeqRange q = seq_range(a.seqs, seq, &bad);
   if (bad && tid == 0 && FULL) atomicOr(&a.status->flags, bad);
-  const long long chunks = (q.len + kL - 1) / kL;
-  const long long c_begin = (long long)seg * a.seg_chunks;
-  const long long c_end = c_begin + a.seg_chunks < chunks ? c_begin + a.seg_chunks : chunks;
-  const bool last = c_end == chunks;
-  if (!q.run || c_begin >= chunks || (!FULL && last)) return;
+  const int chunks = (int)((q.len + kL - 1) / kL), seg_chunks = is_whole ? chunks : a.seg_chunks;
+  const int segs = seg_chunks > 0 ? (chunks + seg_chunks - 1) / seg_chunks : 0;   // of this sequence
+  const bool last = seg == segs - 1;
+  if (!q.run || seg >= segs || (!FULL && last)) {
+    if (FULL && a.nseg > 1) wait_for_first();
+    return;
+  }
   const uint32_t sbase = smem_u32(smem);
   if ((sbase & 1023u) != 0) {   // the swizzled tiles need it; report rather than run misaligned
     if (tid == 0) atomicOr(&a.status->flags, kStatusTimeout);
@@ -280,8 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const bool packed = a.seqs.offsets != nullptr;
   const int row0 = packed ? (int)q.start : 0, batch = packed ? 0 : (int)seq;   // tensor map coordinates
-  const int n_chunks = (int)(c_end - c_begin);
-  const long long t_first = c_begin * kL;
+  const int n_chunks = last ? chunks - seg * seg_chunks : seg_chunks;
+  const int t_first = seg * seg_chunks * kL;
+  const unsigned int left = (unsigned int)((int)q.len - t_first);   // tokens from t_first on
 
   if (tid == 0) {
     constexpr int W = kSide / 32;
@@ -305,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rsw = (uint32_t)(row & 7);
   const uint32_t row_at = (uint32_t)row * 128;
   const int pc = a.P - p0 - 32 * half;   // columns of this thread that exist
-  float* wsq = a.nseg > 1 ? a.ws + (seq * slices + slice) * ws_floats(a.nseg, NN) : nullptr;
+  float* wsq = a.nseg > 1 && !is_whole ? a.ws + (at - a.whole) * ws_floats(a.nseg, NN) : nullptr;
   const int n = row;
   tc::fence_before_sync();
   __syncthreads();
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const int last_i = n_chunks - 1;
   // whether rows of the next sequence lie behind this one's in the last chunk
-  const bool ragged = packed && c_end == chunks && q.len % kL != 0;
+  const bool ragged = packed && last && (left & (kL - 1)) != 0;
 
   const uint64_t minus = pair(-1.f, -1.f), minus_two = pair(-2.f, -2.f), one_half = pair(0.5f, 0.5f);
   // One piece of X~ of chunk i in three terms: 32 tokens and 16 columns
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint4 xa = *reinterpret_cast<const uint4*>(smem + Cf::oX + r * kTile + at0);
     uint4 xb = *reinterpret_cast<const uint4*>(smem + Cf::oX + r * kTile + at1);
     // rows of the next sequence: none of them may reach the product
-    if (ragged && i == last_i && t_first + (long long)i * kL + token >= q.len) xa = xb = make_uint4(0, 0, 0, 0);
+    if (ragged && i == last_i && (unsigned int)(i * kL + token) >= left) xa = xb = make_uint4(0, 0, 0, 0);
     const uint32_t xi[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
     uint32_t t1[8], t2[8], t3[8];
 #pragma unroll
@@ -390,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // y of chunk i: Y, gated
       auto finish = [&](int i) -> bool {
         const long long t = t_first + (long long)i * kL + row;
-        const bool in = t < q.len, tail = ragged && i == last_i;
+        const bool in = (unsigned int)(i * kL + row) < left, tail = ragged && i == last_i;
         const __nv_bfloat16* z = GATE == 2 ? a.z + (packed ? (q.start + t) * a.z_tok : seq * a.z_seq + t * a.z_tok) +
                                                  (long long)head * a.P + p0 + 32 * half
                                            : nullptr;
@@ -498,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Y = D x + the state's part scaled by the row's decay
         if (!wait(kFullX + r, u) || !wait(kFullYi + r, u)) break;
         tc::fence_after_sync();
-        const bool clear = ragged && i == last_i && t_first + (long long)i * kL + row >= q.len;
+        const bool clear = ragged && i == last_i && (unsigned int)(i * kL + row) >= left;
         const uint32_t ty = tlane + kColY + 64 * r + 32 * half;
         const uint64_t f2 = pair(row_decay, row_decay);
 #pragma unroll 1
@@ -531,7 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the state before the segment: state n, columns p (the first tiles and decays are on their way)
     float h[32];
     {
-      const bool from_ws = FULL && chunks > a.seg_chunks;
+      const bool from_ws = FULL && segs > 1;
+      if (from_ws) wait_for_first();
       const float* src = nullptr;
       long long pitch = 0;
       bool mine = n < a.N;
@@ -607,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ragged && i == last_i) {   // rows of the next sequence: none of B's may reach the product
         if (!wait(kFullB + r, u)) break;
-        if (half == 0 && t_first + (long long)i * kL + row >= q.len)
+        if (half == 0 && (unsigned int)(i * kL + row) >= left)
           for (uint32_t k = 0; k < 8 * Cf::NT; ++k)
             *reinterpret_cast<uint4*>(smem + Cf::oB + (r * Cf::NT + (k >> 3)) * kTile + row_at + ((k & 7) << 4)) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
@@ -720,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i <= n_chunks; ++i) {
       if (i > 0 && !wait(kStage, i - 1)) break;
       if (one) {
-        const int t = row0 + (int)(t_first + (long long)i * kL);
+        const int t = row0 + t_first + i * kL;
         if (i > 0) {
           if (!(ragged && i - 1 == last_i)) store_4d(&map_y, p0, head, t - kL, batch, sbase + Cf::oY);
           store_read_done();
@@ -747,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int use = kind == 2 ? i : i >> 1;
       if (use > 0 && !wait(empty, use - 1)) break;
       if (one) {
-        const int t = row0 + (int)(t_first + (long long)i * kL);
+        const int t = row0 + t_first + i * kL;
         const CUtensorMap* map = kind == 0 ? &map_B : kind == 1 ? &map_x : &map_C;
         uint64_t* full = bar + (kind == 0 ? kFullB + r : kind == 1 ? kFullX + r : kFullC);
         const uint32_t to = sbase + (kind == 0 ? Cf::oB + r * Cf::NT * kTile : kind == 1 ? Cf::oX + r * kTile : Cf::oC);
@@ -824,6 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   if (warp == 1) tc::tmem_dealloc(tmem, kCols);
+  if (FULL && a.nseg > 1) wait_for_first();   // the call ends after both
 }
 
 // ---------------------------------------------------------------------------
@@ -867,31 +878,35 @@ bool encode(CUtensorMap* m, const void* base, long long width, long long heads, 
 template <int NN>
 cudaError_t launch(const SsmArgs& s, const PromptArgs& a, const PromptPlan& plan, const CUtensorMap* maps,
                    int gate, cudaStream_t st) {
-  const long long ctas = s.seqs.n_seq * a.H * a.pslices * plan.nseg;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const long long cut = (s.seqs.n_seq * a.H * a.pslices - plan.whole) * plan.nseg;
+  if (cut + plan.whole > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   constexpr int bytes = (int)Cfg<NN>::bytes;
   int device = 0;
   cudaError_t err = cudaGetDevice(&device);
   if (err != cudaSuccess) return err;
-  auto run = [&](auto kern, std::atomic<unsigned long long>& ready) -> cudaError_t {
+  auto run = [&](auto kern, std::atomic<unsigned long long>& ready, bool first) -> cudaError_t {
     // more than 48 KB of shared memory: allowed once a kernel and device (the first 64)
     if (device >= 64 || !(ready.load(std::memory_order_relaxed) >> device & 1)) {
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
       if (e != cudaSuccess) return e;
       if (device < 64) ready.fetch_or(1ull << device, std::memory_order_relaxed);
     }
-    kern<<<(unsigned int)ctas, kThreads, bytes, st>>>(maps[0], maps[1], maps[2], maps[3], maps[4], a);
+    if (!first && plan.nseg > 1)
+      return launch_second(kern, (unsigned int)(plan.whole + cut), kThreads, bytes, st, maps[0], maps[1], maps[2], maps[3],
+                           maps[4], a);
+    kern<<<(unsigned int)(first ? cut : plan.whole + cut), kThreads, bytes, st>>>(maps[0], maps[1], maps[2], maps[3],
+                                                                                maps[4], a);
     return cudaGetLastError();
   };
   static std::atomic<unsigned long long> ready[4];
   if (plan.nseg > 1) {
-    const cudaError_t e = run(ssm_prompt_kernel<NN, false, 0>, ready[0]);
+    const cudaError_t e = run(ssm_prompt_kernel<NN, false, 0>, ready[0], true);
     if (e != cudaSuccess) return e;
   }
   switch (gate) {
-    case 0: return run(ssm_prompt_kernel<NN, true, 0>, ready[1]);
-    case 1: return run(ssm_prompt_kernel<NN, true, 1>, ready[2]);
-    default: return run(ssm_prompt_kernel<NN, true, 2>, ready[3]);
+    case 0: return run(ssm_prompt_kernel<NN, true, 0>, ready[1], false);
+    case 1: return run(ssm_prompt_kernel<NN, true, 1>, ready[2], false);
+    default: return run(ssm_prompt_kernel<NN, true, 2>, ready[3], false);
   }
 }
 
@@ -921,6 +936,21 @@ PromptPlan ssm_prompt_plan(long long n_seq, long long tokens, long long max_len,
       best = cost;
       p.nseg = (int)k;
       p.seg_chunks = per;
+      p.whole = 0;
+    }
+    // or, of sequences of one length, only what the last wave of CTAs would have: its first launch and
+    // the whole ones share the SMs, and so do whole ones and segments.  (8 sequences of 4096 tokens, 64
+    // heads: 56 of 512 are left for a fourth wave; uncut 315 us, cut in 2 306, in 3 297, in 4 about 305.)
+    const long long tail = n_seq * slices % slots, full = n_seq * slices / slots;
+    if (tail == 0 || full == 0 || tokens != n_seq * max_len) continue;
+    const double part = full * (2.3 * chunks + kStart) +
+                        std::max(1.0, (double)(tail * k) / slots) * (2.3 * per + kStart + 0.7 * k) +
+                        (double)(tail * (k - 1)) / slots * (1.2 * per + kStart);
+    if (part < best) {
+      best = part;
+      p.nseg = (int)k;
+      p.seg_chunks = per;
+      p.whole = n_seq * slices - tail;
     }
   }
   // The token-by-token form takes, measured: a launch and the states' traffic, then 0.2 us a token or
@@ -931,7 +961,7 @@ PromptPlan ssm_prompt_plan(long long n_seq, long long tokens, long long max_len,
                        std::max(0.2 * (double)max_len, 0.0017 * (double)tokens * (double)slices * (double)N / 128.0);
   p.fits = best + 2.5 < steps;
   if (!p.fits) return p;
-  if (p.nseg > 1) p.ws_bytes = (size_t)(n_seq * slices) * ws_floats(p.nseg, p.nn) * sizeof(float);
+  if (p.nseg > 1) p.ws_bytes = (size_t)(n_seq * slices - p.whole) * ws_floats(p.nseg, p.nn) * sizeof(float);
   return p;
 }
 
@@ -957,6 +987,7 @@ cudaError_t launch_ssm_prompt(const SsmArgs& s, const PromptPlan& plan, cudaStre
   a.pslices = (int)((s.P + 63) / 64);
   a.nseg = plan.nseg;
   a.seg_chunks = (int)plan.seg_chunks;
+  a.whole = (int)plan.whole;
   a.dt_seq = s.dt_seq; a.dt_tok = s.dt_tok; a.z_seq = s.z_seq; a.z_tok = s.z_tok; a.y_seq = s.y_seq; a.y_tok = s.y_tok;
   a.softplus = s.softplus;
   a.status = s.status;

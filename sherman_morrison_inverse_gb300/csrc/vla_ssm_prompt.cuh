@@ -11,6 +11,7 @@ struct PromptPlan {
   int nn;                 // states rounded up: 64 or 128
   int nseg;               // segments a sequence is cut into
   long long seg_chunks;   // chunks of 128 tokens a segment
+  long long whole;        // the first of the (sequence, slice) pairs that are not cut
   size_t ws_bytes;
 };
 

@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(cta_threads(LPR), 512 / cta_threads(LPR))
   __shared__ float sz[FULL ? 2 : 1][FULL ? kTok : 1][ROWS];
   __shared__ __align__(8) float2 sdec[2][kTok];   // decay, time step
 
+  if (!FULL) all_started();
   const int rb = (int)(blockIdx.x % row_blocks);
   long long rest = blockIdx.x / row_blocks;
   const long long head = rest % a.H;
@@ -68,7 +69,10 @@ __global__ void __launch_bounds__(cta_threads(LPR), 512 / cta_threads(LPR))
   const long long t_begin = seg * seg_len;
   const long long t_end = t_begin + seg_len < q.len ? t_begin + seg_len : q.len;
   const bool last = t_end == q.len;
-  if (!q.run || t_begin >= q.len || (!FULL && last)) return;
+  if (!q.run || t_begin >= q.len || (!FULL && last)) {
+    if (FULL && nseg > 1) wait_for_first();
+    return;
+  }
 
   const bool packed = a.seqs.offsets != nullptr;
   const long long g = head / (a.H / a.G);
@@ -148,6 +152,7 @@ __global__ void __launch_bounds__(cta_threads(LPR), 512 / cta_threads(LPR))
       }
   }
   if (from_ws) {
+    wait_for_first();
     const float* dec = ws + (long long)nseg * PER;
     for (int j = 0; j < (seg == 0 ? 1 : seg); ++j) {
       // segment 0 starts from the state before the sequence; its result holds that state's rest
@@ -275,6 +280,7 @@ __global__ void __launch_bounds__(cta_threads(LPR), 512 / cta_threads(LPR))
     }
     return;
   }
+  if (nseg > 1) wait_for_first();   // the call ends after both
   if (!a.state || !last) return;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -308,6 +314,9 @@ cudaError_t launch(const SsmArgs& a, const StepsPlan& p, cudaStream_t s) {
     ssm_steps_kernel<T, LPR, NI, R, false><<<(unsigned int)ctas, threads, 0, s>>>(a, (int)p.row_blocks, p.nseg, p.seg_len);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    if (p.overlap)
+      return launch_second(ssm_steps_kernel<T, LPR, NI, R, true>, (unsigned int)ctas, threads, 0, s, a,
+                           (int)p.row_blocks, p.nseg, p.seg_len);
   }
   ssm_steps_kernel<T, LPR, NI, R, true><<<(unsigned int)ctas, threads, 0, s>>>(a, (int)p.row_blocks, p.nseg, p.seg_len);
   return cudaGetLastError();
@@ -349,6 +358,10 @@ StepsPlan ssm_steps_plan(long long n_seq, long long max_len, long long H, long l
     if (k > max_len / kSeg) k = max_len / kSeg;
     p.seg_len = ((max_len + k - 1) / k + kTok - 1) / kTok * kTok;
     p.nseg = (int)((max_len + p.seg_len - 1) / p.seg_len);
+    // the second launch's CTAs wait beside the first's where there is room for both (8 heads of 64 x 64, 1000
+    // tokens: 27.2 us, 25.5 beside it); where there is not, the places they get are uneven (4 sequences
+    // of 513 tokens: 30.5 us, 33.3 beside it)
+    p.overlap = 2 * ctas * p.nseg <= most;
     if (p.nseg > 1)
       p.ws_bytes = (size_t)ctas * ws_floats(p.nseg, p.rows * 4 * lpr * (p.ni == 1 ? 1 : 2)) * sizeof(float);
   }
