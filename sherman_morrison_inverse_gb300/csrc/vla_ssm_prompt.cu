@@ -927,11 +927,26 @@ PromptPlan ssm_prompt_plan(long long n_seq, long long tokens, long long max_len,
   // fill the SMs twice, take a third longer.)
   constexpr double kStart = 4.5;
   const auto waves = [&](long long k) { return (double)((n_seq * slices * k + slots - 1) / slots); };
-  double best = waves(1) * (2.3 * chunks + kStart);
+  // Sequences of several lengths, of which the longest and the tokens of all are known: the work that there
+  // is, a CTA without any costing kEmpty, and half of what the longest CTA takes (it may start last).
+  // (3000 and 500 tokens, 32 heads: uncut 61 us, in 2 55, 3 44, 4 42, 6 52; 30 prompts of 100 and one of 4096, 16
+  // heads: 107, 104, 94, 99, 112; nine of 1 to 2047, 16 heads of 128: 51, 60, 64, 73, 88.)
+  constexpr double kEmpty = 2.0;
+  const bool even = tokens >= n_seq * max_len;
+  const auto uneven = [&](long long k, long long per) {
+    const double n = (double)n_seq, segs = (double)tokens / (kL * per) - 0.5 * n;
+    const double first = k == 1 ? 0.0 : std::max((double)(k - 1), std::min(n * (k - 1), segs)), second = n + first;
+    const double work2 = slices * (2.3 * ((double)tokens / kL + 0.5 * n) + kStart * second + kEmpty * (n * k - second)) / slots;
+    const double work1 = slices * (first * (1.2 * per + kStart) + kEmpty * (n * k - first)) / slots;
+    const double longest = 2.3 * per + kStart + (k > 1 ? 0.7 * k : 0.0);
+    return (second * slices <= slots ? longest : std::max(longest, work2 + 0.5 * longest)) +
+           (k == 1 ? 0.0 : std::max(work1, 1.2 * per + kStart));
+  };
+  double best = even ? waves(1) * (2.3 * chunks + kStart) : uneven(1, chunks);
   for (long long k = 2; k <= chunks && k <= 64; ++k) {
     const long long per = (chunks + k - 1) / k;
     if ((chunks + per - 1) / per != k) continue;
-    const double cost = waves(k) * (3.5 * per + 2 * kStart + 0.7 * k);
+    const double cost = even ? waves(k) * (3.5 * per + 2 * kStart + 0.7 * k) : uneven(k, per);
     if (cost < best) {
       best = cost;
       p.nseg = (int)k;
@@ -942,7 +957,7 @@ PromptPlan ssm_prompt_plan(long long n_seq, long long tokens, long long max_len,
     // the whole ones share the SMs, and so do whole ones and segments.  (8 sequences of 4096 tokens, 64
     // heads: 56 of 512 are left for a fourth wave; uncut 315 us, cut in 2 306, in 3 297, in 4 about 305.)
     const long long tail = n_seq * slices % slots, full = n_seq * slices / slots;
-    if (tail == 0 || full == 0 || tokens != n_seq * max_len) continue;
+    if (tail == 0 || full == 0 || !even) continue;
     const double part = full * (2.3 * chunks + kStart) +
                         std::max(1.0, (double)(tail * k) / slots) * (2.3 * per + kStart + 0.7 * k) +
                         (double)(tail * (k - 1)) / slots * (1.2 * per + kStart);
