@@ -43,17 +43,17 @@
 //
 // Few slices: the sequence is cut into segments, one CTA each.  A first launch forms what every
 // segment but a sequence's last adds to the state (B^T X~ alone), the second starts each segment from
-// those, joined in a fixed order.  The second launch's CTAs start beside the first's and wait where they
-// read what it leaves.  Many slices, but the last wave of CTAs far from full: only what is left for that
-// wave is cut, its first launch and the whole slices share the SMs.
+// those, joined in a fixed order.  The second launch's CTAs start beside the first's and wait where
+// they read what it leaves.  Many slices, but the last wave of CTAs far from full: only what is left
+// for that wave is cut, its first launch and the whole slices share the SMs.
 //
-// What bounds it.  8 sequences of 4096 tokens, 64 heads of 64, 128 states: 297 us (315 uncut), about
-// 4450 cycles a chunk and SM.  The 40 products of a chunk take 65 to 75 cycles each, whatever their width up to
-// 128 columns: at least 2800 cycles (the tensor pipe is 43 % busy by the counters, memory 22 %).
-// The chain of the state takes the whole period: X~ 1370, its product 1900 (it shares the pipe with
-// the output's), h 540, hand-overs 700; the output's side needs about 4400.  Side by side in one CTA
-// with everything double-buffered, not as two CTAs an SM that hide each other (328 us, uncut) nor with 16
-// warps a side; dropping a term of X~ would save 4 % and lose the float32 state.
+// What bounds it.  8 sequences of 4096 tokens, 64 heads of 64, 128 states: 291 us (315 uncut), about
+// 4450 cycles a chunk and SM.  The 40 products of a chunk take 65 to 75 cycles each, whatever their
+// width up to 128 columns: at least 2800 cycles (the tensor pipe is 43 % busy by the counters, memory
+// 24 %).  The chain of the state takes the whole period: X~ 1370, its product 1900 (it shares the pipe
+// with the output's), h 540, hand-overs 700; the output's side needs about 4400.  Side by side in one
+// CTA with everything double-buffered, not as two CTAs an SM that hide each other (328 us, uncut) nor
+// with 16 warps a side; dropping a term of X~ would save 4 % and lose the float32 state.
 // One sequence of 16384 tokens, 16 heads, gated: 78.5 us in 9 segments (82 without the overlap of the
 // launches).  Nine packed prompts of 1 to 2047 tokens, 16 heads of 128, 64 states, gated: 53 us.
 #include <cuda.h>   // CUtensorMap and the encode entry point's types (resolved at run time)
@@ -253,11 +253,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slices = a.H * a.pslices;
   if (!FULL) all_started();
-  // the whole pairs' CTAs come first, then the segments
+  // the whole pairs' CTAs come first, then the segments; beside whole pairs the last ones, which are longer, first
   const int pairs = (int)a.seqs.n_seq * slices, block = (int)blockIdx.x + (FULL ? 0 : a.whole);
   const bool is_whole = FULL && block < a.whole;
-  const int seg = is_whole ? 0 : (block - a.whole) / (pairs - a.whole);
-  const int at = block - seg * (pairs - a.whole);
+  const int turn = is_whole ? 0 : (block - a.whole) / (pairs - a.whole);
+  const int at = block - turn * (pairs - a.whole), seg = FULL && !is_whole && a.whole > 0 ? a.nseg - 1 - turn : turn;
   const int seq = at / slices, slice = at - seq * slices;
   const int head = slice / a.pslices, p0 = (slice - head * a.pslices) * 64, group = head / (a.H / a.G);
 
@@ -265,7 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const SeqRange q = seq_range(a.seqs, seq, &bad);
   if (bad && tid == 0 && FULL) atomicOr(&a.status->flags, bad);
   const int chunks = (int)((q.len + kL - 1) / kL), seg_chunks = is_whole ? chunks : a.seg_chunks;
-  const int segs = seg_chunks > 0 ? (chunks + seg_chunks - 1) / seg_chunks : 0;   // of this sequence
+  // segments of this sequence, none without tokens; beside whole pairs the last one takes what is left
+  int segs = seg_chunks > 0 ? (chunks + seg_chunks - 1) / seg_chunks : 0;
+  if (segs > a.nseg) segs = a.nseg;
   const bool last = seg == segs - 1;
   if (!q.run || seg >= segs || (!FULL && last)) {
     if (FULL && a.nseg > 1) wait_for_first();
@@ -894,7 +896,8 @@ cudaError_t launch(const SsmArgs& s, const PromptArgs& a, const PromptPlan& plan
     if (!first && plan.nseg > 1)
       return launch_second(kern, (unsigned int)(plan.whole + cut), kThreads, bytes, st, maps[0], maps[1], maps[2], maps[3],
                            maps[4], a);
-    kern<<<(unsigned int)(first ? cut : plan.whole + cut), kThreads, bytes, st>>>(maps[0], maps[1], maps[2], maps[3],
+    // a sequence's last segment has no first launch
+    kern<<<(unsigned int)(first ? cut / plan.nseg * (plan.nseg - 1) : plan.whole + cut), kThreads, bytes, st>>>(maps[0], maps[1], maps[2], maps[3],
                                                                                 maps[4], a);
     return cudaGetLastError();
   };
@@ -936,7 +939,8 @@ PromptPlan ssm_prompt_plan(long long n_seq, long long tokens, long long max_len,
   const auto uneven = [&](long long k, long long per) {
     const double n = (double)n_seq, segs = (double)tokens / (kL * per) - 0.5 * n;
     const double first = k == 1 ? 0.0 : std::max((double)(k - 1), std::min(n * (k - 1), segs)), second = n + first;
-    const double work2 = slices * (2.3 * ((double)tokens / kL + 0.5 * n) + kStart * second + kEmpty * (n * k - second)) / slots;
+    const double work2 =
+        slices * (2.3 * ((double)tokens / kL + 0.5 * n) + kStart * second + kEmpty * (n * k - second)) / slots;
     const double work1 = slices * (first * (1.2 * per + kStart) + kEmpty * (n * k - first)) / slots;
     const double longest = 2.3 * per + kStart + (k > 1 ? 0.7 * k : 0.0);
     return (second * slices <= slots ? longest : std::max(longest, work2 + 0.5 * longest)) +
@@ -953,19 +957,35 @@ PromptPlan ssm_prompt_plan(long long n_seq, long long tokens, long long max_len,
       p.seg_chunks = per;
       p.whole = 0;
     }
-    // or, of sequences of one length, only what the last wave of CTAs would have: its first launch and
-    // the whole ones share the SMs, and so do whole ones and segments.  (8 sequences of 4096 tokens, 64
-    // heads: 56 of 512 are left for a fourth wave; uncut 315 us, cut in 2 306, in 3 297, in 4 about 305.)
-    const long long tail = n_seq * slices % slots, full = n_seq * slices / slots;
-    if (tail == 0 || full == 0 || !even) continue;
-    const double part = full * (2.3 * chunks + kStart) +
-                        std::max(1.0, (double)(tail * k) / slots) * (2.3 * per + kStart + 0.7 * k) +
-                        (double)(tail * (k - 1)) / slots * (1.2 * per + kStart);
-    if (part < best) {
-      best = part;
-      p.nseg = (int)k;
-      p.seg_chunks = per;
-      p.whole = n_seq * slices - tail;
+  }
+  // Or, of sequences of one length, only what the last wave of CTAs would have.  The CTAs of its first
+  // launch delay as many SMs; the last segments, which have no first launch, are the longer ones and go
+  // to the other SMs.  (8 sequences of 4096 tokens, 64 heads: 56 of 512 are left for a fourth wave;
+  // uncut 315 us, in 3 equal segments 297, in 2 of 12 and 20 chunks 290.  3 of 2048 tokens: 85, 78, 68.)
+  const long long tail = n_seq * slices % slots, full = n_seq * slices / slots;
+  for (long long k = 2; even && tail > 0 && full > 0 && k * tail <= slots && k <= chunks && k <= 16; ++k) {
+    const long long rest = slots - (k - 1) * tail;
+    const auto delay = [&](long long per) { return 1.2 * per + kStart; };
+    const auto lasts = [&](long long per) {
+      return 2.3 * (chunks - (k - 1) * per) + kStart + 0.7 * k + (tail > rest ? delay(per) : 0.0);
+    };
+    const auto others = [&](long long per) {
+      return 2.3 * per + kStart + 0.7 * (k - 1) + (k * tail > rest ? delay(per) : 0.0);
+    };
+    long long lo = 1, hi = (chunks - 1) / (k - 1);   // the shortest segments that take as long as the last ones
+    while (lo < hi) {
+      const long long mid = (lo + hi) / 2;
+      if (others(mid) >= lasts(mid)) hi = mid;
+      else lo = mid + 1;
+    }
+    for (long long per = lo > 1 ? lo - 1 : lo; per <= lo; ++per) {
+      const double cost = full * (2.3 * chunks + kStart) + std::max(lasts(per), others(per));
+      if (cost < best) {
+        best = cost;
+        p.nseg = (int)k;
+        p.seg_chunks = per;
+        p.whole = n_seq * slices - tail;
+      }
     }
   }
   // The token-by-token form takes, measured: a launch and the states' traffic, then 0.2 us a token or

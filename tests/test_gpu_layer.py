@@ -204,6 +204,31 @@ def test_ssm_scan_with_strong_and_with_no_decay(vla, T, dtype):
     check_scan(vla, generator(T), [T, T], False, 4, 64, 1, 64, dtype, True, False, change=change)
 
 
+def test_ssm_scan_with_a_few_heads_more_than_a_wave(vla):
+    """160 heads on 152 SMs: the last 8 are cut into segments of their own lengths, the others are not."""
+    check_scan(vla, generator(61), [700], False, 160, 8, 1, 16, "bf16", True, False)
+    check_scan(vla, generator(62), [400, 400], False, 40, 128, 2, 64, "bf16", False, True)
+
+
+def test_ssm_scan_of_sequences_far_shorter_than_they_may_be(vla):
+    """Rows for two sequences of 700 tokens, 60 and 641 of them used: fewer segments than there is room for."""
+    gen = generator(63)
+    v = scan_inputs(gen, (1400,), 80, 8, 1, 16, torch.bfloat16, True, False)
+    off = torch.tensor([0, 60, 701], dtype=torch.int32, device="cuda")
+    state, y = rand(gen, 2, 80, 8, 16), torch.full_like(v["x"], 7.0)
+    before = f64(state)
+    vla.ssm_scan(**v, state=state, y=y, offsets=off, max_len=700)
+    for s, (a, b) in enumerate(((0, 60), (60, 701))):
+        cut = lambda k: f64(v[k][a:b])   # noqa: E731
+        yr, ya, hr, ha = ref.ssm_scan(cut("x"), cut("dt"), f64(v["A"]), cut("B"), cut("C"), before[s], f64(v["D"]),
+                                      cut("z"), f64(v["dt_bias"]))
+        c = (8 * (b - a) + 4 + 6 * 128 * -(-(b - a) // 128)) * U32   # as in check_scan
+        close(f64(state[s]), hr, c * ha + 1e-30, "state")
+        bound = (U16 + 2.0 ** -20 * (1 + np.abs(cut("z")))) * np.abs(yr) + (c + (16 + 8) * U32 + U16) * ya + 1e-30
+        close(f64(y[a:b]), yr, bound, "y")
+    assert (y[701:] == 7).all()
+
+
 def test_ssm_scan_without_options(vla):
     gen = generator(3)
     v = scan_inputs(gen, (2, 200), 2, 64, 1, 64, torch.bfloat16, False, False)
