@@ -9,7 +9,8 @@
 // for bfloat16 with a residual and e4m3): memory bound, with an instruction count close behind (so
 // values are taken in packed pairs and the warp's maximum is one integer reduction of their bits).
 // 16384 x 4096 of that kind: 81.4 us, 5.77 TB/s, 85 % of a plain copy's rate, warp issue 65 % busy.
-// 4099 x 1001 float32, whose rows start unaligned: 14 us (11 on the GPU), value by value.
+// Rows that start unaligned: 4099 x 1001 float32 12.3 us (9.3 on the GPU), 20000 x 3333 bfloat16 with
+// residual to e4m3 130 us, 3.6 TB/s.
 // v is taken as (r w) / sqrt(..): the largest |v| of a row is then the largest |r w| times the same
 // factor, and the sum and the maximum are reduced together, one barrier a row.  Blocks are persistent: w stays in registers
 // and the next row is loaded before the present one is reduced.  A row has `tpr` threads (whole
@@ -99,6 +100,17 @@ __device__ __forceinline__ void codes(const float (&v)[N], unsigned char* o) {
       asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(r) : "f"(v[0]));
       o[0] = (unsigned char)r;
     }
+  }
+}
+
+// Scale and factor of values r w whose largest magnitude is m: v / scale = r w (full / m), rstd cancels
+// and with it its error.
+__device__ __forceinline__ void norm_factors(float m, float rstd, float full, float& scale, float& f) {
+  scale = m * rstd / full;
+  f = full / m;
+  if (scale < 1.17549435e-38f) {   // false for a NaN
+    scale = 1.f;
+    f = rstd;
   }
 }
 
@@ -229,15 +241,7 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) rms_norm_kernel(const No
     const float full = OUT == VLA_OUT_E4M3 ? 448.f : 127.f;
     const int groups = (D + 127) / 128;
     float scale, f;
-    // v / scale = r w (full / max|r w|): rstd cancels, and with it its error
-    auto factors = [&](float m) {
-      scale = m * rstd / full;
-      f = full / m;
-      if (scale < 1.17549435e-38f) {   // false for a NaN
-        scale = 1.f;
-        f = rstd;
-      }
-    };
+    auto factors = [&](float m) { norm_factors(m, rstd, full, scale, f); };
     if (!a.group) factors(all);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -298,14 +302,200 @@ cudaError_t launch(const NormArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Rows off 16-byte boundaries, most of them (launch_odd): a row's group of warps copies it to shared memory, to
+// a place with the same offset from a 16-byte boundary, so that all but its ends moves in 16-byte
+// pieces; outputs leave the same way.  Blocks of 128 values belong to a warp each, 4 values a lane.  No row is
+// fetched ahead (that took a third more: the memory of a second row costs as many warps).
+constexpr int kOddThreads = 256;
+
+constexpr int kOddMost = 200 * 1024;   // bytes of shared memory
+__host__ __device__ constexpr long long odd_bytes(long long n, int size) { return (n * size + 16 + 15) / 16 * 16; }
+
+// n values at p, moved by threads t of nt: `head` single ones, `pieces` of 16 bytes, then the rest.
+template <typename V>
+struct Span {
+  static constexpr int E = 16 / (int)sizeof(V);
+  int head, pieces, rest;
+  __device__ __forceinline__ Span(const V* p, int n) {
+    head = (int)((16 - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) / (int)sizeof(V);
+    if (head > n) head = n;
+    pieces = (n - head) / E;
+    rest = head + pieces * E;   // where the rest begins
+  }
+};
+template <typename V>
+__device__ __forceinline__ V* odd_place(unsigned char* region, const V* p) {
+  return reinterpret_cast<V*>(region + (reinterpret_cast<uintptr_t>(p) & 15u));
+}
+template <typename V>
+__device__ __forceinline__ void odd_in(unsigned char* region, const V* p, int n, int t, int nt) {
+  const Span<V> s(p, n);
+  V* to = odd_place(region, p);
+  const uint32_t at = smem_u32(to + s.head);
+  for (int i = t; i < s.pieces; i += nt)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 16 * i), "l"(p + s.head + i * Span<V>::E) : "memory");
+  if (t < s.head) to[t] = p[t];
+  if (t < n - s.rest) to[s.rest + t] = p[s.rest + t];
+}
+template <typename V>
+__device__ __forceinline__ void odd_out(unsigned char* region, V* p, int n, int t, int nt) {
+  const Span<V> s(p, n);
+  const V* from = odd_place(region, p);
+  for (int i = t; i < s.pieces; i += nt)
+    *reinterpret_cast<uint4*>(p + s.head + i * Span<V>::E) = *reinterpret_cast<const uint4*>(from + s.head + i * Span<V>::E);
+  if (t < s.head) p[t] = from[t];
+  if (t < n - s.rest) p[s.rest + t] = from[s.rest + t];
+}
+
+template <typename T, int RES, int OUT>
+__global__ void __launch_bounds__(kOddThreads) rms_norm_odd_kernel(const NormArgs a, int warps, float inv_d) {
+  using R = typename std::conditional<RES == 1, __nv_bfloat16, float>::type;
+  using Y = typename std::conditional<OUT == VLA_OUT_IO, T, unsigned char>::type;
+  constexpr bool QUANT = OUT != VLA_OUT_IO;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float part_ss[kOddThreads / 32], part_top[kOddThreads / 32];
+  const int nt = warps * 32, grp = threadIdx.x / nt, t = threadIdx.x - grp * nt, lane = t & 31, gw = t >> 5;
+  const int D = (int)a.D, groups = (D + 127) / 128;
+  const long long x_bytes = odd_bytes(D, sizeof(T)), r_bytes = RES ? odd_bytes(D, sizeof(R)) : 0;
+  float* rw = reinterpret_cast<float*>(smem + grp * (x_bytes + r_bytes + odd_bytes(D, 4)));   // r w
+  unsigned char* xs = reinterpret_cast<unsigned char*>(rw) + odd_bytes(D, 4);   // x, later y
+  unsigned char* rs = xs + x_bytes;
+  auto sync = [&]() {
+    if (warps == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(grp + 1), "r"(nt) : "memory");
+  };
+  const int per = kOddThreads / nt;
+  const long long step = (long long)gridDim.x * per;
+  for (long long row = (long long)blockIdx.x * per + grp; row < a.rows; row += step) {
+    const T* x = static_cast<const T*>(a.x) + row * a.x_row;
+    R* res = static_cast<R*>(a.residual) + row * a.res_row;
+    Y* y = static_cast<Y*>(a.y) + row * a.y_row;
+    odd_in<T>(xs, x, D, t, nt);
+    if (RES) odd_in<R>(rs, res, D, t, nt);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    sync();
+    const T* xr = odd_place(xs, x);
+    R* rr = RES ? odd_place(rs, res) : nullptr;
+    float ss = 0.f, all = 0.f;
+    auto first = [&](int e) {
+      float r = to_f32<T>(xr[e]);
+      if (RES) {
+        r += to_f32<R>(rr[e]);
+        rr[e] = from_f32<R>(r);
+      }
+      ss = fmaf(r, r, ss);
+      r *= a.w[e];
+      rw[e] = r;
+      if (QUANT) all = max_nan(all, fabsf(r));
+    };
+    for (int b = gw; b < groups; b += warps) {
+      const int e = b * 128 + lane;
+      if ((b + 1) * 128 <= D) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) first(e + 32 * j);
+      } else {
+        for (int j = e; j < D; j += 32) first(j);
+      }
+    }
+    const bool row_top = QUANT && a.group == 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (row_top) all = warp_max(all);
+    if (warps > 1 && lane == 0) {
+      part_ss[grp * warps + gw] = ss;
+      part_top[grp * warps + gw] = all;
+    }
+    sync();   // the row's r and rw are there, x is done with
+    if (warps > 1) {
+      const float* ps = part_ss + grp * warps;
+      const float* pt = part_top + grp * warps;
+      ss = 0.f;
+      for (int i = 0; i < warps; ++i) {
+        ss += ps[i];
+        if (row_top) all = max_nan(all, pt[i]);
+      }
+    }
+    const float rstd = rsqrtf(fmaf(ss, inv_d, a.eps));
+    const float full = OUT == VLA_OUT_E4M3 ? 448.f : 127.f;
+    float scale, f = rstd;
+    auto factors = [&](float m) { norm_factors(m, rstd, full, scale, f); };
+    if (row_top) {
+      factors(all);
+      if (t == 0) a.scale[row] = scale;
+    }
+    Y* yr = odd_place(xs, y);
+    for (int b = gw; b < groups; b += warps) {
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = b * 128 + j * 32 + lane;
+        v[j] = e < D ? rw[e] : 0.f;
+      }
+      if (QUANT && a.group) {
+        factors(warp_max(max_nan(max_nan(fabsf(v[0]), fabsf(v[1])), max_nan(fabsf(v[2]), fabsf(v[3])))));
+        if (lane == 0) a.scale[row * groups + b] = scale;
+      }
+      const bool whole = (b + 1) * 128 <= D;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = b * 128 + j * 32 + lane;
+        const float one[1] = {v[j] * f};
+        if (!whole && e >= D) continue;
+        if constexpr (QUANT) codes<OUT, 1>(one, yr + e);
+        else yr[e] = from_f32<T>(one[0]);
+      }
+    }
+    sync();
+    odd_out<Y>(xs, y, D, t, nt);
+    if (RES) odd_out<R>(rs, res, D, t, nt);
+    sync();   // before the next row comes in
+  }
+}
+
 // Values a thread: few, so that many threads have a load in flight (16384 x 4096 bfloat16 with residual
 // and e4m3, before values were taken in pairs: 8 values 87 us, 16 values 94 us, 32 values 195 us).
 template <typename T, int RES, int OUT, int VEC>
 cudaError_t by_width(const NormArgs& a, cudaStream_t s) {
-  if (VEC > 1 && a.D <= 512LL * VEC) return launch<T, RES, OUT, VEC, VEC == 1 ? 2 : 1>(a, s);
-  if (a.D <= 1024LL * VEC) return launch<T, RES, OUT, VEC, 2>(a, s);
+  if constexpr (VEC > 1) {
+    if (a.D <= 512LL * VEC) return launch<T, RES, OUT, VEC, 1>(a, s);
+    if (a.D <= 1024LL * VEC) return launch<T, RES, OUT, VEC, 2>(a, s);
+  }
   if (a.D <= 4096LL * VEC) return launch<T, RES, OUT, VEC, 4>(a, s);
   return launch<T, RES, OUT, VEC, 32 / VEC>(a, s);   // up to 32768 values (the entry point's limit)
+}
+
+// Rows off 16-byte boundaries.  Value by value from global memory where that is quicker: few rows (a
+// shorter chain; 152 rows of 3333 bfloat16 to e4m3 3.9 us against 5.9, 608 rows 11.3 against 7.0; 608
+// rows of 1001 4.3 against 6.5), or narrow ones and float32 without a residual (100000 x 65 float32 19 us
+// against 33, 40990 x 1001 77 against 83, 50000 x 255 bfloat16 23.7 against 25).  Else through shared
+// memory (20000 x 3333 bfloat16 with residual to e4m3 130 us against 424, 40000 x 1001 82 against 197,
+// 20000 x 1001 float32 with residual 79 against 98), where a row fits there.
+template <typename T, int RES, int OUT>
+cudaError_t launch_odd(const NormArgs& a, cudaStream_t s) {
+  const bool few = a.D <= 4096 && a.rows <= 4096LL * a.sm_count / a.D;
+  if (few || (RES == 0 && a.D <= (sizeof(T) == 4 ? 2048 : 256))) return by_width<T, RES, OUT, 1>(a, s);
+  const int warps = a.D <= 1024 ? 1 : a.D <= 2048 ? 2 : a.D <= 4096 ? 4 : 8, per = kOddThreads / 32 / warps;
+  const long long bytes =
+      per * (odd_bytes(a.D, sizeof(T)) + (RES ? odd_bytes(a.D, RES == 1 ? 2 : 4) : 0) + odd_bytes(a.D, 4));
+  if (bytes > kOddMost) return by_width<T, RES, OUT, 1>(a, s);
+  auto kern = rms_norm_odd_kernel<T, RES, OUT>;
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kOddMost);
+    if (e != cudaSuccess) return e;
+  }
+  // blocks an SM for these bytes: asked for once, packed as bytes | blocks
+  static std::atomic<unsigned int> known{0};
+  unsigned int k = known.load(std::memory_order_relaxed);
+  if (k >> 8 != (unsigned int)bytes) {
+    int blocks = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kern, kOddThreads, (size_t)bytes);
+    if (e != cudaSuccess) return e;
+    k = (unsigned int)bytes << 8 | (unsigned int)blocks;
+    known.store(k, std::memory_order_relaxed);
+  }
+  const long long all = (a.rows + per - 1) / per, most = (long long)((k & 0xffu) ? k & 0xffu : 1) * a.sm_count;
+  kern<<<(unsigned int)(all < most ? all : most), kOddThreads, (size_t)bytes, s>>>(a, warps, 1.f / (float)a.D);
+  return cudaGetLastError();
 }
 
 template <typename T, int RES, int OUT>
@@ -319,7 +509,7 @@ cudaError_t by_alignment(const NormArgs& a, cudaStream_t s) {
     const size_t need = VEC * res > 16 ? 16 : VEC * res;
     ok = ok && (reinterpret_cast<uintptr_t>(a.residual) | (unsigned long long)a.res_row * res) % need == 0;
   }
-  return ok ? by_width<T, RES, OUT, VEC>(a, s) : by_width<T, RES, OUT, 1>(a, s);
+  return ok ? by_width<T, RES, OUT, VEC>(a, s) : launch_odd<T, RES, OUT>(a, s);
 }
 
 template <typename T, int RES>

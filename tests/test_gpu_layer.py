@@ -342,6 +342,16 @@ NORM = [  # rows, D, dtype, residual, out, group
     (2, 32768, "f32", None, "e4m3", 0),
     (2, 32768, "bf16", "f32", "io", 0),
     (9, 40, "bf16", None, "int8", 0),
+    # rows off 16-byte boundaries, many or wide: through shared memory, by 1, 2, 4 and 8 warps a row
+    (700, 1001, "bf16", "bf16", "e4m3", 0),
+    (640, 1003, "bf16", "f32", "int8", 128),
+    (2600, 257, "bf16", None, "io", 0),
+    (333, 2003, "f32", "f32", "io", 0),
+    (333, 2003, "bf16", "bf16", "int8", 128),
+    (401, 2047, "f32", "bf16", "e4m3", 0),
+    (3, 7195, "bf16", "bf16", "io", 0),
+    (4, 4099, "f32", None, "e4m3", 128),
+    (5, 20001, "f32", "f32", "int8", 128),
 ]
 
 
@@ -373,6 +383,20 @@ def test_rms_norm_matches_the_reference(vla, rows, D, dtype, res, out, group):
     # half a step: of an integer, or of an e4m3 with 3 bits after the point (2^-4 relative, 2^-10 least)
     step = 0.5 * wide if out == "int8" else np.maximum(np.abs(vr) * 2.0 ** -4, wide * 2.0 ** -10)
     close(q * wide, vr, step * (1 + 1e-3) + (c + 4 * U32) * np.abs(vr) + 1e-30, "codes * scale")
+
+
+@pytest.mark.parametrize("rows,D,dtype", [(700, 1001, "bf16"), (3, 7195, "bf16"), (400, 2003, "f32"), (3, 1001, "bf16")])
+def test_rms_norm_leaves_what_lies_between_rows(vla, rows, D, dtype):
+    """x, residual and y at offsets of their own in wider rows: the same values, and nothing beside them changes."""
+    gen = generator(rows)
+    x, w, r = rand(gen, rows, D, dtype=TYPES[dtype]), rand(gen, D), rand(gen, rows, D)
+    r2, y2 = torch.full((rows, D + 9), 7.0, device="cuda"), torch.full((rows, D + 6), 7.0, device="cuda", dtype=x.dtype)
+    x2 = torch.full((rows, D + 4), float("nan"), device="cuda", dtype=x.dtype)
+    r2[:, 5:D + 5], x2[:, 3:D + 3] = r, x
+    y = vla.rms_norm(x, w, r)
+    vla.rms_norm(x2[:, 3:D + 3], w, r2[:, 5:D + 5], y=y2[:, 1:D + 1])
+    assert torch.equal(y2[:, 1:D + 1], y) and torch.equal(r2[:, 5:D + 5], r)
+    assert (r2[:, :5] == 7).all() and (r2[:, D + 5:] == 7).all() and (y2[:, :1] == 7).all() and (y2[:, D + 1:] == 7).all()
 
 
 def test_rms_norm_of_zeros_and_of_nan(vla):
