@@ -11,14 +11,16 @@
 // Precision.  The state is float32 and lives in the registers of its threads for the whole run.
 // B and x are exact in bfloat16; X~ is carried as three bfloat16 terms (24 bits), so the state is
 // as exact as a float32 scan's.  M and the copy of h that multiplies C are each rounded to bfloat16
-// once (2^-9 relative, as the output itself is).  The suffix sums c_L - c_s are summed from
-// the end, so that what is left of the last tokens does not suffer from a large c_L.
+// once (2^-9 relative, as the output itself is).  No decay is a difference of sums from the chunk's
+// start: after a token that decays by e^-10^5 both would be large and keep few bits of what came since.
+// c_L - c_s is summed from the end, c_t - c_s from the tokens and blocks strictly between.
 //
 // exp(c_t - c_s) takes no exponential a pair: with e_j the sum at the end of block j of 32 tokens s,
-// exp(c_t - e_j) exp(e_j - c_s) is one factor a row and one a column, both at most 1, for the rows
-// behind the block.  In a diagonal block e_j is the sum before the block; the column's factor is
-// then at least 1, so this holds while the block's sums stay below 2^100, and beyond that (nothing
-// is left of a token a few tokens later) the exponentials are taken pair by pair.
+// exp(c_t - e_j) exp(e_j - c_s) is one factor a row (its sum within its own block, and the blocks
+// between) and one a column, both at most 1, for the rows behind the block.  In a diagonal block both
+// factors are of the sums from the block's start; the column's is then at least 1, so this holds while
+// the block's sums stay below 2^100, and beyond that (nothing is left of a token a few tokens later)
+// the exponentials are taken pair by pair, of a running sum from the row's token back.
 //
 // Roles (24 warps, one CTA an SM; they meet on mbarriers and every operand has two places, so the two
 // sides of a chunk run side by side and ahead of each other):
@@ -279,9 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
-  // decays of chunk i at vec + (i mod 4) kVec: cum [128] log2 decay from the chunk's start up to a token;
-  // wcol [128] s exp(e_j - c), j the token's block; wdg [128] the same with the sum before the
-  // block; wx [128] s exp(c_L - c); step [128] s; then [4] sums before the blocks, [4] to their ends,
+  // decays of chunk i at vec + (i mod 4) kVec: inc [128] log2 decay from the block's start up to a token;
+  // wcol [128] s exp(e_j - c), j the token's block; wdg [128] s exp(-inc), or where that does not hold the
+  // token's own log2 decay; wx [128] s exp(c_L - c); step [128] s; then [4] sums before the blocks,
   // [8] the total, [12..16) the blocks' own sums, [16..20) whether wdg holds
   float* vec = reinterpret_cast<float*>(smem + Cf::oVec);
   uint64_t* bar = reinterpret_cast<uint64_t*>(vec + kDec * kVec);
@@ -458,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i < n_chunks) {
           if (!wait(kFullDec + i % kDec, i / kDec) || !wait(kFullS + r, u)) break;
           tc::fence_after_sync();
-          const float my_cum = v[row];
-          row_decay = ex2(my_cum);
+          const float my_inc = v[row], *sums = v + 5 * kL;
+          row_decay = ex2(sums[qd] + my_inc);
           // M from S in place: blocks 2 half and 2 half + 1 of s end up at S's columns 64 half + 0 and + 16
           const uint32_t ts = tlane + kColS + 128 * r + 64 * half;
 #pragma unroll 1
@@ -473,8 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               float s[32];
               tc::tmem_ld32(ts + 32 * g, s);
               const bool diag = j == qd;
-              if (!diag || v[5 * kL + 16 + j] != 0.f) {
-                const float f = ex2(my_cum - v[5 * kL + (diag ? 0 : 4) + j]);
+              if (!diag || sums[16 + j] != 0.f) {
+                // the blocks strictly between: at most two
+                const float f = ex2(my_inc + ((j + 1 < qd ? sums[13 + j] : 0.f) + (j + 2 < qd ? sums[14 + j] : 0.f)));
                 const float* wv = v + (diag ? 2 : 1) * kL + 32 * j;
                 const uint64_t f2 = pair(f, f);
 #pragma unroll
@@ -492,11 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               } else {
                 const float* cv = v + 32 * j;
+                float back = 0.f;   // the tokens behind column k, up to the row's own
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const float e = 2 * k <= lane ? s[2 * k] * ex2(my_cum - cv[2 * k]) * cv[4 * kL + 2 * k] : 0.f;
-                  const float f = 2 * k + 1 <= lane ? s[2 * k + 1] * ex2(my_cum - cv[2 * k + 1]) * cv[4 * kL + 2 * k + 1] : 0.f;
-                  m[k] = pack2(e, f);
+                for (int k = 31; k >= 0; --k) {
+                  const bool in = k <= lane;
+                  s[k] = in ? s[k] * (ex2(back) * cv[4 * kL + k]) : 0.f;
+                  if (in) back += cv[2 * kL + k];
+                  if ((k & 1) == 0) m[k / 2] = pack2(s[k], s[k + 1]);
                 }
               }
             }
@@ -794,7 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float s = in ? time_step(raw, bias, a.softplus) : 0.f;
       t += kL;
       if (t < q.len && i < last_i) raw = __bfloat162float(dt[t * a.dt_tok]);
-      float inc = in ? A2 * s : 0.f, ex = inc;
+      const float own = in ? A2 * s : 0.f;
+      float inc = own, ex = own;
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const float up = __shfl_up_sync(0xffffffffu, inc, o), down = __shfl_down_sync(0xffffffffu, ex, o);
@@ -818,14 +824,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (k > j) behind += e;
       }
       v += 32 * j + lane;
-      v[0] = before + inc;
+      v[0] = inc;
       v[kL] = s * ex2(ex);
-      v[2 * kL] = s * ex2(-inc);
+      v[2 * kL] = small ? s * ex2(-inc) : own;
       v[3 * kL] = s * ex2(ex + behind);
       v[4 * kL] = s;
       if (lane == 31) {
         sums[j] = before;
-        sums[4 + j] = before + inc;
         sums[16 + j] = small ? 1.f : 0.f;
         if (j == 3) sums[8] = before + inc;
       }
