@@ -19,8 +19,8 @@
 // exp(c_t - e_j) exp(e_j - c_s) is one factor a row (its sum within its own block, and the blocks
 // between) and one a column, both at most 1, for the rows behind the block.  In a diagonal block both
 // factors are of the sums from the block's start; the column's is then at least 1, so this holds while
-// the block's sums stay below 2^100, and beyond that (nothing is left of a token a few tokens later)
-// the exponentials are taken pair by pair, of a running sum from the row's token back.
+// the block's sums stay below 2^100 and its steps below 2^26, and beyond that (nothing is left of a token
+// a few tokens later) the exponentials are taken pair by pair, of a running sum from the row's token back.
 //
 // Roles (24 warps, one CTA an SM; they meet on mbarriers and every operand has two places, so the two
 // sides of a chunk run side by side and ahead of each other):
@@ -484,8 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 32; k += 4) {
                   const float4 w = *reinterpret_cast<const float4*>(wv + k);
                   float e0, e1, e2, e3;
-                  unpair(mul2(mul2(pair(s[k], s[k + 1]), pair(w.x, w.y)), f2), e0, e1);
-                  unpair(mul2(mul2(pair(s[k + 2], s[k + 3]), pair(w.z, w.w)), f2), e2, e3);
+                  // the factors first: one may be near 2^127, their product is at most the step
+                  unpair(mul2(pair(s[k], s[k + 1]), mul2(pair(w.x, w.y), f2)), e0, e1);
+                  unpair(mul2(pair(s[k + 2], s[k + 3]), mul2(pair(w.z, w.w), f2)), e2, e3);
                   m[k / 2] = pack2(e0, e1);
                   m[k / 2 + 1] = pack2(e2, e3);
                 }
@@ -809,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ex = __shfl_down_sync(0xffffffffu, ex, 1);
       if (lane == 31) ex = 0.f;
-      const bool small = __all_sync(0xffffffffu, fabsf(inc) < 100.f);
+      const bool small = __all_sync(0xffffffffu, fabsf(inc) < 100.f && s < 1e8f);   // s exp(-inc) is finite
       float* v = vec + (i % kDec) * kVec;
       float* sums = v + 5 * kL;
       // the four warps leave together: each reads the others' sums

@@ -42,3 +42,16 @@ def test_ssm_scan_after_tokens_that_reset_the_state(vla, lens, packed, N, A, sma
             v["dt"][t if packed else (slice(None), t)] = large
             v["x"][t if packed else (slice(None), t)] = 0
     check_scan(vla, generator(N + len(at)), lens, packed, 2, 64, 1, N, "bf16", False, False, change=change)
+
+
+def test_ssm_scan_of_large_values_under_strong_decay(vla):  # noqa: F811
+    """Products C B^T of 1e12 and blocks of 32 tokens that decay by 2^92: every factor's inverse is near the end
+    of float32's range, the outputs are not."""
+    def change(v):
+        v["B"] *= 1e6
+        v["C"] *= 1e6
+        for head in range(2):
+            v["A"][head] = -16.0
+            set_step(v, head, 0.125)
+    for lens, N in (([200], 128), ([140, 140], 64)):
+        check_scan(vla, generator(N), lens, False, 2, 64, 1, N, "bf16", True, False, change=change)
