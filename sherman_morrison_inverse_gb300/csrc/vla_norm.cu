@@ -8,7 +8,7 @@
 // the rounding, so x and the residual are read once and every output written once (7 bytes a value
 // for bfloat16 with a residual and e4m3): memory bound, with an instruction count close behind (so
 // values are taken in packed pairs and the warp's maximum is one integer reduction of their bits).
-// 16384 x 4096 of that kind: 81.4 us, 5.77 TB/s, 85 % of a plain copy's rate, warp issue 65 % busy.
+// 16384 x 4096 of that kind: 82.3 us, 5.71 TB/s, 84 % of a plain copy's rate, warp issue 65 % busy.
 // Rows that start unaligned: 4099 x 1001 float32 12.3 us (9.3 on the GPU), 20000 x 3333 bfloat16 with
 // residual to e4m3 130 us, 3.6 TB/s.
 // v is taken as (r w) / sqrt(..): the largest |v| of a row is then the largest |r w| times the same
@@ -103,8 +103,11 @@ __device__ __forceinline__ void codes(const float (&v)[N], unsigned char* o) {
   }
 }
 
-// Scale and factor of values r w whose largest magnitude is m: v / scale = r w (full / m), rstd cancels
-// and with it its error.
+// Scale and factors of values r w whose largest magnitude is m: v / scale = r w (full / m), rstd cancels
+// and with it its error.  full / m passes float32's range for m below 2^-119, where the scale can still be
+// a normal number (rstd is 1000 for a row of such values with eps 1e-6): where f is infinite, r w and m
+// are first multiplied by kLift (the branch for it: 81.4 -> 82.3 us at 16384 x 4096).
+constexpr float kLift = 0x1p100f;
 __device__ __forceinline__ void norm_factors(float m, float rstd, float full, float& scale, float& f) {
   scale = m * rstd / full;
   f = full / m;
@@ -257,7 +260,13 @@ __global__ void __launch_bounds__(NV <= 2 ? 512 : 1024) rms_norm_kernel(const No
       }
       const int e = (i * tpr + tid) * VEC;
       if (!live || e >= D) continue;
-      const uint64_t f2 = pair(f, f);
+      float fi = f;
+      if (fi == INFINITY) {
+        fi = full / ((a.group ? top[i] : all) * kLift);
+#pragma unroll
+        for (int j = 0; j < PAIRS; ++j) r[i][j] = mul2(r[i][j], pair(kLift, kLift));
+      }
+      const uint64_t f2 = pair(fi, fi);
       float v[2 * PAIRS];
 #pragma unroll
       for (int j = 0; j < PAIRS; ++j) unpair(mul2(r[i][j], f2), v[2 * j], v[2 * j + 1]);
@@ -417,8 +426,12 @@ __global__ void __launch_bounds__(kOddThreads) rms_norm_odd_kernel(const NormArg
     }
     const float rstd = rsqrtf(fmaf(ss, inv_d, a.eps));
     const float full = OUT == VLA_OUT_E4M3 ? 448.f : 127.f;
-    float scale, f = rstd;
-    auto factors = [&](float m) { norm_factors(m, rstd, full, scale, f); };
+    float scale, f = rstd, lift = 1.f;
+    auto factors = [&](float m) {
+      norm_factors(m, rstd, full, scale, f);
+      lift = f == INFINITY ? kLift : 1.f;
+      if (f == INFINITY) f = full / (m * kLift);
+    };
     if (row_top) {
       factors(all);
       if (t == 0) a.scale[row] = scale;
@@ -439,7 +452,7 @@ __global__ void __launch_bounds__(kOddThreads) rms_norm_odd_kernel(const NormArg
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int e = b * 128 + j * 32 + lane;
-        const float one[1] = {v[j] * f};
+        const float one[1] = {v[j] * lift * f};
         if (!whole && e >= D) continue;
         if constexpr (QUANT) codes<OUT, 1>(one, yr + e);
         else yr[e] = from_f32<T>(one[0]);

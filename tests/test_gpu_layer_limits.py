@@ -2,9 +2,12 @@
 float64 references and the bounds of test_gpu_layer.py."""
 import math
 
+import numpy as np
 import pytest
+import torch
 
-from test_gpu_layer import check_scan, generator, vla  # noqa: F401
+from oracle import layer_ref as ref
+from test_gpu_layer import TYPES, U32, check_scan, close, f64, generator, vla  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +58,34 @@ def test_ssm_scan_of_large_values_under_strong_decay(vla):  # noqa: F811
             set_step(v, head, 0.125)
     for lens, N in (([200], 128), ([140, 140], 64)):
         check_scan(vla, generator(N), lens, False, 2, 64, 1, N, "bf16", True, False, change=change)
+
+
+# ---------------------------------------------------------------------------------------------
+# norm: tiny rows
+
+@pytest.mark.parametrize("out,group", [("e4m3", 0), ("e4m3", 128), ("int8", 0), ("int8", 128)])
+@pytest.mark.parametrize("dtype,rows,D", [("f32", 6, 256), ("bf16", 6, 384), ("f32", 6, 255), ("bf16", 900, 1003), ("f32", 900, 2203)])
+def test_rms_norm_codes_of_tiny_rows(vla, dtype, rows, D, out, group):  # noqa: F811
+    """Rows near the least normal float32 (1.2e-38), with zeros and both signs: 1 / sqrt(eps) carries them to
+    ordinary scales, and their codes are those of larger rows.  Rows with aligned and with odd starts."""
+    gen = generator(rows + D)
+    size = torch.tensor([2e-38, 1e-37, 1e-36, 3e-36, 1e-35, 1.0], device="cuda").repeat(rows // 6)
+    x = 2 * torch.rand(rows, D, generator=gen, device="cuda") - 1
+    x[:, 0::128] = 1   # the largest of every 128
+    x[:, 1::128] = -1
+    x[:, 5::7] = 0
+    x = (x * size[:, None]).to(TYPES[dtype])
+    w = torch.ones(D, device="cuda")
+    codes, scale = vla.rms_norm(x, w, eps=1e-6, out=out, group=group)
+    vr, _ = ref.rms_norm(f64(x), f64(w), np.zeros((rows, D)), 1e-6)
+    top = 448.0 if out == "e4m3" else 127.0
+    sr = ref.scales(vr, top, group)
+    scale, q = f64(scale).reshape(rows, -1), f64(codes)
+    c = (D / 2 + 8) * U32
+    # a product below the normal range is off by 2^-150, of at least 1e-38
+    close(scale, sr, (c + 2 * U32 + 2.0 ** -150 / 1e-38) * sr, "scale")
+    assert np.isfinite(q).all() and np.abs(q).max() <= top
+    want = vr / np.repeat(sr, group or D, 1)[:, :D]
+    step = 0.5 if out == "int8" else np.maximum(np.abs(want) * 2.0 ** -4, 2.0 ** -10)
+    close(q, want, step * (1 + 1e-3) + (2 * c + 6 * U32) * np.abs(want) + top * 2.0 ** -150 / 1e-38, "codes")
+    assert (q[f64(x) == 0] == 0).all()
