@@ -373,6 +373,8 @@ vla_err_t vla_short_conv(vla_handle_t h, const void* x, const float* w, const fl
  *   strides   host array {x, dt, B, C, z, y} x {sequence, token}.
  *   workspace device memory of vla_ssm_workspace bytes, 16-byte aligned, that nothing
  *             else uses until the call's work is done; NULL where that is 0.
+ * A NaN or infinity in x reaches its own row of the state and that row's outputs, from its token on:
+ * there they are NaN or infinite (in the chunked form NaN).  It reaches nothing earlier and no other row.
  * State and sums are float32.  Errors (before any launch): as for vla_short_conv;
  * INVALID_ARG also for H no multiple of G, a misaligned state, a workspace that is
  * too small; UNSUPPORTED for N > 256. */

@@ -33,6 +33,11 @@
 // In order: S of the next chunk is formed while M of this one is, M of the next one while M X of
 // this one runs.  The longest chain is X~, U, h, X~ ..: so U comes before S, and h's copy is written
 // after the next X~.
+// A NaN or infinity of x must not meet the zeros above M's diagonal: it would reach earlier tokens.  The
+// warp that issues M X looks the tile over while M is formed; what is not finite it takes out, once the state's
+// warps have read it, and notes its column and token: from there on the column's outputs are NaN (so is its
+// row of the state, where the recurrence may have infinities).  8 x 4096 tokens of 64 heads: 289.3 -> 291.2 us;
+// by the output's warps, on their way to D x, 297.7; by the warp that stores y 300.
 // All of this code runs once a chunk: what does not fit the instruction caches is fetched again
 // every time (written out, 122 KB of it took three times as long), so loops stay rolled, a body
 // takes 16 columns, and a wait that does not succeed at once goes through one shared function.
@@ -79,6 +84,7 @@ constexpr uint32_t kColS = 0, kColY = 256, kColU = 384;
 constexpr int kVec = 5 * kL + 24;  // floats of a chunk's decays
 constexpr int kDec = 4;            // chunks of decays
 constexpr int kUnits = 16;         // pieces of 32 tokens and 16 columns of X~
+constexpr int kOdd = 65;           // words about X's values that are not finite
 
 // mbarriers (where there are two or more, chunk i uses i mod their number)
 enum : int {
@@ -102,16 +108,20 @@ enum : int {
   kStage = 32,     //     y is staged
   kStaged = 33,    //     and its store has read it
   kFullZ = 34,     //     z has landed where y will be staged
-  kBars = 35
+  kReadX = 35,     // [2] X~ has read X
+  kBars = 37
 };
 
-// Shared memory: B [2] | C | X [2] | X~ (three terms) | state (bfloat16, [n][64 p]) | y | decays | barriers
+// Shared memory: B [2] | C | X [2] | X~ (three terms) | state (bfloat16, [n][64 p]) | y | decays | barriers,
+// two words | for each place of X: its columns' first tokens with a value that is not finite [64], and the
+// chunk that has any
 template <int NN>
 struct Cfg {
   static constexpr uint32_t NT = NN / 64;
   static constexpr uint32_t oB = 0, oC = 2 * NT * kTile, oX = oC + NT * kTile, oT = oX + 2 * kTile;
   static constexpr uint32_t oH = oT + 3 * kTile, oY = oH + NN * 128, oVec = oY + kTile;
-  static constexpr uint32_t bytes = oVec + 4 * kDec * kVec + 8 * kBars + 16;
+  static constexpr uint32_t oOdd = oVec + 4 * kDec * kVec + 8 * kBars + 8;
+  static constexpr uint32_t bytes = oOdd + 2 * 4 * kOdd;
 };
 
 // Matrix descriptor of a 128-byte-swizzled operand: `lbo` bytes between blocks of 64 in the
@@ -173,6 +183,31 @@ __device__ __noinline__ bool wait_on(uint64_t* b, uint32_t parity, volatile int*
     }
   }
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// a 0 + b for pairs of bfloat16
+__device__ __forceinline__ uint32_t times_zero(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(0u), "r"(b));
+  return r;
+}
+// Takes what is not finite out of 8 bfloat16 values of X and notes it in their columns' words.  A word is
+// (chunk + 1) 128 + 127 - row, so that the largest is the first row of the latest chunk.
+__device__ __noinline__ void take_out(unsigned char* at, uint32_t* word, uint32_t value) {
+  unsigned short* v = reinterpret_cast<unsigned short*>(at);
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c)
+    if ((v[c] & 0x7f80) == 0x7f80) {
+      v[c] = 0;
+      atomicMax(word + c, value);
+    }
+}
+
+// NaN for those of 8 bfloat16 outputs whose columns had such a value at this row (`value`) or before.
+__device__ __noinline__ void put_nan(void* at, const volatile uint32_t* word, uint32_t value) {
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c)
+    if (word[c] >= value) static_cast<unsigned short*>(at)[c] = 0x7fff;
 }
 
 // Named barrier over n threads that also ORs a flag across them.
@@ -306,11 +341,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i >= kFullDec && i < kFullDec + kDec) count = 4;
       if (i == kM || i == kH || i == kEmptyY || i == kEmptyY + 1 || i == kStage) count = W;
       if (i == kXt) count = FULL ? W : 2 * W;
+      if (i == kReadX || i == kReadX + 1) count = W;
       mbar_init(bar + i, count);
     }
     *fail = 0;
     fence_mbar_init();
   }
+  uint32_t* odd = reinterpret_cast<uint32_t*>(smem + Cf::oOdd);
+  if (tid < 2 * kOdd) odd[tid] = 0;
   if (warp == 1) tc::tmem_alloc(tslot, kCols);
   if (warp == 18 && lane < 4) prefetch_map(lane == 0 ? &map_B : lane == 1 ? &map_x : lane == 2 ? &map_C : &map_y);
 
@@ -445,6 +483,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else if (in && c < pc) {
               *reinterpret_cast<uint4*>(a.y + (q.start + t) * a.y_tok + (long long)head * a.P + p0 + 32 * half + c) = o;
             }
+          }
+        }
+        const uint32_t* word = odd + (i & 1) * kOdd;
+        if (*reinterpret_cast<const volatile uint32_t*>(word + 64) == (uint32_t)i + 1) {
+#pragma unroll 1
+          for (int c = 0; c < 32; c += 8) {
+            void* at = smem + Cf::oY + row_at + (((uint32_t)(4 * half + (c >> 3)) ^ rsw) << 4);
+            if (tail) {
+              if (!in || c >= pc) continue;
+              at = a.y + (q.start + t) * a.y_tok + (long long)head * a.P + p0 + 32 * half + c;
+            }
+            put_nan(at, word + 32 * half + c, ((uint32_t)i + 1) * kL + (kL - 1 - row));
           }
         }
         fence_proxy_async_smem();
@@ -639,6 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (one) {
         arrive_one(kEmptyX + r);
+        if (FULL) arrive_one(kReadX + r);
         arrive_one(kEmptyDec + i % kDec);
       }
       // the copy of the state before this chunk, once the one before it has been read
@@ -682,7 +733,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::mma_commit(bar + kEmptyC);
         }
         __syncwarp();
-        if (!wait(kM, i) || !wait(kFullX + r, u)) break;
+        if (!wait(kFullX + r, u)) break;
+        const unsigned char* xt = smem + Cf::oX + r * kTile + 16 * lane;
+        uint32_t zero = 0, zero2 = 0;   // NaN once a value is not finite
+#pragma unroll 8
+        for (uint32_t k = 0; k < 32; ++k) {
+          const uint4 x = *reinterpret_cast<const uint4*>(xt + 512 * k);
+          zero = times_zero(x.x, times_zero(x.y, zero));
+          zero2 = times_zero(x.z, times_zero(x.w, zero2));
+        }
+        if (__any_sync(0xffffffffu, ((zero | zero2) & 0x7fff7fffu) != 0)) {
+          if (!wait(kReadX + r, u)) break;
+          uint32_t* word = odd + r * kOdd;
+#pragma unroll 1
+          for (uint32_t k = 0; k < 32; ++k) {
+            const uint32_t token = 4 * k + (uint32_t)lane / 8;
+            if (ragged && i == last_i && i * kL + token >= left) continue;   // the next sequence's
+            take_out(smem + Cf::oX + r * kTile + 512 * k + 16 * lane, word + 8 * ((lane ^ token) & 7),
+                     ((uint32_t)i + 1) * kL + (kL - 1 - token));
+          }
+          word[64] = (uint32_t)i + 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!wait(kM, i)) break;
         tc::fence_after_sync();
 #pragma unroll 4
         for (int k = 0; k < kL / 16; ++k)

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from oracle import layer_ref as ref
-from test_gpu_layer import TYPES, U32, check_scan, close, f64, generator, vla  # noqa: F401
+from test_gpu_layer import TYPES, U16, U32, check_scan, close, f64, generator, rand, scan_inputs, vla  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,61 @@ def test_rms_norm_codes_of_tiny_rows(vla, dtype, rows, D, out, group):  # noqa: 
     step = 0.5 if out == "int8" else np.maximum(np.abs(want) * 2.0 ** -4, 2.0 ** -10)
     close(q, want, step * (1 + 1e-3) + (2 * c + 6 * U32) * np.abs(want) + top * 2.0 ** -150 / 1e-38, "codes")
     assert (q[f64(x) == 0] == 0).all()
+
+
+# ---------------------------------------------------------------------------------------------
+# scan: NaN and infinity
+
+CAUSAL = [  # lens, packed, dtype, H, P, N, gate
+    ([300], False, "bf16", 2, 64, 128, False),
+    ([300, 300], False, "bf16", 2, 72, 64, True),
+    ([200, 333, 20], True, "bf16", 2, 128, 64, True),
+    ([3000], False, "bf16", 2, 64, 64, False),
+    ([20], False, "bf16", 2, 64, 64, True),
+    ([300], False, "f32", 2, 64, 64, False),
+]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("lens,packed,dtype,H,P,N,gate", CAUSAL)
+def test_nan_and_infinity_reach_no_earlier_token_and_no_other_row(vla, lens, packed, dtype, H, P, N, gate, bad):  # noqa: F811
+    """x of one row p not finite at some tokens: its outputs are not finite from the first of them on, all
+    other outputs and states are what they are without."""
+    gen = generator(P + N)
+    lead = (sum(lens),) if packed else (len(lens), lens[0])
+    off = torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32, device="cuda") if packed else None
+    v = scan_inputs(gen, lead, H, P, 1, N, TYPES[dtype], gate, False)
+    starts = list(np.cumsum([0, *lens[:-1]]))
+    s0 = rand(gen, len(lens), H, P, N)
+    s1 = s0.clone()
+    want = vla.ssm_scan(**v, state=s0, offsets=off).flatten(0, -3)
+    hit = torch.zeros_like(want, dtype=torch.bool)        # outputs that may not be finite
+    rows = torch.zeros(len(lens), H, P, dtype=torch.bool, device="cuda")
+    x = v["x"].flatten(0, -3)
+    assert x.data_ptr() == v["x"].data_ptr()
+    for s, (at, n) in enumerate(zip(starts, lens)):
+        if s == 1:
+            continue   # a sequence that stays clean
+        for head, p, tokens in ((0, 3, (n - 2, n // 2, n // 2 + 1)), (1, P - 1, (n - 1,)), (1, 33, (min(127, n - 1),)),
+                                (0, 17, (0, n // 3))):
+            for t in tokens:
+                x[at + t, head, p] = bad
+            hit[at + min(tokens):at + n, head, p] = True
+            rows[s, head, p] = True
+    got = vla.ssm_scan(**v, state=s1, offsets=off).flatten(0, -3)
+    assert torch.equal(got[~hit], want[~hit]) and not got[hit].isfinite().any()
+    assert torch.equal(s1[~rows], s0[~rows]) and not s1[rows].isfinite().any()
+
+
+@pytest.mark.parametrize("name", ["dt", "B", "C", "z"])
+@pytest.mark.parametrize("T,dtype", [(300, "bf16"), (20, "bf16"), (300, "f32")])
+def test_other_operands_that_are_nan_reach_no_earlier_token(vla, name, T, dtype):  # noqa: F811
+    gen = generator(T)
+    v = scan_inputs(gen, (1, T), 2, 64, 1, 64, TYPES[dtype], True, False)
+    t0 = T // 2 - 3
+    want = vla.ssm_scan(**v)[0, :t0].double()
+    v[name][:, t0] = float("nan")
+    got = vla.ssm_scan(**v)[0]
+    assert got[t0].isnan().all()
+    # a block of tokens with a NaN step takes its exponentials pair by pair: bfloat16 factors may round otherwise
+    assert (got[:t0].double() - want).norm() <= 2 * U16 * want.norm()
