@@ -13,6 +13,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -78,7 +79,10 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, LIB)
-    build_binding()
+    try:
+        build_binding()
+    except RuntimeError as e:   # no C compiler or no Python headers: the layer's operators raise when called
+        warnings.warn(f"the layer operators' binding was not built, the rest of the library was: {e}", stacklevel=2)
     return LIB
 
 

@@ -1,0 +1,59 @@
+"""The layer operators' argument checks in C: what the library does without them, and with a module that
+is stale or of another interpreter."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from _util import ROOT, ensure_built
+from sherman_morrison_inverse_gb300 import build as b
+
+
+def python(code):
+    """What a fresh interpreter prints."""
+    p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr
+    return p.stdout
+
+
+def test_the_library_loads_without_the_binding():
+    """The scans need nothing of it; the layer's operators say what is missing when they are called."""
+    ensure_built()
+    out = python("""
+import sys
+sys.modules["sherman_morrison_inverse_gb300._layer_binding"] = None   # not to be had
+import sherman_morrison_inverse_gb300 as vla, torch
+vla.layer.BINDING = "nowhere"
+lib = vla.load_library()
+assert lib.vla_scan_fwd.argtypes
+class Detached(vla.Handle):
+    def __init__(self): self.lib, self._h, self._ptr_value, self._device_index = lib, None, 0, 0
+    def __del__(self): pass
+x = torch.zeros(2, 8)
+for call in (lambda h: h.rms_norm(x, x[0]), lambda h: h.short_conv_step(x, x), lambda h: h.ssm_step(x, x, x, x, x)):
+    try:
+        call(Detached())
+    except RuntimeError as e:
+        print(e)
+""")
+    assert out.count("_layer_binding is not built") == 3
+
+
+@pytest.mark.parametrize("headers", [True, False])
+def test_the_library_is_built_where_the_binding_cannot_be(monkeypatch, tmp_path, headers):
+    def run(cmd, **kw):
+        ok = headers or "layer_binding.c" not in " ".join(cmd)
+        if ok:
+            open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0 if ok else 1, "", "" if ok else "Python.h: No such file")
+
+    monkeypatch.setattr(b.subprocess, "run", run)
+    for name in ("LIB", "BINDING", "OUT_DIR"):
+        monkeypatch.setattr(b, name, str(tmp_path / name))
+    if headers:
+        assert b.build() == b.LIB and os.path.exists(b.LIB) and os.path.exists(b.BINDING)
+    else:
+        with pytest.warns(UserWarning, match="Python.h"):
+            assert b.build() == b.LIB
+        assert os.path.exists(b.LIB) and not os.path.exists(b.BINDING)
