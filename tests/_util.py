@@ -12,14 +12,18 @@ HEADER = os.path.join(ROOT, "include", "vla.h")
 
 
 def ensure_built():
-    """Build libvla.so if it is missing or older than any source or the header."""
+    """Build what is missing or older than its sources or the header: libvla.so, the layer's binding."""
     from sherman_morrison_inverse_gb300 import build as b
-    lib = b.LIB
-    deps = b.sources() + [os.path.join(b.CSRC, f) for f in os.listdir(b.CSRC) if f.endswith(".cuh")]
-    deps.append(HEADER)
-    if not os.path.exists(lib) or os.path.getmtime(lib) < max(os.path.getmtime(p) for p in deps):
+
+    def stale(made, deps):
+        return not os.path.exists(made) or os.path.getmtime(made) < max(os.path.getmtime(p) for p in deps)
+
+    cuh = [os.path.join(b.CSRC, f) for f in os.listdir(b.CSRC) if f.endswith(".cuh")]
+    if stale(b.LIB, [*b.sources(), *cuh, HEADER]):
         b.build()
-    return lib
+    if stale(b.BINDING, [os.path.join(b.CSRC, "layer_binding.c"), HEADER]):
+        b.build_binding()
+    return b.LIB
 
 
 def header_functions() -> list[str]:

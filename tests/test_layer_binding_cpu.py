@@ -57,3 +57,20 @@ def test_the_library_is_built_where_the_binding_cannot_be(monkeypatch, tmp_path,
         with pytest.warns(UserWarning, match="Python.h"):
             assert b.build() == b.LIB
         assert os.path.exists(b.LIB) and not os.path.exists(b.BINDING)
+
+
+@pytest.mark.parametrize("state", ["missing", "older than its source", "fresh"])
+def test_tests_do_not_run_on_a_stale_binding(monkeypatch, tmp_path, state):
+    made = tmp_path / "binding"
+    for name, path in (("LIB", tmp_path / "lib"), ("BINDING", made)):
+        monkeypatch.setattr(b, name, str(path))
+        path.touch()   # as new as can be
+    if state == "missing":
+        made.unlink()
+    elif state != "fresh":
+        os.utime(made, (0, 0))
+    calls = []
+    monkeypatch.setattr(b, "build", lambda: calls.append("library"))
+    monkeypatch.setattr(b, "build_binding", lambda: calls.append("binding"))
+    ensure_built()
+    assert calls == ([] if state == "fresh" else ["binding"])
