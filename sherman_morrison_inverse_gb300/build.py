@@ -2,8 +2,8 @@
 
 Each .cu file compiles to an object in parallel; the objects link into
 ``sherman_morrison_inverse_gb300/libvla.so`` with the CUDA runtime linked
-statically.  ``csrc/layer_binding.c`` becomes the Python module ``_layer_binding.so``
-beside it.  Usage: ``python -m sherman_morrison_inverse_gb300.build`` or
+statically.  ``csrc/layer_binding.c`` becomes the Python module ``_layer_binding`` beside it,
+whose file name carries the interpreter's tag.  Usage: ``python -m sherman_morrison_inverse_gb300.build`` or
 ``build()`` from Python.
 """
 from __future__ import annotations
@@ -16,13 +16,14 @@ import sysconfig
 import warnings
 from concurrent.futures import ThreadPoolExecutor
 
+from .layer import BINDING
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvla.so")
-BINDING = os.path.join(PKG, "_layer_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -16,11 +16,17 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import importlib
+import importlib.machinery
+import importlib.util
+import os
+import sysconfig
 
 import torch
 
 STATUS_INDEX = 4
+# The argument checks in C, for this interpreter and machine: a module of another one has another name.
+BINDING = os.path.join(os.path.dirname(os.path.abspath(__file__)),
+                       "_layer_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 _OUT = {"io": 0, "e4m3": 1, "int8": 2}
 
 
@@ -66,7 +72,9 @@ def declare(lib):
     for fn in (lib.vla_short_conv, lib.vla_ssm_scan, lib.vla_ssm_workspace, lib.vla_rms_norm):
         fn.restype = ci
     try:
-        native = importlib.import_module("._layer_binding", __package__)
+        loader = importlib.machinery.ExtensionFileLoader(f"{__package__}._layer_binding", BINDING)
+        native = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+        loader.exec_module(native)
     except ImportError as e:
         _native = _Missing(e)
         return

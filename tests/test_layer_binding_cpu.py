@@ -74,3 +74,28 @@ def test_tests_do_not_run_on_a_stale_binding(monkeypatch, tmp_path, state):
     monkeypatch.setattr(b, "build_binding", lambda: calls.append("binding"))
     ensure_built()
     assert calls == ([] if state == "fresh" else ["binding"])
+
+
+def test_a_module_of_another_interpreter_is_not_loaded(tmp_path):
+    """The file's name carries the interpreter's tag, and an untagged one beside it is not taken for it."""
+    import sysconfig
+    ensure_built()
+    assert os.path.basename(b.BINDING) == "_layer_binding" + sysconfig.get_config_var("EXT_SUFFIX")
+    package = tmp_path / "sherman_morrison_inverse_gb300"
+    package.mkdir()
+    here = os.path.dirname(b.LIB)
+    for name in ("__init__.py", "layer.py", "build.py", "libvla.so"):
+        os.symlink(os.path.join(here, name), package / name)
+    (package / "_layer_binding.so").write_bytes(b"of another interpreter")
+    out = python(f"""
+import importlib.util, os, sys
+sys.path.insert(0, {str(tmp_path)!r})
+import sherman_morrison_inverse_gb300 as vla
+assert vla.__file__.startswith({str(tmp_path)!r}), vla.__file__
+vla.load_library()
+try:
+    vla.layer._native.norm
+except RuntimeError as e:
+    print(e)
+""")
+    assert "not built" in out and "_layer_binding.so" not in out
