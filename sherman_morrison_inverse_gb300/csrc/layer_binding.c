@@ -4,7 +4,8 @@
  * and passing them through ctypes takes ten times that.  This module does the same work with the
  * CPython API: it reads each tensor's public attributes (shape, dtype, get_device(), stride(),
  * data_ptr()), checks them, allocates outputs through torch and calls the C entry points, whose
- * addresses layer.py hands over.  It holds nothing from one call for the next.
+ * addresses layer.py hands over, without the interpreter's lock: a launch waits where the device's queue
+ * is full.  It holds nothing from one call for the next.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -311,9 +312,13 @@ static PyObject* py_conv(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
     Py_DECREF(y);
     return NULL;
   }
-  vla_err_t code = f_conv(c.h, x.ptr, (const float*)wp, (const float*)bias, sp, yt.ptr, b.n_seq, b.T, b.max_len,
-                          (const int*)b.offsets, (const int*)b.slots, b.n_slots, C, K > 100 ? 100 : (int)K, strides,
-                          truth(a[6]), io, c.stream);
+  const int silu = truth(a[6]);
+  vla_err_t code;
+  Py_BEGIN_ALLOW_THREADS
+  code = f_conv(c.h, x.ptr, (const float*)wp, (const float*)bias, sp, yt.ptr, b.n_seq, b.T, b.max_len,
+                (const int*)b.offsets, (const int*)b.slots, b.n_slots, C, K > 100 ? 100 : (int)K, strides, silu, io,
+                c.stream);
+  Py_END_ALLOW_THREADS
   return code ? failed(self, code, y) : y;
 }
 
@@ -379,9 +384,12 @@ static PyObject* py_scan(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
       return NULL;
     }
   }
+  const int softplus = truth(a[11]);
+  Py_BEGIN_ALLOW_THREADS
   code = f_scan(c.h, x.ptr, dt.ptr, (const float*)A, B.ptr, Ct.ptr, (const float*)D, zp, (const float*)bias,
                 (float*)sp, yt.ptr, b.n_seq, b.T, b.max_len, (const int*)b.offsets, (const int*)b.slots, b.n_slots,
-                H, P, G, N, strides, truth(a[11]), io, wsp, need, c.stream);
+                H, P, G, N, strides, softplus, io, wsp, need, c.stream);
+  Py_END_ALLOW_THREADS
   Py_XDECREF(ws);   /* the caching allocator hands it on in stream order */
   return code ? failed(self, code, y) : y;
 }
@@ -468,8 +476,11 @@ static PyObject* py_norm(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
     if (!scale || dense(scale, "scale", shape, nd, t_f32, c.device, &sp)) goto bad;
   }
   {
-    vla_err_t code = f_norm(c.h, x.ptr, (const float*)w, rp, yt.ptr, (float*)sp, count, D, x_row, r_row, y_row,
-                            (float)eps, (int)group, (vla_out_t)out, io, rio, c.stream);
+    vla_err_t code;
+    Py_BEGIN_ALLOW_THREADS
+    code = f_norm(c.h, x.ptr, (const float*)w, rp, yt.ptr, (float*)sp, count, D, x_row, r_row, y_row, (float)eps,
+                  (int)group, (vla_out_t)out, io, rio, c.stream);
+    Py_END_ALLOW_THREADS
     if (code) {
       Py_XDECREF(scale);
       return failed(self, code, y);

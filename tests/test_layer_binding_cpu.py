@@ -99,3 +99,57 @@ except RuntimeError as e:
     print(e)
 """)
     assert "not built" in out and "_layer_binding.so" not in out
+
+
+@pytest.mark.parametrize("call", ["norm", "conv", "scan"])
+def test_other_threads_run_during_a_call(call):
+    """A launch can wait for the device's queue: it does so without the interpreter's lock.  The entry points
+    are replaced by libc's usleep, whose argument is the handle."""
+    ensure_built()
+    out = python(f"""
+import ctypes, threading, time
+from sherman_morrison_inverse_gb300 import layer
+import importlib.util
+loader = importlib.machinery.ExtensionFileLoader("x._layer_binding", layer.BINDING)
+native = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
+sleep = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+nothing = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: 0)
+f32, other = object(), object()
+native.setup(sleep, sleep, ctypes.cast(nothing, ctypes.c_void_p).value, sleep, f32, other, other, other, other,
+             *[lambda *a, **k: 1 / 0] * 5)
+class Handle:
+    _ptr_value, _device_index = 900000, 0
+class Tensor:
+    dtype = f32
+    def __init__(self, *shape):
+        self.shape = shape
+        strides = [1]
+        for n in shape[:0:-1]:
+            strides.insert(0, strides[0] * n)
+        self.strides = tuple(strides)
+    def stride(self): return self.strides
+    def get_device(self): return 0
+    def data_ptr(self): return 64
+seen, stop = [], False
+def watch():
+    while not stop:
+        seen.append(time.monotonic())
+        time.sleep(0.01)
+t = threading.Thread(target=watch)
+t.start()
+T = Tensor
+start = time.monotonic()
+if {call!r} == "norm":
+    native.norm(Handle(), T(2, 8), T(8), None, T(2, 8), 1e-6, 0, 0, None, 0)
+elif {call!r} == "conv":
+    native.conv(Handle(), T(1, 4, 8), T(8, 2), None, None, T(1, 4, 8), True, None, None, None, False, 0)
+else:
+    native.scan(Handle(), T(1, 4, 2, 8), T(1, 4, 2), T(2), T(1, 4, 1, 4), T(1, 4, 1, 4), None, T(1, 4, 2, 8), None, None,
+                None, True, None, None, None, False, 0)
+end = time.monotonic()
+stop = True
+t.join()
+print(end - start, sum(start + 0.1 < s < end - 0.1 for s in seen))
+""")
+    took, seen = out.split()
+    assert float(took) > 0.8 and int(seen) >= 3
