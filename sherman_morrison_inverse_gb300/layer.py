@@ -155,32 +155,3 @@ class LayerOps:
             raise ValueError(f"out must be one of {sorted(_OUT)}")
         with _on(stream):
             return _native.norm(self, x, w, residual, y, eps, kind, group, scale, _raw(stream))
-
-    def _layer_even(self, name, t, shape, dtype):
-        """(rows, elements between rows) of a tensor whose rows are evenly spaced."""
-        self._layer_check(name, t, shape, dtype)
-        if t.is_contiguous():
-            D = shape[-1]
-            return (t.numel() // D if D else 0), D
-        strides = t.stride()
-        if shape[-1] > 1 and strides[-1] != 1:
-            raise ValueError(f"{name}: the values of a row must be adjacent (strides {strides})")
-        step = rows = None
-        for i in range(len(shape) - 2, -1, -1):
-            if shape[i] == 1:
-                continue
-            if step is None:
-                step, rows = strides[i], shape[i]
-            elif strides[i] != step * rows:
-                raise ValueError(f"{name}: rows must be evenly spaced (strides {strides})")
-            else:
-                rows *= shape[i]
-        return (1, shape[-1]) if step is None else (rows, step)
-
-    def _layer_stream(self, stream):
-        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
-
-    def _layer_fail(self, code):
-        from . import VlaError
-        msg = self.lib.vla_last_error(self._h)
-        raise VlaError(code, msg.decode() if msg else "")
