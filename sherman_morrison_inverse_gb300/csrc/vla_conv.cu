@@ -164,13 +164,13 @@ __global__ void __launch_bounds__(kThreads, VEC <= 4 ? 8 : 4)
   for (; i0 < n; ++i0, x += a.x_tok, y += a.y_tok) step(ld_vec<T, VEC>(x), y);
 }
 
-// Tokens a thread: 64 where that still gives every SM 8 blocks, fewer
-// for short or few sequences, down to kBatch.
+// Tokens a thread: 64 where that still gives every SM 8 blocks, fewer for short or few sequences, down to
+// kBatch.
 template <typename T, int K, int VEC>
 cudaError_t launch(const ConvArgs& a, cudaStream_t s) {
   const long long cblocks = (a.C + (long long)kThreads * VEC - 1) / ((long long)kThreads * VEC);
   long long tile = 64;
-  while (tile > kBatch && (a.seqs.T + tile - 1) / tile * (a.seqs.offsets ? 1 : a.seqs.n_seq) * cblocks < 1216) tile /= 2;
+  while (tile > kBatch && (a.seqs.T + tile - 1) / tile * (a.seqs.offsets ? 1 : a.seqs.n_seq) * cblocks < 8LL * a.sm_count) tile /= 2;
   const long long tiles = (a.seqs.max_len + tile - 1) / tile;
   if (tiles > 0x7fffffffLL || cblocks > 0x7fffffffLL || tiles * cblocks > 0x7fffffffLL / a.seqs.n_seq)
     return cudaErrorInvalidConfiguration;

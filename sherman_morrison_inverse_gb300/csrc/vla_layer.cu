@@ -78,6 +78,7 @@ vla_err_t vla_short_conv(vla_handle_t h, const void* x, const float* w, const fl
     return fail(h, VLA_ERR_INVALID_ARG, f + ": rows of y overlap");
   a.x = x; a.w = w; a.bias = bias; a.state = state; a.y = y;
   a.C = C; a.K = K; a.silu = silu != 0;
+  a.sm_count = h->sm_count;
   // a dense batch of one sequence or one token never uses the other stride: 0 keeps it from
   // deciding the vector width
   a.x_seq = offsets || n_seq == 1 ? 0 : strides[0]; a.x_tok = a.seqs.max_len == 1 && !offsets ? 0 : strides[1];

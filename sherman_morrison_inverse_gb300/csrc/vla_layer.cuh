@@ -145,6 +145,7 @@ struct ConvArgs {
   long long x_seq, x_tok, y_seq, y_tok;   // strides in elements (channels are adjacent)
   int K;
   bool silu;
+  int sm_count;
   DevStatus* status;
 };
 cudaError_t launch_short_conv(const ConvArgs& a, bool bf16, cudaStream_t s);
