@@ -375,7 +375,9 @@ vla_err_t vla_short_conv(vla_handle_t h, const void* x, const float* w, const fl
  *             else uses until the call's work is done; NULL where that is 0.
  * A NaN or infinity in x reaches its own row of the state and that row's outputs, from its token on:
  * there they are NaN or infinite (in the chunked form NaN).  It reaches nothing earlier and no other row.
- * State and sums are float32.  Errors (before any launch): as for vla_short_conv;
+ * State and sums are float32.  Long bfloat16 prompts run on tensor cores, whose terms of an output are
+ * rounded to bfloat16: it is off by up to 2^-9 of the sum of its terms' magnitudes,
+ * besides its own rounding; the state is not.  Errors (before any launch): as for vla_short_conv;
  * INVALID_ARG also for H no multiple of G, a misaligned state, a workspace that is
  * too small; UNSUPPORTED for N > 256. */
 vla_err_t vla_ssm_scan(vla_handle_t h, const void* x, const void* dt, const float* A, const void* B, const void* C,

@@ -8,7 +8,7 @@
 // the rounding, so x and the residual are read once and every output written once (7 bytes a value
 // for bfloat16 with a residual and e4m3): memory bound, with an instruction count close behind (so
 // values are taken in packed pairs and the warp's maximum is one integer reduction of their bits).
-// 16384 x 4096 of that kind: 82.3 us, 5.71 TB/s, 84 % of a plain copy's rate, warp issue 65 % busy.
+// 16384 x 4096 of that kind: 82.3 us, 5.71 TB/s, 84 % of a plain copy's rate, warp issue 71 % busy.
 // Rows that start unaligned: 4099 x 1001 float32 12.3 us (9.3 on the GPU), 20000 x 3333 bfloat16 with
 // residual to e4m3 130 us, 3.6 TB/s.
 // v is taken as (r w) / sqrt(..): the largest |v| of a row is then the largest |r w| times the same

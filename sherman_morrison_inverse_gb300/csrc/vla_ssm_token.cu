@@ -7,7 +7,7 @@
 // the rows' sums over N are folded together (each step of the butterfly halves the rows a
 // lane carries), no shared memory and no barrier.
 // 128 sequences, 64 heads of 64 x 128: 86 us, 6.26 TB/s, 92 % of a plain copy's rate.  One sequence:
-// 2.6 us on the GPU, which is about what a kernel of one trip to memory takes; the call takes 13 us on the host.
+// 2.6 us on the GPU, which is about what a kernel of one trip to memory takes; the call takes 15 to 18 us on the host.
 #include "vla_layer.cuh"
 
 namespace vla {
