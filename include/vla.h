@@ -404,7 +404,8 @@ typedef enum { VLA_OUT_IO = 0, VLA_OUT_E4M3 = 1, VLA_OUT_INT8 = 2 } vla_out_t;
  *
  *   x, y, residual   rows at x_row, y_row, res_row elements; residual NULL, or
  *                    res_dtype, updated in place.   w  [D] float32.
- * v is formed in float32 from r before r is rounded to the residual's type.
+ * v is formed in float32 from r before r is rounded to the residual's type; so is the sum of squares (values
+ * from about 1e19 / sqrt(D) on overflow it: v is then 0).
  * Errors (before any launch): INVALID_ARG for NULL pointers, sizes or strides out of
  * range, unknown types, group not 0 or 128, eps < 0 or NaN; UNSUPPORTED for D > 32768;
  * CUDA if the launch fails. */
