@@ -413,6 +413,94 @@ vla_err_t vla_rms_norm(vla_handle_t h, const void* x, const float* w, void* resi
                        long long rows, long long D, long long x_row, long long res_row, long long y_row, float eps,
                        int group, vla_out_t out, vla_dtype_t io_dtype, vla_dtype_t res_dtype, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Products and layer norms around the scans, forward and backward: the projections of a
+ * layer with their epilogue, and the norm before them.  The pages have no counterpart to
+ * them.  Like the operators above they are asynchronous on `stream`, allocate nothing,
+ * read the host's arguments before they return, give the same bits every time, and can
+ * be captured in a CUDA graph.  Rows are evenly spaced, strides count elements and are
+ * >= 0, the values of a row are adjacent, and no alignment beyond a value's type is
+ * required; rows that start on 16-byte boundaries are faster.  Outputs must not overlap
+ * any input or each other (y of the product may be its residual, the norm's residual is
+ * both).  Bias, norm weights, statistics, scales and their gradients are float32. */
+
+typedef enum { VLA_ACT_NONE = 0, VLA_ACT_SILU = 1, VLA_ACT_GELU = 2 } vla_act_t;   /* v; v sigmoid(v); v Phi(v) */
+typedef enum { VLA_MAT_F32 = 0, VLA_MAT_BF16 = 1, VLA_MAT_E4M3 = 2 } vla_mat_t;    /* operands of a product */
+
+/* y = act(v) + residual,  v[m, n] = x_scale[m] w_scale[n] sum_k x[m, k] w[n, k] + bias[n],  pre <- v.
+ *
+ *   x, w      [M, K] and [N, K], both of type `in`.   K == 0: sums are 0.
+ *   x_scale, w_scale   [M] and [N] float32 for VLA_MAT_E4M3 (codes and scales of vla_rms_norm with
+ *             group 0), NULL: 1; NULL for other types.
+ *   bias      [N] float32 or NULL.
+ *   residual  [M, N] in y's type or NULL.      pre  [M, N] in y's type or NULL, written.
+ *   y         [M, N] in `out`: float32, or bfloat16 unless `in` is float32.
+ *   rows      host array of the row strides {x, w, residual, pre, y}.
+ *   workspace device memory of vla_linear_workspace bytes, 16-byte aligned, that nothing else
+ *             uses until the call's work is done; NULL where that is 0.
+ * Products are exact and sums float32 (float32 operands: each is taken as three bfloat16 terms, products to
+ * about 2^-23 of their magnitude; a value of 3.4e38 or more, an infinity or a NaN makes the outputs that it
+ * enters infinite or NaN).  v is rounded once into pre and not before the activation; y is rounded once.
+ * Errors (before any launch): INVALID_ARG for NULL pointers, sizes or strides out of range, unknown types,
+ * scales with a type that has none, a workspace that is too small; UNSUPPORTED for types that do not go
+ * together; CUDA if the launch fails. */
+vla_err_t vla_linear(vla_handle_t h, const void* x, const void* w, const float* x_scale, const float* w_scale,
+                     const float* bias, const void* residual, void* pre, void* y, long long M, long long N, long long K,
+                     const long long* rows, vla_act_t act, vla_mat_t in, vla_dtype_t out, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that vla_linear needs for these arguments (of x and w only the addresses count; NULL
+ * stands for aligned ones).  Errors: as for vla_linear. */
+vla_err_t vla_linear_workspace(vla_handle_t h, const void* x, const void* w, long long M, long long N, long long K,
+                               const long long* rows, vla_mat_t in, vla_dtype_t out, size_t* bytes);
+
+/* The gradients of vla_linear without scales: with g = dy * act'(pre),
+ *   dx[m, k] = sum_n g[m, n] w[n, k],  dw[n, k] = sum_m g[m, n] x[m, k],  db[n] = sum_m g[m, n];
+ * the residual's gradient is dy itself.
+ *
+ *   dy        [M, N];  x [M, K];  w [N, K];  all io dtype.
+ *   pre       [M, N] io dtype, what vla_linear wrote; NULL and unused for VLA_ACT_NONE.
+ *   dx, dw    [M, K] and [N, K] io dtype;  db [N] float32.  Each may be NULL: not computed.
+ *   rows      host array of the row strides {dy, x, w, pre, dx, dw}.
+ * Sums are float32.  With bfloat16 and an activation, g is rounded to bfloat16 for the products (not for db):
+ * each term of dx and dw is off by up to 2^-8 of itself.  A gradient without terms (M or N zero) is zero.
+ * Workspace and errors: as for vla_linear. */
+vla_err_t vla_linear_backward(vla_handle_t h, const void* dy, const void* x, const void* w, const void* pre, void* dx,
+                              void* dw, float* db, long long M, long long N, long long K, const long long* rows,
+                              vla_act_t act, vla_dtype_t io_dtype, void* workspace, size_t workspace_bytes,
+                              void* stream);
+vla_err_t vla_linear_backward_workspace(vla_handle_t h, const void* dy, const void* x, const void* w, int dx, int dw,
+                                        int db, long long M, long long N, long long K, const long long* rows,
+                                        vla_act_t act, vla_dtype_t io_dtype, size_t* bytes);
+
+/* Layer norm of rows of D values (1..32768):
+ *   r = x + residual (residual <- r in its own type),  mu = mean(r),
+ *   rstd = 1 / sqrt(mean((r - mu)^2) + eps),  y = (r - mu) rstd w + b
+ *
+ *   x, y      io dtype, rows at x_row, y_row;  residual  NULL, or res_dtype, updated in place.
+ *   w, b      [D] float32; b may be NULL.   stats  [rows, 2] float32 (mu, rstd), or NULL.
+ * r is not rounded before the norm.  Errors (before any launch): INVALID_ARG for NULL pointers, sizes or
+ * strides out of range, unknown types, eps < 0 or NaN; UNSUPPORTED for D > 32768; CUDA if the launch fails. */
+vla_err_t vla_layer_norm(vla_handle_t h, const void* x, const float* w, const float* b, void* residual, void* y,
+                         float* stats, long long rows, long long D, long long x_row, long long res_row, long long y_row,
+                         float eps, vla_dtype_t io_dtype, vla_dtype_t res_dtype, void* stream);
+
+/* Its gradients: with h = (x - mu) rstd and a = dy w,
+ *   dx = rstd (a - mean(a) - h mean(a h)) + dresidual,  dw = sum over rows of dy h,  db = sum over rows of dy.
+ *
+ *   dy        [rows, D] dy_dtype.
+ *   x         [rows, D] x_dtype: what was normalised (x of the forward pass, or the residual that it left).
+ *   stats     [rows, 2], what vla_layer_norm wrote.
+ *   dresidual [rows, D] x_dtype or NULL: the residual stream's own gradient.   dx  x_dtype.
+ *   dw, db    [D] float32; db may be NULL.   Without rows both are zero.
+ *   strides   host array {dy, x, dresidual, dx}.
+ * Sums are float32.  Workspace and errors: as for the others. */
+vla_err_t vla_layer_norm_backward(vla_handle_t h, const void* dy, const void* x, const float* w, const float* stats,
+                                  const void* dresidual, void* dx, float* dw, float* db, long long rows, long long D,
+                                  const long long* strides, vla_dtype_t dy_dtype, vla_dtype_t x_dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+vla_err_t vla_layer_norm_backward_workspace(vla_handle_t h, long long rows, long long D, size_t* bytes);
+
 #ifdef __cplusplus
 }
 #endif

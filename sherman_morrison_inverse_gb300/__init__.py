@@ -19,7 +19,8 @@ and out with the scan, window by window of the sequence.
 
 ``short_conv``, ``ssm_scan``, their single-token forms ``short_conv_step`` and
 ``ssm_step``, and ``rms_norm`` are the operators of a state space layer (see
-``layer.py``).
+``layer.py``); ``linear`` and ``layer_norm`` with their gradients ``linear_backward`` and
+``layer_norm_backward`` are the projections and the other norm around them.
 """
 from __future__ import annotations
 
@@ -33,7 +34,7 @@ from . import layer as _layer
 from .layer import STATUS_INDEX
 
 __all__ = ["scan_fwd", "scan_fwd_host", "project_u", "short_conv", "short_conv_step", "ssm_scan", "ssm_step",
-           "rms_norm", "Handle", "VlaError", "library_path", "load_library",
+           "rms_norm", "linear", "linear_backward", "layer_norm", "layer_norm_backward", "Handle", "VlaError", "library_path", "load_library",
            "STATUS_NONFINITE", "STATUS_TIMEOUT", "STATUS_INDEX", "SEQUENTIAL", "CHUNKED", "DELTA"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -327,3 +328,23 @@ def ssm_step(x, *args, handle: Handle | None = None, **kw):
 def rms_norm(x, *args, handle: Handle | None = None, **kw):
     """Root-mean-square norm with residual and 8-bit output on x's device (see Handle.rms_norm)."""
     return (handle or default_handle(x.device)).rms_norm(x, *args, **kw)
+
+
+def linear(x, *args, handle: Handle | None = None, **kw):
+    """Matrix product with bias, activation and residual on x's device (see Handle.linear)."""
+    return (handle or default_handle(x.device)).linear(x, *args, **kw)
+
+
+def linear_backward(dy, *args, handle: Handle | None = None, **kw):
+    """Gradients of linear on dy's device (see Handle.linear_backward)."""
+    return (handle or default_handle(dy.device)).linear_backward(dy, *args, **kw)
+
+
+def layer_norm(x, *args, handle: Handle | None = None, **kw):
+    """Layer norm with residual on x's device (see Handle.layer_norm)."""
+    return (handle or default_handle(x.device)).layer_norm(x, *args, **kw)
+
+
+def layer_norm_backward(dy, *args, handle: Handle | None = None, **kw):
+    """Gradients of layer_norm on dy's device (see Handle.layer_norm_backward)."""
+    return (handle or default_handle(dy.device)).layer_norm_backward(dy, *args, **kw)

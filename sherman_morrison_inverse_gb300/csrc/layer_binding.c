@@ -1,4 +1,5 @@
-/* Argument checks and marshalling of the state space layer's operators for Python.
+/* Argument checks and marshalling for Python of the state space layer's operators, and of the products and
+ * layer norms around them.
  *
  * A decoding step of one sequence runs for a few microseconds on the GPU; checking a dozen tensors
  * and passing them through ctypes takes ten times that.  This module does the same work with the
@@ -25,10 +26,35 @@ typedef vla_err_t (*norm_fn)(vla_handle_t, const void*, const float*, void*, voi
                              long long, long long, long long, float, int, vla_out_t, vla_dtype_t, vla_dtype_t,
                              void*);
 
+typedef vla_err_t (*linear_fn)(vla_handle_t, const void*, const void*, const float*, const float*, const float*,
+                               const void*, void*, void*, long long, long long, long long, const long long*, vla_act_t,
+                               vla_mat_t, vla_dtype_t, void*, size_t, void*);
+typedef vla_err_t (*linear_ws_fn)(vla_handle_t, const void*, const void*, long long, long long, long long,
+                                  const long long*, vla_mat_t, vla_dtype_t, size_t*);
+typedef vla_err_t (*linear_back_fn)(vla_handle_t, const void*, const void*, const void*, const void*, void*, void*,
+                                    float*, long long, long long, long long, const long long*, vla_act_t, vla_dtype_t,
+                                    void*, size_t, void*);
+typedef vla_err_t (*linear_back_ws_fn)(vla_handle_t, const void*, const void*, const void*, int, int, int, long long,
+                                       long long, long long, const long long*, vla_act_t, vla_dtype_t, size_t*);
+typedef vla_err_t (*lnorm_fn)(vla_handle_t, const void*, const float*, const float*, void*, void*, float*, long long,
+                              long long, long long, long long, long long, float, vla_dtype_t, vla_dtype_t, void*);
+typedef vla_err_t (*lnorm_back_fn)(vla_handle_t, const void*, const void*, const float*, const float*, const void*, void*,
+                                   float*, float*, long long, long long, const long long*, vla_dtype_t, vla_dtype_t,
+                                   void*, size_t, void*);
+typedef vla_err_t (*lnorm_back_ws_fn)(vla_handle_t, long long, long long, size_t*);
+
 static conv_fn f_conv;
 static scan_fn f_scan;
 static ws_fn f_ws;
 static norm_fn f_norm;
+static linear_fn f_linear;
+static linear_ws_fn f_linear_ws;
+static linear_back_fn f_linear_back;
+static linear_back_ws_fn f_linear_back_ws;
+static lnorm_fn f_lnorm;
+static lnorm_back_fn f_lnorm_back;
+static lnorm_back_ws_fn f_lnorm_back_ws;
+static PyObject* c_new;                                           /* new(like, shape, dtype) */
 static PyObject *t_f32, *t_bf16, *t_i32, *t_e4m3, *t_i8;          /* torch dtypes */
 static PyObject *c_like, *c_dense, *c_empty, *c_bytes, *c_stream; /* allocators and the current stream */
 static PyObject *s_shape, *s_dtype, *s_get_device, *s_stride, *s_data_ptr, *s_ptr, *s_index, *s_fail, *k_dtype;
@@ -281,6 +307,23 @@ static PyObject* want(const char* text) {
 
 static int truth(PyObject* o) { return PyObject_IsTrue(o); }
 
+/* A workspace of `need` bytes (none for 0) from the allocator of the tensor `like`. */
+static int workspace(PyObject* like, size_t need, PyObject** ws, void** ptr) {
+  *ws = NULL;
+  *ptr = NULL;
+  if (!need) return 0;
+  PyObject* size = PyLong_FromSize_t(need);
+  PyObject* args[2] = {like, size};
+  *ws = size ? PyObject_Vectorcall(c_bytes, args, 2, NULL) : NULL;
+  Py_XDECREF(size);
+  PyObject* p = *ws ? call0(*ws, s_data_ptr) : NULL;
+  if (p) *ptr = PyLong_AsVoidPtr(p);
+  Py_XDECREF(p);
+  if (p && !PyErr_Occurred()) return 0;
+  Py_CLEAR(*ws);
+  return -1;
+}
+
 /* conv(handle, x, w, bias, state, y, silu, offsets, slots, max_len, token, stream) */
 static PyObject* py_conv(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
   (void)mod;
@@ -370,19 +413,9 @@ static PyObject* py_scan(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
     Py_DECREF(y);
     return NULL;
   }
-  if (need) {
-    PyObject* size = PyLong_FromSize_t(need);
-    PyObject* args[2] = {a[1], size};
-    ws = size ? PyObject_Vectorcall(c_bytes, args, 2, NULL) : NULL;
-    Py_XDECREF(size);
-    PyObject* p = ws ? call0(ws, s_data_ptr) : NULL;
-    if (p) wsp = PyLong_AsVoidPtr(p);
-    Py_XDECREF(p);
-    if (!p || PyErr_Occurred()) {
-      Py_XDECREF(ws);
-      Py_DECREF(y);
-      return NULL;
-    }
+  if (workspace(a[1], need, &ws, &wsp)) {
+    Py_DECREF(y);
+    return NULL;
   }
   const int softplus = truth(a[11]);
   Py_BEGIN_ALLOW_THREADS
@@ -497,6 +530,307 @@ bad:
   return NULL;
 }
 
+/* The tensor given, or a new contiguous one. */
+static PyObject* given_or_new(PyObject* given, PyObject* like, const long long* shape, int nd, PyObject* dtype) {
+  if (given != Py_None) {
+    Py_INCREF(given);
+    return given;
+  }
+  PyObject* size = shape_tuple(shape, nd);
+  PyObject* args[3] = {like, size, dtype};
+  PyObject* r = size ? PyObject_Vectorcall(c_new, args, 3, NULL) : NULL;
+  Py_XDECREF(size);
+  return r;
+}
+
+/* Reads and checks a tensor of evenly spaced rows, [..., width]. */
+static int even_rows(Tensor* t, PyObject* obj, const char* name, const long long* shape, int nd, PyObject* dtype,
+                     long device, long long* step) {
+  long long ignored;
+  return read_tensor(t, obj, name) || check(t, shape, nd, dtype, device) || even(t, &ignored, step) ? -1 : 0;
+}
+
+/* linear(handle, x, w, bias, residual, y, act, pre, x_scale, w_scale, dtype, stream); act: 0 none, 1 silu, 2 gelu */
+static PyObject* py_linear(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
+  (void)mod;
+  if (n != 12) return want("linear takes 12 arguments");
+  PyObject *self = a[0], *y = NULL, *ws = NULL, *dtype, *odtype;
+  Call c;
+  Tensor x, w, t;
+  vla_mat_t in;
+  vla_dtype_t out;
+  long long M, N, K, ignored, rows[5] = {0}, shape[MAXD], wshape[2];
+  void *bias, *xs, *wsc, *res = NULL, *pre = NULL, *yp, *wsp = NULL;
+  const long act = PyLong_AsLong(a[6]);
+  if (PyErr_Occurred()) return NULL;
+  if (read_call(&c, self, a[11]) || read_tensor(&x, a[1], "x") || read_tensor(&w, a[2], "w")) return NULL;
+  if (x.nd < 1) return want("x must be [..., K]");
+  if (w.nd != 2) return want("w must be [N, K]");
+  if (!(dtype = PyObject_GetAttr(a[1], s_dtype))) return NULL;
+  Py_DECREF(dtype);   /* torch keeps its dtypes */
+  if (dtype == t_f32) in = VLA_MAT_F32;
+  else if (dtype == t_bf16) in = VLA_MAT_BF16;
+  else if (dtype == t_e4m3) in = VLA_MAT_E4M3;
+  else return want("x must be float32, bfloat16 or float8_e4m3fn");
+  if (check_device(&x, c.device) || even(&x, &M, &rows[0])) return NULL;
+  K = x.shape[x.nd - 1];
+  N = w.shape[0];
+  wshape[0] = N; wshape[1] = K;
+  if (check(&w, wshape, 2, dtype, c.device) || even(&w, &ignored, &rows[1])) return NULL;
+  odtype = a[10] != Py_None ? a[10] : dtype == t_e4m3 ? t_bf16 : dtype;
+  if (odtype == t_f32) out = VLA_F32;
+  else if (odtype == t_bf16) out = VLA_BF16;
+  else return want("dtype must be float32 or bfloat16");
+  if (dense(a[3], "bias", &N, 1, t_f32, c.device, &bias) || dense(a[9], "w_scale", &N, 1, t_f32, c.device, &wsc) ||
+      dense(a[8], "x_scale", x.shape, x.nd - 1, t_f32, c.device, &xs))
+    return NULL;
+  for (int i = 0; i < x.nd - 1; ++i) shape[i] = x.shape[i];
+  shape[x.nd - 1] = N;
+  if (a[4] != Py_None) {
+    if (even_rows(&t, a[4], "residual", shape, x.nd, odtype, c.device, &rows[2])) return NULL;
+    res = t.ptr;
+  }
+  if (a[7] != Py_None) {
+    if (even_rows(&t, a[7], "pre", shape, x.nd, odtype, c.device, &rows[3])) return NULL;
+    pre = t.ptr;
+  }
+  if (!(y = given_or_new(a[5], a[1], shape, x.nd, odtype))) return NULL;
+  if (even_rows(&t, y, "y", shape, x.nd, odtype, c.device, &rows[4])) goto bad;
+  yp = t.ptr;
+  M = 1;   /* x without columns has its rows all the same */
+  for (int i = 0; i < x.nd - 1; ++i) M *= x.shape[i];
+  size_t need = 0;
+  vla_err_t code = f_linear_ws(c.h, x.ptr, w.ptr, M, N, K, rows, in, out, &need);
+  if (code) return failed(self, code, y);
+  if (workspace(a[1], need, &ws, &wsp)) goto bad;
+  Py_BEGIN_ALLOW_THREADS
+  code = f_linear(c.h, x.ptr, w.ptr, (const float*)xs, (const float*)wsc, (const float*)bias, res, pre, yp, M, N, K, rows,
+                  (vla_act_t)act, in, out, wsp, need, c.stream);
+  Py_END_ALLOW_THREADS
+  Py_XDECREF(ws);   /* the caching allocator hands it on in stream order */
+  return code ? failed(self, code, y) : y;
+bad:
+  Py_DECREF(y);
+  return NULL;
+}
+
+/* linear_back(handle, dy, x, w, pre, act, dx, dw, db, stream); dx, dw, db: a tensor, None (a new one) or False (not
+ * computed) */
+static PyObject* py_linear_back(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
+  (void)mod;
+  if (n != 10) return want("linear_back takes 10 arguments");
+  PyObject *self = a[0], *ws = NULL, *dtype, *got[3] = {NULL, NULL, NULL}, *made;
+  Call c;
+  Tensor dy, x, w, t;
+  vla_dtype_t io;
+  long long M, N, K, ignored, rows[6] = {0}, shape[MAXD];
+  void *pre = NULL, *out[3] = {NULL, NULL, NULL}, *wsp = NULL;
+  const long act = PyLong_AsLong(a[5]);
+  if (PyErr_Occurred()) return NULL;
+  if (read_call(&c, self, a[9]) || read_tensor(&dy, a[1], "dy") || read_tensor(&x, a[2], "x") || read_tensor(&w, a[3], "w"))
+    return NULL;
+  if (dy.nd < 1 || x.nd != dy.nd) return want("dy must be [..., N] and x [..., K] with the same rows");
+  if (w.nd != 2) return want("w must be [N, K]");
+  if (read_io(&dy, &dtype, &io) || check_device(&dy, c.device)) return NULL;
+  N = w.shape[0];
+  K = w.shape[1];
+  M = 1;
+  for (int i = 0; i < dy.nd - 1; ++i) M *= shape[i] = dy.shape[i];
+  shape[dy.nd - 1] = K;
+  if (check(&x, shape, x.nd, dtype, c.device) || even(&x, &ignored, &rows[1])) return NULL;
+  if (check(&w, w.shape, 2, dtype, c.device) || even(&w, &ignored, &rows[2])) return NULL;
+  shape[dy.nd - 1] = N;
+  if (check(&dy, shape, dy.nd, dtype, c.device) || even(&dy, &ignored, &rows[0])) return NULL;
+  if (act != 0) {
+    if (a[4] == Py_None) return want("pre is needed behind an activation");
+    if (even_rows(&t, a[4], "pre", shape, dy.nd, dtype, c.device, &rows[3])) return NULL;
+    pre = t.ptr;
+  }
+  for (int i = 0; i < 3; ++i) {
+    if (a[6 + i] == Py_False) {
+      Py_INCREF(Py_None);
+      got[i] = Py_None;
+      continue;
+    }
+    const char* name = i == 0 ? "dx" : i == 1 ? "dw" : "db";
+    const long long* sh = i == 0 ? x.shape : i == 1 ? w.shape : &N;
+    const int nd = i == 0 ? x.nd : i == 1 ? 2 : 1;
+    PyObject* dt = i == 2 ? t_f32 : dtype;
+    if (!(got[i] = given_or_new(a[6 + i], a[1], sh, nd, dt))) goto bad;
+    if (i == 2) {
+      if (dense(got[2], name, sh, 1, dt, c.device, &out[2])) goto bad;
+    } else {
+      if (even_rows(&t, got[i], name, sh, nd, dt, c.device, &rows[4 + i])) goto bad;
+      out[i] = t.ptr;
+    }
+  }
+  {
+    size_t need = 0;
+    vla_err_t code = f_linear_back_ws(c.h, dy.ptr, x.ptr, w.ptr, got[0] != Py_None, got[1] != Py_None, got[2] != Py_None,
+                                      M, N, K, rows, (vla_act_t)act, io, &need);
+    if (!code) {
+      if (workspace(a[1], need, &ws, &wsp)) goto bad;
+      Py_BEGIN_ALLOW_THREADS
+      code = f_linear_back(c.h, dy.ptr, x.ptr, w.ptr, pre, out[0], out[1], (float*)out[2], M, N, K, rows, (vla_act_t)act,
+                           io, wsp, need, c.stream);
+      Py_END_ALLOW_THREADS
+      Py_XDECREF(ws);
+    }
+    if (code) {
+      Py_DECREF(got[0]);
+      Py_DECREF(got[1]);
+      return failed(self, code, got[2]);
+    }
+  }
+  made = PyTuple_Pack(3, got[0], got[1], got[2]);
+  for (int i = 0; i < 3; ++i) Py_DECREF(got[i]);
+  return made;
+bad:
+  for (int i = 0; i < 3; ++i) Py_XDECREF(got[i]);
+  return NULL;
+}
+
+/* layer_norm(handle, x, w, b, residual, y, eps, stats, stream); stats: a tensor, True (a new one) or False */
+static PyObject* py_layer_norm(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
+  (void)mod;
+  if (n != 9) return want("layer_norm takes 9 arguments");
+  PyObject *self = a[0], *y = NULL, *stats = NULL, *dtype, *rdtype, *made;
+  Call c;
+  Tensor x, r, t;
+  vla_dtype_t io, rio = VLA_F32;
+  long long count, x_row, r_row = 0, y_row, ignored, shape[MAXD];
+  void *w, *b, *rp = NULL, *sp = NULL;
+  const double eps = PyFloat_AsDouble(a[6]);
+  if (PyErr_Occurred()) return NULL;
+  if (read_call(&c, self, a[8]) || read_tensor(&x, a[1], "x")) return NULL;
+  if (x.nd < 1) return want("x must be [..., D]");
+  if (read_io(&x, &dtype, &io) || check_device(&x, c.device) || even(&x, &count, &x_row)) return NULL;
+  const long long D = x.shape[x.nd - 1];
+  if (a[2] == Py_None) return want("w must be [D] float32");
+  if (dense(a[2], "w", &D, 1, t_f32, c.device, &w) || dense(a[3], "b", &D, 1, t_f32, c.device, &b)) return NULL;
+  if (a[4] != Py_None) {
+    if (read_tensor(&r, a[4], "residual") || read_io(&r, &rdtype, &rio) ||
+        check(&r, x.shape, x.nd, rdtype, c.device) || even(&r, &ignored, &r_row))
+      return NULL;
+    rp = r.ptr;
+  }
+  if (!(y = output(a[5], &x))) return NULL;
+  if (even_rows(&t, y, "y", x.shape, x.nd, dtype, c.device, &y_row)) goto bad;
+  if (a[7] != Py_False) {
+    if (x.nd >= MAXD) {
+      want("statistics are kept of tensors of at most 7 dimensions");
+      goto bad;
+    }
+    for (int i = 0; i < x.nd - 1; ++i) shape[i] = x.shape[i];
+    shape[x.nd - 1] = 2;
+    if (!(stats = given_or_new(a[7] == Py_True ? Py_None : a[7], a[1], shape, x.nd, t_f32))) goto bad;
+    if (dense(stats, "stats", shape, x.nd, t_f32, c.device, &sp)) goto bad;
+  }
+  {
+    vla_err_t code;
+    Py_BEGIN_ALLOW_THREADS
+    code = f_lnorm(c.h, x.ptr, (const float*)w, (const float*)b, rp, t.ptr, (float*)sp, count, D, x_row, r_row, y_row,
+                   (float)eps, io, rio, c.stream);
+    Py_END_ALLOW_THREADS
+    if (code) {
+      Py_XDECREF(stats);
+      return failed(self, code, y);
+    }
+  }
+  if (!stats) return y;
+  made = PyTuple_Pack(2, y, stats);
+  Py_DECREF(y);
+  Py_DECREF(stats);
+  return made;
+bad:
+  Py_XDECREF(y);
+  Py_XDECREF(stats);
+  return NULL;
+}
+
+/* layer_norm_back(handle, dy, x, w, stats, dresidual, dx, dw, db, stream); db: a tensor, None (a new one) or False (not
+ * computed) */
+static PyObject* py_layer_norm_back(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
+  (void)mod;
+  if (n != 10) return want("layer_norm_back takes 10 arguments");
+  PyObject *self = a[0], *dx = NULL, *dw = NULL, *db = NULL, *ws = NULL, *gtype, *dtype, *made;
+  Call c;
+  Tensor dy, x, t;
+  vla_dtype_t gio, io;
+  long long count, strides[4] = {0}, shape[MAXD];
+  void *w, *sp, *res = NULL, *dxp, *dwp = NULL, *dbp = NULL, *wsp = NULL;
+  if (read_call(&c, self, a[9]) || read_tensor(&dy, a[1], "dy") || read_tensor(&x, a[2], "x")) return NULL;
+  if (x.nd < 1) return want("x must be [..., D]");
+  if (read_io(&x, &dtype, &io) || check_device(&x, c.device) || even(&x, &count, &strides[1])) return NULL;
+  if (read_io(&dy, &gtype, &gio) || check(&dy, x.shape, x.nd, gtype, c.device) || even(&dy, &count, &strides[0])) return NULL;
+  const long long D = x.shape[x.nd - 1];
+  if (a[3] == Py_None) return want("w must be [D] float32");
+  if (a[4] == Py_None) return want("stats must be [..., 2] float32");
+  if (dense(a[3], "w", &D, 1, t_f32, c.device, &w)) return NULL;
+  for (int i = 0; i < x.nd - 1; ++i) shape[i] = x.shape[i];
+  shape[x.nd - 1] = 2;
+  if (dense(a[4], "stats", shape, x.nd, t_f32, c.device, &sp)) return NULL;
+  if (a[5] != Py_None) {
+    if (even_rows(&t, a[5], "dresidual", x.shape, x.nd, dtype, c.device, &strides[2])) return NULL;
+    res = t.ptr;
+  }
+  if (!(dx = output(a[6], &x)) || even_rows(&t, dx, "dx", x.shape, x.nd, dtype, c.device, &strides[3])) goto bad;
+  dxp = t.ptr;
+  if (!(dw = given_or_new(a[7], a[1], &D, 1, t_f32)) || dense(dw, "dw", &D, 1, t_f32, c.device, &dwp)) goto bad;
+  if (a[8] == Py_False) {
+    Py_INCREF(Py_None);
+    db = Py_None;
+  } else if (!(db = given_or_new(a[8], a[1], &D, 1, t_f32)) || dense(db, "db", &D, 1, t_f32, c.device, &dbp)) {
+    goto bad;
+  }
+  {
+    size_t need = 0;
+    vla_err_t code = f_lnorm_back_ws(c.h, count, D, &need);
+    if (!code) {
+      if (workspace(a[1], need, &ws, &wsp)) goto bad;
+      Py_BEGIN_ALLOW_THREADS
+      code = f_lnorm_back(c.h, dy.ptr, x.ptr, (const float*)w, (const float*)sp, res, dxp, (float*)dwp, (float*)dbp, count,
+                          D, strides, gio, io, wsp, need, c.stream);
+      Py_END_ALLOW_THREADS
+      Py_XDECREF(ws);
+    }
+    if (code) {
+      Py_DECREF(dx);
+      Py_DECREF(dw);
+      return failed(self, code, db);
+    }
+  }
+  made = PyTuple_Pack(3, dx, dw, db);
+  Py_DECREF(dx);
+  Py_DECREF(dw);
+  Py_DECREF(db);
+  return made;
+bad:
+  Py_XDECREF(dx);
+  Py_XDECREF(dw);
+  Py_XDECREF(db);
+  return NULL;
+}
+
+/* setup_dense(addresses of the entry points and workspace queries, new): after setup */
+static PyObject* py_setup_dense(PyObject* mod, PyObject* args) {
+  (void)mod;
+  unsigned long long p[7];
+  PyObject* make;
+  if (!PyArg_ParseTuple(args, "KKKKKKKO", p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6, &make)) return NULL;
+  f_linear = (linear_fn)(uintptr_t)p[0];
+  f_linear_ws = (linear_ws_fn)(uintptr_t)p[1];
+  f_linear_back = (linear_back_fn)(uintptr_t)p[2];
+  f_linear_back_ws = (linear_back_ws_fn)(uintptr_t)p[3];
+  f_lnorm = (lnorm_fn)(uintptr_t)p[4];
+  f_lnorm_back = (lnorm_back_fn)(uintptr_t)p[5];
+  f_lnorm_back_ws = (lnorm_back_ws_fn)(uintptr_t)p[6];
+  Py_INCREF(make);
+  Py_XDECREF(c_new);
+  c_new = make;
+  Py_RETURN_NONE;
+}
+
 /* setup(addresses of the four entry points, dtypes f32 bf16 i32 e4m3 i8, like, dense, empty, bytes, stream) */
 static PyObject* py_setup(PyObject* mod, PyObject* args) {
   (void)mod;
@@ -523,6 +857,11 @@ static PyMethodDef methods[] = {
     {"conv", (PyCFunction)(void (*)(void))py_conv, METH_FASTCALL, NULL},
     {"scan", (PyCFunction)(void (*)(void))py_scan, METH_FASTCALL, NULL},
     {"norm", (PyCFunction)(void (*)(void))py_norm, METH_FASTCALL, NULL},
+    {"setup_dense", py_setup_dense, METH_VARARGS, NULL},
+    {"linear", (PyCFunction)(void (*)(void))py_linear, METH_FASTCALL, NULL},
+    {"linear_back", (PyCFunction)(void (*)(void))py_linear_back, METH_FASTCALL, NULL},
+    {"layer_norm", (PyCFunction)(void (*)(void))py_layer_norm, METH_FASTCALL, NULL},
+    {"layer_norm_back", (PyCFunction)(void (*)(void))py_layer_norm_back, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -1,4 +1,4 @@
-"""Operators of a state space layer on GB300: short causal convolution, selective scan, norm.
+"""Operators of a state space layer on GB300: short causal convolution, selective scan, norms, projections.
 
 The methods here are part of ``Handle`` (see the package's docstring); like the rest of the
 binding they check and marshal arguments, and every step runs in the library's CUDA kernels.
@@ -7,6 +7,11 @@ binding they check and marshal arguments, and every step runs in the library's C
     u  = short_conv(u, w, bias, conv_state)              # x | B | C of the layer's input projection
     y  = ssm_scan(x, dt, A, B, C, ssm_state, D=D, z=z, dt_bias=dt_bias)
     y  = ssm_step(...); u = short_conv_step(...)         # the same states, one token a sequence
+
+    h, st = layer_norm(x, w, b, residual, stats=True)    # the other norm, and its gradients
+    dx, dw, db = layer_norm_backward(dh, residual, w, st, dresidual)
+    y  = linear(codes, w, bias, residual, act="silu", x_scale=scale, w_scale=ws)   # bfloat16, float32 or e4m3
+    dx, dw, db = linear_backward(dy, x, w, pre, act="silu")
 
 A batch of prompts is dense, [S, T, ...], or packed, [tokens, ...] with ``offsets`` (int32 [S + 1]
 on the device).  States live in pools, [n_slots, ...], and are updated in place; ``slots`` (int32
@@ -28,6 +33,7 @@ STATUS_INDEX = 4
 BINDING = os.path.join(os.path.dirname(os.path.abspath(__file__)),
                        "_layer_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 _OUT = {"io": 0, "e4m3": 1, "int8": 2}
+_ACT = {"none": 0, "silu": 1, "gelu": 2}
 
 
 def _dense(x, dtype=None):
@@ -40,6 +46,10 @@ def _empty(x, shape):
 
 def _bytes(x, n):
     return x.new_empty(n, dtype=torch.uint8)
+
+
+def _new(x, shape, dtype):
+    return x.new_empty(shape, dtype=dtype)
 
 
 def _current_stream(index):
@@ -69,7 +79,17 @@ def declare(lib):
     lib.vla_ssm_scan.argtypes = [vp] * 11 + [cll] * 3 + [vp] * 2 + [cll] * 5 + [vp, ci, ci, vp, ctypes.c_size_t, vp]
     lib.vla_ssm_workspace.argtypes = [vp, cll, cll, cll, ci, cll, cll, cll, ci, ctypes.POINTER(ctypes.c_size_t)]
     lib.vla_rms_norm.argtypes = [vp] * 6 + [cll] * 5 + [cf, ci, ci, ci, ci, vp]
-    for fn in (lib.vla_short_conv, lib.vla_ssm_scan, lib.vla_ssm_workspace, lib.vla_rms_norm):
+    size = ctypes.POINTER(ctypes.c_size_t)
+    lib.vla_linear.argtypes = [vp] * 9 + [cll] * 3 + [vp, ci, ci, ci, vp, ctypes.c_size_t, vp]
+    lib.vla_linear_workspace.argtypes = [vp] * 3 + [cll] * 3 + [vp, ci, ci, size]
+    lib.vla_linear_backward.argtypes = [vp] * 8 + [cll] * 3 + [vp, ci, ci, vp, ctypes.c_size_t, vp]
+    lib.vla_linear_backward_workspace.argtypes = [vp] * 4 + [ci] * 3 + [cll] * 3 + [vp, ci, ci, size]
+    lib.vla_layer_norm.argtypes = [vp] * 7 + [cll] * 5 + [cf, ci, ci, vp]
+    lib.vla_layer_norm_backward.argtypes = [vp] * 9 + [cll] * 2 + [vp, ci, ci, vp, ctypes.c_size_t, vp]
+    lib.vla_layer_norm_backward_workspace.argtypes = [vp, cll, cll, size]
+    dense = (lib.vla_linear, lib.vla_linear_workspace, lib.vla_linear_backward, lib.vla_linear_backward_workspace,
+             lib.vla_layer_norm, lib.vla_layer_norm_backward, lib.vla_layer_norm_backward_workspace)
+    for fn in (lib.vla_short_conv, lib.vla_ssm_scan, lib.vla_ssm_workspace, lib.vla_rms_norm, *dense):
         fn.restype = ci
     try:
         loader = importlib.machinery.ExtensionFileLoader(f"{__package__}._layer_binding", BINDING)
@@ -84,6 +104,7 @@ def declare(lib):
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
     native.setup(*at, torch.float32, torch.bfloat16, torch.int32, torch.float8_e4m3fn, torch.int8,
                  torch.empty_like, _dense, _empty, _bytes, stream)
+    native.setup_dense(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in dense], _new)
     _native = native
 
 
@@ -99,8 +120,15 @@ def _raw(stream):
     return None if stream is None else stream.cuda_stream
 
 
+def _activation(act):
+    kind = _ACT.get(act)
+    if kind is None:
+        raise ValueError(f"act must be one of {sorted(_ACT)}")
+    return kind
+
+
 class LayerOps:
-    """Methods of Handle: the state space layer's operators."""
+    """Methods of Handle: the state space layer's operators, and the products and layer norms around them."""
 
     def _layer_fail(self, code):
         from . import VlaError
@@ -155,3 +183,52 @@ class LayerOps:
             raise ValueError(f"out must be one of {sorted(_OUT)}")
         with _on(stream):
             return _native.norm(self, x, w, residual, y, eps, kind, group, scale, _raw(stream))
+
+    def linear(self, x, w, bias=None, residual=None, y=None, *, act: str = "none", pre=None, x_scale=None, w_scale=None,
+               dtype=None, stream=None):
+        """y = act(v) + residual, v = x w^T + bias, the product of a projection with its epilogue.
+
+        x [..., K] and w [N, K] in one type, bfloat16, float32 or e4m3 codes, their rows evenly
+        spaced; codes stand for codes * x_scale[..., None] (rms_norm's scales) and codes *
+        w_scale[:, None], [...] and [N] float32 (None: 1).  bias [N] float32.  act "none", "silu"
+        or "gelu" (v Phi(v)).  Returns y [..., N] in `dtype`: x's type, bfloat16 for codes, or
+        float32.  residual and pre have y's shape and type; pre receives v, for the gradient; y may
+        be the residual itself."""
+        kind = _activation(act)
+        with _on(stream):
+            return _native.linear(self, x, w, bias, residual, y, kind, pre, x_scale, w_scale, dtype, _raw(stream))
+
+    def linear_backward(self, dy, x, w, pre=None, dx=None, dw=None, db=None, *, act: str = "none", input: bool = True,
+                        weight: bool = True, bias: bool = True, stream=None):
+        """Gradients of linear: g = dy * act'(pre); dx = g w, dw = g^T x, db = the sum of g's rows.
+
+        dy [..., N], x [..., K], w [N, K] and pre [..., N] (what linear left there; not needed
+        without an activation) in one type, bfloat16 or float32.  Returns (dx, dw, db), dx and dw in
+        that type, db float32; None in the place of those that input, weight or bias say not to
+        compute.  The residual's gradient is dy."""
+        kind = _activation(act)
+        with _on(stream):
+            return _native.linear_back(self, dy, x, w, pre, kind, dx if input else False, dw if weight else False,
+                                       db if bias else False, _raw(stream))
+
+    def layer_norm(self, x, w, b=None, residual=None, y=None, *, eps: float = 1e-5, stats=False, stream=None):
+        """y = (r - mean(r)) / sqrt(var(r) + eps) * w + b over the last dimension, r = x + residual.
+
+        x [..., D] float32 or bfloat16, its rows evenly spaced; w, b [D] float32; residual (x's
+        shape, float32 or bfloat16) is updated in place to r.  Returns y in x's type; with stats=True
+        (y, stats), stats [..., 2] float32 the rows' mean and 1 / sqrt(var + eps) for the gradient."""
+        if stats is None:
+            stats = False
+        with _on(stream):
+            return _native.layer_norm(self, x, w, b, residual, y, eps, stats, _raw(stream))
+
+    def layer_norm_backward(self, dy, x, w, stats, dresidual=None, dx=None, dw=None, db=None, *, bias: bool = True,
+                            stream=None):
+        """Gradients of layer_norm: dx = (a - mean(a) - h mean(a h)) rstd + dresidual, a = dy w and h the
+        normalised row; dw = the rows' sum of dy h, db = that of dy.
+
+        dy [..., D]; x what was normalised (x, or the residual that the call left), stats as
+        layer_norm returned them; dresidual (x's shape and type) the gradient that the residual
+        stream already has.  dx has x's type.  Returns (dx, dw, db), dw and db float32; db None without bias."""
+        with _on(stream):
+            return _native.layer_norm_back(self, dy, x, w, stats, dresidual, dx, dw, db if bias else False, _raw(stream))
