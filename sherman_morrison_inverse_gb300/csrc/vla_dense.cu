@@ -56,7 +56,7 @@ vla::ProductArgs linear_product(vla_handle_t h, const void* x, const void* w, lo
   vla::ProductArgs p{};
   p.a = x; p.b = w;
   p.M = M; p.N = N; p.Kd = K;
-  p.a_m = rows[0]; p.a_k = 1; p.b_n = rows[1]; p.b_k = 1;
+  p.a_row = rows[0]; p.b_row = rows[1];
   p.sm_count = h->sm_count;
   p.status = h->status;
   return p;
@@ -81,16 +81,18 @@ BackPlan back_plan(vla_handle_t h, const void* dy, const void* x, const void* w,
   b.part_bytes = want_db ? up16(vla::slope_ws(M, N, h->sm_count)) : 0;
   const void* g = need_g ? nullptr : dy;
   const long long g_row = need_g ? b.slope.g_row : rows[0];
-  b.dx.a = g; b.dx.a_m = g_row; b.dx.a_k = 1;
-  b.dx.b = w; b.dx.b_n = 1; b.dx.b_k = rows[2];
+  b.dx.a = g; b.dx.a_row = g_row;
+  b.dx.b = w; b.dx.b_row = rows[2]; b.dx.b_mn = true;
   b.dx.M = M; b.dx.N = K; b.dx.Kd = N;
-  b.dw.a = g; b.dw.a_m = 1; b.dw.a_k = g_row;
-  b.dw.b = x; b.dw.b_n = 1; b.dw.b_k = rows[1];
+  b.dw.a = g; b.dw.a_row = g_row; b.dw.a_mn = true;
+  b.dw.b = x; b.dw.b_row = rows[1]; b.dw.b_mn = true;
   b.dw.M = N; b.dw.N = K; b.dw.Kd = M;
   b.dx.sm_count = b.dw.sm_count = h->sm_count;
   b.dx.status = b.dw.status = h->status;
   b.dx.out.y_bf16 = b.dw.out.y_bf16 = io == VLA_BF16;
-  b.ws_bytes = b.g_bytes + b.part_bytes;
+  const int mat = io == VLA_BF16 ? VLA_MAT_BF16 : VLA_MAT_F32;
+  const size_t x_ws = want_dx && N ? vla::product_ws(b.dx, mat) : 0, w_ws = want_dw && M ? vla::product_ws(b.dw, mat) : 0;
+  b.ws_bytes = b.g_bytes + b.part_bytes + (x_ws > w_ws ? x_ws : w_ws);   // one product after the other
   return b;
 }
 

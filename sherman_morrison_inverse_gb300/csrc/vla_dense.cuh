@@ -86,25 +86,14 @@ struct Epilogue {
   bool y_bf16;
 };
 
-template <typename T>
-__device__ __forceinline__ void epilogue_one(const Epilogue& e, float v, long long m, long long n) {
-  constexpr bool FAST = sizeof(T) == 2;
-  if (e.x_scale) v *= e.x_scale[m];
-  if (e.w_scale) v *= e.w_scale[n];
-  if (e.bias) v += e.bias[n];
-  if (e.pre) static_cast<T*>(e.pre)[m * e.pre_row + n] = from_f32<T>(v);
-  v = activate<FAST>(v, e.act);
-  if (e.residual) v += to_f32<T>(static_cast<const T*>(e.residual)[m * e.res_row + n]);
-  static_cast<T*>(e.y)[m * e.y_row + n] = from_f32<T>(v);
-}
-
-// C [M, N] = A B over Kd: element (m, k) of A at a[m * a_m + k * a_k], (k, n) of B at b[n * b_n + k * b_k];
-// of each operand one of its two strides is 1.
+// C [M, N] = sum over Kd of A B.  A lies in memory as M rows of Kd adjacent values, or (a_mn) as Kd rows of M;
+// B as N rows of Kd, or (b_mn) as Kd rows of N.  Built: neither, b_mn alone, both; e4m3: neither.
 struct ProductArgs {
   const void* a;
   const void* b;
   long long M, N, Kd;
-  long long a_m, a_k, b_n, b_k;
+  long long a_row, b_row;   // distance of rows in values
+  bool a_mn, b_mn;
   Epilogue out;
   void* ws;
   int sm_count;

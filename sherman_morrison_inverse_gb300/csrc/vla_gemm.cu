@@ -1,0 +1,646 @@
+// Matrix products on the tensor cores: C [M, N] = sum over terms of A B, with an epilogue.
+//
+// Two CTAs of a cluster share a tile of 256 x BN outputs (tcgen05.mma.cta_group::2): each holds 128 rows of A
+// and BN / 2 columns of B in shared memory and 128 rows of the float32 sums in tensor memory.  Clusters are
+// persistent and walk the tiles in blocks of 8 tiles of M, so that what runs at one time shares rows and columns in L2.
+//   warp 0     one thread keeps a ring of kStages stages filled by TMA: 128 bytes of Kd of both operands (64
+//              bfloat16 or 128 e4m3), 128-byte swizzle.  Both CTAs' copies complete on the leader's barrier.
+//   warp 1     of the leader issues the products of both CTAs, four a stage, into one of two accumulators.
+//   warps 2..9 take the other accumulator out: 32 columns at a time from tensor memory through shared memory,
+//              so that a row's values are adjacent over lanes, and then through the epilogue to memory.
+// Operands lie in memory with Kd adjacent (as in x w^T) or with M or N adjacent (as in g w and g^T x): tiles
+// of 64 along what is adjacent, and the matrix descriptors say which.
+// float32 operands arrive as three bfloat16 terms each (x = x1 + x2 + x3 to 2^-24): six products, the small ones
+// first.  Kd is split over clusters where there are fewer tiles than clusters; the parts are then added in order.
+// Every wait is bounded: one that runs out sets the handle's timeout flag, and the cluster drains and returns.
+#include <cuda.h>   // CUtensorMap and the encode entry point's types (resolved at run time)
+
+#include <atomic>
+
+#include "vla_dense.cuh"
+#include "vla_tc.cuh"
+
+namespace vla {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kGroup = 8;          // tiles of M that are walked together
+constexpr int kChunk = 32 * 32 * 4;   // a warp's staging: 32 rows of 32 float32
+
+// Passes over the terms of the operands: float32 takes (a, b) = 3-1, 1-3, 2-2, 2-1, 1-2, 1-1.
+constexpr int kPasses = 6;
+__device__ __forceinline__ int term_a(int pass) { return (0x201100 >> (4 * (5 - pass))) & 3; }
+__device__ __forceinline__ int term_b(int pass) { return (0x021010 >> (4 * (5 - pass))) & 3; }
+
+template <int BN>
+struct Cfg {
+  static constexpr int stages = BN == 256 ? 6 : 8;
+  static constexpr uint32_t a_bytes = 128 * 128, b_bytes = BN / 2 * 128, stage = a_bytes + b_bytes;
+  static constexpr uint32_t o_chunk = stages * stage, o_bar = o_chunk + 8 * kChunk;
+  static constexpr uint32_t bars = 2 * stages + 5;
+  static constexpr uint32_t bytes = o_bar + 8 * bars + 16;
+  static constexpr uint32_t cols = 2 * BN;
+};
+
+struct GemmArgs {
+  long long M, N;
+  int tiles_m, tiles_n, splits;
+  int k_iters, passes;      // stages of one pass over Kd; passes over the terms
+  float* partial;           // [splits][M][N] where splits > 1
+  Epilogue out;
+  bool y_vec, res_vec, pre_vec;
+  unsigned long long limit;   // of a wait, in ns: 2 s, and 4 us for every stage of a tile
+  DevStatus* status;
+};
+
+__device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024u >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// One product of both CTAs for 32 bytes of Kd, issued by the lane whose `one` is set.  The whole warp runs the loop
+// around it, predicated and not branched, so that descriptors stay in uniform registers.
+template <bool E4M3>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t one) {
+  if (E4M3)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(one)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(one)
+        : "memory");
+}
+// Arrive on `bar` of both CTAs once the products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"((unsigned short)3), "r"(one)
+      : "memory");
+}
+// A tile into this CTA's shared memory, its bytes counted on a barrier of either CTA (a cluster address).
+__device__ __forceinline__ void tma_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void alloc_pair(uint32_t slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void dealloc_pair(uint32_t t, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(cols) : "memory");
+}
+
+// Waits for a phase that the other CTA can complete too; false when the limit runs out or the CTA has failed.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
+  const unsigned long long start = globaltimer_ns();
+  while (!mbar_try_wait_cluster(bar, parity)) {
+    if (*failed) return false;
+    if (globaltimer_ns() - start > limit) {
+      *failed = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  return wait_slow(bar, parity, limit, failed);
+}
+
+struct Tile {
+  int m, n, split;
+};
+__device__ __forceinline__ Tile tile_at(int t, int tiles_m, int tiles_n) {
+  const int all = tiles_m * tiles_n, split = t / all, r = t - split * all;
+  const int span = kGroup * tiles_n, group = r / span, at = r - group * span;
+  const int first = group * kGroup, size = tiles_m - first < kGroup ? tiles_m - first : kGroup;
+  const int n = at / size;
+  return {first + at - n * size, n, split};
+}
+
+// Four adjacent values of a row, those from `left` on absent.
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, bool vec, int left, float (&v)[4]) {
+  if (vec && left >= 4) {
+    const Vec<T, 4> x = ld_vec<T, 4>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = to_f32<T>(x.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = i < left ? to_f32<T>(p[i]) : 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, bool vec, int left, const float (&v)[4]) {
+  if (vec && left >= 4) {
+    Vec<T, 4> x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x.v[i] = from_f32<T>(v[i]);
+    st_vec<T, 4>(p, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < left) p[i] = from_f32<T>(v[i]);
+  }
+}
+
+// The epilogue of 32 rows x 32 columns in shared memory (rows of 32 float32, 16-byte pieces c of row r at
+// c ^ (r & 7)): a lane has 4 adjacent columns of every fourth row.
+template <typename T>
+__device__ __forceinline__ void chunk_out(const GemmArgs& g, uint32_t chunk, long long m0, long long n0, int lane) {
+  const Epilogue& e = g.out;
+  const long long n = n0 + (lane & 7) * 4;
+  const int left = g.N - n < 4 ? (int)(g.N - n) : 4;
+  if (left <= 0) return;
+  float bias[4] = {}, scale[4] = {1.f, 1.f, 1.f, 1.f};
+  if (e.bias) load4<float>(e.bias + n, false, left, bias);
+  if (e.w_scale) load4<float>(e.w_scale + n, false, left, scale);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = i * 4 + (lane >> 3);
+    const long long m = m0 + r;
+    if (m >= g.M) return;
+    float v[4], res[4] = {};
+    if (e.residual) load4<T>(static_cast<const T*>(e.residual) + m * e.res_row + n, g.res_vec, left, res);
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(chunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
+    const float xs = e.x_scale ? e.x_scale[m] : 1.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j] * xs, scale[j], bias[j]);
+    if (e.pre) store4<T>(static_cast<T*>(e.pre) + m * e.pre_row + n, g.pre_vec, left, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = activate<sizeof(T) == 2>(v[j], e.act) + res[j];
+    store4<T>(static_cast<T*>(e.y) + m * e.y_row + n, g.y_vec, left, v);
+  }
+}
+
+template <int BN, bool A_MN, bool B_MN, bool E4M3>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemmArgs g) {
+  using C = Cfg<BN>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = smem_u32(smem);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::o_bar);
+  uint64_t *empty = full + C::stages, *acc_full = empty + C::stages, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile uint32_t* failed = slot + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int n_tiles = g.tiles_m * g.tiles_n * g.splits, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int all_iters = g.k_iters * g.passes;
+  // stages of split s: [s * all / splits, (s + 1) * all / splits)
+  auto k_begin = [&](int s) { return (int)((long long)all_iters * s / g.splits); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::stages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_empty + i, 16);
+    }
+    mbar_init(drain, 1);
+    *failed = (base & 1023u) != 0;   // the swizzled tiles need it; report rather than run misaligned
+    fence_mbar_init();
+  }
+  if (warp == 1) alloc_pair(smem_u32(slot), C::cols);
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();
+  tc::fence_after_sync();
+  const uint32_t tmem = *slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t rank_m = rank * 128, rank_n = rank * (BN / 2);
+      uint32_t stage = 0, phase = 1, issued = 0;
+      bool ok = !*failed;
+      for (int t = first; ok && t < n_tiles; t += step) {
+        const Tile at = tile_at(t, g.tiles_m, g.tiles_n);
+        const int m0 = at.m * 256 + rank_m, n0 = at.n * BN + rank_n;
+        const int k1 = k_begin(at.split + 1);
+        int k = k_begin(at.split), pass = k / g.k_iters, it = k - pass * g.k_iters;
+        for (; k < k1; ++k) {
+          if (!(ok = wait_for(empty + stage, phase, g.limit, failed))) break;
+          const uint32_t sa = base + stage * C::stage, sb = sa + C::a_bytes;
+          const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
+          if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * C::stage);
+          const int ta = g.passes > 1 ? term_a(pass) : 0, tb = g.passes > 1 ? term_b(pass) : 0;
+          constexpr int BK = E4M3 ? 128 : 64;
+          if (A_MN) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) tma_pair(sa + j * 8192, &map_a, m0 + 64 * j, it * BK, ta, bar);
+          } else {
+            tma_pair(sa, &map_a, it * BK, m0, ta, bar);
+          }
+          if (B_MN) {
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j) tma_pair(sb + j * 8192, &map_b, n0 + 64 * j, it * BK, tb, bar);
+          } else {
+            tma_pair(sb, &map_b, it * BK, n0, tb, bar);
+          }
+          ++issued;
+          if (++stage == C::stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+          if (++it == g.k_iters) {
+            it = 0;
+            ++pass;
+          }
+        }
+      }
+      if (!ok && rank == 0) {   // let what is in flight arrive before the memory is given up
+        const uint32_t n = issued < C::stages ? issued : C::stages;
+        for (uint32_t i = 1; i <= n; ++i) {
+          const uint32_t at = issued - i;
+          mbar_wait_cluster_bounded(full + at % C::stages, at / C::stages & 1);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t one = lane == 0;
+      constexpr uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (A_MN ? 1u << 15 : 0u) |
+                                 (B_MN ? 1u << 16 : 0u) | (uint32_t)(BN >> 3) << 17 | (256u >> 4) << 24;
+      constexpr uint32_t step_a = A_MN ? 2048 >> 4 : 32 >> 4, step_b = B_MN ? 2048 >> 4 : 32 >> 4;
+      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1;
+      bool ok = !*failed;
+      for (int t = first; ok && t < n_tiles; t += step) {
+        const int split = t / (g.tiles_m * g.tiles_n);
+        const int k0 = k_begin(split), k1 = k_begin(split + 1);
+        if (!(ok = wait_for(acc_empty + buf, buf_phase, g.limit, failed))) break;
+        tc::fence_after_sync();
+        const uint32_t d = tmem + buf * BN;
+        for (int k = k0; k < k1; ++k) {
+          if (!(ok = wait_for(full + stage, phase, g.limit, failed))) break;
+          tc::fence_after_sync();
+          const uint32_t sa = base + stage * C::stage;
+          const uint64_t da = desc128(sa, 8192), db = desc128(sa + C::a_bytes, 8192);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma_pair<E4M3>(d, da + i * step_a, db + i * step_b, idesc, k > k0 || i > 0, one);
+          commit_pair(smem_u32(empty + stage), one);
+          if (++stage == C::stages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        commit_pair(smem_u32(acc_full + buf), one);
+        if (++buf == 2) {
+          buf = 0;
+          buf_phase ^= 1;
+        }
+      }
+      if (!ok) {
+        commit_pair(smem_u32(drain), one);
+        mbar_wait_cluster_bounded(drain, 0);
+      }
+    }
+  } else {
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t chunk = base + C::o_chunk + (warp - 2) * kChunk;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    uint32_t buf = 0, phase = 0;
+    for (int t = first; t < n_tiles; t += step) {
+      const Tile at = tile_at(t, g.tiles_m, g.tiles_n);
+      if (!wait_for(acc_full + buf, phase, g.limit, failed)) break;
+      tc::fence_after_sync();
+      const long long m0 = (long long)at.m * 256 + rank * 128 + quad * 32;
+#pragma unroll 1
+      for (int c = 0; c < BN / 64; ++c) {
+        const int col = half * (BN / 2) + c * 32;
+        float v[32];
+        tc::tmem_ld32(tmem + buf * BN + col + lanes, v);
+        if (c == BN / 64 - 1) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(acc_empty + buf), 0));
+        }
+        const long long n0 = (long long)at.n * BN + col;
+        __syncwarp();   // the last chunk has been read
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(chunk + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                       "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3])
+                       : "memory");
+        __syncwarp();
+        if (g.splits > 1) {
+          const long long n = n0 + (lane & 7) * 4;
+          const int left = g.N - n < 4 ? (int)(g.N - n) : 4;
+          float* p = g.partial + (long long)at.split * g.M * g.N;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            float o[4];
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
+                         : "r"(chunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
+            if (left > 0 && m0 + r < g.M) store4<float>(p + (m0 + r) * g.N + n, g.N % 4 == 0, left, o);
+          }
+        } else if (g.out.y_bf16) {
+          chunk_out<__nv_bfloat16>(g, chunk, m0, n0, lane);
+        } else {
+          chunk_out<float>(g, chunk, m0, n0, lane);
+        }
+      }
+      if (++buf == 2) {
+        buf = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_sync_all();   // neither CTA leaves while the other can still signal it
+  tc::fence_after_sync();
+  if (warp == 1) dealloc_pair(tmem, C::cols);
+  if (threadIdx.x == 0 && *failed) atomicOr(&g.status->flags, kStatusTimeout);
+}
+
+// ---------------------------------------------------------------------------------------------
+// parts of a split Kd, added in their order, and the epilogue; without parts the sum is 0
+
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(const float* partial, int parts, const GemmArgs g) {
+  const long long across = (g.N + 3) / 4, all = g.M * across;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+    const long long m = i / across, n = (i - m * across) * 4;
+    const int left = g.N - n < 4 ? (int)(g.N - n) : 4;
+    float v[4] = {}, p[4], bias[4] = {}, scale[4] = {1.f, 1.f, 1.f, 1.f}, res[4] = {};
+    const Epilogue& e = g.out;
+    if (e.residual) load4<T>(static_cast<const T*>(e.residual) + m * e.res_row + n, g.res_vec, left, res);
+    if (e.bias) load4<float>(e.bias + n, false, left, bias);
+    if (e.w_scale) load4<float>(e.w_scale + n, false, left, scale);
+    for (int s = 0; s < parts; ++s) {
+      load4<float>(partial + ((long long)s * g.M + m) * g.N + n, g.N % 4 == 0, left, p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += p[j];
+    }
+    const float xs = e.x_scale ? e.x_scale[m] : 1.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j] * xs, scale[j], bias[j]);
+    if (e.pre) store4<T>(static_cast<T*>(e.pre) + m * e.pre_row + n, g.pre_vec, left, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = activate<sizeof(T) == 2>(v[j], e.act) + res[j];
+    store4<T>(static_cast<T*>(e.y) + m * e.y_row + n, g.y_vec, left, v);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// operands that TMA cannot read as they are: float32 as three bfloat16 terms, rows off 16-byte boundaries
+
+// One row piece of 8 values a thread.  x1 = x rounded, x2 = x - x1 rounded, x3 = x - x1 - x2 rounded: the differences
+// are exact.  A value beyond bfloat16's range, an infinity or a NaN has only its first term.
+template <typename I>
+__global__ void __launch_bounds__(256) pack_kernel(const I* src, long long rows, long long cols, long long row, I* same,
+                                                   __nv_bfloat16* terms, long long out_row, bool vec) {
+  const long long across = (cols + 7) / 8, all = rows * across;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+    const long long r = i / across, c = (i - r * across) * 8;
+    const I* p = src + r * row + c;
+    const int left = cols - c < 8 ? (int)(cols - c) : 8;
+    if constexpr (sizeof(I) == 4) {
+      float v[8];
+      if (vec && left == 8) {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : 0.f;
+      }
+      Vec<__nv_bfloat16, 8> o[3];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o[0].v[j] = __float2bfloat16_rn(v[j]);
+        float rest = v[j] - __bfloat162float(o[0].v[j]);
+        if (!isfinite(rest)) rest = 0.f;
+        o[1].v[j] = __float2bfloat16_rn(rest);
+        o[2].v[j] = __float2bfloat16_rn(rest - __bfloat162float(o[1].v[j]));
+      }
+#pragma unroll
+      for (int t = 0; t < 3; ++t) st_vec<__nv_bfloat16, 8>(terms + (t * rows + r) * out_row + c, o[t]);
+    } else {
+      Vec<I, 8> o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o.v[j] = p[j < left ? j : 0];   // the row's end is not read by anyone
+      st_vec<I, 8>(same + r * out_row + c, o);
+    }
+  }
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_fn() {
+  static EncodeTiled fn = []() -> EncodeTiled {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// An operand as it lies in memory: rows of `cols` adjacent values.
+struct Operand {
+  const void* p;
+  long long rows, cols, row;   // row: distance of rows in values
+  int size;                    // bytes a value
+  bool mn;                     // what is adjacent is M or N, not Kd
+  bool pack;                   // TMA reads a copy
+  size_t bytes;                // of the copy
+  long long out_row;
+};
+
+Operand operand(const void* p, long long side, long long kd, long long row, bool mn, int size) {
+  Operand o{};
+  o.p = p;
+  o.size = size;
+  o.mn = mn;
+  o.rows = mn ? kd : side;
+  o.cols = mn ? side : kd;
+  o.row = row;
+  o.out_row = (o.cols + 15) / 16 * 16;
+  if (o.rows == 1) o.row = o.out_row;   // not used
+  o.pack = size == 4 || (reinterpret_cast<uintptr_t>(p) & 15u) || o.row * size % 16 || o.row < o.cols;
+  o.bytes = o.pack ? (size_t)o.rows * o.out_row * (size == 4 ? 6 : size) : 0;
+  return o;
+}
+
+// box: adjacent values x rows of a tile
+bool encode(CUtensorMap* m, const Operand& o, const void* base, int box_x, int box_y) {
+  EncodeTiled fn = encode_fn();
+  if (!fn) return false;
+  const int size = o.size == 1 ? 1 : 2;
+  const cuuint64_t row = (cuuint64_t)((o.pack ? o.out_row : o.row) * size);
+  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, o.size == 4 ? 3ull : 1ull};
+  const cuuint64_t strides[2] = {row, row * (cuuint64_t)o.rows};
+  const cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, o.size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t pack(const Operand& o, void* to, int sm_count, cudaStream_t s) {
+  const long long pieces = o.rows * ((o.cols + 7) / 8), want = (pieces + 255) / 256, most = 16LL * sm_count;
+  const unsigned int ctas = (unsigned int)(want < most ? want : most);
+  const bool vec = ((reinterpret_cast<uintptr_t>(o.p) | (uintptr_t)(o.row * o.size)) & 15u) == 0;
+  __nv_bfloat16* terms = static_cast<__nv_bfloat16*>(to);
+  if (o.size == 4)
+    pack_kernel<float><<<ctas, 256, 0, s>>>(static_cast<const float*>(o.p), o.rows, o.cols, o.row, nullptr, terms, o.out_row, vec);
+  else if (o.size == 2)
+    pack_kernel<__nv_bfloat16><<<ctas, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(o.p), o.rows, o.cols, o.row, terms, nullptr, o.out_row, vec);
+  else
+    pack_kernel<unsigned char><<<ctas, 256, 0, s>>>(static_cast<const unsigned char*>(o.p), o.rows, o.cols, o.row,
+                                                    static_cast<unsigned char*>(to), nullptr, o.out_row, vec);
+  return cudaGetLastError();
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Where four values of a row can move as one.
+bool four(const void* p, long long row, size_t size) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)((size_t)row * size)) & (4 * size - 1)) == 0;
+}
+
+struct Plan {
+  Operand a, b;
+  int bn, splits, tiles_m, tiles_n, k_iters, passes;
+  size_t ws;
+};
+
+int size_of(int mat) { return mat == kMatF32 ? 4 : mat == kMatBf16 ? 2 : 1; }
+
+Plan plan_of(const ProductArgs& p, int mat) {
+  Plan q{};
+  const int size = size_of(mat);
+  q.a = operand(p.a, p.M, p.Kd, p.a_row, p.a_mn, size);
+  q.b = operand(p.b, p.N, p.Kd, p.b_row, p.b_mn, size);
+  q.passes = mat == kMatF32 ? kPasses : 1;
+  q.k_iters = (int)((p.Kd + (mat == kMatE4m3 ? 127 : 63)) / (mat == kMatE4m3 ? 128 : 64));
+  q.tiles_m = (int)((p.M + 255) / 256);
+  // Cost of a choice in stages of a 256 x 256 tile: waves of tiles, each with its stages and about 3 of latency at its
+  // ends, and the parts' way through memory.
+  const int clusters = p.sm_count / 2 > 0 ? p.sm_count / 2 : 1;
+  double best = 1e300;
+  for (int bn = 256; bn >= 128; bn /= 2) {
+    const long long tn = (p.N + bn - 1) / bn, tiles = q.tiles_m * tn;
+    const int most = q.k_iters * q.passes / 4 < 16 ? q.k_iters * q.passes / 4 : 16;
+    for (int s = 1; s == 1 || (s <= most && tiles * s <= 2 * clusters); ++s) {
+      const long long waves = (tiles * s + clusters - 1) / clusters;
+      double cost = (double)waves * ((double)q.k_iters * q.passes / s * (bn == 256 ? 1.0 : 0.55) + 3.0);
+      if (s > 1) cost += 8.0 + (double)s * p.M * p.N * 8.0 / 1.2e6;
+      if (cost < best) {
+        best = cost;
+        q.bn = bn;
+        q.splits = s;
+        q.tiles_n = (int)tn;
+      }
+    }
+  }
+  if (p.Kd == 0) q.splits = 0;
+  q.ws = p.Kd == 0 ? 0 : up256(q.a.bytes) + up256(q.b.bytes) + (q.splits > 1 ? (size_t)q.splits * p.M * p.N * 4 : 0);
+  return q;
+}
+
+template <int BN, bool A_MN, bool B_MN, bool E4M3>
+cudaError_t launch(const Plan& q, const GemmArgs& g, const void* a, const void* b, cudaStream_t s) {
+  CUtensorMap ma, mb;
+  constexpr int BK = E4M3 ? 128 : 64;
+  if (!encode(&ma, q.a, a, A_MN ? 64 : BK, A_MN ? BK : 128) || !encode(&mb, q.b, b, B_MN ? 64 : BK, B_MN ? BK : BN / 2))
+    return cudaErrorInvalidValue;
+  auto kern = gemm_kernel<BN, A_MN, B_MN, E4M3>;
+  constexpr int bytes = (int)Cfg<BN>::bytes;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  // clusters that fit at once, asked for once a kernel and device (the first 64)
+  static std::atomic<int> known[64];
+  int clusters = device < 64 ? known[device].load(std::memory_order_relaxed) : 0;
+  if (clusters == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(2);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = bytes;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    c.attrs = &attr;
+    c.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &c);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) clusters = 1;
+    if (device < 64) known[device].store(clusters, std::memory_order_relaxed);
+  }
+  const long long tiles = (long long)g.tiles_m * g.tiles_n * g.splits;
+  if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
+  kern<<<(unsigned int)(2 * (tiles < clusters ? tiles : clusters)), kThreads, bytes, s>>>(ma, mb, g);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t product_ws(const ProductArgs& p, int mat) { return plan_of(p, mat).ws; }
+
+cudaError_t launch_product(const ProductArgs& p, int mat, cudaStream_t s) {
+  const Plan q = plan_of(p, mat);
+  GemmArgs g{};
+  g.M = p.M; g.N = p.N;
+  g.tiles_m = q.tiles_m; g.tiles_n = q.tiles_n; g.splits = q.splits;
+  g.k_iters = q.k_iters; g.passes = q.passes;
+  g.out = p.out;
+  g.status = p.status;
+  g.limit = kWaitLimitNs + 4000ull * (unsigned long long)q.k_iters * q.passes;
+  const size_t ysize = p.out.y_bf16 ? 2 : 4;
+  g.y_vec = four(p.out.y, p.out.y_row, ysize);
+  g.res_vec = four(p.out.residual, p.out.res_row, ysize);
+  g.pre_vec = four(p.out.pre, p.out.pre_row, ysize);
+  char* ws = static_cast<char*>(p.ws);
+  const void *a = p.a, *b = p.b;
+  cudaError_t e = cudaSuccess;
+  if (q.splits > 0) {
+    if (q.a.pack) e = pack(q.a, const_cast<void*>(a = ws), p.sm_count, s);
+    if (q.b.pack && e == cudaSuccess) e = pack(q.b, const_cast<void*>(b = ws + up256(q.a.bytes)), p.sm_count, s);
+    if (e != cudaSuccess) return e;
+    g.partial = reinterpret_cast<float*>(ws + up256(q.a.bytes) + up256(q.b.bytes));
+    auto run = [&](auto bn) -> cudaError_t {
+      constexpr int BN = decltype(bn)::value;
+      if (mat == kMatE4m3) return launch<BN, false, false, true>(q, g, a, b, s);
+      if (!q.a.mn) return q.b.mn ? launch<BN, false, true, false>(q, g, a, b, s) : launch<BN, false, false, false>(q, g, a, b, s);
+      return launch<BN, true, true, false>(q, g, a, b, s);
+    };
+    e = q.bn == 256 ? run(std::integral_constant<int, 256>()) : run(std::integral_constant<int, 128>());
+    if (e != cudaSuccess || q.splits == 1) return e;
+  }
+  const long long pieces = p.M * ((p.N + 3) / 4), want = (pieces + 255) / 256, most = 16LL * p.sm_count;
+  const unsigned int ctas = (unsigned int)(want < most ? want : most);
+  if (p.out.y_bf16) join_kernel<__nv_bfloat16><<<ctas, 256, 0, s>>>(g.partial, q.splits, g);
+  else join_kernel<float><<<ctas, 256, 0, s>>>(g.partial, q.splits, g);
+  return cudaGetLastError();
+}
+
+}  // namespace vla

@@ -437,7 +437,7 @@ def test_a_feed_forward_block_and_its_gradients(vla, dtype):
     # independently; six of them add up to less than 6 x 2^-8 of the norm.  float32: 2^-20.
     tol = 6 * U16 if dtype == "bf16" else 2.0 ** -19
     for g, w in zip((got_y, *got), (y, *want)):
-        assert float((g.double() - w).norm() / w.norm()) <= tol
+        assert float((g.double() - w.detach()).norm() / w.detach().norm()) <= tol
 
 
 def test_a_block_captured_in_a_graph_on_another_stream(vla):
