@@ -11,7 +11,9 @@
 // Operands lie in memory with Kd adjacent (as in x w^T) or with M or N adjacent (as in g w and g^T x): tiles
 // of 64 along what is adjacent, and the matrix descriptors say which.
 // float32 operands arrive as three bfloat16 terms each (x = x1 + x2 + x3 to 2^-24): six products, the small ones
-// first.  Kd is split over clusters where there are fewer tiles than clusters; the parts are then added in order.
+// first.  Where the result is float32, sums stay in tensor memory for 4 stages and are then added to float32 registers:
+// a tensor core cuts the bits off that an addition shifts out, always towards zero, and the error of a chain of them
+// grows with its length (K = 1161: 6.8e-7 of the result without, against 3.6e-7 of plain float32 products).  Kd is split over clusters where there are fewer tiles than clusters; the parts are then added in order.
 // Every wait is bounded: one that runs out sets the handle's timeout flag, and the cluster drains and returns.
 #include <cuda.h>   // CUtensorMap and the encode entry point's types (resolved at run time)
 
@@ -25,6 +27,7 @@ namespace {
 
 constexpr int kThreads = 320;
 constexpr int kGroup = 8;          // tiles of M that are walked together
+constexpr int kPart = 4;           // stages that add up in tensor memory before float32 results take them over
 constexpr int kChunk = 32 * 32 * 4;   // a warp's staging: 32 rows of 32 float32
 
 // Passes over the terms of the operands: float32 takes (a, b) = 3-1, 1-3, 2-2, 2-1, 1-2, 1-1.
@@ -129,15 +132,12 @@ __device__ __forceinline__ Tile tile_at(int t, int tiles_m, int tiles_n) {
 
 // Four adjacent values of a row, those from `left` on absent.
 template <typename T>
-__device__ __forceinline__ void load4(const T* p, bool vec, int left, float (&v)[4]) {
-  if (vec && left >= 4) {
-    const Vec<T, 4> x = ld_vec<T, 4>(p);
+__device__ __forceinline__ Vec<T, 4> load4(const T* p, bool vec, int left) {
+  if (vec && left >= 4) return ld_vec<T, 4>(p);
+  Vec<T, 4> x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = to_f32<T>(x.v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < left ? to_f32<T>(p[i]) : 0.f;
-  }
+  for (int i = 0; i < 4; ++i) x.v[i] = i < left ? p[i] : from_f32<T>(0.f);
+  return x;
 }
 template <typename T>
 __device__ __forceinline__ void store4(T* p, bool vec, int left, const float (&v)[4]) {
@@ -153,38 +153,165 @@ __device__ __forceinline__ void store4(T* p, bool vec, int left, const float (&v
   }
 }
 
-// The epilogue of 32 rows x 32 columns in shared memory (rows of 32 float32, 16-byte pieces c of row r at
-// c ^ (r & 7)): a lane has 4 adjacent columns of every fourth row.
+// bias and weight scale of four columns
+struct Columns {
+  float bias[4], scale[4];
+};
+__device__ __forceinline__ Columns columns_of(const Epilogue& e, long long n, int left) {
+  Columns c;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    c.bias[j] = e.bias && j < left ? e.bias[n + j] : 0.f;
+    c.scale[j] = e.w_scale && j < left ? e.w_scale[n + j] : 1.f;
+  }
+  return c;
+}
+// Four sums of row m to pre and y.
 template <typename T>
-__device__ __forceinline__ void chunk_out(const GemmArgs& g, uint32_t chunk, long long m0, long long n0, int lane) {
+__device__ __forceinline__ void out4(const GemmArgs& g, float (&v)[4], const Columns& c, const Vec<T, 4>& res, long long m,
+                                     long long n, int left) {
   const Epilogue& e = g.out;
-  const long long n = n0 + (lane & 7) * 4;
-  const int left = g.N - n < 4 ? (int)(g.N - n) : 4;
-  if (left <= 0) return;
-  float bias[4] = {}, scale[4] = {1.f, 1.f, 1.f, 1.f};
-  if (e.bias) load4<float>(e.bias + n, false, left, bias);
-  if (e.w_scale) load4<float>(e.w_scale + n, false, left, scale);
+  const float xs = e.x_scale ? e.x_scale[m] : 1.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = i * 4 + (lane >> 3);
-    const long long m = m0 + r;
-    if (m >= g.M) return;
-    float v[4], res[4] = {};
-    if (e.residual) load4<T>(static_cast<const T*>(e.residual) + m * e.res_row + n, g.res_vec, left, res);
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-                 : "r"(chunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
-    const float xs = e.x_scale ? e.x_scale[m] : 1.f;
+  for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j] * xs, c.scale[j], c.bias[j]);
+  if (e.pre) store4<T>(static_cast<T*>(e.pre) + m * e.pre_row + n, g.pre_vec, left, v);
+  if (e.act == kActSilu) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j] * xs, scale[j], bias[j]);
-    if (e.pre) store4<T>(static_cast<T*>(e.pre) + m * e.pre_row + n, g.pre_vec, left, v);
+    for (int j = 0; j < 4; ++j) v[j] = activate<sizeof(T) == 2>(v[j], kActSilu);
+  } else if (e.act == kActGelu) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = activate<sizeof(T) == 2>(v[j], e.act) + res[j];
-    store4<T>(static_cast<T*>(e.y) + m * e.y_row + n, g.y_vec, left, v);
+    for (int j = 0; j < 4; ++j) v[j] = activate<sizeof(T) == 2>(v[j], kActGelu);
+  }
+  if (e.residual) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] += to_f32<T>(res.v[j]);
+  }
+  store4<T>(static_cast<T*>(e.y) + m * e.y_row + n, g.y_vec, left, v);
+}
+
+// A warp's 32 x 32 sums, a row a lane, into its staging: rows of 32 float32, 16-byte piece j of row r at j ^ (r & 7).
+__device__ __forceinline__ void stage_in(uint32_t chunk, int lane, const float* v) {
+  __syncwarp();   // the last chunk has been read
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(chunk + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                 "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3])
+                 : "memory");
+  __syncwarp();
+}
+// Four columns of row r out of it: a lane has columns 4 (lane & 7).. of every fourth row.
+__device__ __forceinline__ void stage_out(uint32_t chunk, int lane, int r, float (&v)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(chunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
+}
+
+// Stages [k, part_end) add up in tensor memory; parts are added to float32 registers (PROMOTE).
+__device__ __forceinline__ int part_end(const GemmArgs& g, int k, int k1) {
+  const int last = (g.passes - 1) * g.k_iters, end = k < last ? last : k + kPart;
+  return end < k1 ? end : k1;
+}
+__device__ __forceinline__ int k_begin(const GemmArgs& g, int split) {
+  return (int)((long long)g.k_iters * g.passes * split / g.splits);
+}
+
+// Warps 2..9: a warp takes 32 rows (those of the tensor memory lanes that it can reach) and half the columns.
+template <typename T, int BN, bool PROMOTE>
+__device__ __forceinline__ void epilogue(const GemmArgs& g, uint32_t tmem, uint32_t chunk, uint64_t* acc_full,
+                                         uint64_t* acc_empty, uint32_t rank, int warp, int lane, int first, int step,
+                                         int n_tiles, volatile uint32_t* failed) {
+  constexpr int CHUNKS = BN / 64;
+  const int quad = warp & 3, half = (warp - 2) >> 2, r0 = lane >> 3;
+  const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+  uint32_t buf = 0, phase = 0;
+  auto next = [&]() {
+    if (++buf == 2) {
+      buf = 0;
+      phase ^= 1;
+    }
+  };
+  auto release = [&]() {
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(acc_empty + buf), 0));
+  };
+  for (int t = first; t < n_tiles; t += step) {
+    const Tile at = tile_at(t, g.tiles_m, g.tiles_n);
+    const long long m0 = (long long)at.m * 256 + rank * 128 + quad * 32 + r0;
+    const long long n0 = (long long)at.n * BN + half * (BN / 2) + (lane & 7) * 4;
+    // the residual's values are fetched a chunk ahead
+    Vec<T, 4> res[8];
+    auto fetch = [&](int i, int c) {
+      const long long n = n0 + c * 32, m = m0 + 4 * i;
+      if (n < g.N && m < g.M)
+        res[i] = load4<T>(static_cast<const T*>(g.out.residual) + m * g.out.res_row + n, g.res_vec, g.N - n < 4 ? (int)(g.N - n) : 4);
+    };
+    const bool has_res = g.out.residual && g.splits == 1;
+    if (has_res) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) fetch(i, 0);
+    }
+    float sums[PROMOTE ? CHUNKS : 1][32];
+    if (PROMOTE) {
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sums[PROMOTE ? c : 0][j] = 0.f;
+      const int k1 = k_begin(g, at.split + 1);
+      for (int k = k_begin(g, at.split); k < k1; k = part_end(g, k, k1)) {
+        if (!wait_for(acc_full + buf, phase, g.limit, failed)) return;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+          float v[32];
+          tc::tmem_ld32(tmem + buf * BN + half * (BN / 2) + c * 32 + lanes, v);
+          if (c == CHUNKS - 1) release();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sums[PROMOTE ? c : 0][j] += v[j];
+        }
+        next();
+      }
+    } else {
+      if (!wait_for(acc_full + buf, phase, g.limit, failed)) return;
+      tc::fence_after_sync();
+    }
+#pragma unroll(PROMOTE ? CHUNKS : 1)
+    for (int c = 0; c < CHUNKS; ++c) {
+      if (PROMOTE) {
+        stage_in(chunk, lane, sums[PROMOTE ? c : 0]);
+      } else {
+        float v[32];
+        tc::tmem_ld32(tmem + buf * BN + half * (BN / 2) + c * 32 + lanes, v);
+        if (c == CHUNKS - 1) release();
+        stage_in(chunk, lane, v);
+      }
+      const long long n = n0 + c * 32;
+      const int left = g.N - n < 4 ? (int)(g.N - n) : 4;
+      if (left <= 0) continue;
+      if (g.splits > 1) {
+        float* p = g.partial + (long long)at.split * g.M * g.N + n;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v[4];
+          stage_out(chunk, lane, r0 + 4 * i, v);
+          if (m0 + 4 * i < g.M) store4<float>(p + (m0 + 4 * i) * g.N, g.N % 4 == 0, left, v);
+        }
+        continue;
+      }
+      const Columns cols = columns_of(g.out, n, left);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v[4];
+        stage_out(chunk, lane, r0 + 4 * i, v);
+        if (m0 + 4 * i < g.M) out4<T>(g, v, cols, res[i], m0 + 4 * i, n, left);
+        if (has_res && c + 1 < CHUNKS) fetch(i, c + 1);
+      }
+    }
+    if (!PROMOTE) next();
   }
 }
 
-template <int BN, bool A_MN, bool B_MN, bool E4M3>
+template <int BN, bool A_MN, bool B_MN, bool E4M3, bool PROMOTE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemmArgs g) {
   using C = Cfg<BN>;
@@ -197,9 +324,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int n_tiles = g.tiles_m * g.tiles_n * g.splits, first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  const int all_iters = g.k_iters * g.passes;
-  // stages of split s: [s * all / splits, (s + 1) * all / splits)
-  auto k_begin = [&](int s) { return (int)((long long)all_iters * s / g.splits); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::stages; ++i) {
@@ -229,8 +353,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int t = first; ok && t < n_tiles; t += step) {
         const Tile at = tile_at(t, g.tiles_m, g.tiles_n);
         const int m0 = at.m * 256 + rank_m, n0 = at.n * BN + rank_n;
-        const int k1 = k_begin(at.split + 1);
-        int k = k_begin(at.split), pass = k / g.k_iters, it = k - pass * g.k_iters;
+        const int k1 = k_begin(g, at.split + 1);
+        int k = k_begin(g, at.split), pass = k / g.k_iters, it = k - pass * g.k_iters;
         for (; k < k1; ++k) {
           if (!(ok = wait_for(empty + stage, phase, g.limit, failed))) break;
           const uint32_t sa = base + stage * C::stage, sb = sa + C::a_bytes;
@@ -280,28 +404,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = !*failed;
       for (int t = first; ok && t < n_tiles; t += step) {
         const int split = t / (g.tiles_m * g.tiles_n);
-        const int k0 = k_begin(split), k1 = k_begin(split + 1);
-        if (!(ok = wait_for(acc_empty + buf, buf_phase, g.limit, failed))) break;
-        tc::fence_after_sync();
-        const uint32_t d = tmem + buf * BN;
-        for (int k = k0; k < k1; ++k) {
-          if (!(ok = wait_for(full + stage, phase, g.limit, failed))) break;
+        const int k1 = k_begin(g, split + 1);
+        for (int k = k_begin(g, split); ok && k < k1;) {
+          const int end = PROMOTE ? part_end(g, k, k1) : k1;
+          if (!(ok = wait_for(acc_empty + buf, buf_phase, g.limit, failed))) break;
           tc::fence_after_sync();
-          const uint32_t sa = base + stage * C::stage;
-          const uint64_t da = desc128(sa, 8192), db = desc128(sa + C::a_bytes, 8192);
+          const uint32_t d = tmem + buf * BN;
+          for (bool more = false; k < end; ++k, more = true) {
+            if (!(ok = wait_for(full + stage, phase, g.limit, failed))) break;
+            tc::fence_after_sync();
+            const uint32_t sa = base + stage * C::stage;
+            const uint64_t da = desc128(sa, 8192), db = desc128(sa + C::a_bytes, 8192);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_pair<E4M3>(d, da + i * step_a, db + i * step_b, idesc, k > k0 || i > 0, one);
-          commit_pair(smem_u32(empty + stage), one);
-          if (++stage == C::stages) {
-            stage = 0;
-            phase ^= 1;
+            for (int i = 0; i < 4; ++i) mma_pair<E4M3>(d, da + i * step_a, db + i * step_b, idesc, more || i > 0, one);
+            commit_pair(smem_u32(empty + stage), one);
+            if (++stage == C::stages) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
-        }
-        if (!ok) break;
-        commit_pair(smem_u32(acc_full + buf), one);
-        if (++buf == 2) {
-          buf = 0;
-          buf_phase ^= 1;
+          if (!ok) break;
+          commit_pair(smem_u32(acc_full + buf), one);
+          if (++buf == 2) {
+            buf = 0;
+            buf_phase ^= 1;
+          }
         }
       }
       if (!ok) {
@@ -310,57 +437,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t chunk = base + C::o_chunk + (warp - 2) * kChunk;
-    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    uint32_t buf = 0, phase = 0;
-    for (int t = first; t < n_tiles; t += step) {
-      const Tile at = tile_at(t, g.tiles_m, g.tiles_n);
-      if (!wait_for(acc_full + buf, phase, g.limit, failed)) break;
-      tc::fence_after_sync();
-      const long long m0 = (long long)at.m * 256 + rank * 128 + quad * 32;
-#pragma unroll 1
-      for (int c = 0; c < BN / 64; ++c) {
-        const int col = half * (BN / 2) + c * 32;
-        float v[32];
-        tc::tmem_ld32(tmem + buf * BN + col + lanes, v);
-        if (c == BN / 64 - 1) {
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(acc_empty + buf), 0));
-        }
-        const long long n0 = (long long)at.n * BN + col;
-        __syncwarp();   // the last chunk has been read
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(chunk + lane * 128 + ((j ^ (lane & 7)) << 4)),
-                       "f"(v[4 * j]), "f"(v[4 * j + 1]), "f"(v[4 * j + 2]), "f"(v[4 * j + 3])
-                       : "memory");
-        __syncwarp();
-        if (g.splits > 1) {
-          const long long n = n0 + (lane & 7) * 4;
-          const int left = g.N - n < 4 ? (int)(g.N - n) : 4;
-          float* p = g.partial + (long long)at.split * g.M * g.N;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3);
-            float o[4];
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
-                         : "r"(chunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
-            if (left > 0 && m0 + r < g.M) store4<float>(p + (m0 + r) * g.N + n, g.N % 4 == 0, left, o);
-          }
-        } else if (g.out.y_bf16) {
-          chunk_out<__nv_bfloat16>(g, chunk, m0, n0, lane);
-        } else {
-          chunk_out<float>(g, chunk, m0, n0, lane);
-        }
-      }
-      if (++buf == 2) {
-        buf = 0;
-        phase ^= 1;
-      }
-    }
+    using T = typename std::conditional<PROMOTE, float, __nv_bfloat16>::type;   // y's type
+    epilogue<T, BN, PROMOTE>(g, tmem, chunk, acc_full, acc_empty, rank, warp, lane, first, step, n_tiles, failed);
   }
   __syncwarp();
   tc::fence_before_sync();
@@ -380,23 +459,15 @@ __global__ void __launch_bounds__(256) join_kernel(const float* partial, int par
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
     const long long m = i / across, n = (i - m * across) * 4;
     const int left = g.N - n < 4 ? (int)(g.N - n) : 4;
-    float v[4] = {}, p[4], bias[4] = {}, scale[4] = {1.f, 1.f, 1.f, 1.f}, res[4] = {};
-    const Epilogue& e = g.out;
-    if (e.residual) load4<T>(static_cast<const T*>(e.residual) + m * e.res_row + n, g.res_vec, left, res);
-    if (e.bias) load4<float>(e.bias + n, false, left, bias);
-    if (e.w_scale) load4<float>(e.w_scale + n, false, left, scale);
+    float v[4] = {};
+    Vec<T, 4> res;
+    if (g.out.residual) res = load4<T>(static_cast<const T*>(g.out.residual) + m * g.out.res_row + n, g.res_vec, left);
     for (int s = 0; s < parts; ++s) {
-      load4<float>(partial + ((long long)s * g.M + m) * g.N + n, g.N % 4 == 0, left, p);
+      const Vec<float, 4> p = load4<float>(partial + ((long long)s * g.M + m) * g.N + n, g.N % 4 == 0, left);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += p[j];
+      for (int j = 0; j < 4; ++j) v[j] += p.v[j];
     }
-    const float xs = e.x_scale ? e.x_scale[m] : 1.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j] * xs, scale[j], bias[j]);
-    if (e.pre) store4<T>(static_cast<T*>(e.pre) + m * e.pre_row + n, g.pre_vec, left, v);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = activate<sizeof(T) == 2>(v[j], e.act) + res[j];
-    store4<T>(static_cast<T*>(e.y) + m * e.y_row + n, g.y_vec, left, v);
+    out4<T>(g, v, columns_of(g.out, n, left), res, m, n, left);
   }
 }
 
@@ -544,7 +615,7 @@ Plan plan_of(const ProductArgs& p, int mat) {
   // ends, and the parts' way through memory.
   const int clusters = p.sm_count / 2 > 0 ? p.sm_count / 2 : 1;
   double best = 1e300;
-  for (int bn = 256; bn >= 128; bn /= 2) {
+  for (int bn = p.out.y_bf16 ? 256 : 128; bn >= 128; bn /= 2) {
     const long long tn = (p.N + bn - 1) / bn, tiles = q.tiles_m * tn;
     const int most = q.k_iters * q.passes / 4 < 16 ? q.k_iters * q.passes / 4 : 16;
     for (int s = 1; s == 1 || (s <= most && tiles * s <= 2 * clusters); ++s) {
@@ -564,13 +635,13 @@ Plan plan_of(const ProductArgs& p, int mat) {
   return q;
 }
 
-template <int BN, bool A_MN, bool B_MN, bool E4M3>
+template <int BN, bool A_MN, bool B_MN, bool E4M3, bool PROMOTE>
 cudaError_t launch(const Plan& q, const GemmArgs& g, const void* a, const void* b, cudaStream_t s) {
   CUtensorMap ma, mb;
   constexpr int BK = E4M3 ? 128 : 64;
   if (!encode(&ma, q.a, a, A_MN ? 64 : BK, A_MN ? BK : 128) || !encode(&mb, q.b, b, B_MN ? 64 : BK, B_MN ? BK : BN / 2))
     return cudaErrorInvalidValue;
-  auto kern = gemm_kernel<BN, A_MN, B_MN, E4M3>;
+  auto kern = gemm_kernel<BN, A_MN, B_MN, E4M3, PROMOTE>;
   constexpr int bytes = (int)Cfg<BN>::bytes;
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
@@ -627,13 +698,17 @@ cudaError_t launch_product(const ProductArgs& p, int mat, cudaStream_t s) {
     if (q.b.pack && e == cudaSuccess) e = pack(q.b, const_cast<void*>(b = ws + up256(q.a.bytes)), p.sm_count, s);
     if (e != cudaSuccess) return e;
     g.partial = reinterpret_cast<float*>(ws + up256(q.a.bytes) + up256(q.b.bytes));
-    auto run = [&](auto bn) -> cudaError_t {
+    auto run = [&](auto bn, auto promote) -> cudaError_t {
       constexpr int BN = decltype(bn)::value;
-      if (mat == kMatE4m3) return launch<BN, false, false, true>(q, g, a, b, s);
-      if (!q.a.mn) return q.b.mn ? launch<BN, false, true, false>(q, g, a, b, s) : launch<BN, false, false, false>(q, g, a, b, s);
-      return launch<BN, true, true, false>(q, g, a, b, s);
+      constexpr bool P = decltype(promote)::value;
+      if (mat == kMatE4m3) return launch<BN, false, false, true, P>(q, g, a, b, s);
+      if (q.a.mn) return launch<BN, true, true, false, P>(q, g, a, b, s);
+      return q.b.mn ? launch<BN, false, true, false, P>(q, g, a, b, s) : launch<BN, false, false, false, P>(q, g, a, b, s);
     };
-    e = q.bn == 256 ? run(std::integral_constant<int, 256>()) : run(std::integral_constant<int, 128>());
+    using N128 = std::integral_constant<int, 128>;
+    if (!p.out.y_bf16) e = run(N128(), std::true_type());
+    else if (q.bn == 128) e = run(N128(), std::false_type());
+    else e = run(std::integral_constant<int, 256>(), std::false_type());
     if (e != cudaSuccess || q.splits == 1) return e;
   }
   const long long pieces = p.M * ((p.N + 3) / 4), want = (pieces + 255) / 256, most = 16LL * p.sm_count;

@@ -1,55 +1,115 @@
 // The element-wise part of a product's gradient: g = dy * act'(pre), and db, the sum of g's rows.
+//
+// One pass over dy and pre (memory bound).  A warp's lanes take VEC adjacent columns each (16 bytes where rows allow
+// it), a block's 8 warps every eighth row of a stretch of rows, four rows at a time so that their loads are in flight
+// together.  A column's sum is taken by a thread over its rows, over the block's warps in shared memory, and
+// over the stretches by a second kernel, in a fixed order: float32, chains of a few hundred additions at most.
 #include "vla_dense.cuh"
 
 namespace vla {
 namespace {
 
-// A block takes a stretch of rows and 256 columns, a thread one of them.
-template <typename T>
+constexpr int kRows = 4;   // rows in flight a warp
+
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, long long stretch) {
-  const long long n = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (n >= a.N) return;
+  __shared__ float part[8][32 * VEC];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long n = ((long long)blockIdx.x * 32 + lane) * VEC;
   const long long m0 = blockIdx.y * stretch, m1 = m0 + stretch < a.M ? m0 + stretch : a.M;
-  float sum = 0.f;
-  for (long long m = m0; m < m1; ++m) {
-    float g = to_f32<T>(static_cast<const T*>(a.dy)[m * a.dy_row + n]);
-    if (a.pre) {
-      g *= activate_slope<sizeof(T) == 2>(to_f32<T>(static_cast<const T*>(a.pre)[m * a.pre_row + n]), a.act);
-      static_cast<T*>(a.g)[m * a.g_row + n] = from_f32<T>(g);
+  float sum[VEC] = {};
+  if (n < a.N) {
+    const T* dy = static_cast<const T*>(a.dy) + n;
+    const T* pre = static_cast<const T*>(a.pre) + n;
+    T* out = static_cast<T*>(a.g) + n;
+    for (long long m = m0 + warp; m < m1; m += 8 * kRows) {
+      Vec<T, VEC> d[kRows], p[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (m + 8 * i < m1) {
+          d[i] = ld_vec<T, VEC>(dy + (m + 8 * i) * a.dy_row);
+          if (a.pre) p[i] = ld_vec<T, VEC>(pre + (m + 8 * i) * a.pre_row);
+        }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (m + 8 * i < m1) {
+          Vec<T, VEC> o;
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) {
+            float g = to_f32<T>(d[i].v[v]);
+            if (a.pre) g *= activate_slope<sizeof(T) == 2>(to_f32<T>(p[i].v[v]), a.act);
+            sum[v] += g;
+            o.v[v] = from_f32<T>(g);
+          }
+          if (a.g) st_vec<T, VEC>(out + (m + 8 * i) * a.g_row, o);
+        }
     }
-    sum += g;
   }
-  if (a.db) a.partial[blockIdx.y * a.N + n] = sum;
+  if (!a.db) return;
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) part[warp][v * 32 + lane] = sum[v];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * VEC; i += 256) {
+    const long long col = (long long)blockIdx.x * 32 * VEC + i;   // column i is value i % VEC of lane i / VEC
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += part[w][i % VEC * 32 + i / VEC];
+    if (col < a.N) a.partial[blockIdx.y * a.N + col] = s;
+  }
 }
 
+// A block has 32 columns; its 8 warps take every eighth stretch.
 __global__ void __launch_bounds__(256) slope_sum_kernel(const float* partial, float* db, long long N, long long parts) {
-  const long long n = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+  __shared__ float part[8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long n = (long long)blockIdx.x * 32 + lane;
   float sum = 0.f;
-  for (long long i = 0; i < parts; ++i) sum += partial[i * N + n];
-  db[n] = sum;
+  if (n < N)
+    for (long long i = warp; i < parts; i += 8) sum += partial[i * N + n];
+  part[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && n < N) {
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += part[w][lane];
+    db[n] = sum;
+  }
 }
 
-long long slope_parts(long long M, long long N, int sm_count) {
-  const long long across = (N + 255) / 256, want = (8LL * sm_count + across - 1) / across;
+// Stretches of rows: enough blocks for 6 an SM, with 32 rows at least in each.  The workspace is counted for the widest
+// blocks, which have the most stretches.
+long long slope_parts(long long M, long long N, int vec, int sm_count) {
+  const long long across = (N + 32 * vec - 1) / (32 * vec), want = (6LL * sm_count + across - 1) / across;
   const long long most = (M + 31) / 32;
   return want < most ? want : most;
 }
 
-}  // namespace
-
-size_t slope_ws(long long M, long long N, int sm_count) { return (size_t)(slope_parts(M, N, sm_count) * N) * 4; }
-
-cudaError_t launch_slope(const SlopeArgs& a, bool bf16, cudaStream_t s) {
-  const long long want = slope_parts(a.M, a.N, a.sm_count), stretch = (a.M + want - 1) / want;
+template <typename T, int VEC>
+cudaError_t launch(const SlopeArgs& a, cudaStream_t s) {
+  const long long want = slope_parts(a.M, a.N, VEC, a.sm_count), stretch = (a.M + want - 1) / want;
   const long long parts = (a.M + stretch - 1) / stretch;
-  const dim3 grid((unsigned int)((a.N + 255) / 256), (unsigned int)parts);
-  if (bf16) slope_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a, stretch);
-  else slope_kernel<float><<<grid, 256, 0, s>>>(a, stretch);
+  const dim3 grid((unsigned int)((a.N + 32 * VEC - 1) / (32 * VEC)), (unsigned int)parts);
+  if (parts > 65535) return cudaErrorInvalidConfiguration;   // at most 6 an SM
+  slope_kernel<T, VEC><<<grid, 256, 0, s>>>(a, stretch);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.db) return e;
-  slope_sum_kernel<<<grid.x, 256, 0, s>>>(a.partial, a.db, a.N, parts);
+  slope_sum_kernel<<<(unsigned int)((a.N + 31) / 32), 256, 0, s>>>(a.partial, a.db, a.N, parts);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t slope_ws(long long M, long long N, int sm_count) { return (size_t)(slope_parts(M, N, 8, sm_count) * N) * 4; }
+
+cudaError_t launch_slope(const SlopeArgs& a, bool bf16, cudaStream_t s) {
+  const size_t size = bf16 ? 2 : 4;
+  const long long vec = 16 / (long long)size;
+  auto whole = [&](const void* p, long long row) {
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)((size_t)row * size)) & 15u) == 0;
+  };
+  const bool wide = a.N % vec == 0 && whole(a.dy, a.dy_row) && (!a.pre || whole(a.pre, a.pre_row)) && (!a.g || whole(a.g, a.g_row));
+  if (bf16) return wide ? launch<__nv_bfloat16, 8>(a, s) : launch<__nv_bfloat16, 1>(a, s);
+  return wide ? launch<float, 4>(a, s) : launch<float, 1>(a, s);
 }
 
 }  // namespace vla
