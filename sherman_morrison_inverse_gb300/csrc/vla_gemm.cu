@@ -6,8 +6,9 @@
 //   warp 0     one thread keeps a ring of kStages stages filled by TMA: 128 bytes of Kd of both operands (64
 //              bfloat16 or 128 e4m3), 128-byte swizzle.  Both CTAs' copies complete on the leader's barrier.
 //   warp 1     of the leader issues the products of both CTAs, four a stage, into one of two accumulators.
-//   warps 2..9 take the other accumulator out: 32 columns at a time from tensor memory through shared memory,
-//              so that a row's values are adjacent over lanes, and then through the epilogue to memory.
+//   warps 2, 3 only leave their registers to the others.
+//   warps 4..11 take the other accumulator out, 32 columns of a lane's row at a time, through the epilogue to memory in
+//              32-byte pieces; rows off 32-byte boundaries go through shared memory first.
 // Operands lie in memory with Kd adjacent (as in x w^T) or with M or N adjacent (as in g w and g^T x): tiles
 // of 64 along what is adjacent, and the matrix descriptors say which.
 // float32 operands arrive as three bfloat16 terms each (x = x1 + x2 + x3 to 2^-24): six products, the small ones
@@ -25,7 +26,7 @@
 namespace vla {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kGroup = 8;          // tiles of M that are walked together
 constexpr int kPart = 4;           // stages that add up in tensor memory before float32 results take them over
 constexpr int kChunk = 32 * 32 * 4;   // a warp's staging: 32 rows of 32 float32
@@ -49,9 +50,11 @@ struct GemmArgs {
   long long M, N;
   int tiles_m, tiles_n, splits;
   int k_iters, passes;      // stages of one pass over Kd; passes over the terms
-  float* partial;           // [splits][M][N] where splits > 1
+  float* partial;           // [splits][M][part_row] where splits > 1
+  long long part_row;       // N, rounded up to 8
   Epilogue out;
-  bool y_vec, res_vec, pre_vec;
+  bool direct;                    // rows of y, pre, residual on 32-byte boundaries, N in whole pieces of 32 bytes
+  bool y_vec, res_vec, pre_vec;   // four values at a time
   unsigned long long limit;   // of a wait, in ns: 2 s, and 4 us for every stage of a tile
   DevStatus* status;
 };
@@ -103,7 +106,7 @@ __device__ __forceinline__ void dealloc_pair(uint32_t t, uint32_t cols) {
 }
 
 // Waits for a phase that the other CTA can complete too; false when the limit runs out or the CTA has failed.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
   const unsigned long long start = globaltimer_ns();
   while (!mbar_try_wait_cluster(bar, parity)) {
     if (*failed) return false;
@@ -215,13 +218,122 @@ __device__ __forceinline__ int k_begin(const GemmArgs& g, int split) {
   return (int)((long long)g.k_iters * g.passes * split / g.splits);
 }
 
-// Warps 2..9: a warp takes 32 rows (those of the tensor memory lanes that it can reach) and half the columns.
+// 32 bytes of a row, as one access.
+struct Piece {
+  uint32_t r[8];
+};
+__device__ __forceinline__ void ld_piece(Piece& x, const void* p) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(x.r[0]), "=r"(x.r[1]), "=r"(x.r[2]), "=r"(x.r[3]), "=r"(x.r[4]), "=r"(x.r[5]), "=r"(x.r[6]), "=r"(x.r[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st_piece(void* p, const Piece& x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x.r[0]), "r"(x.r[1]), "r"(x.r[2]),
+               "r"(x.r[3]), "r"(x.r[4]), "r"(x.r[5]), "r"(x.r[6]), "r"(x.r[7])
+               : "memory");
+}
+template <typename T, int COLS>
+__device__ __forceinline__ Piece to_piece(const float* v) {
+  Piece x;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.r[i] = pack2(v[2 * i], v[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x.r[i] = __float_as_uint(v[i]);
+  }
+  return x;
+}
+
+// 32 sums of a lane's row to memory, 32 bytes (whole sectors) an access.  n: their first column, the same in every lane;
+// alive: the lane's row exists.
+template <typename T>
+__device__ __forceinline__ void chunk_direct(const GemmArgs& g, float* v, float xs, long long m, long long n, bool alive) {
+  constexpr int PIECES = (int)sizeof(T), COLS = 32 / PIECES;
+  const Epilogue& e = g.out;
+  Piece res[PIECES];
+  if (e.residual) {
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+      if (alive && n + p * COLS < g.N) ld_piece(res[p], static_cast<const T*>(e.residual) + m * e.res_row + n + p * COLS);
+  }
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p) {
+    const long long at = n + p * COLS;
+    if (at >= g.N) break;
+    float* u = v + p * COLS;
+    if (e.x_scale) {
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) u[j] *= xs;
+    }
+    if (e.w_scale) {
+#pragma unroll
+      for (int j = 0; j < COLS; j += 4) {
+        const float4 s = *reinterpret_cast<const float4*>(e.w_scale + at + j);
+        u[j] *= s.x; u[j + 1] *= s.y; u[j + 2] *= s.z; u[j + 3] *= s.w;
+      }
+    }
+    if (e.bias) {
+#pragma unroll
+      for (int j = 0; j < COLS; j += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(e.bias + at + j);
+        u[j] += b.x; u[j + 1] += b.y; u[j + 2] += b.z; u[j + 3] += b.w;
+      }
+    }
+    if (e.pre && alive) st_piece(static_cast<T*>(e.pre) + m * e.pre_row + at, to_piece<T, COLS>(u));
+    if (e.act == kActSilu) {
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) u[j] = activate<sizeof(T) == 2>(u[j], kActSilu);
+    } else if (e.act == kActGelu) {
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) u[j] = activate<sizeof(T) == 2>(u[j], kActGelu);
+    }
+    if (e.residual) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(T) == 2) {
+          u[2 * i] += lo_f(res[p].r[i]);
+          u[2 * i + 1] += hi_f(res[p].r[i]);
+        } else {
+          u[i] += __uint_as_float(res[p].r[i]);
+        }
+      }
+    }
+    if (alive) st_piece(static_cast<T*>(e.y) + m * e.y_row + at, to_piece<T, COLS>(u));
+  }
+}
+
+// The same through a warp's staging, for rows that do not start on 32-byte boundaries: a lane has four columns of every
+// fourth row, so that a row's values are adjacent over lanes.
+template <typename T>
+__device__ __forceinline__ void chunk_staged(const GemmArgs& g, const float* v, uint32_t chunk, long long m0, long long n0, int lane) {
+  stage_in(chunk, lane, v);
+  const long long n = n0 + (lane & 7) * 4, m = m0 + (lane >> 3);
+  const int left = g.N - n < 4 ? (int)(g.N - n) : 4;
+  if (left <= 0) return;
+  Vec<T, 4> res[8];
+  if (g.out.residual) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (m + 4 * i < g.M) res[i] = load4<T>(static_cast<const T*>(g.out.residual) + (m + 4 * i) * g.out.res_row + n, g.res_vec, left);
+  }
+  const Columns cols = columns_of(g.out, n, left);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float u[4];
+    stage_out(chunk, lane, (lane >> 3) + 4 * i, u);
+    if (m + 4 * i < g.M) out4<T>(g, u, cols, res[i], m + 4 * i, n, left);
+  }
+}
+
+// Warps 4..11: a warp takes 32 rows (those of the tensor memory lanes that it can reach) and half the columns.
 template <typename T, int BN, bool PROMOTE>
 __device__ __forceinline__ void epilogue(const GemmArgs& g, uint32_t tmem, uint32_t chunk, uint64_t* acc_full,
                                          uint64_t* acc_empty, uint32_t rank, int warp, int lane, int first, int step,
                                          int n_tiles, volatile uint32_t* failed) {
   constexpr int CHUNKS = BN / 64;
-  const int quad = warp & 3, half = (warp - 2) >> 2, r0 = lane >> 3;
+  const int quad = warp & 3, half = (warp - 4) >> 2;
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
   uint32_t buf = 0, phase = 0;
   auto next = [&]() {
@@ -237,26 +349,25 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, uint32_t tmem, uint3
   };
   for (int t = first; t < n_tiles; t += step) {
     const Tile at = tile_at(t, g.tiles_m, g.tiles_n);
-    const long long m0 = (long long)at.m * 256 + rank * 128 + quad * 32 + r0;
-    const long long n0 = (long long)at.n * BN + half * (BN / 2) + (lane & 7) * 4;
-    // the residual's values are fetched a chunk ahead
-    Vec<T, 4> res[8];
-    auto fetch = [&](int i, int c) {
-      const long long n = n0 + c * 32, m = m0 + 4 * i;
-      if (n < g.N && m < g.M)
-        res[i] = load4<T>(static_cast<const T*>(g.out.residual) + m * g.out.res_row + n, g.res_vec, g.N - n < 4 ? (int)(g.N - n) : 4);
+    const long long m0 = (long long)at.m * 256 + rank * 128 + quad * 32, m = m0 + lane;
+    const long long n0 = (long long)at.n * BN + half * (BN / 2);
+    const bool alive = m < g.M;
+    const float xs = g.out.x_scale && alive ? g.out.x_scale[m] : 1.f;
+    auto out = [&](float* v, int c) {
+      const long long n = n0 + c * 32;
+      if (g.splits > 1) {   // rows of `partial` start on 32-byte boundaries
+        float* p = g.partial + ((long long)at.split * g.M + m) * g.part_row + n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (alive && n + 8 * i < g.N) st_piece(p + 8 * i, to_piece<float, 8>(v + 8 * i));
+      } else if (g.direct) {
+        chunk_direct<T>(g, v, xs, m, n, alive);
+      } else {
+        chunk_staged<T>(g, v, chunk, m0, n, lane);
+      }
     };
-    const bool has_res = g.out.residual && g.splits == 1;
-    if (has_res) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) fetch(i, 0);
-    }
-    float sums[PROMOTE ? CHUNKS : 1][32];
-    if (PROMOTE) {
-#pragma unroll
-      for (int c = 0; c < CHUNKS; ++c)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) sums[PROMOTE ? c : 0][j] = 0.f;
+    if constexpr (PROMOTE) {
+      float sums[CHUNKS][32] = {};
       const int k1 = k_begin(g, at.split + 1);
       for (int k = k_begin(g, at.split); k < k1; k = part_end(g, k, k1)) {
         if (!wait_for(acc_full + buf, phase, g.limit, failed)) return;
@@ -267,47 +378,24 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, uint32_t tmem, uint3
           tc::tmem_ld32(tmem + buf * BN + half * (BN / 2) + c * 32 + lanes, v);
           if (c == CHUNKS - 1) release();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sums[PROMOTE ? c : 0][j] += v[j];
+          for (int j = 0; j < 32; ++j) sums[c][j] += v[j];
         }
         next();
       }
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) out(sums[c], c);
     } else {
       if (!wait_for(acc_full + buf, phase, g.limit, failed)) return;
       tc::fence_after_sync();
-    }
-#pragma unroll(PROMOTE ? CHUNKS : 1)
-    for (int c = 0; c < CHUNKS; ++c) {
-      if (PROMOTE) {
-        stage_in(chunk, lane, sums[PROMOTE ? c : 0]);
-      } else {
+#pragma unroll 1
+      for (int c = 0; c < CHUNKS; ++c) {
         float v[32];
         tc::tmem_ld32(tmem + buf * BN + half * (BN / 2) + c * 32 + lanes, v);
         if (c == CHUNKS - 1) release();
-        stage_in(chunk, lane, v);
+        out(v, c);
       }
-      const long long n = n0 + c * 32;
-      const int left = g.N - n < 4 ? (int)(g.N - n) : 4;
-      if (left <= 0) continue;
-      if (g.splits > 1) {
-        float* p = g.partial + (long long)at.split * g.M * g.N + n;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float v[4];
-          stage_out(chunk, lane, r0 + 4 * i, v);
-          if (m0 + 4 * i < g.M) store4<float>(p + (m0 + 4 * i) * g.N, g.N % 4 == 0, left, v);
-        }
-        continue;
-      }
-      const Columns cols = columns_of(g.out, n, left);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float v[4];
-        stage_out(chunk, lane, r0 + 4 * i, v);
-        if (m0 + 4 * i < g.M) out4<T>(g, v, cols, res[i], m0 + 4 * i, n, left);
-        if (has_res && c + 1 < CHUNKS) fetch(i, c + 1);
-      }
+      next();
     }
-    if (!PROMOTE) next();
   }
 }
 
@@ -345,101 +433,106 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t rank_m = rank * 128, rank_n = rank * (BN / 2);
-      uint32_t stage = 0, phase = 1, issued = 0;
-      bool ok = !*failed;
-      for (int t = first; ok && t < n_tiles; t += step) {
-        const Tile at = tile_at(t, g.tiles_m, g.tiles_n);
-        const int m0 = at.m * 256 + rank_m, n0 = at.n * BN + rank_n;
-        const int k1 = k_begin(g, at.split + 1);
-        int k = k_begin(g, at.split), pass = k / g.k_iters, it = k - pass * g.k_iters;
-        for (; k < k1; ++k) {
-          if (!(ok = wait_for(empty + stage, phase, g.limit, failed))) break;
-          const uint32_t sa = base + stage * C::stage, sb = sa + C::a_bytes;
-          const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
-          if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * C::stage);
-          const int ta = g.passes > 1 ? term_a(pass) : 0, tb = g.passes > 1 ? term_b(pass) : 0;
-          constexpr int BK = E4M3 ? 128 : 64;
-          if (A_MN) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) tma_pair(sa + j * 8192, &map_a, m0 + 64 * j, it * BK, ta, bar);
-          } else {
-            tma_pair(sa, &map_a, it * BK, m0, ta, bar);
-          }
-          if (B_MN) {
-#pragma unroll
-            for (int j = 0; j < BN / 128; ++j) tma_pair(sb + j * 8192, &map_b, n0 + 64 * j, it * BK, tb, bar);
-          } else {
-            tma_pair(sb, &map_b, it * BK, n0, tb, bar);
-          }
-          ++issued;
-          if (++stage == C::stages) {
-            stage = 0;
-            phase ^= 1;
-          }
-          if (++it == g.k_iters) {
-            it = 0;
-            ++pass;
-          }
-        }
-      }
-      if (!ok && rank == 0) {   // let what is in flight arrive before the memory is given up
-        const uint32_t n = issued < C::stages ? issued : C::stages;
-        for (uint32_t i = 1; i <= n; ++i) {
-          const uint32_t at = issued - i;
-          mbar_wait_cluster_bounded(full + at % C::stages, at / C::stages & 1);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (rank == 0) {
-      const uint32_t one = lane == 0;
-      constexpr uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (A_MN ? 1u << 15 : 0u) |
-                                 (B_MN ? 1u << 16 : 0u) | (uint32_t)(BN >> 3) << 17 | (256u >> 4) << 24;
-      constexpr uint32_t step_a = A_MN ? 2048 >> 4 : 32 >> 4, step_b = B_MN ? 2048 >> 4 : 32 >> 4;
-      uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1;
-      bool ok = !*failed;
-      for (int t = first; ok && t < n_tiles; t += step) {
-        const int split = t / (g.tiles_m * g.tiles_n);
-        const int k1 = k_begin(g, split + 1);
-        for (int k = k_begin(g, split); ok && k < k1;) {
-          const int end = PROMOTE ? part_end(g, k, k1) : k1;
-          if (!(ok = wait_for(acc_empty + buf, buf_phase, g.limit, failed))) break;
-          tc::fence_after_sync();
-          const uint32_t d = tmem + buf * BN;
-          for (bool more = false; k < end; ++k, more = true) {
-            if (!(ok = wait_for(full + stage, phase, g.limit, failed))) break;
-            tc::fence_after_sync();
-            const uint32_t sa = base + stage * C::stage;
-            const uint64_t da = desc128(sa, 8192), db = desc128(sa + C::a_bytes, 8192);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mma_pair<E4M3>(d, da + i * step_a, db + i * step_b, idesc, more || i > 0, one);
-            commit_pair(smem_u32(empty + stage), one);
+  // the block's registers, 168 a thread at launch: 128 x 40 + 256 x 232 = 384 x 168
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const uint32_t chunk = base + C::o_chunk + (warp - 4) * kChunk;
+    using T = typename std::conditional<PROMOTE, float, __nv_bfloat16>::type;   // y's type
+    epilogue<T, BN, PROMOTE>(g, tmem, chunk, acc_full, acc_empty, rank, warp, lane, first, step, n_tiles, failed);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      if (lane == 0) {
+        const uint32_t rank_m = rank * 128, rank_n = rank * (BN / 2);
+        uint32_t stage = 0, phase = 1, issued = 0;
+        bool ok = !*failed;
+        for (int t = first; ok && t < n_tiles; t += step) {
+          const Tile at = tile_at(t, g.tiles_m, g.tiles_n);
+          const int m0 = at.m * 256 + rank_m, n0 = at.n * BN + rank_n;
+          const int k1 = k_begin(g, at.split + 1);
+          int k = k_begin(g, at.split), pass = k / g.k_iters, it = k - pass * g.k_iters;
+          for (; k < k1; ++k) {
+            if (!(ok = wait_for(empty + stage, phase, g.limit, failed))) break;
+            const uint32_t sa = base + stage * C::stage, sb = sa + C::a_bytes;
+            const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
+            if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * C::stage);
+            const int ta = g.passes > 1 ? term_a(pass) : 0, tb = g.passes > 1 ? term_b(pass) : 0;
+            constexpr int BK = E4M3 ? 128 : 64;
+            if (A_MN) {
+  #pragma unroll
+              for (int j = 0; j < 2; ++j) tma_pair(sa + j * 8192, &map_a, m0 + 64 * j, it * BK, ta, bar);
+            } else {
+              tma_pair(sa, &map_a, it * BK, m0, ta, bar);
+            }
+            if (B_MN) {
+  #pragma unroll
+              for (int j = 0; j < BN / 128; ++j) tma_pair(sb + j * 8192, &map_b, n0 + 64 * j, it * BK, tb, bar);
+            } else {
+              tma_pair(sb, &map_b, it * BK, n0, tb, bar);
+            }
+            ++issued;
             if (++stage == C::stages) {
               stage = 0;
               phase ^= 1;
             }
+            if (++it == g.k_iters) {
+              it = 0;
+              ++pass;
+            }
           }
-          if (!ok) break;
-          commit_pair(smem_u32(acc_full + buf), one);
-          if (++buf == 2) {
-            buf = 0;
-            buf_phase ^= 1;
+        }
+        if (!ok && rank == 0) {   // let what is in flight arrive before the memory is given up
+          const uint32_t n = issued < C::stages ? issued : C::stages;
+          for (uint32_t i = 1; i <= n; ++i) {
+            const uint32_t at = issued - i;
+            mbar_wait_cluster_bounded(full + at % C::stages, at / C::stages & 1);
           }
         }
       }
-      if (!ok) {
-        commit_pair(smem_u32(drain), one);
-        mbar_wait_cluster_bounded(drain, 0);
+      __syncwarp();
+    } else if (warp == 1) {
+      if (rank == 0) {
+        const uint32_t one = lane == 0;
+        constexpr uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (A_MN ? 1u << 15 : 0u) |
+                                   (B_MN ? 1u << 16 : 0u) | (uint32_t)(BN >> 3) << 17 | (256u >> 4) << 24;
+        constexpr uint32_t step_a = A_MN ? 2048 >> 4 : 32 >> 4, step_b = B_MN ? 2048 >> 4 : 32 >> 4;
+        uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1;
+        bool ok = !*failed;
+        for (int t = first; ok && t < n_tiles; t += step) {
+          const int split = t / (g.tiles_m * g.tiles_n);
+          const int k1 = k_begin(g, split + 1);
+          for (int k = k_begin(g, split); ok && k < k1;) {
+            const int end = PROMOTE ? part_end(g, k, k1) : k1;
+            if (!(ok = wait_for(acc_empty + buf, buf_phase, g.limit, failed))) break;
+            tc::fence_after_sync();
+            const uint32_t d = tmem + buf * BN;
+            for (bool more = false; k < end; ++k, more = true) {
+              if (!(ok = wait_for(full + stage, phase, g.limit, failed))) break;
+              tc::fence_after_sync();
+              const uint32_t sa = base + stage * C::stage;
+              const uint64_t da = desc128(sa, 8192), db = desc128(sa + C::a_bytes, 8192);
+  #pragma unroll
+              for (int i = 0; i < 4; ++i) mma_pair<E4M3>(d, da + i * step_a, db + i * step_b, idesc, more || i > 0, one);
+              commit_pair(smem_u32(empty + stage), one);
+              if (++stage == C::stages) {
+                stage = 0;
+                phase ^= 1;
+              }
+            }
+            if (!ok) break;
+            commit_pair(smem_u32(acc_full + buf), one);
+            if (++buf == 2) {
+              buf = 0;
+              buf_phase ^= 1;
+            }
+          }
+        }
+        if (!ok) {
+          commit_pair(smem_u32(drain), one);
+          mbar_wait_cluster_bounded(drain, 0);
+        }
       }
     }
-  } else {
-    const uint32_t chunk = base + C::o_chunk + (warp - 2) * kChunk;
-    using T = typename std::conditional<PROMOTE, float, __nv_bfloat16>::type;   // y's type
-    epilogue<T, BN, PROMOTE>(g, tmem, chunk, acc_full, acc_empty, rank, warp, lane, first, step, n_tiles, failed);
   }
   __syncwarp();
   tc::fence_before_sync();
@@ -463,7 +556,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float* partial, int par
     Vec<T, 4> res;
     if (g.out.residual) res = load4<T>(static_cast<const T*>(g.out.residual) + m * g.out.res_row + n, g.res_vec, left);
     for (int s = 0; s < parts; ++s) {
-      const Vec<float, 4> p = load4<float>(partial + ((long long)s * g.M + m) * g.N + n, g.N % 4 == 0, left);
+      const Vec<float, 4> p = load4<float>(partial + ((long long)s * g.M + m) * g.part_row + n, true, 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] += p.v[j];
     }
@@ -615,12 +708,12 @@ Plan plan_of(const ProductArgs& p, int mat) {
   // ends, and the parts' way through memory.
   const int clusters = p.sm_count / 2 > 0 ? p.sm_count / 2 : 1;
   double best = 1e300;
-  for (int bn = p.out.y_bf16 ? 256 : 128; bn >= 128; bn /= 2) {
+  for (int bn = 256; bn >= 128; bn /= 2) {
     const long long tn = (p.N + bn - 1) / bn, tiles = q.tiles_m * tn;
     const int most = q.k_iters * q.passes / 4 < 16 ? q.k_iters * q.passes / 4 : 16;
     for (int s = 1; s == 1 || (s <= most && tiles * s <= 2 * clusters); ++s) {
       const long long waves = (tiles * s + clusters - 1) / clusters;
-      double cost = (double)waves * ((double)q.k_iters * q.passes / s * (bn == 256 ? 1.0 : 0.55) + 3.0);
+      double cost = (double)waves * ((double)q.k_iters * q.passes / s * (bn == 256 ? 1.0 : 0.9) + 3.0);
       if (s > 1) cost += 8.0 + (double)s * p.M * p.N * 8.0 / 1.2e6;
       if (cost < best) {
         best = cost;
@@ -631,7 +724,7 @@ Plan plan_of(const ProductArgs& p, int mat) {
     }
   }
   if (p.Kd == 0) q.splits = 0;
-  q.ws = p.Kd == 0 ? 0 : up256(q.a.bytes) + up256(q.b.bytes) + (q.splits > 1 ? (size_t)q.splits * p.M * p.N * 4 : 0);
+  q.ws = p.Kd == 0 ? 0 : up256(q.a.bytes) + up256(q.b.bytes) + (q.splits > 1 ? (size_t)q.splits * p.M * ((p.N + 7) / 8 * 8) * 4 + 32 : 0);
   return q;
 }
 
@@ -687,6 +780,13 @@ cudaError_t launch_product(const ProductArgs& p, int mat, cudaStream_t s) {
   g.status = p.status;
   g.limit = kWaitLimitNs + 4000ull * (unsigned long long)q.k_iters * q.passes;
   const size_t ysize = p.out.y_bf16 ? 2 : 4;
+  g.part_row = (p.N + 7) / 8 * 8;
+  auto sectors = [&](const void* x, long long row) {
+    return ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)((size_t)row * ysize)) & 31u) == 0;
+  };
+  g.direct = p.N * ysize % 32 == 0 && sectors(p.out.y, p.out.y_row) && (!p.out.pre || sectors(p.out.pre, p.out.pre_row)) &&
+             (!p.out.residual || sectors(p.out.residual, p.out.res_row)) &&
+             ((reinterpret_cast<uintptr_t>(p.out.bias) | reinterpret_cast<uintptr_t>(p.out.w_scale)) & 15u) == 0;
   g.y_vec = four(p.out.y, p.out.y_row, ysize);
   g.res_vec = four(p.out.residual, p.out.res_row, ysize);
   g.pre_vec = four(p.out.pre, p.out.pre_row, ysize);
@@ -697,7 +797,8 @@ cudaError_t launch_product(const ProductArgs& p, int mat, cudaStream_t s) {
     if (q.a.pack) e = pack(q.a, const_cast<void*>(a = ws), p.sm_count, s);
     if (q.b.pack && e == cudaSuccess) e = pack(q.b, const_cast<void*>(b = ws + up256(q.a.bytes)), p.sm_count, s);
     if (e != cudaSuccess) return e;
-    g.partial = reinterpret_cast<float*>(ws + up256(q.a.bytes) + up256(q.b.bytes));
+    // the parts' rows are written in pieces of 32 bytes
+    g.partial = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + up256(q.a.bytes) + up256(q.b.bytes) + 31) & ~(uintptr_t)31);
     auto run = [&](auto bn, auto promote) -> cudaError_t {
       constexpr int BN = decltype(bn)::value;
       constexpr bool P = decltype(promote)::value;
@@ -706,9 +807,9 @@ cudaError_t launch_product(const ProductArgs& p, int mat, cudaStream_t s) {
       return q.b.mn ? launch<BN, false, true, false, P>(q, g, a, b, s) : launch<BN, false, false, false, P>(q, g, a, b, s);
     };
     using N128 = std::integral_constant<int, 128>;
-    if (!p.out.y_bf16) e = run(N128(), std::true_type());
-    else if (q.bn == 128) e = run(N128(), std::false_type());
-    else e = run(std::integral_constant<int, 256>(), std::false_type());
+    using N256 = std::integral_constant<int, 256>;
+    if (p.out.y_bf16) e = q.bn == 128 ? run(N128(), std::false_type()) : run(N256(), std::false_type());
+    else e = q.bn == 128 ? run(N128(), std::true_type()) : run(N256(), std::true_type());
     if (e != cudaSuccess || q.splits == 1) return e;
   }
   const long long pieces = p.M * ((p.N + 3) / 4), want = (pieces + 255) / 256, most = 16LL * p.sm_count;

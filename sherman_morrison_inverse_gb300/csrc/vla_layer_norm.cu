@@ -193,8 +193,8 @@ cudaError_t forward_of(const LayerNormArgs& a, cudaStream_t s) {
   };
   const bool vec = a.D % VEC == 0 && whole(a.x, a.x_row, sizeof(T)) && whole(a.y, a.y_row, sizeof(T)) &&
                    (RES == 0 || whole(a.residual, a.res_row, RS));
-  if (vec) {   // 8 values a thread while that takes 512 threads at most, then 16, then 32
-    if (a.D <= 4096) return forward<T, RES, VEC, 8 / VEC>(a, s);
+  if (vec) {
+    if (a.D <= 2048) return forward<T, RES, VEC, 8 / VEC>(a, s);
     if (a.D <= 8192) return forward<T, RES, VEC, 16 / VEC>(a, s);
     return forward<T, RES, VEC, 32 / VEC>(a, s);
   }
@@ -475,7 +475,7 @@ struct BackShape {
 };
 BackShape back_shape(long long D) {
   BackShape b{};
-  b.n = D <= 8 * kBackThreads ? 8 : 16;
+  b.n = D <= 2048 ? 8 : 16;
   b.tpr = (int)(((D + b.n - 1) / b.n + 31) / 32 * 32);
   b.rows = b.tpr >= 256 ? 1 : 256 / b.tpr;
   b.per_sm = b.tpr * b.rows > 256 ? 1 : 2;
