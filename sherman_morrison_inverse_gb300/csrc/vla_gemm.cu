@@ -16,25 +16,19 @@
 // a tensor core cuts the bits off that an addition shifts out, always towards zero, and the error of a chain of them
 // grows with its length (K = 1161: 6.8e-7 of the result without, against 3.6e-7 of plain float32 products).  Kd is split over clusters where there are fewer tiles than clusters; the parts are then added in order.
 // Every wait is bounded: one that runs out sets the handle's timeout flag, and the cluster drains and returns.
-#include <cuda.h>   // CUtensorMap and the encode entry point's types (resolved at run time)
-
 #include <atomic>
 
-#include "vla_dense.cuh"
-#include "vla_tc.cuh"
+#include "vla_gemm.cuh"
 
 namespace vla {
+
+using namespace gemm;
+
 namespace {
 
 constexpr int kThreads = 384;
 constexpr int kGroup = 8;          // tiles of M that are walked together
-constexpr int kPart = 4;           // stages that add up in tensor memory before float32 results take them over
 constexpr int kChunk = 32 * 32 * 4;   // a warp's staging: 32 rows of 32 float32
-
-// Passes over the terms of the operands: float32 takes (a, b) = 3-1, 1-3, 2-2, 2-1, 1-2, 1-1.
-constexpr int kPasses = 6;
-__device__ __forceinline__ int term_a(int pass) { return (0x201100 >> (4 * (5 - pass))) & 3; }
-__device__ __forceinline__ int term_b(int pass) { return (0x021010 >> (4 * (5 - pass))) & 3; }
 
 template <int BN>
 struct Cfg {
@@ -45,24 +39,6 @@ struct Cfg {
   static constexpr uint32_t bytes = o_bar + 8 * bars + 16;
   static constexpr uint32_t cols = 2 * BN;
 };
-
-struct GemmArgs {
-  long long M, N;
-  int tiles_m, tiles_n, splits;
-  int k_iters, passes;      // stages of one pass over Kd; passes over the terms
-  float* partial;           // [splits][M][part_row] where splits > 1
-  long long part_row;       // N, rounded up to 8
-  Epilogue out;
-  bool direct;                    // rows of y, pre, residual on 32-byte boundaries, N in whole pieces of 32 bytes
-  bool y_vec, res_vec, pre_vec;   // four values at a time
-  unsigned long long limit;   // of a wait, in ns: 2 s, and 4 us for every stage of a tile
-  DevStatus* status;
-};
-
-__device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 | (uint64_t)(1024u >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
 
 // One product of both CTAs for 32 bytes of Kd, issued by the lane whose `one` is set.  The whole warp runs the loop
 // around it, predicated and not branched, so that descriptors stay in uniform registers.
@@ -105,23 +81,6 @@ __device__ __forceinline__ void dealloc_pair(uint32_t t, uint32_t cols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(cols) : "memory");
 }
 
-// Waits for a phase that the other CTA can complete too; false when the limit runs out or the CTA has failed.
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
-  const unsigned long long start = globaltimer_ns();
-  while (!mbar_try_wait_cluster(bar, parity)) {
-    if (*failed) return false;
-    if (globaltimer_ns() - start > limit) {
-      *failed = 1;
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  return wait_slow(bar, parity, limit, failed);
-}
-
 struct Tile {
   int m, n, split;
 };
@@ -131,65 +90,6 @@ __device__ __forceinline__ Tile tile_at(int t, int tiles_m, int tiles_n) {
   const int first = group * kGroup, size = tiles_m - first < kGroup ? tiles_m - first : kGroup;
   const int n = at / size;
   return {first + at - n * size, n, split};
-}
-
-// Four adjacent values of a row, those from `left` on absent.
-template <typename T>
-__device__ __forceinline__ Vec<T, 4> load4(const T* p, bool vec, int left) {
-  if (vec && left >= 4) return ld_vec<T, 4>(p);
-  Vec<T, 4> x;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x.v[i] = i < left ? p[i] : from_f32<T>(0.f);
-  return x;
-}
-template <typename T>
-__device__ __forceinline__ void store4(T* p, bool vec, int left, const float (&v)[4]) {
-  if (vec && left >= 4) {
-    Vec<T, 4> x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x.v[i] = from_f32<T>(v[i]);
-    st_vec<T, 4>(p, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) p[i] = from_f32<T>(v[i]);
-  }
-}
-
-// bias and weight scale of four columns
-struct Columns {
-  float bias[4], scale[4];
-};
-__device__ __forceinline__ Columns columns_of(const Epilogue& e, long long n, int left) {
-  Columns c;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    c.bias[j] = e.bias && j < left ? e.bias[n + j] : 0.f;
-    c.scale[j] = e.w_scale && j < left ? e.w_scale[n + j] : 1.f;
-  }
-  return c;
-}
-// Four sums of row m to pre and y.
-template <typename T>
-__device__ __forceinline__ void out4(const GemmArgs& g, float (&v)[4], const Columns& c, const Vec<T, 4>& res, long long m,
-                                     long long n, int left) {
-  const Epilogue& e = g.out;
-  const float xs = e.x_scale ? e.x_scale[m] : 1.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j] * xs, c.scale[j], c.bias[j]);
-  if (e.pre) store4<T>(static_cast<T*>(e.pre) + m * e.pre_row + n, g.pre_vec, left, v);
-  if (e.act == kActSilu) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = activate<sizeof(T) == 2>(v[j], kActSilu);
-  } else if (e.act == kActGelu) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = activate<sizeof(T) == 2>(v[j], kActGelu);
-  }
-  if (e.residual) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] += to_f32<T>(res.v[j]);
-  }
-  store4<T>(static_cast<T*>(e.y) + m * e.y_row + n, g.y_vec, left, v);
 }
 
 // A warp's 32 x 32 sums, a row a lane, into its staging: rows of 32 float32, 16-byte piece j of row r at j ^ (r & 7).
@@ -207,15 +107,6 @@ __device__ __forceinline__ void stage_out(uint32_t chunk, int lane, int r, float
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
                : "r"(chunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
-}
-
-// Stages [k, part_end) add up in tensor memory; parts are added to float32 registers (PROMOTE).
-__device__ __forceinline__ int part_end(const GemmArgs& g, int k, int k1) {
-  const int last = (g.passes - 1) * g.k_iters, end = k < last ? last : k + kPart;
-  return end < k1 ? end : k1;
-}
-__device__ __forceinline__ int k_begin(const GemmArgs& g, int split) {
-  return (int)((long long)g.k_iters * g.passes * split / g.splits);
 }
 
 // 32 bytes of a row, as one access.
@@ -564,132 +455,28 @@ __global__ void __launch_bounds__(256) join_kernel(const float* partial, int par
   }
 }
 
-// ---------------------------------------------------------------------------------------------
-// operands that TMA cannot read as they are: float32 as three bfloat16 terms, rows off 16-byte boundaries
-
-// One row piece of 8 values a thread.  x1 = x rounded, x2 = x - x1 rounded, x3 = x - x1 - x2 rounded: the differences
-// are exact.  A value beyond bfloat16's range, an infinity or a NaN has only its first term.
-template <typename I>
-__global__ void __launch_bounds__(256) pack_kernel(const I* src, long long rows, long long cols, long long row, I* same,
-                                                   __nv_bfloat16* terms, long long out_row, bool vec) {
-  const long long across = (cols + 7) / 8, all = rows * across;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
-    const long long r = i / across, c = (i - r * across) * 8;
-    const I* p = src + r * row + c;
-    const int left = cols - c < 8 ? (int)(cols - c) : 8;
-    if constexpr (sizeof(I) == 4) {
-      float v[8];
-      if (vec && left == 8) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : 0.f;
-      }
-      Vec<__nv_bfloat16, 8> o[3];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        o[0].v[j] = __float2bfloat16_rn(v[j]);
-        float rest = v[j] - __bfloat162float(o[0].v[j]);
-        if (!isfinite(rest)) rest = 0.f;
-        o[1].v[j] = __float2bfloat16_rn(rest);
-        o[2].v[j] = __float2bfloat16_rn(rest - __bfloat162float(o[1].v[j]));
-      }
-#pragma unroll
-      for (int t = 0; t < 3; ++t) st_vec<__nv_bfloat16, 8>(terms + (t * rows + r) * out_row + c, o[t]);
-    } else {
-      Vec<I, 8> o;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o.v[j] = p[j < left ? j : 0];   // the row's end is not read by anyone
-      st_vec<I, 8>(same + r * out_row + c, o);
-    }
-  }
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_fn() {
-  static EncodeTiled fn = []() -> EncodeTiled {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      return nullptr;
-    }
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return fn;
-}
-
-// An operand as it lies in memory: rows of `cols` adjacent values.
-struct Operand {
-  const void* p;
-  long long rows, cols, row;   // row: distance of rows in values
-  int size;                    // bytes a value
-  bool mn;                     // what is adjacent is M or N, not Kd
-  bool pack;                   // TMA reads a copy
-  size_t bytes;                // of the copy
-  long long out_row;
-};
-
-Operand operand(const void* p, long long side, long long kd, long long row, bool mn, int size) {
-  Operand o{};
-  o.p = p;
-  o.size = size;
-  o.mn = mn;
-  o.rows = mn ? kd : side;
-  o.cols = mn ? side : kd;
-  o.row = row;
-  o.out_row = (o.cols + 15) / 16 * 16;
-  if (o.rows == 1) o.row = o.out_row;   // not used
-  o.pack = size == 4 || (reinterpret_cast<uintptr_t>(p) & 15u) || o.row * size % 16 || o.row < o.cols;
-  o.bytes = o.pack ? (size_t)o.rows * o.out_row * (size == 4 ? 6 : size) : 0;
-  return o;
-}
-
-// box: adjacent values x rows of a tile
-bool encode(CUtensorMap* m, const Operand& o, const void* base, int box_x, int box_y) {
-  EncodeTiled fn = encode_fn();
-  if (!fn) return false;
-  const int size = o.size == 1 ? 1 : 2;
-  const cuuint64_t row = (cuuint64_t)((o.pack ? o.out_row : o.row) * size);
-  const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, o.size == 4 ? 3ull : 1ull};
-  const cuuint64_t strides[2] = {row, row * (cuuint64_t)o.rows};
-  const cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, o.size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-cudaError_t pack(const Operand& o, void* to, int sm_count, cudaStream_t s) {
-  const long long pieces = o.rows * ((o.cols + 7) / 8), want = (pieces + 255) / 256, most = 16LL * sm_count;
-  const unsigned int ctas = (unsigned int)(want < most ? want : most);
-  const bool vec = ((reinterpret_cast<uintptr_t>(o.p) | (uintptr_t)(o.row * o.size)) & 15u) == 0;
-  __nv_bfloat16* terms = static_cast<__nv_bfloat16*>(to);
-  if (o.size == 4)
-    pack_kernel<float><<<ctas, 256, 0, s>>>(static_cast<const float*>(o.p), o.rows, o.cols, o.row, nullptr, terms, o.out_row, vec);
-  else if (o.size == 2)
-    pack_kernel<__nv_bfloat16><<<ctas, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(o.p), o.rows, o.cols, o.row, terms, nullptr, o.out_row, vec);
-  else
-    pack_kernel<unsigned char><<<ctas, 256, 0, s>>>(static_cast<const unsigned char*>(o.p), o.rows, o.cols, o.row,
-                                                    static_cast<unsigned char*>(to), nullptr, o.out_row, vec);
-  return cudaGetLastError();
-}
-
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Where four values of a row can move as one.
-bool four(const void* p, long long row, size_t size) {
-  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)((size_t)row * size)) & (4 * size - 1)) == 0;
+// Whether CUDA cores take the product (vla_rowvec.cu), eight rows of x at a time: with one or two rows (e4m3), four
+// (bfloat16) or sixteen (float32) the weights' way from memory bounds them; with more, their arithmetic does, and they win only
+// where the tensor cores' fixed cost is the larger part.  Measured (us, CUDA cores against vla_gemm_tokens.cu): bfloat16
+// N 8192, K 8192: 24.6 against 32 (1 row), 33.6 against 32 (4), 65 against 33 (8); N 520, K 264, 16 rows: 5.0 against 5.5,
+// 4.8 against 9.7 with rows that a copy has to align; float32 N 8192, K 8192: 208 against 216 (16), 366 against 218 (32);
+// e4m3: 17.4 against 18.8 (1), 22.0 against 18.9 (2), 31.7 against 18.9 (4).
+bool few_rows(const ProductArgs& p, int mat, bool copies) {
+  const long long most = mat == kMatF32 ? 16 : mat == kMatBf16 ? 4 : 2, eights = (p.M + 7) / 8;
+  return p.M <= most || (p.M <= 128 && p.N * p.Kd <= (1LL << (mat == kMatF32 || copies ? 23 : 21)) / eights);
 }
+
+// Whether w's rows are the long side of the tensor cores' product (vla_gemm_tokens.cu): up to 128 rows of x, and up to 512
+// where the weights are few (bfloat16, us against tiles of 256 rows: N 8192, K 8192: 37.6 against 43.2 with 128 rows,
+// 46.0 against 45.5 with 256; N 2048, K 4096: 14.2 against 16.9, and 17.9 against 20.7 with 512).
+bool tokens(const ProductArgs& p) { return p.M <= 128 || (p.M <= 512 && p.N * p.Kd <= 1LL << 23); }
 
 struct Plan {
   Operand a, b;
+  bool few;             // rows of x: CUDA cores
+  TokensPlan tokens;    // rows 0: tiles of 256 rows
   int bn, splits, tiles_m, tiles_n, k_iters, passes;
   size_t ws;
 };
@@ -703,6 +490,17 @@ Plan plan_of(const ProductArgs& p, int mat) {
   q.b = operand(p.b, p.N, p.Kd, p.b_row, p.b_mn, size);
   q.passes = mat == kMatF32 ? kPasses : 1;
   q.k_iters = (int)((p.Kd + (mat == kMatE4m3 ? 127 : 63)) / (mat == kMatE4m3 ? 128 : 64));
+  const bool rows_of_k = !p.a_mn && !p.b_mn && p.Kd > 0;
+  if (rows_of_k && few_rows(p, mat, q.a.pack || q.b.pack)) {
+    q.few = true;
+    return q;
+  }
+  if (rows_of_k && tokens(p)) {
+    q.tokens = tokens_plan(p.M, p.N, q.k_iters * q.passes, p.sm_count);
+    q.splits = 1;
+    q.ws = up256(q.a.bytes) + up256(q.b.bytes);
+    return q;
+  }
   q.tiles_m = (int)((p.M + 255) / 256);
   // Cost of a choice in stages of a 256 x 256 tile: waves of tiles, each with its stages and about 3 of latency at its
   // ends, and the parts' way through memory.
@@ -772,24 +570,11 @@ size_t product_ws(const ProductArgs& p, int mat) { return plan_of(p, mat).ws; }
 
 cudaError_t launch_product(const ProductArgs& p, int mat, cudaStream_t s) {
   const Plan q = plan_of(p, mat);
-  GemmArgs g{};
-  g.M = p.M; g.N = p.N;
+  if (q.few) return launch_few_rows(p, mat, s);
+  GemmArgs g = args_of(p);
   g.tiles_m = q.tiles_m; g.tiles_n = q.tiles_n; g.splits = q.splits;
   g.k_iters = q.k_iters; g.passes = q.passes;
-  g.out = p.out;
-  g.status = p.status;
   g.limit = kWaitLimitNs + 4000ull * (unsigned long long)q.k_iters * q.passes;
-  const size_t ysize = p.out.y_bf16 ? 2 : 4;
-  g.part_row = (p.N + 7) / 8 * 8;
-  auto sectors = [&](const void* x, long long row) {
-    return ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)((size_t)row * ysize)) & 31u) == 0;
-  };
-  g.direct = p.N * ysize % 32 == 0 && sectors(p.out.y, p.out.y_row) && (!p.out.pre || sectors(p.out.pre, p.out.pre_row)) &&
-             (!p.out.residual || sectors(p.out.residual, p.out.res_row)) &&
-             ((reinterpret_cast<uintptr_t>(p.out.bias) | reinterpret_cast<uintptr_t>(p.out.w_scale)) & 15u) == 0;
-  g.y_vec = four(p.out.y, p.out.y_row, ysize);
-  g.res_vec = four(p.out.residual, p.out.res_row, ysize);
-  g.pre_vec = four(p.out.pre, p.out.pre_row, ysize);
   char* ws = static_cast<char*>(p.ws);
   const void *a = p.a, *b = p.b;
   cudaError_t e = cudaSuccess;
@@ -797,6 +582,7 @@ cudaError_t launch_product(const ProductArgs& p, int mat, cudaStream_t s) {
     if (q.a.pack) e = pack(q.a, const_cast<void*>(a = ws), p.sm_count, s);
     if (q.b.pack && e == cudaSuccess) e = pack(q.b, const_cast<void*>(b = ws + up256(q.a.bytes)), p.sm_count, s);
     if (e != cudaSuccess) return e;
+    if (q.tokens.rows) return launch_tokens(q.tokens, g, q.a, q.b, a, b, s);
     // the parts' rows are written in pieces of 32 bytes
     g.partial = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + up256(q.a.bytes) + up256(q.b.bytes) + 31) & ~(uintptr_t)31);
     auto run = [&](auto bn, auto promote) -> cudaError_t {
