@@ -72,6 +72,22 @@ __device__ __forceinline__ float activate_slope(float v, int act) {
   return 1.f;
 }
 
+// A launch whose CTAs may start before the one before it on the stream is done (see launch_second): they wait for it in
+// wait_for_first before they touch memory.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3((unsigned int)threads);
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, static_cast<A&&>(args)...);
+}
+
 // What happens to the accumulator of output (m, n):
 //   v = acc * x_scale[m] * w_scale[n] + bias[n];  pre <- v;  y <- act(v) + residual
 struct Epilogue {

@@ -6,6 +6,7 @@
 #include "vla_dense.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace vla {
 namespace {
@@ -212,17 +213,52 @@ cudaError_t forward_of(const LayerNormArgs& a, cudaStream_t s) {
 constexpr int kBackStages = 8;
 constexpr int kBackThreads = 512;
 
+// The column of a thread's value v: VEC adjacent ones, then the next vector's.
+template <int VEC>
+__device__ __forceinline__ int column_of(int v, int tpr, int tid) { return (v / VEC * tpr + tid) * VEC + v % VEC; }
+
+// A thread's values of a row as float32 pairs (2 i, 2 i + 1), zero where there is no column or, without `on`, no row.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void get_row(const T* p, bool on, int tpr, int tid, int D, uint64_t (&o)[VEC * NV / 2]) {
+  if constexpr (VEC == 4) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = column_of<VEC>(4 * i, tpr, tid);
+      o[2 * i] = o[2 * i + 1] = 0;
+      if (!on || e >= D) continue;
+      const Vec<T, 4> x = ld_vec<T, 4>(p + e);
+      if constexpr (sizeof(T) == 2) {
+        o[2 * i] = pair(lo_f(x.raw.x), hi_f(x.raw.x));
+        o[2 * i + 1] = pair(lo_f(x.raw.y), hi_f(x.raw.y));
+      } else {
+        o[2 * i] = pair(__uint_as_float(x.raw.x), __uint_as_float(x.raw.y));
+        o[2 * i + 1] = pair(__uint_as_float(x.raw.z), __uint_as_float(x.raw.w));
+      }
+    }
+  } else {
+    T x[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = column_of<VEC>(i, tpr, tid);
+      x[i] = on && e < D ? p[e] : from_f32<T>(0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < NV / 2; ++i) o[i] = pair(to_f32<T>(x[2 * i]), to_f32<T>(x[2 * i + 1]));
+  }
+}
+
 template <typename TD, typename TX, int VEC, int NV>
 __global__ void __launch_bounds__(kBackThreads, 1)
     back_kernel(const LayerNormBackArgs a, int tpr, int rows_per_cta, int stages, int row_bytes, float inv_d, DevStatus* status) {
   extern __shared__ __align__(128) unsigned char smem[];   // the ring; at the end the rows' sums
   __shared__ uint64_t full[kBackStages];
-  __shared__ float part[2][2][kBackThreads / 32];
+  __shared__ float2 part[2][kBackThreads / 32];
   const int slot = threadIdx.x / tpr, tid = threadIdx.x - slot * tpr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w0 = slot * (tpr >> 5), wn = tpr >> 5;
   const int D = (int)a.D;
   const long long step = (long long)gridDim.x * rows_per_cta, base = (long long)blockIdx.x * rows_per_cta;
+  all_started();   // the sums' kernel
   const uint32_t dy_bytes = (uint32_t)(D * sizeof(TD)), x_bytes = (uint32_t)(D * sizeof(TX));
 
   auto fill = [&](long long first, int stage) {   // one thread
@@ -247,25 +283,21 @@ __global__ void __launch_bounds__(kBackThreads, 1)
     if (threadIdx.x == 0)
       for (int i = 0; i < stages; ++i) fill(base + i * step, i);
   }
-  float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const int e = (i * tpr + tid) * VEC;
-      w[i][v] = e < D ? a.w[e + v] : 0.f;
-      dw[i][v] = db[i][v] = 0.f;
-    }
+  constexpr int P = VEC * NV / 2;
+  auto column = [&](int v) { return column_of<VEC>(v, tpr, tid); };
+  // 16 values a thread leave no registers for w: it is read again every row, from the first-level cache
+  constexpr bool KEEP = VEC * NV <= 8;
+  uint64_t w[P], dw[P] = {}, db[P] = {};
+  if (KEEP) get_row<float, VEC, NV>(a.w, true, tpr, tid, D, w);
   long long row = base + slot;
   float mean = 0.f, rstd = 0.f;
-  auto stats = [&](long long r) {
-    if (r < a.rows) {
-      mean = a.stats[2 * r];
-      rstd = a.stats[2 * r + 1];
-    }
+  auto stats = [&](long long r) {   // a row that there is not counts nothing
+    mean = r < a.rows ? a.stats[2 * r] : 0.f;
+    rstd = r < a.rows ? a.stats[2 * r + 1] : 0.f;
   };
   stats(row);
-  int par = 0, stage = 0;
+  int par = 0, stage = 0, span = 2;   // span: the power of two from wn on
+  while (span < wn) span *= 2;
   uint32_t phase = 0;
   bool ok = true;
   for (long long first = base; first < a.rows; first += step, row += step, par ^= 1) {
@@ -280,40 +312,34 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       dres = reinterpret_cast<const TX*>(at + dy_bytes + x_bytes);
       ok = mbar_wait_bounded(full + stage, phase);
     }
-    const float mu = mean, rs = rstd;
+    uint64_t g[P], h[P], t1 = 0, t2 = 0;
+    get_row<TD, VEC, NV>(dy, live, tpr, tid, D, g);
+    get_row<TX, VEC, NV>(x, live, tpr, tid, D, h);
+    const float rs = rstd;
+    const uint64_t scale = pair(rs, rs), shift = pair(-mean * rs, -mean * rs);
     stats(row + step);
-    float g[NV][VEC], h[NV][VEC], s1 = 0.f, s2 = 0.f;
+    if (!KEEP) get_row<float, VEC, NV>(a.w, true, tpr, tid, D, w);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = (i * tpr + tid) * VEC;
-      Vec<TD, VEC> d;
-      Vec<TX, VEC> c;
-      const bool on = live && ok && e < D;
-      if (on) {
-        d = ld_vec<TD, VEC>(dy + e);
-        c = ld_vec<TX, VEC>(x + e);
-      }
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float y = on ? to_f32<TD>(d.v[v]) : 0.f;
-        h[i][v] = on ? (to_f32<TX>(c.v[v]) - mu) * rs : 0.f;
-        g[i][v] = y * w[i][v];
-        dw[i][v] = fmaf(y, h[i][v], dw[i][v]);
-        db[i][v] += y;
-        s1 += g[i][v];
-        s2 = fmaf(g[i][v], h[i][v], s2);
-      }
+    for (int i = 0; i < P; ++i) {
+      h[i] = fma2(h[i], scale, shift);
+      dw[i] = fma2(g[i], h[i], dw[i]);
+      db[i] = add2(g[i], db[i]);
+      g[i] = mul2(g[i], w[i]);
+      t1 = add2(t1, g[i]);
+      t2 = fma2(g[i], h[i], t2);
     }
+    float s1, s2, other;
+    unpair(t1, s1, other);
+    s1 += other;
+    unpair(t2, s2, other);
+    s2 += other;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       s1 += __shfl_xor_sync(0xffffffffu, s1, o);
       s2 += __shfl_xor_sync(0xffffffffu, s2, o);
     }
     // the other half of the parts is still read by warps that are a row behind
-    if (lane == 0) {
-      part[par][0][warp] = s1;
-      part[par][1][warp] = s2;
-    }
+    if (lane == 0) part[par][warp] = make_float2(s1, s2);
     if (VEC > 1) {
       if (__syncthreads_or(!ok)) {   // a copy that did not arrive: give up, all threads alike
         if (threadIdx.x == 0) atomicOr(&status->flags, kStatusTimeout);
@@ -325,33 +351,46 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       __syncthreads();
     }
     if (wn > 1) {
-      s1 = lane < wn ? part[par][0][w0 + lane] : 0.f;
-      s2 = lane < wn ? part[par][1][w0 + lane] : 0.f;
-#pragma unroll
-      for (int o = kBackThreads / 64; o > 0; o >>= 1) {
+      const int at = lane & (span - 1);   // every lane ends up with the row's sums
+      const float2 q = at < wn ? part[par][w0 + at] : make_float2(0.f, 0.f);
+      s1 = q.x;
+      s2 = q.y;
+      for (int o = span >> 1; o > 0; o >>= 1) {
         s1 += __shfl_xor_sync(0xffffffffu, s1, o);
         s2 += __shfl_xor_sync(0xffffffffu, s2, o);
       }
-      s1 = __shfl_sync(0xffffffffu, s1, 0);
-      s2 = __shfl_sync(0xffffffffu, s2, 0);
     }
-    s1 *= inv_d;
-    s2 *= inv_d;
+    const uint64_t m1 = pair(-s1 * inv_d, -s1 * inv_d), m2 = pair(-s2 * inv_d, -s2 * inv_d);
     if (live) {
       TX* dx = static_cast<TX*>(a.dx) + row * a.dx_row;
+      uint64_t r[P] = {};
+      if (a.dres) get_row<TX, VEC, NV>(dres, true, tpr, tid, D, r);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = (i * tpr + tid) * VEC;
-        if (e >= D) continue;
-        Vec<TX, VEC> o, r;
-        if (a.dres) r = ld_vec<TX, VEC>(dres + e);
+      for (int i = 0; i < P; ++i) r[i] = fma2(fma2(h[i], m2, add2(g[i], m1)), scale, r[i]);
+      if constexpr (VEC == 4) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-          float t = rs * (g[i][v] - fmaf(h[i][v], s2, s1));
-          if (a.dres) t += to_f32<TX>(r.v[v]);
-          o.v[v] = from_f32<TX>(t);
+        for (int i = 0; i < NV; ++i) {
+          if (column(4 * i) >= D) continue;
+          float v[4];
+          unpair(r[2 * i], v[0], v[1]);
+          unpair(r[2 * i + 1], v[2], v[3]);
+          Vec<TX, 4> o;
+          if constexpr (sizeof(TX) == 2) {
+            o.raw = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o.v[k] = v[k];
+          }
+          st_vec<TX, 4>(dx + column(4 * i), o);
         }
-        st_vec<TX, VEC>(dx + e, o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          float u, v;
+          unpair(r[i], u, v);
+          if (column(2 * i) < D) dx[column(2 * i)] = from_f32<TX>(u);
+          if (column(2 * i + 1) < D) dx[column(2 * i + 1)] = from_f32<TX>(v);
+        }
       }
     }
     if (++stage == stages) {
@@ -364,24 +403,21 @@ __global__ void __launch_bounds__(kBackThreads, 1)
   for (int r = 0; r < rows_per_cta; ++r) {
     if (rows_per_cta > 1) __syncthreads();   // the ring is read no more; the last slot has added its sums
     if (slot != r) continue;
+    float* to_w = r + 1 < rows_per_cta ? sums : a.partial + 2 * blockIdx.x * a.D;
+    float* to_b = to_w + D;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < P; ++i) {
+      float u[2], v[2];
+      unpair(dw[i], u[0], u[1]);
+      unpair(db[i], v[0], v[1]);
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const int e = (i * tpr + tid) * VEC + v;
+      for (int k = 0; k < 2; ++k) {
+        const int e = column(2 * i + k);
         if (e >= D) continue;
-        if (r > 0) {
-          dw[i][v] += sums[e];
-          db[i][v] += sums[D + e];
-        }
-        if (r + 1 < rows_per_cta) {
-          sums[e] = dw[i][v];
-          sums[D + e] = db[i][v];
-        } else {
-          a.partial[2 * blockIdx.x * a.D + e] = dw[i][v];
-          a.partial[(2 * blockIdx.x + 1) * a.D + e] = db[i][v];
-        }
+        to_w[e] = r > 0 ? u[k] + sums[e] : u[k];
+        to_b[e] = r > 0 ? v[k] + sums[D + e] : v[k];
       }
+    }
   }
 }
 
@@ -445,25 +481,23 @@ __global__ void __launch_bounds__(256) back_column_kernel(const LayerNormBackArg
   a.partial[(2 * blockIdx.y + 1) * a.D + e] = db;
 }
 
-// The parts' sums, of dw (blockIdx.y 0) and db: a block has 32 columns, its 8 warps take every eighth part.
-__global__ void __launch_bounds__(256) back_sum_kernel(const float* partial, float* dw, float* db, long long D, long long parts) {
-  __shared__ float sums[8][32];
+// The parts' sums, of dw (blockIdx.y 0) and db: a block has 32 columns, its 32 warps take every 32nd part.
+__global__ void __launch_bounds__(1024) back_sum_kernel(const float* partial, float* dw, float* db, long long D, long long parts) {
+  __shared__ float sums[32][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long e = (long long)blockIdx.x * 32 + lane;
   const float* p = partial + blockIdx.y * D + e;
   float sum = 0.f;
+  wait_for_first();
   if (e < D) {
-#pragma unroll 8
-    for (long long i = warp; i < parts; i += 8) sum += p[2 * i * D];
+#pragma unroll 4
+    for (long long i = warp; i < parts; i += 32) sum += p[2 * i * D];
   }
   sums[warp][lane] = sum;
   __syncthreads();
-  if (warp == 0 && e < D) {
-    sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += sums[i][lane];
-    (blockIdx.y ? db : dw)[e] = sum;
-  }
+  sum = warp_sum(sums[lane][warp]);   // column `warp` of the block
+  const long long c = (long long)blockIdx.x * 32 + warp;
+  if (lane == 0 && c < D) (blockIdx.y ? db : dw)[c] = sum;
 }
 
 constexpr long long kOnePass = 8192;   // values of a row that back_kernel takes
@@ -531,7 +565,7 @@ cudaError_t backward(const LayerNormBackArgs& a, cudaStream_t s) {
     };
     constexpr size_t SD = sizeof(TD), SX = sizeof(TX);
     const bool ring = a.D * SD % 16 == 0 && a.D * SX % 16 == 0 && whole(a.dy, a.dy_row, SD) && whole(a.x, a.x_row, SX) &&
-                      whole(a.dx, a.dx_row, SX) && (!a.dres || whole(a.dres, a.dres_row, SX));
+                      whole(a.dx, a.dx_row, SX) && (!a.dres || whole(a.dres, a.dres_row, SX)) && whole(a.w, 0, 4);
     if (back_shape(a.D).n == 8) e = ring ? one_pass<TD, TX, 4, 2>(a, s) : one_pass<TD, TX, 1, 8>(a, s);
     else e = ring ? one_pass<TD, TX, 4, 4>(a, s) : one_pass<TD, TX, 1, 16>(a, s);
   } else {
@@ -542,8 +576,7 @@ cudaError_t backward(const LayerNormBackArgs& a, cudaStream_t s) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  back_sum_kernel<<<dim3((unsigned int)((a.D + 31) / 32), a.db ? 2 : 1), 256, 0, s>>>(a.partial, a.dw, a.db, a.D, parts);
-  return cudaGetLastError();
+  return launch_after(back_sum_kernel, dim3((unsigned int)((a.D + 31) / 32), a.db ? 2 : 1), 1024, s, a.partial, a.dw, a.db, a.D, parts);
 }
 
 }  // namespace
