@@ -64,7 +64,8 @@ vla::ProductArgs linear_product(vla_handle_t h, const void* x, const void* w, lo
 
 // The two products of a gradient and what they share of the workspace: g, the partial sums of db.
 struct BackPlan {
-  vla::ProductArgs dx, dw;
+  vla::ProductArgs dx, dw, run[2];   // run: those that are asked for
+  int count;
   vla::SlopeArgs slope;
   size_t g_bytes, part_bytes, ws_bytes;
 };
@@ -90,9 +91,11 @@ BackPlan back_plan(vla_handle_t h, const void* dy, const void* x, const void* w,
   b.dx.sm_count = b.dw.sm_count = h->sm_count;
   b.dx.status = b.dw.status = h->status;
   b.dx.out.y_bf16 = b.dw.out.y_bf16 = io == VLA_BF16;
-  const int mat = io == VLA_BF16 ? VLA_MAT_BF16 : VLA_MAT_F32;
-  const size_t x_ws = want_dx && N ? vla::product_ws(b.dx, mat) : 0, w_ws = want_dw && M ? vla::product_ws(b.dw, mat) : 0;
-  b.ws_bytes = b.g_bytes + b.part_bytes + (x_ws > w_ws ? x_ws : w_ws);   // one product after the other
+  b.count = 0;
+  if (want_dx) b.run[b.count++] = b.dx;
+  if (want_dw) b.run[b.count++] = b.dw;
+  b.ws_bytes = b.g_bytes + b.part_bytes;
+  if (b.count) b.ws_bytes += vla::products_ws(b.run, b.count, io == VLA_BF16 ? VLA_MAT_BF16 : VLA_MAT_F32);
   return b;
 }
 
@@ -128,9 +131,9 @@ vla_err_t vla_linear(vla_handle_t h, const void* x, const void* w, const float* 
   o.x_scale = x_scale; o.w_scale = w_scale; o.bias = bias; o.residual = residual; o.pre = pre; o.y = y;
   o.res_row = rows[2]; o.pre_row = rows[3]; o.y_row = rows[4];
   o.act = act; o.y_bf16 = out == VLA_BF16;
-  if ((err = check_ws(h, f, workspace, workspace_bytes, vla::product_ws(p, in))) != VLA_OK) return err;
+  if ((err = check_ws(h, f, workspace, workspace_bytes, vla::products_ws(&p, 1, in))) != VLA_OK) return err;
   p.ws = workspace;
-  cudaError_t e = on_device(h->device, [&]() { return vla::launch_product(p, in, static_cast<cudaStream_t>(stream)); });
+  cudaError_t e = on_device(h->device, [&]() { return vla::launch_products(&p, 1, in, static_cast<cudaStream_t>(stream)); });
   if (e != cudaSuccess) return fail(h, VLA_ERR_CUDA, cuda_msg("vla_linear: launch", e));
   return VLA_OK;
 } catch (const std::exception&) {   // no memory for a message
@@ -151,7 +154,7 @@ vla_err_t vla_linear_workspace(vla_handle_t h, const void* x, const void* w, lon
   if ((err = check_strides(h, f, rows, 2)) != VLA_OK) return err;
   vla::ProductArgs p = linear_product(h, x, w, M, N, K, rows);
   p.out.y_bf16 = out == VLA_BF16;
-  *bytes = vla::product_ws(p, in);
+  *bytes = vla::products_ws(&p, 1, in);
   return VLA_OK;
 } catch (const std::exception&) {   // no memory for a message
   return VLA_ERR_NOMEM;
@@ -187,10 +190,15 @@ vla_err_t vla_linear_backward(vla_handle_t h, const void* dy, const void* x, con
   char* ws = static_cast<char*>(workspace);
   b.slope.dy = dy; b.slope.pre = has_act ? pre : nullptr; b.slope.act = act; b.slope.db = db;
   b.slope.partial = reinterpret_cast<float*>(ws + b.g_bytes);
-  if (b.g_bytes) b.slope.g = const_cast<void*>(b.dx.a = b.dw.a = ws);
-  b.dx.ws = b.dw.ws = ws + b.g_bytes + b.part_bytes;
-  b.dx.out.y = dx; b.dx.out.y_row = rows[4];
-  b.dw.out.y = dw; b.dw.out.y_row = rows[5];
+  if (b.g_bytes) b.slope.g = ws;
+  for (int i = 0; i < b.count; ++i) {
+    vla::ProductArgs& p = b.run[i];
+    if (b.g_bytes) p.a = ws;
+    p.ws = ws + b.g_bytes + b.part_bytes;
+    p.follows = terms && (b.g_bytes || db);
+    p.out.y = p.a_mn ? dw : dx;
+    p.out.y_row = rows[p.a_mn ? 5 : 4];
+  }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = io_dtype == VLA_BF16;
   const int mat = bf16 ? VLA_MAT_BF16 : VLA_MAT_F32;
@@ -198,8 +206,7 @@ vla_err_t vla_linear_backward(vla_handle_t h, const void* dy, const void* x, con
     cudaError_t r = cudaSuccess;
     if (terms && (b.g_bytes || db)) r = vla::launch_slope(b.slope, bf16, s);
     if (r == cudaSuccess && !terms && db) r = cudaMemsetAsync(db, 0, (size_t)N * 4, s);
-    if (r == cudaSuccess && dx) r = vla::launch_product(b.dx, mat, s);
-    if (r == cudaSuccess && dw) r = vla::launch_product(b.dw, mat, s);
+    if (r == cudaSuccess && b.count) r = vla::launch_products(b.run, b.count, mat, s);
     return r;
   });
   if (e != cudaSuccess) return fail(h, VLA_ERR_CUDA, cuda_msg("vla_linear_backward: launch", e));

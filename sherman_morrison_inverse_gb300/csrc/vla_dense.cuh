@@ -14,66 +14,89 @@ enum Mat { kMatF32 = 0, kMatBf16 = 1, kMatE4m3 = 2 };    // vla_mat_t
 template <>
 __device__ __forceinline__ float to_f32<__nv_fp8_e4m3>(__nv_fp8_e4m3 x) { return static_cast<float>(x); }
 
-// erfc(z) for z = |v| / sqrt(2), and e = exp(-z^2) (approximate exponential and reciprocal):
-// erfc(z) = e t P(t) with t = 1 / (1 + 0.44 z), P a polynomial of degree 7 fitted to the smallest largest
-// relative error over z >= 0: 6e-7 in float32, some thousandth of half a step of bfloat16, the type that the
-// results of this form are rounded to (and of the size of a bias gradient's own rounding).
-__device__ __forceinline__ float erfc_fast(float z, float* e) {
-  const float t = rcp(fmaf(0.44f, z, 1.f));
-  *e = ex2(z * z * -1.44269504088896341f);
-  float p = 0.06916839629411697f;
-  p = fmaf(p, t, -0.27031081914901733f);
-  p = fmaf(p, t, 0.28519880771636963f);
-  p = fmaf(p, t, -0.01120822038501501f);
-  p = fmaf(p, t, 0.21193894743919373f);
-  p = fmaf(p, t, 0.21821904182434082f);
-  p = fmaf(p, t, 0.24876849353313446f);
-  p = fmaf(p, t, 0.24822503328323364f);
-  return p * t * *e;
-}
-
 constexpr float kSqrtHalf = 0.70710678118654752f, kInvSqrt2Pi = 0.39894228040143268f;
 
-// Phi(v) = erfc(-v / sqrt(2)) / 2, and (DERIV) the density phi(v).  FAST: for results rounded to bfloat16.
+__device__ __forceinline__ uint64_t both(float x) { return pair(x, x); }
+
+// Phi(v) = erfc(-v / sqrt(2)) / 2 and e = exp(-v^2 / 2) of a pair, for results rounded to bfloat16 (approximate exponential and
+// reciprocal).  With z = |v| / sqrt(2), erfc(z) = e t P(t), t = 1 / (1 + 0.44 z), P a polynomial of degree 7 fitted to the
+// smallest largest relative error over z >= 0: 6e-7 in float32, some thousandth of half a step of bfloat16 and the size of
+// a bias gradient's own rounding.  The coefficients here are halved: c = Phi(-|v|).
+__device__ __forceinline__ uint64_t gauss_cdf2(uint64_t v, uint64_t* e) {
+  const uint64_t a = v & 0x7fffffff7fffffffull;
+  float x, y;
+  unpair(fma2(a, both(0.44f * kSqrtHalf), both(1.f)), x, y);
+  const uint64_t t = pair(rcp(x), rcp(y));
+  unpair(mul2(mul2(v, v), both(-0.72134752044448170f)), x, y);   // log2(e) / 2
+  *e = pair(ex2(x), ex2(y));
+  uint64_t p = both(0.034584198147058487f);
+  p = fma2(p, t, both(-0.13515540957450867f));
+  p = fma2(p, t, both(0.14259940385818481f));
+  p = fma2(p, t, both(-0.005604110192507505f));
+  p = fma2(p, t, both(0.10596947371959686f));
+  p = fma2(p, t, both(0.10910952091217041f));
+  p = fma2(p, t, both(0.12438424676656723f));
+  p = fma2(p, t, both(0.12411251664161682f));
+  const uint64_t c = mul2(mul2(p, t), *e);
+  float cx, cy, vx, vy;
+  unpair(c, cx, cy);
+  unpair(fma2(c, both(-1.f), both(1.f)), x, y);
+  unpair(v, vx, vy);
+  return pair(vx < 0.f ? cx : x, vy < 0.f ? cy : y);
+}
+
+// The activation of a pair.  FAST: for results rounded to bfloat16.
 template <bool FAST>
-__device__ __forceinline__ float gauss_cdf(float v, float* density) {
+__device__ __forceinline__ uint64_t activate2(uint64_t v, int act) {
+  if (act == kActNone) return v;
   if (FAST) {
-    float e;
-    const float c = 0.5f * erfc_fast(fabsf(v) * kSqrtHalf, &e);
-    *density = kInvSqrt2Pi * e;
-    return v < 0.f ? c : 1.f - c;
+    if (act == kActSilu) return silu2(v);
+    uint64_t e;
+    return mul2(v, gauss_cdf2(v, &e));
   }
-  *density = kInvSqrt2Pi * expf(-0.5f * v * v);
-  return 0.5f * erfcf(-v * kSqrtHalf);
+  float x, y;
+  unpair(v, x, y);
+  if (act == kActSilu) return pair(silu<false>(x), silu<false>(y));
+  return pair(x * (0.5f * erfcf(-x * kSqrtHalf)), y * (0.5f * erfcf(-y * kSqrtHalf)));
+}
+
+__device__ __forceinline__ float slope_of(float v, int act) {
+  if (act == kActSilu) {
+    const float s = 1.f / (1.f + expf(-v));
+    return s * fmaf(v, 1.f - s, 1.f);
+  }
+  return fmaf(v, kInvSqrt2Pi * expf(-0.5f * v * v), 0.5f * erfcf(-v * kSqrtHalf));
+}
+
+// Its derivative (act is not kActNone).
+template <bool FAST>
+__device__ __forceinline__ uint64_t slope2(uint64_t v, int act) {
+  float x, y;
+  if (!FAST) {
+    unpair(v, x, y);
+    return pair(slope_of(x, act), slope_of(y, act));
+  }
+  if (act == kActSilu) {
+    unpair(mul2(v, both(-1.44269504088896341f)), x, y);
+    unpair(add2(pair(ex2(x), ex2(y)), both(1.f)), x, y);
+    const uint64_t s = pair(rcp(x), rcp(y));
+    return mul2(s, fma2(v, fma2(s, both(-1.f), both(1.f)), both(1.f)));
+  }
+  uint64_t e;
+  const uint64_t cdf = gauss_cdf2(v, &e);
+  return fma2(v, mul2(e, both(kInvSqrt2Pi)), cdf);
 }
 
 template <bool FAST>
 __device__ __forceinline__ float activate(float v, int act) {
-  if (act == kActSilu) return silu<FAST>(v);
-  if (act == kActGelu) {
-    float d;
-    return v * gauss_cdf<FAST>(v, &d);
-  }
-  return v;
+  float x, y;
+  unpair(activate2<FAST>(pair(v, 0.f), act), x, y);
+  return x;
 }
 
-// The activation's derivative at v.
-template <bool FAST>
-__device__ __forceinline__ float activate_slope(float v, int act) {
-  if (act == kActSilu) {
-    const float s = FAST ? __fdividef(1.f, 1.f + __expf(-v)) : 1.f / (1.f + expf(-v));
-    return s * fmaf(v, 1.f - s, 1.f);
-  }
-  if (act == kActGelu) {
-    float d;
-    const float c = gauss_cdf<FAST>(v, &d);
-    return fmaf(v, d, c);
-  }
-  return 1.f;
-}
-
-// A launch whose CTAs may start before the one before it on the stream is done (see launch_second): they wait for it in
-// wait_for_first before they touch memory.
+// A launch whose CTAs may start before the one before it on the stream is done (see launch_second).  Every thread of them waits for
+// it in wait_for_first before it touches memory, and only a launch of the same call may lie before, of which the same holds:
+// so what is done when it is done includes everything earlier on the stream.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, A&&... args) {
   cudaLaunchAttribute attr{};
@@ -103,21 +126,23 @@ struct Epilogue {
 };
 
 // C [M, N] = sum over Kd of A B.  A lies in memory as M rows of Kd adjacent values, or (a_mn) as Kd rows of M;
-// B as N rows of Kd, or (b_mn) as Kd rows of N.  Built: neither, b_mn alone, both; e4m3: neither.
+// B as N rows of Kd, or (b_mn) as Kd rows of N.  e4m3: neither MN.
 struct ProductArgs {
   const void* a;
   const void* b;
   long long M, N, Kd;
   long long a_row, b_row;   // distance of rows in values
   bool a_mn, b_mn;
+  bool follows;             // a launch of the same call, whose CTAs say all_started, lies before on the stream
   Epilogue out;
   void* ws;
   int sm_count;
   DevStatus* status;
 };
-cudaError_t launch_product(const ProductArgs& p, int mat, cudaStream_t s);
-// Bytes that it needs at p.ws; of the operands only sizes, strides and alignment count.
-size_t product_ws(const ProductArgs& p, int mat);
+// One or two products (count) that may run together, of one type and with one workspace (p[0].ws).
+cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream_t s);
+// Bytes that they need there; of the operands only sizes, strides, alignment and which are the same count.
+size_t products_ws(const ProductArgs* p, int count, int mat);
 
 // g = dy * act'(pre) [M, N] (when pre is not NULL), and db[n] = sum_m g (when db is not NULL; float32, from g
 // before it is rounded).

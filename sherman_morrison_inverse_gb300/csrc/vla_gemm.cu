@@ -9,6 +9,7 @@
 //   warps 2, 3 only leave their registers to the others.
 //   warps 4..11 take the other accumulator out, 32 columns of a lane's row at a time, through the epilogue to memory in
 //              32-byte pieces; rows off 32-byte boundaries go through shared memory first.
+// A launch holds one or two products (a gradient's): their tiles follow one another, so that one's last wave is the other's first.
 // Operands lie in memory with Kd adjacent (as in x w^T) or with M or N adjacent (as in g w and g^T x): tiles
 // of 64 along what is adjacent, and the matrix descriptors say which.
 // float32 operands arrive as three bfloat16 terms each (x = x1 + x2 + x3 to 2^-24): six products, the small ones
@@ -38,6 +39,14 @@ struct Cfg {
   static constexpr uint32_t bars = 2 * stages + 5;
   static constexpr uint32_t bytes = o_bar + 8 * bars + 16;
   static constexpr uint32_t cols = 2 * BN;
+};
+
+// Two products of a launch: tiles [0, g[0].tiles) are the first one's.
+struct GemmPair {
+  GemmArgs g[2];
+};
+struct Maps {
+  CUtensorMap a[2], b[2];
 };
 
 // One product of both CTAs for 32 bytes of Kd, issued by the lane whose `one` is set.  The whole warp runs the loop
@@ -175,10 +184,10 @@ __device__ __forceinline__ void chunk_direct(const GemmArgs& g, float* v, float 
     if (e.pre && alive) st_piece(static_cast<T*>(e.pre) + m * e.pre_row + at, to_piece<T, COLS>(u));
     if (e.act == kActSilu) {
 #pragma unroll
-      for (int j = 0; j < COLS; ++j) u[j] = activate<sizeof(T) == 2>(u[j], kActSilu);
+      for (int j = 0; j < COLS; j += 2) unpair(activate2<sizeof(T) == 2>(pair(u[j], u[j + 1]), kActSilu), u[j], u[j + 1]);
     } else if (e.act == kActGelu) {
 #pragma unroll
-      for (int j = 0; j < COLS; ++j) u[j] = activate<sizeof(T) == 2>(u[j], kActGelu);
+      for (int j = 0; j < COLS; j += 2) unpair(activate2<sizeof(T) == 2>(pair(u[j], u[j + 1]), kActGelu), u[j], u[j + 1]);
     }
     if (e.residual) {
 #pragma unroll
@@ -220,7 +229,7 @@ __device__ __forceinline__ void chunk_staged(const GemmArgs& g, const float* v, 
 
 // Warps 4..11: a warp takes 32 rows (those of the tensor memory lanes that it can reach) and half the columns.
 template <typename T, int BN, bool PROMOTE>
-__device__ __forceinline__ void epilogue(const GemmArgs& g, uint32_t tmem, uint32_t chunk, uint64_t* acc_full,
+__device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, uint32_t chunk, uint64_t* acc_full,
                                          uint64_t* acc_empty, uint32_t rank, int warp, int lane, int first, int step,
                                          int n_tiles, volatile uint32_t* failed) {
   constexpr int CHUNKS = BN / 64;
@@ -239,7 +248,9 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, uint32_t tmem, uint3
     if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(acc_empty + buf), 0));
   };
   for (int t = first; t < n_tiles; t += step) {
-    const Tile at = tile_at(t, g.tiles_m, g.tiles_n);
+    const bool second = t >= pair.g[0].tiles;
+    const GemmArgs& g = pair.g[second];
+    const Tile at = tile_at(second ? t - pair.g[0].tiles : t, g.tiles_m, g.tiles_n);
     const long long m0 = (long long)at.m * 256 + rank * 128 + quad * 32, m = m0 + lane;
     const long long n0 = (long long)at.n * BN + half * (BN / 2);
     const bool alive = m < g.M;
@@ -290,9 +301,9 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, uint32_t tmem, uint3
   }
 }
 
-template <int BN, bool A_MN, bool B_MN, bool E4M3, bool PROMOTE>
+template <int BN, bool E4M3, bool PROMOTE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemmArgs g) {
+    gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmPair pair) {
   using C = Cfg<BN>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = smem_u32(smem);
@@ -302,7 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile uint32_t* failed = slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int n_tiles = g.tiles_m * g.tiles_n * g.splits, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int n_tiles = pair.g[0].tiles + pair.g[1].tiles, first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::stages; ++i) {
@@ -323,13 +334,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();
   tc::fence_after_sync();
   const uint32_t tmem = *slot;
+  wait_for_first();   // copies, g
+  all_started();      // the joining of parts
 
   // the block's registers, 168 a thread at launch: 128 x 40 + 256 x 232 = 384 x 168
   if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const uint32_t chunk = base + C::o_chunk + (warp - 4) * kChunk;
     using T = typename std::conditional<PROMOTE, float, __nv_bfloat16>::type;   // y's type
-    epilogue<T, BN, PROMOTE>(g, tmem, chunk, acc_full, acc_empty, rank, warp, lane, first, step, n_tiles, failed);
+    epilogue<T, BN, PROMOTE>(pair, tmem, chunk, acc_full, acc_empty, rank, warp, lane, first, step, n_tiles, failed);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
@@ -338,7 +351,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t stage = 0, phase = 1, issued = 0;
         bool ok = !*failed;
         for (int t = first; ok && t < n_tiles; t += step) {
-          const Tile at = tile_at(t, g.tiles_m, g.tiles_n);
+          const bool second = t >= pair.g[0].tiles;
+          const GemmArgs& g = pair.g[second];
+          const CUtensorMap *map_a = &maps.a[second], *map_b = &maps.b[second];
+          const Tile at = tile_at(second ? t - pair.g[0].tiles : t, g.tiles_m, g.tiles_n);
           const int m0 = at.m * 256 + rank_m, n0 = at.n * BN + rank_n;
           const int k1 = k_begin(g, at.split + 1);
           int k = k_begin(g, at.split), pass = k / g.k_iters, it = k - pass * g.k_iters;
@@ -348,18 +364,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t bar = mapa_shared(smem_u32(full + stage), 0);
             if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * C::stage);
             const int ta = g.passes > 1 ? term_a(pass) : 0, tb = g.passes > 1 ? term_b(pass) : 0;
-            constexpr int BK = E4M3 ? 128 : 64;
-            if (A_MN) {
-  #pragma unroll
-              for (int j = 0; j < 2; ++j) tma_pair(sa + j * 8192, &map_a, m0 + 64 * j, it * BK, ta, bar);
+            const int at_k = it * (E4M3 ? 128 : 64);
+            if (g.a_mn) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) tma_pair(sa + j * 8192, map_a, m0 + 64 * j, at_k, ta, bar);
             } else {
-              tma_pair(sa, &map_a, it * BK, m0, ta, bar);
+              tma_pair(sa, map_a, at_k, m0, ta, bar);
             }
-            if (B_MN) {
-  #pragma unroll
-              for (int j = 0; j < BN / 128; ++j) tma_pair(sb + j * 8192, &map_b, n0 + 64 * j, it * BK, tb, bar);
+            if (g.b_mn) {
+#pragma unroll
+              for (int j = 0; j < BN / 128; ++j) tma_pair(sb + j * 8192, map_b, n0 + 64 * j, at_k, tb, bar);
             } else {
-              tma_pair(sb, &map_b, it * BK, n0, tb, bar);
+              tma_pair(sb, map_b, at_k, n0, tb, bar);
             }
             ++issued;
             if (++stage == C::stages) {
@@ -384,14 +400,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       if (rank == 0) {
         const uint32_t one = lane == 0;
-        constexpr uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (A_MN ? 1u << 15 : 0u) |
-                                   (B_MN ? 1u << 16 : 0u) | (uint32_t)(BN >> 3) << 17 | (256u >> 4) << 24;
-        constexpr uint32_t step_a = A_MN ? 2048 >> 4 : 32 >> 4, step_b = B_MN ? 2048 >> 4 : 32 >> 4;
         uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1;
         bool ok = !*failed;
         for (int t = first; ok && t < n_tiles; t += step) {
-          const int split = t / (g.tiles_m * g.tiles_n);
+          const bool second = t >= pair.g[0].tiles;
+          const GemmArgs& g = pair.g[second];
+          const int split = (second ? t - pair.g[0].tiles : t) / (g.tiles_m * g.tiles_n);
           const int k1 = k_begin(g, split + 1);
+          const uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (g.a_mn ? 1u << 15 : 0u) |
+                                 (g.b_mn ? 1u << 16 : 0u) | (uint32_t)(BN >> 3) << 17 | (256u >> 4) << 24;
+          const uint32_t step_a = g.a_mn ? 2048 >> 4 : 32 >> 4, step_b = g.b_mn ? 2048 >> 4 : 32 >> 4;
           for (int k = k_begin(g, split); ok && k < k1;) {
             const int end = PROMOTE ? part_end(g, k, k1) : k1;
             if (!(ok = wait_for(acc_empty + buf, buf_phase, g.limit, failed))) break;
@@ -402,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               tc::fence_after_sync();
               const uint32_t sa = base + stage * C::stage;
               const uint64_t da = desc128(sa, 8192), db = desc128(sa + C::a_bytes, 8192);
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < 4; ++i) mma_pair<E4M3>(d, da + i * step_a, db + i * step_b, idesc, more || i > 0, one);
               commit_pair(smem_u32(empty + stage), one);
               if (++stage == C::stages) {
@@ -431,14 +449,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();   // neither CTA leaves while the other can still signal it
   tc::fence_after_sync();
   if (warp == 1) dealloc_pair(tmem, C::cols);
-  if (threadIdx.x == 0 && *failed) atomicOr(&g.status->flags, kStatusTimeout);
+  if (threadIdx.x == 0 && *failed) atomicOr(&pair.g[0].status->flags, kStatusTimeout);
 }
 
 // ---------------------------------------------------------------------------------------------
 // parts of a split Kd, added in their order, and the epilogue; without parts the sum is 0
 
 template <typename T>
-__global__ void __launch_bounds__(256) join_kernel(const float* partial, int parts, const GemmArgs g) {
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ GemmPair pair) {
+  const GemmArgs& g = pair.g[blockIdx.y];
+  wait_for_first();
+  if (g.splits == 1) return;
   const long long across = (g.N + 3) / 4, all = g.M * across;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
     const long long m = i / across, n = (i - m * across) * 4;
@@ -446,10 +467,12 @@ __global__ void __launch_bounds__(256) join_kernel(const float* partial, int par
     float v[4] = {};
     Vec<T, 4> res;
     if (g.out.residual) res = load4<T>(static_cast<const T*>(g.out.residual) + m * g.out.res_row + n, g.res_vec, left);
-    for (int s = 0; s < parts; ++s) {
-      const Vec<float, 4> p = load4<float>(partial + ((long long)s * g.M + m) * g.part_row + n, true, 4);
+    const float* p = g.partial + m * g.part_row + n;
+#pragma unroll 4
+    for (int s = 0; s < g.splits; ++s) {
+      const Vec<float, 4> x = ld_vec<float, 4>(p + s * g.M * g.part_row);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += p.v[j];
+      for (int j = 0; j < 4; ++j) v[j] += x.v[j];
     }
     out4<T>(g, v, columns_of(g.out, n, left), res, m, n, left);
   }
@@ -474,79 +497,113 @@ bool few_rows(const ProductArgs& p, int mat, bool copies) {
 bool tokens(const ProductArgs& p) { return p.M <= 128 || (p.M <= 512 && p.N * p.Kd <= 1LL << 23); }
 
 struct Plan {
-  Operand a, b;
+  Operand a[2], b[2];
   bool few;             // rows of x: CUDA cores
   TokensPlan tokens;    // rows 0: tiles of 256 rows
-  int bn, splits, tiles_m, tiles_n, k_iters, passes;
-  size_t ws;
+  int bn, passes, splits[2], tiles_m[2], tiles_n[2], k_iters[2];   // splits 0: no terms
+  Copies copies;
+  size_t at[4], parts_at[2], ws;   // where in the workspace copies and parts lie
 };
 
-int size_of(int mat) { return mat == kMatF32 ? 4 : mat == kMatBf16 ? 2 : 1; }
+// The copy of an operand, one for all that are the same.
+int copy_of(const Plan& q, const Operand& o) {
+  for (int i = 0; i < q.copies.count; ++i) {
+    const Operand& c = q.copies.o[i];
+    if (c.p == o.p && c.rows == o.rows && c.cols == o.cols && c.row == o.row) return i;
+  }
+  return -1;
+}
 
-Plan plan_of(const ProductArgs& p, int mat) {
+Plan plan_of(const ProductArgs* p, int count, int mat) {
   Plan q{};
-  const int size = size_of(mat);
-  q.a = operand(p.a, p.M, p.Kd, p.a_row, p.a_mn, size);
-  q.b = operand(p.b, p.N, p.Kd, p.b_row, p.b_mn, size);
+  const int size = mat == kMatF32 ? 4 : mat == kMatBf16 ? 2 : 1, per = mat == kMatE4m3 ? 128 : 64;
   q.passes = mat == kMatF32 ? kPasses : 1;
-  q.k_iters = (int)((p.Kd + (mat == kMatE4m3 ? 127 : 63)) / (mat == kMatE4m3 ? 128 : 64));
-  const bool rows_of_k = !p.a_mn && !p.b_mn && p.Kd > 0;
-  if (rows_of_k && few_rows(p, mat, q.a.pack || q.b.pack)) {
+  for (int i = 0; i < count; ++i) {
+    q.a[i] = operand(p[i].a, p[i].M, p[i].Kd, p[i].a_row, p[i].a_mn, size);
+    q.b[i] = operand(p[i].b, p[i].N, p[i].Kd, p[i].b_row, p[i].b_mn, size);
+    q.k_iters[i] = (int)((p[i].Kd + per - 1) / per);
+    q.tiles_m[i] = (int)((p[i].M + 255) / 256);
+  }
+  auto copy = [&](const Operand& o) {
+    if (!o.pack || copy_of(q, o) >= 0) return;
+    q.at[q.copies.count] = q.ws;
+    q.copies.o[q.copies.count++] = o;
+    q.ws += up256(o.bytes);
+  };
+  const bool rows_of_k = count == 1 && !p[0].a_mn && !p[0].b_mn && p[0].Kd > 0;
+  if (rows_of_k && few_rows(p[0], mat, q.a[0].pack || q.b[0].pack)) {
     q.few = true;
     return q;
   }
-  if (rows_of_k && tokens(p)) {
-    q.tokens = tokens_plan(p.M, p.N, q.k_iters * q.passes, p.sm_count);
-    q.splits = 1;
-    q.ws = up256(q.a.bytes) + up256(q.b.bytes);
+  for (int i = 0; i < count; ++i) {
+    if (p[i].Kd == 0) continue;
+    copy(q.a[i]);
+    copy(q.b[i]);
+  }
+  if (rows_of_k && tokens(p[0])) {
+    q.tokens = tokens_plan(p[0].M, p[0].N, q.k_iters[0] * q.passes, p[0].sm_count);
     return q;
   }
-  q.tiles_m = (int)((p.M + 255) / 256);
-  // Cost of a choice in stages of a 256 x 256 tile: waves of tiles, each with its stages and about 3 of latency at its
-  // ends, and the parts' way through memory.
-  const int clusters = p.sm_count / 2 > 0 ? p.sm_count / 2 : 1;
+  // Cost of a choice in stages: waves of units of a tile's stages or a share of them, each with about 3 of latency at its
+  // ends; the parts' way through memory.  A stage of a tile half as wide takes nearly as long (shared memory bounds it).
+  const int clusters = p[0].sm_count / 2 > 0 ? p[0].sm_count / 2 : 1;
+  int longest = 1;
+  for (int i = 0; i < count; ++i) longest = q.k_iters[i] * q.passes > longest ? q.k_iters[i] * q.passes : longest;
   double best = 1e300;
   for (int bn = 256; bn >= 128; bn /= 2) {
-    const long long tn = (p.N + bn - 1) / bn, tiles = q.tiles_m * tn;
-    const int most = q.k_iters * q.passes / 4 < 16 ? q.k_iters * q.passes / 4 : 16;
-    for (int s = 1; s == 1 || (s <= most && tiles * s <= 2 * clusters); ++s) {
-      const long long waves = (tiles * s + clusters - 1) / clusters;
-      double cost = (double)waves * ((double)q.k_iters * q.passes / s * (bn == 256 ? 1.0 : 0.9) + 3.0);
-      if (s > 1) cost += 8.0 + (double)s * p.M * p.N * 8.0 / 1.2e6;
-      if (cost < best) {
-        best = cost;
-        q.bn = bn;
-        q.splits = s;
-        q.tiles_n = (int)tn;
+    for (int shares = 1; shares == 1 || (shares <= 16 && longest >= 4 * shares); ++shares) {
+      const int unit = (longest + shares - 1) / shares;   // stages at most
+      long long units = 0;
+      double parts = 0.0;
+      int splits[2] = {};
+      for (int i = 0; i < count; ++i) {
+        const int all = q.k_iters[i] * q.passes;
+        splits[i] = p[i].Kd == 0 ? 0 : (all + unit - 1) / unit;
+        units += (long long)q.tiles_m[i] * ((p[i].N + bn - 1) / bn) * splits[i];
+        if (splits[i] > 1) parts += (double)splits[i] * p[i].M * p[i].N;
+      }
+      if (shares > 1 && units > 2 * clusters) break;
+      const long long waves = (units + clusters - 1) / clusters;
+      double cost = (double)waves * (unit * (bn == 256 ? 1.0 : 0.9) + 3.0);
+      if (parts > 0.0) cost += 8.0 + parts * 8.0 / 1.2e6;
+      if (cost >= best) continue;
+      best = cost;
+      q.bn = bn;
+      for (int i = 0; i < count; ++i) {
+        q.splits[i] = splits[i];
+        q.tiles_n[i] = (int)((p[i].N + bn - 1) / bn);
       }
     }
   }
-  if (p.Kd == 0) q.splits = 0;
-  q.ws = p.Kd == 0 ? 0 : up256(q.a.bytes) + up256(q.b.bytes) + (q.splits > 1 ? (size_t)q.splits * p.M * ((p.N + 7) / 8 * 8) * 4 + 32 : 0);
+  for (int i = 0; i < count; ++i) {
+    if (q.splits[i] <= 1) continue;
+    q.ws = up256(q.ws);
+    q.parts_at[i] = q.ws;
+    q.ws += (size_t)q.splits[i] * p[i].M * ((p[i].N + 7) / 8 * 8) * 4;
+  }
+  if (q.ws) q.ws += 32;   // parts lie on 32-byte boundaries
   return q;
 }
 
-template <int BN, bool A_MN, bool B_MN, bool E4M3, bool PROMOTE>
-cudaError_t launch(const Plan& q, const GemmArgs& g, const void* a, const void* b, cudaStream_t s) {
-  CUtensorMap ma, mb;
-  constexpr int BK = E4M3 ? 128 : 64;
-  if (!encode(&ma, q.a, a, A_MN ? 64 : BK, A_MN ? BK : 128) || !encode(&mb, q.b, b, B_MN ? 64 : BK, B_MN ? BK : BN / 2))
-    return cudaErrorInvalidValue;
-  auto kern = gemm_kernel<BN, A_MN, B_MN, E4M3, PROMOTE>;
+// follows: the launch before it on the stream is of the same call (see launch_after); others are waited for whole
+template <int BN, bool E4M3, bool PROMOTE>
+cudaError_t launch(const Maps& maps, const GemmPair& pair, bool follows, cudaStream_t s) {
+  auto kern = gemm_kernel<BN, E4M3, PROMOTE>;
   constexpr int bytes = (int)Cfg<BN>::bytes;
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(2);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = bytes;
+  c.stream = s;
   // clusters that fit at once, asked for once a kernel and device (the first 64)
   static std::atomic<int> known[64];
   int clusters = device < 64 ? known[device].load(std::memory_order_relaxed) : 0;
   if (clusters == 0) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3(2);
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = bytes;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -558,51 +615,74 @@ cudaError_t launch(const Plan& q, const GemmArgs& g, const void* a, const void* 
     if (clusters < 1) clusters = 1;
     if (device < 64) known[device].store(clusters, std::memory_order_relaxed);
   }
-  const long long tiles = (long long)g.tiles_m * g.tiles_n * g.splits;
-  if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
-  kern<<<(unsigned int)(2 * (tiles < clusters ? tiles : clusters)), kThreads, bytes, s>>>(ma, mb, g);
-  return cudaGetLastError();
+  const long long tiles = (long long)pair.g[0].tiles + pair.g[1].tiles;
+  c.gridDim = dim3((unsigned int)(2 * (tiles < clusters ? tiles : clusters)));
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &attr;
+  c.numAttrs = follows ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kern, maps, pair);
 }
 
 }  // namespace
 
-size_t product_ws(const ProductArgs& p, int mat) { return plan_of(p, mat).ws; }
+size_t products_ws(const ProductArgs* p, int count, int mat) { return plan_of(p, count, mat).ws; }
 
-cudaError_t launch_product(const ProductArgs& p, int mat, cudaStream_t s) {
-  const Plan q = plan_of(p, mat);
-  if (q.few) return launch_few_rows(p, mat, s);
-  GemmArgs g = args_of(p);
-  g.tiles_m = q.tiles_m; g.tiles_n = q.tiles_n; g.splits = q.splits;
-  g.k_iters = q.k_iters; g.passes = q.passes;
-  g.limit = kWaitLimitNs + 4000ull * (unsigned long long)q.k_iters * q.passes;
-  char* ws = static_cast<char*>(p.ws);
-  const void *a = p.a, *b = p.b;
+cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream_t s) {
+  Plan q = plan_of(p, count, mat);
+  if (q.few) return launch_few_rows(p[0], mat, s);
+  char* ws = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p[0].ws) + 31) & ~(uintptr_t)31);
   cudaError_t e = cudaSuccess;
-  if (q.splits > 0) {
-    if (q.a.pack) e = pack(q.a, const_cast<void*>(a = ws), p.sm_count, s);
-    if (q.b.pack && e == cudaSuccess) e = pack(q.b, const_cast<void*>(b = ws + up256(q.a.bytes)), p.sm_count, s);
+  if (q.copies.count) {
+    for (int i = 0; i < q.copies.count; ++i) q.copies.to[i] = ws + q.at[i];
+    e = pack(q.copies, p[0].sm_count, s);
     if (e != cudaSuccess) return e;
-    if (q.tokens.rows) return launch_tokens(q.tokens, g, q.a, q.b, a, b, s);
-    // the parts' rows are written in pieces of 32 bytes
-    g.partial = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws) + up256(q.a.bytes) + up256(q.b.bytes) + 31) & ~(uintptr_t)31);
+  }
+  auto place = [&](const Operand& o) -> const void* { return o.pack ? ws + q.at[copy_of(q, o)] : o.p; };
+  GemmPair pair{};
+  Maps maps;
+  bool join = false;
+  long long pieces = 0;
+  const int per = mat == kMatE4m3 ? 128 : 64;
+  for (int i = 0; i < count; ++i) {
+    GemmArgs& g = pair.g[i];
+    g = args_of(p[i]);
+    g.k_iters = q.k_iters[i]; g.passes = q.passes;
+    g.limit = kWaitLimitNs + 4000ull * (unsigned long long)q.k_iters[i] * q.passes;
+    if (q.tokens.rows) return launch_tokens(q.tokens, g, q.a[0], q.b[0], place(q.a[0]), place(q.b[0]), s);
+    g.tiles_m = q.tiles_m[i]; g.tiles_n = q.tiles_n[i]; g.splits = q.splits[i];
+    const long long tiles = (long long)g.tiles_m * g.tiles_n * g.splits;
+    if (tiles > 0x1fffffff) return cudaErrorInvalidConfiguration;
+    g.tiles = (int)tiles;
+    g.a_mn = p[i].a_mn; g.b_mn = p[i].b_mn;
+    g.partial = reinterpret_cast<float*>(ws + q.parts_at[i]);
+    if (g.splits != 1) {
+      join = true;
+      if (g.M * ((g.N + 3) / 4) > pieces) pieces = g.M * ((g.N + 3) / 4);
+    }
+    if (g.splits > 0 &&
+        (!encode(&maps.a[i], q.a[i], place(q.a[i]), g.a_mn ? 64 : per, g.a_mn ? per : 128) ||
+         !encode(&maps.b[i], q.b[i], place(q.b[i]), g.b_mn ? 64 : per, g.b_mn ? per : q.bn / 2)))
+      return cudaErrorInvalidValue;
+  }
+  if (pair.g[0].tiles + pair.g[1].tiles > 0) {
+    const bool wide = q.bn == 256, y16 = p[0].out.y_bf16, follows = p[0].follows || q.copies.count > 0;
     auto run = [&](auto bn, auto promote) -> cudaError_t {
       constexpr int BN = decltype(bn)::value;
       constexpr bool P = decltype(promote)::value;
-      if (mat == kMatE4m3) return launch<BN, false, false, true, P>(q, g, a, b, s);
-      if (q.a.mn) return launch<BN, true, true, false, P>(q, g, a, b, s);
-      return q.b.mn ? launch<BN, false, true, false, P>(q, g, a, b, s) : launch<BN, false, false, false, P>(q, g, a, b, s);
+      return mat == kMatE4m3 ? launch<BN, true, P>(maps, pair, follows, s) : launch<BN, false, P>(maps, pair, follows, s);
     };
     using N128 = std::integral_constant<int, 128>;
     using N256 = std::integral_constant<int, 256>;
-    if (p.out.y_bf16) e = q.bn == 128 ? run(N128(), std::false_type()) : run(N256(), std::false_type());
-    else e = q.bn == 128 ? run(N128(), std::true_type()) : run(N256(), std::true_type());
-    if (e != cudaSuccess || q.splits == 1) return e;
+    if (y16) e = wide ? run(N256(), std::false_type()) : run(N128(), std::false_type());
+    else e = wide ? run(N256(), std::true_type()) : run(N128(), std::true_type());
+    if (e != cudaSuccess) return e;
   }
-  const long long pieces = p.M * ((p.N + 3) / 4), want = (pieces + 255) / 256, most = 16LL * p.sm_count;
-  const unsigned int ctas = (unsigned int)(want < most ? want : most);
-  if (p.out.y_bf16) join_kernel<__nv_bfloat16><<<ctas, 256, 0, s>>>(g.partial, q.splits, g);
-  else join_kernel<float><<<ctas, 256, 0, s>>>(g.partial, q.splits, g);
-  return cudaGetLastError();
+  if (!join) return e;
+  const long long want = (pieces + 255) / 256, most = 16LL * p[0].sm_count;
+  const dim3 grid((unsigned int)(want < most ? want : most), (unsigned int)count);
+  return p[0].out.y_bf16 ? launch_after(join_kernel<__nv_bfloat16>, grid, 256, s, pair) : launch_after(join_kernel<float>, grid, 256, s, pair);
 }
 
 }  // namespace vla

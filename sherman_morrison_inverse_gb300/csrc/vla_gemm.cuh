@@ -12,10 +12,12 @@ namespace gemm {
 
 constexpr int kPart = 4;   // stages that add up in tensor memory before float32 registers take the sums over
 
+// One product of a launch.
 struct GemmArgs {
   long long M, N;
-  int tiles_m, tiles_n, splits;
+  int tiles_m, tiles_n, splits, tiles;   // tiles: of all splits
   int k_iters, passes;      // stages of one pass over Kd; passes over the terms
+  bool a_mn, b_mn;
   float* partial;           // [splits][M][part_row] where splits > 1
   long long part_row;       // N, rounded up to 8
   Epilogue out;
@@ -108,12 +110,9 @@ __device__ __forceinline__ void out4(const GemmArgs& g, float (&v)[4], const Col
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j] * xs, c.scale[j], c.bias[j]);
   if (e.pre) store4<T>(static_cast<T*>(e.pre) + m * e.pre_row + n, g.pre_vec, left, v);
-  if (e.act == kActSilu) {
+  if (e.act != kActNone) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = activate<sizeof(T) == 2>(v[j], kActSilu);
-  } else if (e.act == kActGelu) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = activate<sizeof(T) == 2>(v[j], kActGelu);
+    for (int j = 0; j < 4; j += 2) unpair(activate2<sizeof(T) == 2>(pair(v[j], v[j + 1]), e.act), v[j], v[j + 1]);
   }
   if (e.residual) {
 #pragma unroll
@@ -137,8 +136,13 @@ Operand operand(const void* p, long long side, long long kd, long long row, bool
 // The map of its tiles: box_x adjacent values x box_y rows.  base: where it lies, or its copy.
 bool encode(CUtensorMap* m, const Operand& o, const void* base, int box_x, int box_y);
 
-// Makes the copy.
-cudaError_t pack(const Operand& o, void* to, int sm_count, cudaStream_t s);
+// Makes the copies of up to four operands.
+struct Copies {
+  Operand o[4];
+  void* to[4];
+  int count;
+};
+cudaError_t pack(const Copies& c, int sm_count, cudaStream_t s);
 
 // What the epilogue needs, but for the tiles.
 GemmArgs args_of(const ProductArgs& p);

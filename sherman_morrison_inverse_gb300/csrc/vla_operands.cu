@@ -9,13 +9,15 @@ namespace {
 // One row piece of 8 values a thread.  x1 = x rounded, x2 = x - x1 rounded, x3 = x - x1 - x2 rounded: the differences
 // are exact.  A value beyond bfloat16's range, an infinity or a NaN has only its first term.
 template <typename I>
-__global__ void __launch_bounds__(256) pack_kernel(const I* src, long long rows, long long cols, long long row, I* same,
-                                                   __nv_bfloat16* terms, long long out_row, bool vec) {
-  const long long across = (cols + 7) / 8, all = rows * across;
+__global__ void __launch_bounds__(256) pack_kernel(const Copies c) {
+  all_started();   // the products
+  const Operand& o = c.o[blockIdx.y];
+  const long long across = (o.cols + 7) / 8, all = o.rows * across;
+  const bool vec = ((reinterpret_cast<uintptr_t>(o.p) | (uintptr_t)(o.row * o.size)) & 15u) == 0;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
-    const long long r = i / across, c = (i - r * across) * 8;
-    const I* p = src + r * row + c;
-    const int left = cols - c < 8 ? (int)(cols - c) : 8;
+    const long long r = i / across, at = (i - r * across) * 8;
+    const I* p = static_cast<const I*>(o.p) + r * o.row + at;
+    const int left = o.cols - at < 8 ? (int)(o.cols - at) : 8;
     if constexpr (sizeof(I) == 4) {
       float v[8];
       if (vec && left == 8) {
@@ -26,22 +28,23 @@ __global__ void __launch_bounds__(256) pack_kernel(const I* src, long long rows,
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = j < left ? p[j] : 0.f;
       }
-      Vec<__nv_bfloat16, 8> o[3];
+      Vec<__nv_bfloat16, 8> t[3];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        o[0].v[j] = __float2bfloat16_rn(v[j]);
-        float rest = v[j] - __bfloat162float(o[0].v[j]);
+        t[0].v[j] = __float2bfloat16_rn(v[j]);
+        float rest = v[j] - __bfloat162float(t[0].v[j]);
         if (!isfinite(rest)) rest = 0.f;
-        o[1].v[j] = __float2bfloat16_rn(rest);
-        o[2].v[j] = __float2bfloat16_rn(rest - __bfloat162float(o[1].v[j]));
+        t[1].v[j] = __float2bfloat16_rn(rest);
+        t[2].v[j] = __float2bfloat16_rn(rest - __bfloat162float(t[1].v[j]));
       }
+      __nv_bfloat16* to = static_cast<__nv_bfloat16*>(c.to[blockIdx.y]);
 #pragma unroll
-      for (int t = 0; t < 3; ++t) st_vec<__nv_bfloat16, 8>(terms + (t * rows + r) * out_row + c, o[t]);
+      for (int k = 0; k < 3; ++k) st_vec<__nv_bfloat16, 8>(to + (k * o.rows + r) * o.out_row + at, t[k]);
     } else {
-      Vec<I, 8> o;
+      Vec<I, 8> t;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o.v[j] = p[j < left ? j : 0];   // the row's end is not read by anyone
-      st_vec<I, 8>(same + r * out_row + c, o);
+      for (int j = 0; j < 8; ++j) t.v[j] = p[j < left ? j : 0];   // the row's end is not read by anyone
+      st_vec<I, 8>(static_cast<I*>(c.to[blockIdx.y]) + r * o.out_row + at, t);
     }
   }
 }
@@ -95,18 +98,17 @@ bool encode(CUtensorMap* m, const Operand& o, const void* base, int box_x, int b
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t pack(const Operand& o, void* to, int sm_count, cudaStream_t s) {
-  const long long pieces = o.rows * ((o.cols + 7) / 8), want = (pieces + 255) / 256, most = 16LL * sm_count;
-  const unsigned int ctas = (unsigned int)(want < most ? want : most);
-  const bool vec = ((reinterpret_cast<uintptr_t>(o.p) | (uintptr_t)(o.row * o.size)) & 15u) == 0;
-  __nv_bfloat16* terms = static_cast<__nv_bfloat16*>(to);
-  if (o.size == 4)
-    pack_kernel<float><<<ctas, 256, 0, s>>>(static_cast<const float*>(o.p), o.rows, o.cols, o.row, nullptr, terms, o.out_row, vec);
-  else if (o.size == 2)
-    pack_kernel<__nv_bfloat16><<<ctas, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(o.p), o.rows, o.cols, o.row, terms, nullptr, o.out_row, vec);
-  else
-    pack_kernel<unsigned char><<<ctas, 256, 0, s>>>(static_cast<const unsigned char*>(o.p), o.rows, o.cols, o.row,
-                                                    static_cast<unsigned char*>(to), nullptr, o.out_row, vec);
+cudaError_t pack(const Copies& c, int sm_count, cudaStream_t s) {
+  long long most = 0;
+  for (int i = 0; i < c.count; ++i) {
+    const long long ctas = (c.o[i].rows * ((c.o[i].cols + 7) / 8) + 255) / 256;
+    if (ctas > most) most = ctas;
+  }
+  const long long cap = 16LL * sm_count;
+  const dim3 grid((unsigned int)(most < cap ? most : cap), (unsigned int)c.count);
+  if (c.o[0].size == 4) pack_kernel<float><<<grid, 256, 0, s>>>(c);
+  else if (c.o[0].size == 2) pack_kernel<unsigned short><<<grid, 256, 0, s>>>(c);
+  else pack_kernel<unsigned char><<<grid, 256, 0, s>>>(c);
   return cudaGetLastError();
 }
 

@@ -14,10 +14,11 @@ constexpr int kRows = 4;   // rows in flight a warp
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, long long stretch) {
   __shared__ float part[8][32 * VEC];
+  all_started();   // the sums' kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long n = ((long long)blockIdx.x * 32 + lane) * VEC;
   const long long m0 = blockIdx.y * stretch, m1 = m0 + stretch < a.M ? m0 + stretch : a.M;
-  float sum[VEC] = {};
+  uint64_t sum[(VEC + 1) / 2] = {};
   if (n < a.N) {
     const T* dy = static_cast<const T*>(a.dy) + n;
     const T* pre = static_cast<const T*>(a.pre) + n;
@@ -35,11 +36,16 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, long long
         if (m + 8 * i < m1) {
           Vec<T, VEC> o;
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) {
-            float g = to_f32<T>(d[i].v[v]);
-            if (a.pre) g *= activate_slope<sizeof(T) == 2>(to_f32<T>(p[i].v[v]), a.act);
-            sum[v] += g;
-            o.v[v] = from_f32<T>(g);
+          for (int v = 0; v < VEC; v += 2) {
+            constexpr bool TWO = VEC > 1;
+            uint64_t g = pair(to_f32<T>(d[i].v[v]), TWO ? to_f32<T>(d[i].v[v + (TWO ? 1 : 0)]) : 0.f);
+            if (a.pre)
+              g = mul2(g, slope2<sizeof(T) == 2>(pair(to_f32<T>(p[i].v[v]), TWO ? to_f32<T>(p[i].v[v + (TWO ? 1 : 0)]) : 0.f), a.act));
+            sum[v / 2] = add2(sum[v / 2], g);
+            float x, y;
+            unpair(g, x, y);
+            o.v[v] = from_f32<T>(x);
+            if (TWO) o.v[v + (TWO ? 1 : 0)] = from_f32<T>(y);
           }
           if (a.g) st_vec<T, VEC>(out + (m + 8 * i) * a.g_row, o);
         }
@@ -47,7 +53,12 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, long long
   }
   if (!a.db) return;
 #pragma unroll
-  for (int v = 0; v < VEC; ++v) part[warp][v * 32 + lane] = sum[v];
+  for (int v = 0; v < VEC; v += 2) {
+    float x, y;
+    unpair(sum[v / 2], x, y);
+    part[warp][v * 32 + lane] = x;
+    if (VEC > 1) part[warp][(v + 1) * 32 + lane] = y;
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < 32 * VEC; i += 256) {
     const long long col = (long long)blockIdx.x * 32 * VEC + i;   // column i is value i % VEC of lane i / VEC
@@ -64,6 +75,7 @@ __global__ void __launch_bounds__(256) slope_sum_kernel(const float* partial, fl
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long n = (long long)blockIdx.x * 32 + lane;
   float sum = 0.f;
+  wait_for_first();
   if (n < N)
     for (long long i = warp; i < parts; i += 8) sum += partial[i * N + n];
   part[warp][lane] = sum;
@@ -93,8 +105,7 @@ cudaError_t launch(const SlopeArgs& a, cudaStream_t s) {
   slope_kernel<T, VEC><<<grid, 256, 0, s>>>(a, stretch);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.db) return e;
-  slope_sum_kernel<<<(unsigned int)((a.N + 31) / 32), 256, 0, s>>>(a.partial, a.db, a.N, parts);
-  return cudaGetLastError();
+  return launch_after(slope_sum_kernel, dim3((unsigned int)((a.N + 31) / 32)), 256, s, a.partial, a.db, a.N, parts);
 }
 
 }  // namespace

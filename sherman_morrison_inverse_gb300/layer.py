@@ -48,10 +48,6 @@ def _bytes(x, n):
     return x.new_empty(n, dtype=torch.uint8)
 
 
-def _new(x, shape, dtype):
-    return x.new_empty(shape, dtype=dtype)
-
-
 def _current_stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
@@ -104,7 +100,7 @@ def declare(lib):
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
     native.setup(*at, torch.float32, torch.bfloat16, torch.int32, torch.float8_e4m3fn, torch.int8,
                  torch.empty_like, _dense, _empty, _bytes, stream)
-    native.setup_dense(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in dense], _new)
+    native.setup_dense(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in dense], torch.empty, torch.uint8)
     _native = native
 
 
