@@ -126,7 +126,7 @@ struct Epilogue {
 };
 
 // C [M, N] = sum over Kd of A B.  A lies in memory as M rows of Kd adjacent values, or (a_mn) as Kd rows of M;
-// B as N rows of Kd, or (b_mn) as Kd rows of N.  e4m3: neither MN.
+// B as N rows of Kd, or (b_mn) as Kd rows of N.  Built: neither; b_mn alone and both, as a gradient's dx and dw;  e4m3: neither MN.
 struct ProductArgs {
   const void* a;
   const void* b;

@@ -41,9 +41,12 @@ struct Cfg {
   static constexpr uint32_t cols = 2 * BN;
 };
 
-// Two products of a launch: tiles [0, g[0].tiles) are the first one's.
+// The products of a launch.  Forward: g[0] alone, Kd adjacent in both operands.  Backward: tiles [0, g[0].tiles) are dx's
+// (B lies with N adjacent), the others dw's (both lie with M or N adjacent); either may have none.  Which layout a product has is
+// known to the compiler: with descriptors' steps in registers the issue of the products takes a fifth longer.
 struct GemmPair {
   GemmArgs g[2];
+  DevStatus* status;
 };
 struct Maps {
   CUtensorMap a[2], b[2];
@@ -228,7 +231,7 @@ __device__ __forceinline__ void chunk_staged(const GemmArgs& g, const float* v, 
 }
 
 // Warps 4..11: a warp takes 32 rows (those of the tensor memory lanes that it can reach) and half the columns.
-template <typename T, int BN, bool PROMOTE>
+template <typename T, int BN, bool PROMOTE, bool BACK>
 __device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, uint32_t chunk, uint64_t* acc_full,
                                          uint64_t* acc_empty, uint32_t rank, int warp, int lane, int first, int step,
                                          int n_tiles, volatile uint32_t* failed) {
@@ -248,7 +251,7 @@ __device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, ui
     if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(acc_empty + buf), 0));
   };
   for (int t = first; t < n_tiles; t += step) {
-    const bool second = t >= pair.g[0].tiles;
+    const bool second = BACK && t >= pair.g[0].tiles;
     const GemmArgs& g = pair.g[second];
     const Tile at = tile_at(second ? t - pair.g[0].tiles : t, g.tiles_m, g.tiles_n);
     const long long m0 = (long long)at.m * 256 + rank * 128 + quad * 32, m = m0 + lane;
@@ -301,7 +304,7 @@ __device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, ui
   }
 }
 
-template <int BN, bool E4M3, bool PROMOTE>
+template <int BN, bool E4M3, bool PROMOTE, bool BACK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmPair pair) {
   using C = Cfg<BN>;
@@ -313,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile uint32_t* failed = slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
-  const int n_tiles = pair.g[0].tiles + pair.g[1].tiles, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int n_tiles = pair.g[0].tiles + (BACK ? pair.g[1].tiles : 0), first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::stages; ++i) {
@@ -342,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const uint32_t chunk = base + C::o_chunk + (warp - 4) * kChunk;
     using T = typename std::conditional<PROMOTE, float, __nv_bfloat16>::type;   // y's type
-    epilogue<T, BN, PROMOTE>(pair, tmem, chunk, acc_full, acc_empty, rank, warp, lane, first, step, n_tiles, failed);
+    epilogue<T, BN, PROMOTE, BACK>(pair, tmem, chunk, acc_full, acc_empty, rank, warp, lane, first, step, n_tiles, failed);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
@@ -351,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t stage = 0, phase = 1, issued = 0;
         bool ok = !*failed;
         for (int t = first; ok && t < n_tiles; t += step) {
-          const bool second = t >= pair.g[0].tiles;
+          const bool second = BACK && t >= pair.g[0].tiles;
           const GemmArgs& g = pair.g[second];
           const CUtensorMap *map_a = &maps.a[second], *map_b = &maps.b[second];
           const Tile at = tile_at(second ? t - pair.g[0].tiles : t, g.tiles_m, g.tiles_n);
@@ -365,13 +368,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (rank == 0) mbar_arrive_expect_tx(full + stage, 2 * C::stage);
             const int ta = g.passes > 1 ? term_a(pass) : 0, tb = g.passes > 1 ? term_b(pass) : 0;
             const int at_k = it * (E4M3 ? 128 : 64);
-            if (g.a_mn) {
+            if (BACK && second) {
 #pragma unroll
               for (int j = 0; j < 2; ++j) tma_pair(sa + j * 8192, map_a, m0 + 64 * j, at_k, ta, bar);
             } else {
               tma_pair(sa, map_a, at_k, m0, ta, bar);
             }
-            if (g.b_mn) {
+            if (BACK) {
 #pragma unroll
               for (int j = 0; j < BN / 128; ++j) tma_pair(sb + j * 8192, map_b, n0 + 64 * j, at_k, tb, bar);
             } else {
@@ -402,21 +405,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t one = lane == 0;
         uint32_t stage = 0, phase = 0, buf = 0, buf_phase = 1;
         bool ok = !*failed;
-        for (int t = first; ok && t < n_tiles; t += step) {
-          const bool second = t >= pair.g[0].tiles;
-          const GemmArgs& g = pair.g[second];
-          const int split = (second ? t - pair.g[0].tiles : t) / (g.tiles_m * g.tiles_n);
-          const int k1 = k_begin(g, split + 1);
-          const uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (g.a_mn ? 1u << 15 : 0u) |
-                                 (g.b_mn ? 1u << 16 : 0u) | (uint32_t)(BN >> 3) << 17 | (256u >> 4) << 24;
-          const uint32_t step_a = g.a_mn ? 2048 >> 4 : 32 >> 4, step_b = g.b_mn ? 2048 >> 4 : 32 >> 4;
+        auto tile = [&](const GemmArgs& g, int t, auto a_mn, auto b_mn) {
+          constexpr bool A = decltype(a_mn)::value, B = decltype(b_mn)::value;
+          constexpr uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (A ? 1u << 15 : 0u) | (B ? 1u << 16 : 0u) |
+                                     (uint32_t)(BN >> 3) << 17 | (256u >> 4) << 24;
+          constexpr uint32_t step_a = A ? 2048 >> 4 : 32 >> 4, step_b = B ? 2048 >> 4 : 32 >> 4;
+          const int split = t / (g.tiles_m * g.tiles_n), k1 = k_begin(g, split + 1);
           for (int k = k_begin(g, split); ok && k < k1;) {
             const int end = PROMOTE ? part_end(g, k, k1) : k1;
-            if (!(ok = wait_for(acc_empty + buf, buf_phase, g.limit, failed))) break;
+            if (!(ok = wait_for(acc_empty + buf, buf_phase, g.limit, failed))) return;
             tc::fence_after_sync();
             const uint32_t d = tmem + buf * BN;
             for (bool more = false; k < end; ++k, more = true) {
-              if (!(ok = wait_for(full + stage, phase, g.limit, failed))) break;
+              if (!(ok = wait_for(full + stage, phase, g.limit, failed))) return;
               tc::fence_after_sync();
               const uint32_t sa = base + stage * C::stage;
               const uint64_t da = desc128(sa, 8192), db = desc128(sa + C::a_bytes, 8192);
@@ -428,13 +429,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 phase ^= 1;
               }
             }
-            if (!ok) break;
             commit_pair(smem_u32(acc_full + buf), one);
             if (++buf == 2) {
               buf = 0;
               buf_phase ^= 1;
             }
           }
+        };
+        for (int t = first; ok && t < n_tiles; t += step) {
+          if (!BACK) tile(pair.g[0], t, std::false_type(), std::false_type());
+          else if (t < pair.g[0].tiles) tile(pair.g[0], t, std::false_type(), std::true_type());
+          else tile(pair.g[1], t - pair.g[0].tiles, std::true_type(), std::true_type());
         }
         if (!ok) {
           commit_pair(smem_u32(drain), one);
@@ -449,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();   // neither CTA leaves while the other can still signal it
   tc::fence_after_sync();
   if (warp == 1) dealloc_pair(tmem, C::cols);
-  if (threadIdx.x == 0 && *failed) atomicOr(&pair.g[0].status->flags, kStatusTimeout);
+  if (threadIdx.x == 0 && *failed) atomicOr(&pair.status->flags, kStatusTimeout);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -586,9 +591,9 @@ Plan plan_of(const ProductArgs* p, int count, int mat) {
 }
 
 // follows: the launch before it on the stream is of the same call (see launch_after); others are waited for whole
-template <int BN, bool E4M3, bool PROMOTE>
+template <int BN, bool E4M3, bool PROMOTE, bool BACK>
 cudaError_t launch(const Maps& maps, const GemmPair& pair, bool follows, cudaStream_t s) {
-  auto kern = gemm_kernel<BN, E4M3, PROMOTE>;
+  auto kern = gemm_kernel<BN, E4M3, PROMOTE, BACK>;
   constexpr int bytes = (int)Cfg<BN>::bytes;
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
@@ -645,8 +650,12 @@ cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream
   bool join = false;
   long long pieces = 0;
   const int per = mat == kMatE4m3 ? 128 : 64;
+  const bool back = p[0].b_mn;
+  pair.status = p[0].status;
+  pair.g[0].splits = pair.g[1].splits = 1;   // nothing to join
   for (int i = 0; i < count; ++i) {
-    GemmArgs& g = pair.g[i];
+    const int at = back && p[i].a_mn;   // a gradient's dw is the second
+    GemmArgs& g = pair.g[at];
     g = args_of(p[i]);
     g.k_iters = q.k_iters[i]; g.passes = q.passes;
     g.limit = kWaitLimitNs + 4000ull * (unsigned long long)q.k_iters[i] * q.passes;
@@ -655,15 +664,14 @@ cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream
     const long long tiles = (long long)g.tiles_m * g.tiles_n * g.splits;
     if (tiles > 0x1fffffff) return cudaErrorInvalidConfiguration;
     g.tiles = (int)tiles;
-    g.a_mn = p[i].a_mn; g.b_mn = p[i].b_mn;
     g.partial = reinterpret_cast<float*>(ws + q.parts_at[i]);
     if (g.splits != 1) {
       join = true;
       if (g.M * ((g.N + 3) / 4) > pieces) pieces = g.M * ((g.N + 3) / 4);
     }
     if (g.splits > 0 &&
-        (!encode(&maps.a[i], q.a[i], place(q.a[i]), g.a_mn ? 64 : per, g.a_mn ? per : 128) ||
-         !encode(&maps.b[i], q.b[i], place(q.b[i]), g.b_mn ? 64 : per, g.b_mn ? per : q.bn / 2)))
+        (!encode(&maps.a[at], q.a[i], place(q.a[i]), p[i].a_mn ? 64 : per, p[i].a_mn ? per : 128) ||
+         !encode(&maps.b[at], q.b[i], place(q.b[i]), back ? 64 : per, back ? per : q.bn / 2)))
       return cudaErrorInvalidValue;
   }
   if (pair.g[0].tiles + pair.g[1].tiles > 0) {
@@ -671,7 +679,8 @@ cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream
     auto run = [&](auto bn, auto promote) -> cudaError_t {
       constexpr int BN = decltype(bn)::value;
       constexpr bool P = decltype(promote)::value;
-      return mat == kMatE4m3 ? launch<BN, true, P>(maps, pair, follows, s) : launch<BN, false, P>(maps, pair, follows, s);
+      if (back) return launch<BN, false, P, true>(maps, pair, follows, s);
+      return mat == kMatE4m3 ? launch<BN, true, P, false>(maps, pair, follows, s) : launch<BN, false, P, false>(maps, pair, follows, s);
     };
     using N128 = std::integral_constant<int, 128>;
     using N256 = std::integral_constant<int, 256>;
@@ -681,7 +690,7 @@ cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream
   }
   if (!join) return e;
   const long long want = (pieces + 255) / 256, most = 16LL * p[0].sm_count;
-  const dim3 grid((unsigned int)(want < most ? want : most), (unsigned int)count);
+  const dim3 grid((unsigned int)(want < most ? want : most), back ? 2u : 1u);
   return p[0].out.y_bf16 ? launch_after(join_kernel<__nv_bfloat16>, grid, 256, s, pair) : launch_after(join_kernel<float>, grid, 256, s, pair);
 }
 

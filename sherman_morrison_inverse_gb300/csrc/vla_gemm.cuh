@@ -17,7 +17,6 @@ struct GemmArgs {
   long long M, N;
   int tiles_m, tiles_n, splits, tiles;   // tiles: of all splits
   int k_iters, passes;      // stages of one pass over Kd; passes over the terms
-  bool a_mn, b_mn;
   float* partial;           // [splits][M][part_row] where splits > 1
   long long part_row;       // N, rounded up to 8
   Epilogue out;
