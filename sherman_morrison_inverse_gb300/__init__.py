@@ -330,21 +330,27 @@ def rms_norm(x, *args, handle: Handle | None = None, **kw):
     return (handle or default_handle(x.device)).rms_norm(x, *args, **kw)
 
 
+def _handle_of(t) -> Handle:
+    """The default handle of a tensor's device."""
+    h = _default_handles.get(t.get_device())
+    return h if h is not None else default_handle(t.device)
+
+
 def linear(x, *args, handle: Handle | None = None, **kw):
     """Matrix product with bias, activation and residual on x's device (see Handle.linear)."""
-    return (handle or default_handle(x.device)).linear(x, *args, **kw)
+    return (handle or _handle_of(x)).linear(x, *args, **kw)
 
 
 def linear_backward(dy, *args, handle: Handle | None = None, **kw):
     """Gradients of linear on dy's device (see Handle.linear_backward)."""
-    return (handle or default_handle(dy.device)).linear_backward(dy, *args, **kw)
+    return (handle or _handle_of(dy)).linear_backward(dy, *args, **kw)
 
 
 def layer_norm(x, *args, handle: Handle | None = None, **kw):
     """Layer norm with residual on x's device (see Handle.layer_norm)."""
-    return (handle or default_handle(x.device)).layer_norm(x, *args, **kw)
+    return (handle or _handle_of(x)).layer_norm(x, *args, **kw)
 
 
 def layer_norm_backward(dy, *args, handle: Handle | None = None, **kw):
     """Gradients of layer_norm on dy's device (see Handle.layer_norm_backward)."""
-    return (handle or default_handle(dy.device)).layer_norm_backward(dy, *args, **kw)
+    return (handle or _handle_of(dy)).layer_norm_backward(dy, *args, **kw)

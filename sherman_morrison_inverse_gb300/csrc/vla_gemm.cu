@@ -546,7 +546,7 @@ Plan plan_of(const ProductArgs* p, int count, int mat) {
     copy(q.b[i]);
   }
   if (rows_of_k && tokens(p[0])) {
-    q.tokens = tokens_plan(p[0].M, p[0].N, q.k_iters[0] * q.passes, p[0].sm_count);
+    q.tokens = tokens_plan(p[0].M, p[0].N, p[0].N * p[0].Kd, q.k_iters[0] * q.passes, p[0].sm_count);
     return q;
   }
   // Cost of a choice in stages: waves of units of a tile's stages or a share of them, each with about 3 of latency at its

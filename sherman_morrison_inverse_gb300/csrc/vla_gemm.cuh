@@ -150,7 +150,7 @@ GemmArgs args_of(const ProductArgs& p);
 struct TokensPlan {
   int rows, splits;   // tokens a tile; shares of Kd, one CTA of a cluster each
 };
-TokensPlan tokens_plan(long long M, long long N, int all_iters, int sm_count);
+TokensPlan tokens_plan(long long M, long long N, long long w_values, int all_iters, int sm_count);
 cudaError_t launch_tokens(const TokensPlan& t, GemmArgs g, const Operand& x, const Operand& w, const void* x_at, const void* w_at,
                           cudaStream_t s);
 

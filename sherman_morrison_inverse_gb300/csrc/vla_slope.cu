@@ -1,7 +1,7 @@
 // The element-wise part of a product's gradient: g = dy * act'(pre), and db, the sum of g's rows.
 //
 // One pass over dy and pre (memory bound).  A warp's lanes take VEC adjacent columns each (16 bytes where rows allow
-// it), a block's 8 warps every eighth row of a stretch of rows, four rows at a time so that their loads are in flight
+// it), a block's 8 warps every eighth row of a stretch of rows, three rows at a time so that their loads are in flight
 // together.  A column's sum is taken by a thread over its rows, over the block's warps in shared memory, and
 // over the stretches by a second kernel, in a fixed order: float32, chains of a few hundred additions at most.
 #include "vla_dense.cuh"
@@ -9,10 +9,11 @@
 namespace vla {
 namespace {
 
-constexpr int kRows = 4;   // rows in flight a warp
+constexpr int kRows = 3;     // rows in flight a warp
+constexpr int kBlocks = 3;   // blocks an SM
 
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, long long stretch) {
+__global__ void __launch_bounds__(256, kBlocks) slope_kernel(const SlopeArgs a, long long stretch) {
   __shared__ float part[8][32 * VEC];
   all_started();   // the sums' kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -88,11 +89,11 @@ __global__ void __launch_bounds__(256) slope_sum_kernel(const float* partial, fl
   }
 }
 
-// Stretches of rows: enough blocks for 6 an SM, with 32 rows at least in each.  The workspace is counted for the widest
-// blocks, which have the most stretches.
+// Stretches of rows: one wave of blocks, with 32 rows at least in each.  The workspace is counted for the widest blocks, which
+// have the most stretches.
 long long slope_parts(long long M, long long N, int vec, int sm_count) {
-  const long long across = (N + 32 * vec - 1) / (32 * vec), want = (6LL * sm_count + across - 1) / across;
-  const long long most = (M + 31) / 32;
+  const long long across = (N + 32 * vec - 1) / (32 * vec), wave = (long long)kBlocks * sm_count / across;
+  const long long want = wave > 0 ? wave : 1, most = (M + 31) / 32;
   return want < most ? want : most;
 }
 
@@ -101,7 +102,7 @@ cudaError_t launch(const SlopeArgs& a, cudaStream_t s) {
   const long long want = slope_parts(a.M, a.N, VEC, a.sm_count), stretch = (a.M + want - 1) / want;
   const long long parts = (a.M + stretch - 1) / stretch;
   const dim3 grid((unsigned int)((a.N + 32 * VEC - 1) / (32 * VEC)), (unsigned int)parts);
-  if (parts > 65535) return cudaErrorInvalidConfiguration;   // at most 6 an SM
+  if (parts > 65535) return cudaErrorInvalidConfiguration;   // at most 3 an SM
   slope_kernel<T, VEC><<<grid, 256, 0, s>>>(a, stretch);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.db) return e;

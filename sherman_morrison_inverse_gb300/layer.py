@@ -52,6 +52,12 @@ def _current_stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
 
+def _there(call, args, stream):
+    """A call on a stream other than the current one, its outputs allocated from that stream's memory."""
+    with torch.cuda.stream(stream):
+        return call(*args, stream.cuda_stream)
+
+
 class _Missing:
     """Stands in for the argument checks in C where they are not built: the layer's operators say so
     when they are called, and the rest of the library loads without them."""
@@ -191,8 +197,8 @@ class LayerOps:
         float32.  residual and pre have y's shape and type; pre receives v, for the gradient; y may
         be the residual itself."""
         kind = _activation(act)
-        with _on(stream):
-            return _native.linear(self, x, w, bias, residual, y, kind, pre, x_scale, w_scale, dtype, _raw(stream))
+        args = (self, x, w, bias, residual, y, kind, pre, x_scale, w_scale, dtype)
+        return _native.linear(*args, None) if stream is None else _there(_native.linear, args, stream)
 
     def linear_backward(self, dy, x, w, pre=None, dx=None, dw=None, db=None, *, act: str = "none", input: bool = True,
                         weight: bool = True, bias: bool = True, stream=None):
@@ -203,9 +209,8 @@ class LayerOps:
         that type, db float32; None in the place of those that input, weight or bias say not to
         compute.  The residual's gradient is dy."""
         kind = _activation(act)
-        with _on(stream):
-            return _native.linear_back(self, dy, x, w, pre, kind, dx if input else False, dw if weight else False,
-                                       db if bias else False, _raw(stream))
+        args = (self, dy, x, w, pre, kind, dx if input else False, dw if weight else False, db if bias else False)
+        return _native.linear_back(*args, None) if stream is None else _there(_native.linear_back, args, stream)
 
     def layer_norm(self, x, w, b=None, residual=None, y=None, *, eps: float = 1e-5, stats=False, stream=None):
         """y = (r - mean(r)) / sqrt(var(r) + eps) * w + b over the last dimension, r = x + residual.
@@ -215,8 +220,8 @@ class LayerOps:
         (y, stats), stats [..., 2] float32 the rows' mean and 1 / sqrt(var + eps) for the gradient."""
         if stats is None:
             stats = False
-        with _on(stream):
-            return _native.layer_norm(self, x, w, b, residual, y, eps, stats, _raw(stream))
+        args = (self, x, w, b, residual, y, eps, stats)
+        return _native.layer_norm(*args, None) if stream is None else _there(_native.layer_norm, args, stream)
 
     def layer_norm_backward(self, dy, x, w, stats, dresidual=None, dx=None, dw=None, db=None, *, bias: bool = True,
                             stream=None):
@@ -226,5 +231,5 @@ class LayerOps:
         dy [..., D]; x what was normalised (x, or the residual that the call left), stats as
         layer_norm returned them; dresidual (x's shape and type) the gradient that the residual
         stream already has.  dx has x's type.  Returns (dx, dw, db), dw and db float32; db None without bias."""
-        with _on(stream):
-            return _native.layer_norm_back(self, dy, x, w, stats, dresidual, dx, dw, db if bias else False, _raw(stream))
+        args = (self, dy, x, w, stats, dresidual, dx, dw, db if bias else False)
+        return _native.layer_norm_back(*args, None) if stream is None else _there(_native.layer_norm_back, args, stream)
