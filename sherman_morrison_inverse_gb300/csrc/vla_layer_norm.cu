@@ -206,7 +206,7 @@ cudaError_t forward_of(const LayerNormArgs& a, cudaStream_t s) {
 
 // Backward up to 8192 values a row, one pass.  A thread has the same VEC NV columns of every row of its block, and
 // with them its sums of dw and db; a row's two sums (of a and of a h) are joined by one barrier.
-// VEC 4 or 8: rows on 16-byte boundaries arrive by bulk copies in a ring of stages of rows_per_cta rows, as many as shared
+// VEC 4: rows on 16-byte boundaries arrive by bulk copies in a ring of stages of rows_per_cta rows, as many as shared
 // memory holds, so that some 200 KB an SM are on their way whatever the registers hold; a stage is filled again
 // behind the barrier of the next one, when nobody reads it any more.  VEC 1: rows anywhere, read directly.
 // Blocks leave their sums of dw and db as rows of `partial`, which back_sum_kernel adds in their order.
@@ -220,28 +220,7 @@ __device__ __forceinline__ int column_of(int v, int tpr, int tid) { return (v / 
 // A thread's values of a row as float32 pairs (2 i, 2 i + 1), zero where there is no column or, without `on`, no row.
 template <typename T, int VEC, int NV>
 __device__ __forceinline__ void get_row(const T* p, bool on, int tpr, int tid, int D, uint64_t (&o)[VEC * NV / 2]) {
-  if constexpr (VEC == 8) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = column_of<VEC>(8 * i, tpr, tid);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[4 * i + k] = 0;
-      if (!on || e >= D) continue;
-#pragma unroll
-      for (int k = 0; k < (int)sizeof(T) / 2; ++k) {   // 16 bytes at a time
-        const uint4 x = *reinterpret_cast<const uint4*>(p + e + k * (16 / (int)sizeof(T)));
-        if constexpr (sizeof(T) == 2) {
-          o[4 * i] = pair(lo_f(x.x), hi_f(x.x));
-          o[4 * i + 1] = pair(lo_f(x.y), hi_f(x.y));
-          o[4 * i + 2] = pair(lo_f(x.z), hi_f(x.z));
-          o[4 * i + 3] = pair(lo_f(x.w), hi_f(x.w));
-        } else {
-          o[4 * i + 2 * k] = pair(__uint_as_float(x.x), __uint_as_float(x.y));
-          o[4 * i + 2 * k + 1] = pair(__uint_as_float(x.z), __uint_as_float(x.w));
-        }
-      }
-    }
-  } else if constexpr (VEC == 4) {
+  if constexpr (VEC == 4) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = column_of<VEC>(4 * i, tpr, tid);
@@ -273,7 +252,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
     back_kernel(const LayerNormBackArgs a, int tpr, int rows_per_cta, int stages, int row_bytes, float inv_d, DevStatus* status) {
   extern __shared__ __align__(128) unsigned char smem[];   // the ring; at the end the rows' sums
   __shared__ uint64_t full[kBackStages];
-  __shared__ float part[2][2][kBackThreads / 32];
+  __shared__ float2 part[2][kBackThreads / 32];
   const int slot = threadIdx.x / tpr, tid = threadIdx.x - slot * tpr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w0 = slot * (tpr >> 5), wn = tpr >> 5;
@@ -354,13 +333,13 @@ __global__ void __launch_bounds__(kBackThreads, 1)
     s1 += other;
     unpair(t2, s2, other);
     s2 += other;
-    // both sums at once: the lower half of the lanes goes on with the first, the upper half with the second
-    const bool upper = lane & 16;
-    float s = (upper ? s2 : s1) + __shfl_xor_sync(0xffffffffu, upper ? s1 : s2, 16);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+      s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+    }
     // the other half of the parts is still read by warps that are a row behind
-    if ((lane & 15) == 0) part[par][upper][warp] = s;
+    if (lane == 0) part[par][warp] = make_float2(s1, s2);
     if (VEC > 1) {
       if (__syncthreads_or(!ok)) {   // a copy that did not arrive: give up, all threads alike
         if (threadIdx.x == 0) atomicOr(&status->flags, kStatusTimeout);
@@ -372,12 +351,15 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       __syncthreads();
     }
     if (wn > 1) {
-      const int at = lane & (span - 1);   // span is 16 at most: each half of the lanes ends up with its sum
-      s = at < wn ? part[par][upper][w0 + at] : 0.f;
-      for (int o = span >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const int at = lane & (span - 1);   // every lane ends up with the row's sums
+      const float2 q = at < wn ? part[par][w0 + at] : make_float2(0.f, 0.f);
+      s1 = q.x;
+      s2 = q.y;
+      for (int o = span >> 1; o > 0; o >>= 1) {
+        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+      }
     }
-    s1 = __shfl_sync(0xffffffffu, s, 0);
-    s2 = __shfl_sync(0xffffffffu, s, 16);
     const uint64_t m1 = pair(-s1 * inv_d, -s1 * inv_d), m2 = pair(-s2 * inv_d, -s2 * inv_d);
     if (live) {
       TX* dx = static_cast<TX*>(a.dx) + row * a.dx_row;
@@ -385,20 +367,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       if (a.dres) get_row<TX, VEC, NV>(dres, true, tpr, tid, D, r);
 #pragma unroll
       for (int i = 0; i < P; ++i) r[i] = fma2(fma2(h[i], m2, add2(g[i], m1)), scale, r[i]);
-      if constexpr (VEC == 8) {   // bfloat16
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          if (column(8 * i) >= D) continue;
-          uint32_t v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float a0, a1;
-            unpair(r[4 * i + k], a0, a1);
-            v[k] = pack2(a0, a1);
-          }
-          *reinterpret_cast<uint4*>(dx + column(8 * i)) = make_uint4(v[0], v[1], v[2], v[3]);
-        }
-      } else if constexpr (VEC == 4) {
+      if constexpr (VEC == 4) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           if (column(4 * i) >= D) continue;
@@ -597,10 +566,8 @@ cudaError_t backward(const LayerNormBackArgs& a, cudaStream_t s) {
     constexpr size_t SD = sizeof(TD), SX = sizeof(TX);
     const bool ring = a.D * SD % 16 == 0 && a.D * SX % 16 == 0 && whole(a.dy, a.dy_row, SD) && whole(a.x, a.x_row, SX) &&
                       whole(a.dx, a.dx_row, SX) && (!a.dres || whole(a.dres, a.dres_row, SX)) && whole(a.w, 0, 4);
-    // 16 bytes a lane; where one of the types is float32, 4 values, so that a warp's reads of shared memory are adjacent
-    constexpr int VEC = SD + SX == 4 ? 8 : 4;
-    if (back_shape(a.D).n == 8) e = ring ? one_pass<TD, TX, VEC, 8 / VEC>(a, s) : one_pass<TD, TX, 1, 8>(a, s);
-    else e = ring ? one_pass<TD, TX, VEC, 16 / VEC>(a, s) : one_pass<TD, TX, 1, 16>(a, s);
+    if (back_shape(a.D).n == 8) e = ring ? one_pass<TD, TX, 4, 2>(a, s) : one_pass<TD, TX, 1, 8>(a, s);
+    else e = ring ? one_pass<TD, TX, 4, 4>(a, s) : one_pass<TD, TX, 1, 16>(a, s);
   } else {
     const long long stretch = (a.rows + parts - 1) / parts, most = 8LL * a.sm_count;
     parts = (a.rows + stretch - 1) / stretch;
