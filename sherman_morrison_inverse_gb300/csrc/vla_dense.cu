@@ -80,7 +80,8 @@ BackPlan back_plan(vla_handle_t h, const void* dy, const void* x, const void* w,
   b.slope.sm_count = h->sm_count;
   b.g_bytes = need_g ? up16((size_t)(M * b.slope.g_row * size)) : 0;
   b.part_bytes = want_db ? up16(vla::slope_ws(M, N, h->sm_count)) : 0;
-  const void* g = need_g ? nullptr : dy;
+  // g's place in the workspace is not known yet: an aligned address that is not one
+  const void* g = need_g ? reinterpret_cast<const void*>(uintptr_t{256}) : dy;
   const long long g_row = need_g ? b.slope.g_row : rows[0];
   b.dx.a = g; b.dx.a_row = g_row;
   b.dx.b = w; b.dx.b_row = rows[2]; b.dx.b_mn = true;

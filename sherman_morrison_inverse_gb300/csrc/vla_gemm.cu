@@ -510,11 +510,11 @@ struct Plan {
   size_t at[4], parts_at[2], ws;   // where in the workspace copies and parts lie
 };
 
-// The copy of an operand, one for all that are the same.
+// The copy of an operand, one for all that are the same.  (Without addresses, in a query, every operand has its own.)
 int copy_of(const Plan& q, const Operand& o) {
   for (int i = 0; i < q.copies.count; ++i) {
     const Operand& c = q.copies.o[i];
-    if (c.p == o.p && c.rows == o.rows && c.cols == o.cols && c.row == o.row) return i;
+    if (o.p && c.p == o.p && c.rows == o.rows && c.cols == o.cols && c.row == o.row) return i;
   }
   return -1;
 }

@@ -89,6 +89,24 @@ LINEAR = [  # M, N, K, in, out, act, bias, residual, pre, gap
     (1000, 24, 56, "bf16", "bf16", "none", True, True, False, 0),
     (1024, 1024, 4096, "bf16", "bf16", "none", False, True, False, 0),
     (2050, 520, 72, "e4m3", "f32", "silu", True, True, True, 0),
+    (1, 16, 8192, "bf16", "bf16", "none", True, False, False, 0),      # Kd shared by the warps of a block
+    (3, 20, 6001, "f32", "f32", "none", False, True, False, 0),
+    (2, 4104, 4096, "e4m3", "bf16", "none", True, True, False, 0),
+    (4, 2056, 1024, "bf16", "bf16", "silu", True, True, True, 0),
+    (6, 131, 259, "e4m3", "bf16", "gelu", True, True, False, 0),
+    (20, 300, 200, "f32", "f32", "gelu", True, True, True, 0),          # several eights of rows on CUDA cores
+    (120, 70, 90, "bf16", "f32", "none", True, False, False, 0),
+    (16, 1000, 2048, "bf16", "f32", "gelu", True, True, True, 0),       # a cluster's shares of Kd, every tile width
+    (30, 1016, 2048, "bf16", "bf16", "none", True, True, True, 0),
+    (40, 4096, 1024, "e4m3", "f32", "none", False, True, False, 0),
+    (100, 1001, 4096, "bf16", "bf16", "silu", True, True, True, 0),
+    (128, 8192, 4160, "bf16", "bf16", "none", True, True, False, 0),
+    (127, 2048, 1024, "f32", "f32", "silu", True, True, True, 0),
+    (130, 2000, 1000, "f32", "f32", "none", False, False, False, 0),
+    (500, 1000, 1040, "bf16", "bf16", "gelu", True, True, True, 0),
+    (600, 2000, 2048, "e4m3", "bf16", "none", True, False, False, 0),
+    (530, 140, 8192, "bf16", "f32", "silu", True, True, True, 0),       # parts of Kd joined by a second kernel
+    (700, 141, 4100, "bf16", "bf16", "gelu", True, True, True, 3),
     (3000, 2000, 40, "bf16", "bf16", "silu", True, True, False, 0),
 ]
 
@@ -139,6 +157,77 @@ def test_linear_into_its_residual_and_other_shapes(vla):
     assert torch.equal(vla.linear(same, w), vla.linear(same.contiguous(), w))
 
 
+def test_linear_writes_rows_of_a_wider_tensor(vla):
+    """y and the residual as slices, on 32-byte boundaries and off them; what lies between is left alone."""
+    gen = generator(17)
+    for M in (3, 60, 300):
+        x, w = rand(gen, M, 72, dtype=torch.bfloat16), rand(gen, 96, 72, dtype=torch.bfloat16)
+        res, b = rand(gen, M, 96, dtype=torch.bfloat16), rand(gen, 97)
+        want = vla.linear(x, w, b[:96], res, act="silu")
+        for before, width in ((16, 128), (3, 131), (8, 120)):
+            wide = torch.full((M, width), 7.0, dtype=torch.bfloat16, device="cuda")
+            room = torch.zeros(M, width, dtype=torch.bfloat16, device="cuda")
+            room[:, before:before + 96] = res
+            got = vla.linear(x, w, b[:96], room[:, before:before + 96], wide[:, before:before + 96], act="silu")
+            assert torch.equal(got, want)
+            assert (wide[:, :before] == 7).all() and (wide[:, before + 96:] == 7).all()
+            off = torch.empty(97, device="cuda")[1:].copy_(b[:96])   # a bias on a 4-byte boundary
+            assert torch.equal(vla.linear(x, w, off, room[:, before:before + 96], act="silu"), want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("M", [1, 40, 200, 600])
+def test_linear_gives_the_same_bits_every_time(vla, M, dtype):
+    gen = generator(M)
+    x, w, xs, ws = operands(gen, M, 520, 1040, dtype, 0)
+    y = vla.linear(x, w, x_scale=xs, w_scale=ws)
+    assert all(torch.equal(vla.linear(x, w, x_scale=xs, w_scale=ws), y) for _ in range(5))
+
+
+def test_weights_and_gradients_of_repeated_rows(vla):
+    """Operands whose rows lie in one place (stride 0), for every product that reads them."""
+    gen = generator(23)
+    for dt in (torch.bfloat16, torch.float32):
+        row, x = rand(gen, 1, 64, dtype=dt), rand(gen, 300, 64, dtype=dt)
+        for M in (1, 30, 300):
+            assert torch.equal(vla.linear(x[:M], row.expand(48, 64)), vla.linear(x[:M], row.repeat(48, 1)))
+        dy, w = rand(gen, 1, 48, dtype=dt), rand(gen, 48, 64, dtype=dt)
+        a = vla.linear_backward(dy.expand(300, 48), x, w)
+        b = vla.linear_backward(dy.repeat(300, 1), x, w)
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    assert torch.equal(vla.linear(x, x), vla.linear(x, x.clone()))   # one tensor as both operands
+
+
+def test_offsets_past_32_bits(vla):
+    """Outputs, inputs and rows of more than 2^31 values: the last rows are those of a small call, or the reference's."""
+    gen = generator(29)
+    M, N, K = 530000, 4104, 40
+    x, w, b = rand(gen, M, K, dtype=torch.bfloat16), rand(gen, N, K, dtype=torch.bfloat16), rand(gen, N)
+    y = vla.linear(x, w, b, act="silu")
+    assert torch.equal(y[-700:], vla.linear(x[-700:], w, b, act="silu"))
+    pre = vla.linear(x, w, b)
+    assert torch.equal(pre[-700:], vla.linear(x[-700:], w, b))
+    dx, dw, db = vla.linear_backward(y, x, w, pre, act="silu")
+    (want, _, _), (mag, _, _) = ref.linear_backward(f64(y[-50:]), f64(x[-50:]), f64(w), f64(pre[-50:]), "silu")
+    close(f64(dx[-50:]), want, product_error(N, mag, "bf16") + (FAST + PRECISE * 30 + U16) * mag + U16 * np.abs(want) + TINY, "dx")
+    parts = [vla.linear_backward(y[i:i + 53000], x[i:i + 53000], w, pre[i:i + 53000], act="silu", input=False) for i in range(0, M, 53000)]
+    for got, i in ((dw, 1), (db, 2)):
+        want = sum(p[i].double() for p in parts)
+        # ten roundings to bfloat16 of parts of the sum and one of the whole; float32 sums of 53000 against 530000 terms, the
+        # longest chain of additions 2600
+        assert float((got.double() - want).norm() / want.norm()) < (2 * U16 if i == 1 else 2600 * U32 * 2)
+    del dx, dw, pre
+    nw, nb = rand(gen, N), rand(gen, N)
+    h, stats = vla.layer_norm(y, nw, nb, stats=True)
+    want, last = vla.layer_norm(y[-9:], nw, nb, stats=True)
+    assert torch.equal(h[-9:], want) and torch.equal(stats[-9:], last)
+    dx, dw, db = vla.layer_norm_backward(h, y, nw, stats)
+    assert torch.equal(dx[-9:], vla.layer_norm_backward(h[-9:], y[-9:], nw, stats[-9:])[0])
+    far = torch.empty(3, 2 ** 31 + 64, dtype=torch.bfloat16, device="cuda")[:, 7:7 + K]   # rows 4 GB apart
+    far.copy_(x[:3])
+    assert torch.equal(vla.linear(far, w, b), vla.linear(x[:3], w, b))
+
+
 def test_linear_without_terms_and_without_rows(vla):
     x, w = torch.empty(3, 0, device="cuda"), torch.empty(5, 0, device="cuda")
     b, r = torch.randn(5, device="cuda"), torch.randn(3, 5, device="cuda")
@@ -186,6 +275,10 @@ BACK = [  # M, N, K, dtype, act, bias, gap
     (2049, 264, 136, "bf16", "gelu", True, 16),
     (4096, 512, 512, "bf16", "silu", False, 0),
     (5000, 16, 32, "f32", "silu", True, 0),
+    (20000, 40, 24, "bf16", "gelu", True, 0),
+    (3000, 1032, 1, "bf16", "silu", True, 0),
+    (2000, 1, 1000, "bf16", "gelu", True, 0),
+    (700, 300, 520, "bf16", "none", True, 5),
 ]
 
 
@@ -574,5 +667,13 @@ def test_c_refusals(vla):
         assert call(x.data_ptr(), None, size.value) == 1
         assert call(x.data_ptr(), ws.data_ptr(), size.value - 1) == 1
         assert call(x.data_ptr(), ws.data_ptr() + 8, size.value) == 1
+    need = size.value   # without addresses a query may say more, never less
+    assert h.lib.vla_linear_workspace(h.ptr, None, None, *args, 0, 0, ctypes.byref(size)) == 0 and size.value >= need > 0
     rows[0] = -1
     assert call(x.data_ptr(), None, 0) == 1
+    assert h.lib.vla_linear(h.ptr, x.data_ptr(), w.data_ptr(), *(None,) * 5, y.data_ptr(), 2 ** 31, 40, 333, rows, 0, 0, 0, None, 0, None) == 1
+    assert b"2^30" in h.lib.vla_last_error(h.ptr)
+    assert h.lib.vla_linear(h.ptr, x.data_ptr(), w.data_ptr(), *(None,) * 5, y.data_ptr(), -1, 40, 333, rows, 0, 0, 0, None, 0, None) == 1
+    assert h.lib.vla_layer_norm(h.ptr, x.data_ptr(), *(None,) * 3, y.data_ptr(), None, 4, 8, 8, 0, 8, 1e-5, 0, 0, None) == 1   # no w
+    assert h.lib.vla_layer_norm_backward(h.ptr, *(x.data_ptr(),) * 4, None, y.data_ptr(), x.data_ptr(), None, 4, 8,
+                                         (ctypes.c_longlong * 4)(8, 8, 0, 8), 0, 0, None, 0, None) == 1                     # no workspace
