@@ -106,7 +106,12 @@ def declare(lib):
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
     native.setup(*at, torch.float32, torch.bfloat16, torch.int32, torch.float8_e4m3fn, torch.int8,
                  torch.empty_like, _dense, _empty, _bytes, stream)
-    native.setup_dense(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in dense], torch.empty, torch.uint8)
+    # the caching allocator without the dispatcher around it, and the current device, where torch has both
+    strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+    here = getattr(torch._C, "_cuda_getDevice", None)
+    if strided is None or here is None:
+        strided = here = None
+    native.setup_dense(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in dense], torch.empty, torch.uint8, strided, here)
     _native = native
 
 

@@ -592,6 +592,23 @@ def test_the_norms_codes_go_into_the_product(vla):
     close(f64(y), want, product_error(512, mag, "e4m3") + U16 * np.abs(want) + TINY, "y")
 
 
+def test_outputs_without_torchs_short_way_to_its_allocator(vla, monkeypatch):
+    """Where torch lacks it, outputs come from torch.empty: the same results."""
+    gen = generator(41)
+    x, w, b = rand(gen, 33, 136), rand(gen, 24, 136), rand(gen, 24)
+    calls = lambda: [vla.linear(x, w, b), *vla.linear_backward(x[:, :24].contiguous(), x, w),   # noqa: E731
+                     *vla.layer_norm(x, x[0].contiguous(), stats=True)]
+    want = calls()
+    lib = vla.load_library()
+    with monkeypatch.context() as m:
+        m.delattr(torch._C, "_cuda_getDevice")
+        vla.layer.declare(lib)
+        got = calls()
+    vla.layer.declare(lib)
+    for a, b in ((got, want), (calls(), want)):
+        assert all(torch.equal(p, q) and p.stride() == q.stride() for p, q in zip(a, b))
+
+
 # ---------------------------------------------------------------------------------------------
 # refusals
 
