@@ -296,6 +296,13 @@ __global__ void __launch_bounds__(kBackThreads, 1)
     rstd = r < a.rows ? a.stats[2 * r + 1] : 0.f;
   };
   stats(row);
+  // rows read directly: up to 8 values a thread, the next row's are on their way while the present one is reduced
+  constexpr bool AHEAD = VEC == 1 && NV <= 8;
+  uint64_t g_next[AHEAD ? P : 1], h_next[AHEAD ? P : 1];
+  if constexpr (AHEAD) {
+    get_row<TD, VEC, NV>(static_cast<const TD*>(a.dy) + row * a.dy_row, row < a.rows, tpr, tid, D, g_next);
+    get_row<TX, VEC, NV>(static_cast<const TX*>(a.x) + row * a.x_row, row < a.rows, tpr, tid, D, h_next);
+  }
   int par = 0, stage = 0, span = 2;   // span: the power of two from wn on
   while (span < wn) span *= 2;
   uint32_t phase = 0;
@@ -312,9 +319,20 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       dres = reinterpret_cast<const TX*>(at + dy_bytes + x_bytes);
       ok = mbar_wait_bounded(full + stage, phase);
     }
-    uint64_t g[P], h[P], t1 = 0, t2 = 0;
-    get_row<TD, VEC, NV>(dy, live, tpr, tid, D, g);
-    get_row<TX, VEC, NV>(x, live, tpr, tid, D, h);
+    uint64_t g[P], h[P], r[P] = {}, t1 = 0, t2 = 0;
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        g[i] = g_next[i];
+        h[i] = h_next[i];
+      }
+      get_row<TD, VEC, NV>(dy + step * a.dy_row, row + step < a.rows, tpr, tid, D, g_next);
+      get_row<TX, VEC, NV>(x + step * a.x_row, row + step < a.rows, tpr, tid, D, h_next);
+      if (a.dres) get_row<TX, VEC, NV>(dres, live, tpr, tid, D, r);
+    } else {
+      get_row<TD, VEC, NV>(dy, live, tpr, tid, D, g);
+      get_row<TX, VEC, NV>(x, live, tpr, tid, D, h);
+    }
     const float rs = rstd;
     const uint64_t scale = pair(rs, rs), shift = pair(-mean * rs, -mean * rs);
     stats(row + step);
@@ -363,8 +381,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
     const uint64_t m1 = pair(-s1 * inv_d, -s1 * inv_d), m2 = pair(-s2 * inv_d, -s2 * inv_d);
     if (live) {
       TX* dx = static_cast<TX*>(a.dx) + row * a.dx_row;
-      uint64_t r[P] = {};
-      if (a.dres) get_row<TX, VEC, NV>(dres, true, tpr, tid, D, r);
+      if (!AHEAD && a.dres) get_row<TX, VEC, NV>(dres, true, tpr, tid, D, r);
 #pragma unroll
       for (int i = 0; i < P; ++i) r[i] = fma2(fma2(h[i], m2, add2(g[i], m1)), scale, r[i]);
       if constexpr (VEC == 4) {
