@@ -2,8 +2,8 @@
 
     python examples/state_space_layer.py [--width 512] [--heads 16] [--layers 2] [--tokens 8]
 
-Each layer normalises the residual stream into 8-bit codes with a scale a token, projects them,
-runs the short convolution over x | B | C, the gated selective scan, and an 8-bit norm before the
+Each layer normalises the residual stream into 8-bit codes with a scale a token, projects them by 8-bit
+weights with a scale a row, runs the short convolution over x | B | C, the gated selective scan, and an 8-bit norm before the
 output projection.  Random weights; the program prefills prompts of several lengths, decodes some
 tokens with the states it kept, and prints how far the decoded hidden states are from those that
 prefilling the longer sequences gives.
@@ -20,9 +20,10 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import sherman_morrison_inverse_gb300 as vla  # noqa: E402
 
 
-def project(codes, scale, w):
-    """(codes * scale) w^T: e4m3 codes are exact in bfloat16, the scale goes to the result's rows."""
-    return (codes.to(torch.bfloat16) @ w.t()).float().mul_(scale[..., None]).to(torch.bfloat16)
+def quantise(w):
+    """e4m3 codes of a weight and a scale for each of its rows."""
+    scale = w.abs().amax(1) / 448
+    return (w / scale[:, None]).to(torch.float8_e4m3fn), scale
 
 
 class Layer:
@@ -34,8 +35,8 @@ class Layer:
         self.inner, self.conv = inner, inner + 2 * groups * states
         rand = lambda *s: torch.randn(*s, generator=gen, device=dev)   # noqa: E731
         self.norm_w, self.out_norm_w = torch.ones(width, device=dev), torch.ones(inner, device=dev)
-        self.w_in = (rand(inner + self.conv + heads, width) * width ** -0.5).bfloat16()
-        self.w_out = (rand(width, inner) * inner ** -0.5).bfloat16()
+        self.w_in, self.w_in_scale = quantise(rand(inner + self.conv + heads, width) * width ** -0.5)
+        self.w_out, self.w_out_scale = quantise(rand(width, inner) * inner ** -0.5)
         self.conv_w, self.conv_b = rand(self.conv, taps) * taps ** -0.5, torch.zeros(self.conv, device=dev)
         self.A, self.D = -torch.linspace(1, 16, heads, device=dev), torch.ones(heads, device=dev)
         self.dt_bias = torch.log(torch.expm1(torch.logspace(-3, -1, heads, device=dev)))
@@ -45,7 +46,8 @@ class Layer:
     def __call__(self, x, residual, slots, offsets=None):
         """x, residual [tokens, width] -> the layer's output; one token a sequence without offsets."""
         codes, scale = vla.rms_norm(x, self.norm_w, residual, out="e4m3")
-        z, u, dt = project(codes, scale, self.w_in).split([self.inner, self.conv, self.heads], -1)
+        zu = vla.linear(codes, self.w_in, x_scale=scale, w_scale=self.w_in_scale)
+        z, u, dt = zu.split([self.inner, self.conv, self.heads], -1)
         if offsets is None:
             u = vla.short_conv_step(u, self.conv_w, self.conv_b, self.conv_state, slots=slots)
         else:
@@ -56,7 +58,7 @@ class Layer:
         more = dict(D=self.D, z=z.unflatten(-1, (self.heads, self.head)), dt_bias=self.dt_bias, slots=slots)
         y = vla.ssm_step(*args, **more) if offsets is None else vla.ssm_scan(*args, offsets=offsets, **more)
         codes, scale = vla.rms_norm(y.flatten(1), self.out_norm_w, out="e4m3")
-        return project(codes, scale, self.w_out)
+        return vla.linear(codes, self.w_out, x_scale=scale, w_scale=self.w_out_scale)
 
 
 def run(layers, x, slots, offsets=None):

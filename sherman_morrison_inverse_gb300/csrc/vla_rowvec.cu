@@ -160,11 +160,11 @@ cudaError_t launch(const ProductArgs& p, cudaStream_t s) {
   // K 8192, 7.8 against 6.6 with N 2048, K 4096.)
   constexpr int E = Wide<T>::E, R = 4;
   constexpr int AHEAD = !VEC ? (MT <= 4 ? 8 : 4) : E * MT <= 16 ? 4 : E * MT <= 32 ? 2 : 1;
-  // as many shares of Kd as give the SMs 16 warps each, of 4 steps at least
+  // as many shares of Kd as keep the warps within 16 an SM, which is one wave, of 4 steps at least
   const long long rows = (p.N + R - 1) / R, tall = (p.M + MT - 1) / MT;
   const long long pieces = p.Kd / (32 * (VEC ? Wide<T>::E : 1));
   int shares = 1;
-  while (shares < 8 && rows * tall * shares < 16LL * p.sm_count && pieces >= 8LL * shares) shares *= 2;
+  while (shares < 8 && 2 * rows * tall * shares <= 16LL * p.sm_count && pieces >= 8LL * shares) shares *= 2;
   const dim3 grid((unsigned int)((rows * shares + 7) / 8), (unsigned int)tall);
   few_rows_kernel<T, VEC, MT, R, AHEAD><<<grid, 256, 0, s>>>(p, shares);
   return cudaGetLastError();
