@@ -85,6 +85,10 @@ __device__ __forceinline__ void tma_pair(uint32_t dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// Arrive on a barrier of either CTA (see wait_for on the scope).
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void alloc_pair(uint32_t slot, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
   asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -96,12 +100,17 @@ __device__ __forceinline__ void dealloc_pair(uint32_t t, uint32_t cols) {
 struct Tile {
   int m, n, split;
 };
-__device__ __forceinline__ Tile tile_at(int t, int tiles_m, int tiles_n) {
-  const int all = tiles_m * tiles_n, split = t / all, r = t - split * all;
-  const int span = kGroup * tiles_n, group = r / span, at = r - group * span;
-  const int first = group * kGroup, size = tiles_m - first < kGroup ? tiles_m - first : kGroup;
-  const int n = at / size;
-  return {first + at - n * size, n, split};
+__device__ __forceinline__ Tile tile_at(const GemmArgs& g, int t) {
+  const uint32_t tiles_m = g.tiles_m, tiles_n = g.tiles_n;
+  uint32_t split = 0, r = t;
+  if (g.splits > 1) {
+    split = r / (tiles_m * tiles_n);
+    r -= split * tiles_m * tiles_n;
+  }
+  const uint32_t span = kGroup * tiles_n, group = r / span, at = r - group * span;
+  const uint32_t first = group * kGroup, size = tiles_m - first < kGroup ? tiles_m - first : kGroup;
+  const uint32_t n = size == kGroup ? at / kGroup : at / size;
+  return {(int)(first + at - n * size), (int)n, (int)split};
 }
 
 // A warp's 32 x 32 sums, a row a lane, into its staging: rows of 32 float32, 16-byte piece j of row r at j ^ (r & 7).
@@ -149,10 +158,20 @@ __device__ __forceinline__ Piece to_piece(const float* v) {
   return x;
 }
 
+__device__ __forceinline__ float4 ld_shared4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared4(uint32_t at, float4 v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
 // 32 sums of a lane's row to memory, 32 bytes (whole sectors) an access.  n: their first column, the same in every lane;
-// alive: the lane's row exists.
+// alive: the lane's row exists; bias, scale: their columns' values in shared memory.
 template <typename T>
-__device__ __forceinline__ void chunk_direct(const GemmArgs& g, float* v, float xs, long long m, long long n, bool alive) {
+__device__ __forceinline__ void chunk_direct(const GemmArgs& g, float* v, float xs, long long m, long long n, bool alive, uint32_t bias,
+                                             uint32_t scale) {
   constexpr int PIECES = (int)sizeof(T), COLS = 32 / PIECES;
   const Epilogue& e = g.out;
   Piece res[PIECES];
@@ -173,14 +192,14 @@ __device__ __forceinline__ void chunk_direct(const GemmArgs& g, float* v, float 
     if (e.w_scale) {
 #pragma unroll
       for (int j = 0; j < COLS; j += 4) {
-        const float4 s = *reinterpret_cast<const float4*>(e.w_scale + at + j);
+        const float4 s = ld_shared4(scale + (p * COLS + j) * 4);
         u[j] *= s.x; u[j + 1] *= s.y; u[j + 2] *= s.z; u[j + 3] *= s.w;
       }
     }
     if (e.bias) {
 #pragma unroll
       for (int j = 0; j < COLS; j += 4) {
-        const float4 b = *reinterpret_cast<const float4*>(e.bias + at + j);
+        const float4 b = ld_shared4(bias + (p * COLS + j) * 4);
         u[j] += b.x; u[j + 1] += b.y; u[j + 2] += b.z; u[j + 3] += b.w;
       }
     }
@@ -248,16 +267,27 @@ __device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, ui
   auto release = [&]() {
     tc::fence_before_sync();
     __syncwarp();
-    if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(acc_empty + buf), 0));
+    if (lane == 0) arrive_at(mapa_shared(smem_u32(acc_empty + buf), 0));
   };
   for (int t = first; t < n_tiles; t += step) {
     const bool second = BACK && t >= pair.g[0].tiles;
     const GemmArgs& g = pair.g[second];
-    const Tile at = tile_at(second ? t - pair.g[0].tiles : t, g.tiles_m, g.tiles_n);
+    const Tile at = tile_at(g, second ? t - pair.g[0].tiles : t);
     const long long m0 = (long long)at.m * 256 + rank * 128 + quad * 32, m = m0 + lane;
     const long long n0 = (long long)at.n * BN + half * (BN / 2);
     const bool alive = m < g.M;
     const float xs = g.out.x_scale && alive ? g.out.x_scale[m] : 1.f;
+    // bias and weight scale of the warp's columns wait in its staging, which rows on 32-byte boundaries do not need
+    if (g.direct && (g.out.bias || g.out.w_scale)) {
+      const long long n = n0 + lane * 4;
+      const bool mine = lane < BN / 8 && n < g.N;
+      const float4 b = mine && g.out.bias ? *reinterpret_cast<const float4*>(g.out.bias + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 s = mine && g.out.w_scale ? *reinterpret_cast<const float4*>(g.out.w_scale + n) : make_float4(1.f, 1.f, 1.f, 1.f);
+      __syncwarp();   // the last tile's have been read
+      st_shared4(chunk + lane * 16, b);
+      st_shared4(chunk + kChunk / 2 + lane * 16, s);
+      __syncwarp();
+    }
     auto out = [&](float* v, int c) {
       const long long n = n0 + c * 32;
       if (g.splits > 1) {   // rows of `partial` start on 32-byte boundaries
@@ -266,7 +296,7 @@ __device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, ui
         for (int i = 0; i < 4; ++i)
           if (alive && n + 8 * i < g.N) st_piece(p + 8 * i, to_piece<float, 8>(v + 8 * i));
       } else if (g.direct) {
-        chunk_direct<T>(g, v, xs, m, n, alive);
+        chunk_direct<T>(g, v, xs, m, n, alive, chunk + c * 128, chunk + kChunk / 2 + c * 128);
       } else {
         chunk_staged<T>(g, v, chunk, m0, n, lane);
       }
@@ -357,10 +387,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const bool second = BACK && t >= pair.g[0].tiles;
           const GemmArgs& g = pair.g[second];
           const CUtensorMap *map_a = &maps.a[second], *map_b = &maps.b[second];
-          const Tile at = tile_at(second ? t - pair.g[0].tiles : t, g.tiles_m, g.tiles_n);
+          const Tile at = tile_at(g, second ? t - pair.g[0].tiles : t);
           const int m0 = at.m * 256 + rank_m, n0 = at.n * BN + rank_n;
           const int k1 = k_begin(g, at.split + 1);
-          int k = k_begin(g, at.split), pass = k / g.k_iters, it = k - pass * g.k_iters;
+          int k = k_begin(g, at.split), pass = g.passes == 1 ? 0 : k / g.k_iters, it = k - pass * g.k_iters;
           for (; k < k1; ++k) {
             if (!(ok = wait_for(empty + stage, phase, g.limit, failed))) break;
             const uint32_t sa = base + stage * C::stage, sb = sa + C::a_bytes;
@@ -395,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t n = issued < C::stages ? issued : C::stages;
           for (uint32_t i = 1; i <= n; ++i) {
             const uint32_t at = issued - i;
-            mbar_wait_cluster_bounded(full + at % C::stages, at / C::stages & 1);
+            mbar_wait_bounded(full + at % C::stages, at / C::stages & 1);
           }
         }
       }
@@ -410,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           constexpr uint32_t idesc = (1u << 4) | (E4M3 ? 0u : (1u << 7) | (1u << 10)) | (A ? 1u << 15 : 0u) | (B ? 1u << 16 : 0u) |
                                      (uint32_t)(BN >> 3) << 17 | (256u >> 4) << 24;
           constexpr uint32_t step_a = A ? 2048 >> 4 : 32 >> 4, step_b = B ? 2048 >> 4 : 32 >> 4;
-          const int split = t / (g.tiles_m * g.tiles_n), k1 = k_begin(g, split + 1);
+          const int split = g.splits == 1 ? 0 : t / (g.tiles_m * g.tiles_n), k1 = k_begin(g, split + 1);
           for (int k = k_begin(g, split); ok && k < k1;) {
             const int end = PROMOTE ? part_end(g, k, k1) : k1;
             if (!(ok = wait_for(acc_empty + buf, buf_phase, g.limit, failed))) return;
@@ -443,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!ok) {
           commit_pair(smem_u32(drain), one);
-          mbar_wait_cluster_bounded(drain, 0);
+          mbar_wait_bounded(drain, 0);
         }
       }
     }

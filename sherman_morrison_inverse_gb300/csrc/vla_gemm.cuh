@@ -36,8 +36,10 @@ __device__ __forceinline__ int part_end(const GemmArgs& g, int k, int k1) {
   const int last = (g.passes - 1) * g.k_iters, end = k < last ? last : k + kPart;
   return end < k1 ? end : k1;
 }
+// The first stage of a share of Kd.  (The product is below 2^31: at most 2^24 stages, 6 passes, 16 shares.)
 __device__ __forceinline__ int k_begin(const GemmArgs& g, int split) {
-  return (int)((long long)g.k_iters * g.passes * split / g.splits);
+  const uint32_t at = (uint32_t)(g.k_iters * g.passes) * (uint32_t)split;
+  return (int)(g.splits == 1 ? at : at / (uint32_t)g.splits);
 }
 
 // Matrix descriptor of a 128-byte-swizzled operand: `lbo` bytes between blocks of 64 values in the adjacent dimension of
@@ -47,10 +49,13 @@ __device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo) {
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// Waits for a phase that another CTA can complete too; false when the limit runs out or the CTA has failed.
+// Waits for a phase; false when the limit runs out or the CTA has failed.  The scope is the CTA's also where another CTA completes the
+// phase: what these phases order are copies and products, and reads of tensor memory behind tcgen05's own fences; no thread
+// reads memory here that a thread of another CTA wrote.  (With the cluster's scope every wait empties the first-level cache and
+// every arrival waits for the thread's stores: a tile of 64 of Kd took 4.1 us instead of 2.)
 __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
   const unsigned long long start = globaltimer_ns();
-  while (!mbar_try_wait_cluster(bar, parity)) {
+  while (!mbar_try_wait(bar, parity)) {
     if (*failed) return false;
     if (globaltimer_ns() - start > limit) {
       *failed = 1;
@@ -60,7 +65,7 @@ __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsign
   return true;
 }
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   return wait_slow(bar, parity, limit, failed);
 }
 
