@@ -438,9 +438,9 @@ typedef enum { VLA_MAT_F32 = 0, VLA_MAT_BF16 = 1, VLA_MAT_E4M3 = 2 } vla_mat_t; 
  *   rows      host array of the row strides {x, w, residual, pre, y}.
  *   workspace device memory of vla_linear_workspace bytes, 16-byte aligned, that nothing else
  *             uses until the call's work is done; NULL where that is 0.
- * Products are exact and sums float32 (float32 operands: each is taken as three bfloat16 terms, products to
- * about 2^-23 of their magnitude; a value of 3.4e38 or more, an infinity or a NaN makes the outputs that it
- * enters infinite or NaN).  v is rounded once into pre and not before the activation; y is rounded once.
+ * Products are exact and sums float32.  Float32 operands: up to 16 rows of x (128 of few weights) the same; else each is
+ * taken as three bfloat16 terms, products to about 2^-23 of their magnitude (with fewer bits for values below
+ * 2^-110), and a value of 3.39e38 or more, an infinity or a NaN makes the outputs that it enters infinite or NaN.  v is rounded once into pre and not before the activation; y is rounded once.
  * Errors (before any launch): INVALID_ARG for NULL pointers, sizes or strides out of range, unknown types,
  * scales with a type that has none, a workspace that is too small; UNSUPPORTED for types that do not go
  * together; CUDA if the launch fails. */

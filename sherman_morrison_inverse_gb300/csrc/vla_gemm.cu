@@ -1,22 +1,31 @@
-// Matrix products on the tensor cores: C [M, N] = sum over terms of A B, with an epilogue.
+// Matrix products on the tensor cores: C [M, N] = sum over Kd of A B, with an epilogue.
 //
 // Two CTAs of a cluster share a tile of 256 x BN outputs (tcgen05.mma.cta_group::2): each holds 128 rows of A
 // and BN / 2 columns of B in shared memory and 128 rows of the float32 sums in tensor memory.  Clusters are
 // persistent and walk the tiles in blocks of 8 tiles of M, so that what runs at one time shares rows and columns in L2.
-//   warp 0     one thread keeps a ring of kStages stages filled by TMA: 128 bytes of Kd of both operands (64
+//   warp 0     one thread keeps a ring of stages filled by TMA: 128 bytes of Kd of both operands (64
 //              bfloat16 or 128 e4m3), 128-byte swizzle.  Both CTAs' copies complete on the leader's barrier.
 //   warp 1     of the leader issues the products of both CTAs, four a stage, into one of two accumulators.
 //   warps 2, 3 only leave their registers to the others.
 //   warps 4..11 take the other accumulator out, 32 columns of a lane's row at a time, through the epilogue to memory in
 //              32-byte pieces; rows off 32-byte boundaries go through shared memory first.
-// A launch holds one or two products (a gradient's): their tiles follow one another, so that one's last wave is the other's first.
+// A launch holds one product, or the two of a gradient: their tiles follow one another, so that one's last wave is
+// the other's first (8192 x 8192 x 2048, dx and dw: 345 us in two launches, 339 in one, of 4 + 4 and 7 waves).
 // Operands lie in memory with Kd adjacent (as in x w^T) or with M or N adjacent (as in g w and g^T x): tiles
 // of 64 along what is adjacent, and the matrix descriptors say which.
 // float32 operands arrive as three bfloat16 terms each (x = x1 + x2 + x3 to 2^-24): six products, the small ones
 // first.  Where the result is float32, sums stay in tensor memory for 4 stages and are then added to float32 registers:
 // a tensor core cuts the bits off that an addition shifts out, always towards zero, and the error of a chain of them
-// grows with its length (K = 1161: 6.8e-7 of the result without, against 3.6e-7 of plain float32 products).  Kd is split over clusters where there are fewer tiles than clusters; the parts are then added in order.
+// grows with its length (float32, K = 1161: 6.8e-7 of the result without, 1.4e-7 with; plain float32 products 3.6e-7).
+// Kd is split over clusters where there are fewer tiles than clusters; the parts are then added in order.
 // Every wait is bounded: one that runs out sets the handle's timeout flag, and the cluster drains and returns.
+//
+// What bounds it: the tensor pipe, and with it shared memory (a tile of 256 x 256 takes 64 bytes a cycle for the products'
+// operands and 64 for the copies, all that there is; of 256 x 128 half as much again, so that its stages take as
+// long).  bfloat16 8192 x 8192 x 2048: 148 us, 1.86 PFLOP/s, 99 % of cuBLAS's burst rate (with gelu 162); 32768 x 8512 x 2048
+// in a row of calls, at the power limit: 701 us, 1.63 PFLOP/s, 96 % of cuBLAS's rate of that kind; e4m3 16384 x 2048 x 4096
+// with a residual 99 us, 2.8 PFLOP/s.  With little Kd the epilogue bounds it: 8192 x 8192 x 512 51 us, with gelu 84 (four
+// special functions a pair of values).
 #include <atomic>
 
 #include "vla_gemm.cuh"
@@ -577,6 +586,7 @@ Plan plan_of(const ProductArgs* p, int count, int mat) {
   }
   if (rows_of_k && tokens(p[0])) {
     q.tokens = tokens_plan(p[0].M, p[0].N, p[0].N * p[0].Kd, q.k_iters[0] * q.passes, p[0].sm_count);
+    if (q.ws) q.ws += 32;   // what the workspace's start is moved by at most
     return q;
   }
   // Cost of a choice in stages: waves of units of a tile's stages or a share of them, each with about 3 of latency at its
@@ -616,7 +626,7 @@ Plan plan_of(const ProductArgs* p, int count, int mat) {
     q.parts_at[i] = q.ws;
     q.ws += (size_t)q.splits[i] * p[i].M * ((p[i].N + 7) / 8 * 8) * 4;
   }
-  if (q.ws) q.ws += 32;   // parts lie on 32-byte boundaries
+  if (q.ws) q.ws += 32;   // parts lie on 32-byte boundaries, the workspace on a 16-byte one
   return q;
 }
 

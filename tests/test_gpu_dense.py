@@ -664,6 +664,42 @@ def test_refusals(vla):
     assert vla.default_handle().status()["flags"] == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(20, 4096, 2051), (300, 333, 200), (700, 130, 2048), (2000, 520, 77)])
+def test_workspaces_on_16_byte_boundaries(vla, M, N, K):
+    """A workspace of just the size asked for, 16 bytes off a 32-byte boundary: nothing behind it is touched."""
+    import ctypes
+    h, gen = vla.default_handle(), generator(M)
+    x, w, dy = rand(gen, M, K), rand(gen, N, K), rand(gen, M, N)
+    size, ptr = ctypes.c_size_t(), lambda t: None if t is None else t.data_ptr()   # noqa: E731
+
+    def guarded(call):
+        room = torch.full((size.value + 16 + 4096,), 7, dtype=torch.uint8, device="cuda")
+        assert room.data_ptr() % 32 == 0
+        torch.cuda.synchronize()
+        assert call(room.data_ptr() + 16) == 0
+        torch.cuda.synchronize()
+        assert (room[:16] == 7).all() and (room[16 + size.value:] == 7).all()
+
+    y = torch.empty(M, N, device="cuda")
+    rows = (ctypes.c_longlong * 5)(K, K, 0, 0, N)
+    assert h.lib.vla_linear_workspace(h.ptr, ptr(x), ptr(w), M, N, K, rows, 0, 0, ctypes.byref(size)) == 0 and size.value
+    guarded(lambda ws: h.lib.vla_linear(h.ptr, ptr(x), ptr(w), *(None,) * 5, ptr(y), M, N, K, rows, 0, 0, 0, ws, size, None))
+    assert torch.equal(y, vla.linear(x, w))
+    pre, dx, dw, db = rand(gen, M, N), torch.empty(M, K, device="cuda"), torch.empty(N, K, device="cuda"), torch.empty(N, device="cuda")
+    rows = (ctypes.c_longlong * 6)(N, K, K, N, K, K)
+    assert h.lib.vla_linear_backward_workspace(h.ptr, ptr(dy), ptr(x), ptr(w), 1, 1, 1, M, N, K, rows, 2, 0, ctypes.byref(size)) == 0
+    guarded(lambda ws: h.lib.vla_linear_backward(h.ptr, ptr(dy), ptr(x), ptr(w), ptr(pre), ptr(dx), ptr(dw), ptr(db), M, N, K, rows,
+                                                 2, 0, ws, size, None))
+    assert all(torch.equal(a, b) for a, b in zip((dx, dw, db), vla.linear_backward(dy, x, w, pre, act="gelu")))
+    stats = torch.stack([x.mean(1), torch.rsqrt(x.var(1, unbiased=False) + 1e-5)], 1).contiguous()
+    nw, dn, dnw, dnb = rand(gen, K), torch.empty_like(x), torch.empty(K, device="cuda"), torch.empty(K, device="cuda")
+    assert h.lib.vla_layer_norm_backward_workspace(h.ptr, M, K, ctypes.byref(size)) == 0
+    strides = (ctypes.c_longlong * 4)(K, K, 0, K)
+    guarded(lambda ws: h.lib.vla_layer_norm_backward(h.ptr, ptr(x), ptr(x), ptr(nw), ptr(stats), None, ptr(dn), ptr(dnw), ptr(dnb), M, K,
+                                                     strides, 0, 0, ws, size, None))
+    assert all(torch.equal(a, b) for a, b in zip((dn, dnw, dnb), vla.layer_norm_backward(x, x, nw, stats)))
+
+
 def test_c_refusals(vla):
     """Pointers and workspaces that the binding never passes."""
     import ctypes
