@@ -45,6 +45,10 @@ __device__ __forceinline__ uint64_t gauss_cdf2(uint64_t v, uint64_t* e) {
   return pair(vx < 0.f ? cx : x, vy < 0.f ? cy : y);
 }
 
+// 1 / (1 + e^-v) for float32 results: expf's 2 ulp and the approximate reciprocal's 1, where a rounded division takes
+// eight instructions (21459 x 440 x 72 float32 with silu: 67 us with it).  0 below -87.
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + expf(-v)); }
+
 // The activation of a pair.  FAST: for results rounded to bfloat16.
 template <bool FAST>
 __device__ __forceinline__ uint64_t activate2(uint64_t v, int act) {
@@ -56,13 +60,13 @@ __device__ __forceinline__ uint64_t activate2(uint64_t v, int act) {
   }
   float x, y;
   unpair(v, x, y);
-  if (act == kActSilu) return pair(silu<false>(x), silu<false>(y));
+  if (act == kActSilu) return pair(x * sigmoid(x), y * sigmoid(y));
   return pair(x * (0.5f * erfcf(-x * kSqrtHalf)), y * (0.5f * erfcf(-y * kSqrtHalf)));
 }
 
 __device__ __forceinline__ float slope_of(float v, int act) {
   if (act == kActSilu) {
-    const float s = 1.f / (1.f + expf(-v));
+    const float s = sigmoid(v);
     return s * fmaf(v, 1.f - s, 1.f);
   }
   return fmaf(v, kInvSqrt2Pi * expf(-0.5f * v * v), 0.5f * erfcf(-v * kSqrtHalf));

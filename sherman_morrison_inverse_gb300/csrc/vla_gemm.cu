@@ -132,13 +132,6 @@ __device__ __forceinline__ void stage_in(uint32_t chunk, int lane, const float* 
                  : "memory");
   __syncwarp();
 }
-// Four columns of row r out of it: a lane has columns 4 (lane & 7).. of every fourth row.
-__device__ __forceinline__ void stage_out(uint32_t chunk, int lane, int r, float (&v)[4]) {
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-               : "r"(chunk + r * 128 + (((lane & 7) ^ (r & 7)) << 4)));
-}
-
 // 32 bytes of a row, as one access.
 struct Piece {
   uint32_t r[8];
@@ -235,26 +228,60 @@ __device__ __forceinline__ void chunk_direct(const GemmArgs& g, float* v, float 
   }
 }
 
-// The same through a warp's staging, for rows that do not start on 32-byte boundaries: a lane has four columns of every
-// fourth row, so that a row's values are adjacent over lanes.
+// The same through a warp's staging, for rows that do not start on 32-byte boundaries: a lane has one column and the
+// warp a row at a time, so that what it reads and writes of the row is adjacent: 8000 x 4171 x 64 bfloat16 41 us (4176
+// columns, directly: 22).
 template <typename T>
 __device__ __forceinline__ void chunk_staged(const GemmArgs& g, const float* v, uint32_t chunk, long long m0, long long n0, int lane) {
+  constexpr int ROWS = 8;   // fetched together
+  const Epilogue& e = g.out;
   stage_in(chunk, lane, v);
-  const long long n = n0 + (lane & 7) * 4, m = m0 + (lane >> 3);
-  const int left = g.N - n < 4 ? (int)(g.N - n) : 4;
-  if (left <= 0) return;
-  Vec<T, 4> res[8];
-  if (g.out.residual) {
+  const long long n = n0 + lane;
+  if (n >= g.N) return;
+  const int rows = g.M - m0 < 32 ? (int)(g.M - m0) : 32;
+  const float scale = e.w_scale ? e.w_scale[n] : 1.f, bias = e.bias ? e.bias[n] : 0.f;
+  const T* res = static_cast<const T*>(e.residual) + m0 * e.res_row + n;
+  T* pre = static_cast<T*>(e.pre) + m0 * e.pre_row + n;
+  T* y = static_cast<T*>(e.y) + m0 * e.y_row + n;
+  // no branch within the eight rows but at the tile's last ones: their reads, sums and writes overlap
+  auto eight = [&](int r0, auto all) {
+    constexpr bool ALL = decltype(all)::value;
+    float u[ROWS], add[ROWS] = {}, xs[ROWS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (m + 4 * i < g.M) res[i] = load4<T>(static_cast<const T*>(g.out.residual) + (m + 4 * i) * g.out.res_row + n, g.res_vec, left);
-  }
-  const Columns cols = columns_of(g.out, n, left);
+    for (int i = 0; i < ROWS; ++i) {
+      const int r = r0 + i;
+      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(u[i]) : "r"(chunk + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4));
+      xs[i] = 1.f;
+    }
+    if (e.residual) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float u[4];
-    stage_out(chunk, lane, (lane >> 3) + 4 * i, u);
-    if (m + 4 * i < g.M) out4<T>(g, u, cols, res[i], m + 4 * i, n, left);
+      for (int i = 0; i < ROWS; ++i)
+        if (ALL || r0 + i < rows) add[i] = to_f32<T>(res[(r0 + i) * e.res_row]);
+    }
+    if (e.x_scale) {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+        if (ALL || r0 + i < rows) xs[i] = e.x_scale[m0 + r0 + i];
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) u[i] = fmaf(u[i] * xs[i], scale, bias);
+    if (e.pre) {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+        if (ALL || r0 + i < rows) pre[(r0 + i) * e.pre_row] = from_f32<T>(u[i]);
+    }
+    if (e.act != kActNone) {
+#pragma unroll
+      for (int i = 0; i < ROWS; i += 2) unpair(activate2<sizeof(T) == 2>(pair(u[i], u[i + 1]), e.act), u[i], u[i + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      if (ALL || r0 + i < rows) y[(r0 + i) * e.y_row] = from_f32<T>(u[i] + add[i]);
+  };
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += ROWS) {
+    if (r0 + ROWS <= rows) eight(r0, std::true_type());
+    else eight(r0, std::false_type());
   }
 }
 
