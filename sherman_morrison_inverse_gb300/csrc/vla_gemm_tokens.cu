@@ -7,6 +7,8 @@
 // and each then adds a share of the tokens from all of them, in order, over distributed shared memory, and takes it
 // through the epilogue: no pass over memory and no second launch.
 // Sums move from tensor memory to float32 registers every 4 stages (see vla_gemm.cu).  Waits are bounded.
+// bfloat16, us on the GPU: N 8192, K 8192 with 16 to 128 rows 32 to 38, 4.2 to 3.5 TB/s; N 2048, K 4096 with 128 rows 11.8; N 520, K 264
+// 5.0, which is what a call costs before its size does.
 #include <atomic>
 
 #include "vla_gemm.cuh"

@@ -21,7 +21,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 // values each, and is read once; up to 16 values a thread, the next row is fetched before the present one is reduced
 // and w and b stay in registers.  Each warp takes the mean and the squares around it of its own values, and one
 // exchange joins them: sum of squares around mu = sum over warps of (theirs + n_w (mean_w - mu)^2), with no
-// difference of large sums.  Memory bound.
+// difference of large sums.  Memory bound: 16384 x 4096 bfloat16 with residual and statistics 91 us, 5.9 TB/s, 88 % of a
+// copy's rate (with 8 values a thread, 512 threads a row, 115 us); 24 x 5120 4.4 us.
 // RES: 0 none, 1 bfloat16, 2 float32
 template <typename T, int RES, int VEC, int NV>
 __global__ void __launch_bounds__(VEC * NV <= 16 ? 512 : 1024, 1)
@@ -210,6 +211,8 @@ cudaError_t forward_of(const LayerNormArgs& a, cudaStream_t s) {
 // memory holds, so that some 200 KB an SM are on their way whatever the registers hold; a stage is filled again
 // behind the barrier of the next one, when nobody reads it any more.  VEC 1: rows anywhere, read directly.
 // Blocks leave their sums of dw and db as rows of `partial`, which back_sum_kernel adds in their order.
+// 16384 x 4096 bfloat16 with the residual's gradient 103 us, 5.2 TB/s, 78 % of a copy's rate: a row's chain of barriers on the 16 warps
+// that the registers of 16 values a thread allow.  4099 x 1001 float32, value by value, 15 us.
 constexpr int kBackStages = 8;
 constexpr int kBackThreads = 512;
 
