@@ -616,28 +616,47 @@ Plan plan_of(const ProductArgs* p, int count, int mat) {
     if (q.ws) q.ws += 32;   // what the workspace's start is moved by at most
     return q;
   }
-  // Cost of a choice in stages: waves of units of a tile's stages or a share of them, each with about 3 of latency at its
-  // ends; the parts' way through memory.  A stage of a tile half as wide takes nearly as long (shared memory bounds it).
+  // Cost of a choice in stages: what the cluster with the most has to do, units of a tile's stages or a share of them, each with
+  // about 3 of latency at its ends; the parts' way through memory.  Each product's Kd is cut on its own, as long as its units are
+  // two waves at most: of a gradient, one can have a few tiles with a long Kd and the other many short ones (float32, M 20781,
+  // N 303, K 1232: 874 us with dw's 10 tiles whole).  A stage of a tile half as wide takes nearly as long (shared memory
+  // bounds it).
   const int clusters = p[0].sm_count / 2 > 0 ? p[0].sm_count / 2 : 1;
   int longest = 1;
   for (int i = 0; i < count; ++i) longest = q.k_iters[i] * q.passes > longest ? q.k_iters[i] * q.passes : longest;
   double best = 1e300;
   for (int bn = 256; bn >= 128; bn /= 2) {
-    for (int shares = 1; shares == 1 || (shares <= 16 && longest >= 4 * shares); ++shares) {
+    const double stage = bn == 256 ? 1.0 : 0.9;
+    int last[2] = {-1, -1};
+    for (int shares = 1; shares == 1 || (shares <= 32 && longest >= 4 * shares); ++shares) {
       const int unit = (longest + shares - 1) / shares;   // stages at most
-      long long units = 0;
-      double parts = 0.0;
+      long long units[2] = {}, all_units = 0;
+      double parts = 0.0, length[2] = {};
       int splits[2] = {};
       for (int i = 0; i < count; ++i) {
         const int all = q.k_iters[i] * q.passes;
+        const long long tiles = (long long)q.tiles_m[i] * ((p[i].N + bn - 1) / bn), most = 2 * clusters / tiles;
         splits[i] = p[i].Kd == 0 ? 0 : (all + unit - 1) / unit;
-        units += (long long)q.tiles_m[i] * ((p[i].N + bn - 1) / bn) * splits[i];
+        if (splits[i] > most) splits[i] = most > 1 ? (int)most : splits[i] > 0;
+        units[i] = tiles * splits[i];
+        all_units += units[i];
+        if (splits[i] > 0) length[i] = (double)all / splits[i] * stage + 3.0;
         if (splits[i] > 1) parts += (double)splits[i] * p[i].M * p[i].N;
       }
-      if (shares > 1 && units > 2 * clusters) break;
-      const long long waves = (units + clusters - 1) / clusters;
-      double cost = (double)waves * (unit * (bn == 256 ? 1.0 : 0.9) + 3.0);
-      if (parts > 0.0) cost += 8.0 + parts * 8.0 / 1.2e6;
+      if (splits[0] == last[0] && splits[1] == last[1]) continue;
+      last[0] = splits[0];
+      last[1] = splits[1];
+      // units are dealt out in turn: a cluster's number of the first product's, and of both, changes where a wave of either ends
+      double cost = 0.0;
+      const long long ends[3] = {0, units[0] % clusters, all_units % clusters};
+      for (int e = 0; e < (count == 1 ? 1 : 3); ++e) {
+        const long long c = ends[e], first = c < units[0] ? (units[0] - c + clusters - 1) / clusters : 0;
+        const long long both = c < all_units ? (all_units - c + clusters - 1) / clusters : 0;
+        const double mine = (double)first * length[0] + (double)(both - first) * length[1];
+        if (mine > cost) cost = mine;
+      }
+      // a launch, a part's read after the other, their bytes
+      if (parts > 0.0) cost += 8.0 + 0.5 * (splits[0] > splits[1] ? splits[0] : splits[1]) + parts * 8.0 / 1.2e6;
       if (cost >= best) continue;
       best = cost;
       q.bn = bn;

@@ -36,7 +36,7 @@ __device__ __forceinline__ int part_end(const GemmArgs& g, int k, int k1) {
   const int last = (g.passes - 1) * g.k_iters, end = k < last ? last : k + kPart;
   return end < k1 ? end : k1;
 }
-// The first stage of a share of Kd.  (The product is below 2^31: at most 2^24 stages, 6 passes, 16 shares.)
+// The first stage of a share of Kd.  (The product is below 2^32: at most 2^24 stages, 6 passes, 32 shares.)
 __device__ __forceinline__ int k_begin(const GemmArgs& g, int split) {
   const uint32_t at = (uint32_t)(g.k_iters * g.passes) * (uint32_t)split;
   return (int)(g.splits == 1 ? at : at / (uint32_t)g.splits);
@@ -52,7 +52,7 @@ __device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo) {
 // Waits for a phase; false when the limit runs out or the CTA has failed.  The scope is the CTA's also where another CTA completes the
 // phase: what these phases order are copies and products, and reads of tensor memory behind tcgen05's own fences; no thread
 // reads memory here that a thread of another CTA wrote.  (With the cluster's scope every wait empties the first-level cache and
-// every arrival waits for the thread's stores: a tile of 64 of Kd took 4.1 us instead of 2.)
+// every arrival waits for the thread's stores: 8192 x 8192 x 64 bfloat16 58 us, 46 without.)
 __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
   const unsigned long long start = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
