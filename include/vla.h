@@ -235,6 +235,14 @@ vla_err_t vla_project_u(vla_handle_t h, const void* k_raw, const float* W_u, voi
  * NULL handle or limit_ms outside 1..5000; CUDA if the launch fails. */
 vla_err_t vla_selftest_wait(vla_handle_t h, unsigned int limit_ms, void* stream);
 
+/* How long a wait of vla_linear's and vla_linear_backward's kernels may take on calls of this
+ * handle from now on: limit_ms milliseconds (0..5000; 2000 at first), and 4 us for every stage
+ * of a tile.  A call whose wait runs out ends what it has under way, sets VLA_STATUS_TIMEOUT and
+ * leaves its outputs undefined.  0: a product on the tensor cores gives up without waiting for its
+ * sums, copies and products under way: the self-test of that path.  Errors: INVALID_ARG for a NULL
+ * handle or a limit out of range. */
+vla_err_t vla_wait_limit(vla_handle_t h, unsigned int limit_ms);
+
 /* Measurement helper, not part of the scan (the pages have no counterpart): the FP32
  * CUDA-core throughput of the handle's device, against which the scan's roofline is
  * quoted.  Launches 4 CTAs of 256 threads per SM; each thread runs 8 independent chains

@@ -100,6 +100,8 @@ def load_library():
         lib.vla_scan_fwd_host.restype = ci
         lib.vla_selftest_wait.argtypes = [vp, ctypes.c_uint, vp]
         lib.vla_selftest_wait.restype = ci
+        lib.vla_wait_limit.argtypes = [vp, ctypes.c_uint]
+        lib.vla_wait_limit.restype = ci
         lib.vla_ffma_probe.argtypes = [vp, cll, ctypes.POINTER(ctypes.c_double), vp]
         lib.vla_ffma_probe.restype = ci
         lib.vla_host_path_info.argtypes = [vp, ctypes.POINTER(ci), ctypes.POINTER(cll)]
@@ -239,6 +241,11 @@ class Handle(_layer.LayerOps):
         """Launch a wait that nothing completes; it gives up after limit_ms and sets the
         timeout flag in status() (the bounded-wait path of the scan kernels)."""
         _check(self.lib, self._h, self.lib.vla_selftest_wait(self._h, int(limit_ms), _stream_ptr(stream, self.device)))
+
+    def wait_limit(self, limit_ms: int = 2000):
+        """How long a wait inside linear and linear_backward may take before the call gives up and sets
+        the timeout flag in status(); 0: it gives up at once (the self-test of that path)."""
+        _check(self.lib, self._h, self.lib.vla_wait_limit(self._h, int(limit_ms)))
 
     def host_path_info(self) -> dict:
         """How the last scan_fwd_host call moved its inputs: {"gathered": 1 (SM gather),

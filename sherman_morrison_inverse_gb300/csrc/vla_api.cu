@@ -456,6 +456,14 @@ vla_err_t vla_selftest_wait(vla_handle_t h, unsigned int limit_ms, void* stream)
   return VLA_OK;
 }
 
+vla_err_t vla_wait_limit(vla_handle_t h, unsigned int limit_ms) {
+  if (!h) return fail(nullptr, VLA_ERR_INVALID_ARG, "vla_wait_limit: handle is NULL");
+  h->last_error.clear();
+  if (limit_ms > 5000) return fail(h, VLA_ERR_INVALID_ARG, "vla_wait_limit: limit_ms must be 0..5000");
+  h->wait_limit = 1000000ull * limit_ms;
+  return VLA_OK;
+}
+
 }  // extern "C"
 
 namespace vla {

@@ -59,6 +59,7 @@ vla::ProductArgs linear_product(vla_handle_t h, const void* x, const void* w, lo
   p.a_row = rows[0]; p.b_row = rows[1];
   p.sm_count = h->sm_count;
   p.status = h->status;
+  p.wait_limit = h->wait_limit;
   return p;
 }
 
@@ -91,6 +92,7 @@ BackPlan back_plan(vla_handle_t h, const void* dy, const void* x, const void* w,
   b.dw.M = N; b.dw.N = K; b.dw.Kd = M;
   b.dx.sm_count = b.dw.sm_count = h->sm_count;
   b.dx.status = b.dw.status = h->status;
+  b.dx.wait_limit = b.dw.wait_limit = h->wait_limit;
   b.dx.out.y_bf16 = b.dw.out.y_bf16 = io == VLA_BF16;
   b.count = 0;
   if (want_dx) b.run[b.count++] = b.dx;

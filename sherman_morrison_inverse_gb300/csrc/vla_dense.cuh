@@ -142,6 +142,7 @@ struct ProductArgs {
   void* ws;
   int sm_count;
   DevStatus* status;
+  unsigned long long wait_limit;   // of a wait, in ns (0: its self-test)
 };
 // One or two products (count) that may run together, of one type and with one workspace (p[0].ws).
 cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream_t s);

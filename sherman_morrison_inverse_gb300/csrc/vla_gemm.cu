@@ -18,7 +18,8 @@
 // a tensor core cuts the bits off that an addition shifts out, always towards zero, and the error of a chain of them
 // grows with its length (float32, K = 1161: 6.8e-7 of the result without, 1.4e-7 with; plain float32 products 3.6e-7).
 // Kd is split over clusters where there are fewer tiles than clusters; the parts are then added in order.
-// Every wait is bounded: one that runs out sets the handle's timeout flag, and the cluster drains and returns.
+// Every wait is bounded: one that runs out sets the handle's timeout flag, and the cluster waits (bounded too) for the products and
+// copies that both CTAs have under way and returns.
 //
 // What bounds it: the tensor pipe, and with it shared memory (a tile of 256 x 256 takes 64 bytes a cycle for the products'
 // operands and 64 for the copies, all that there is; of 256 x 128 half as much again, so that its stages take as
@@ -97,6 +98,10 @@ __device__ __forceinline__ void tma_pair(uint32_t dst, const CUtensorMap* map, i
 // Arrive on a barrier of either CTA (see wait_for on the scope).
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Bytes that will not arrive, counted as if they had.
+__device__ __forceinline__ void complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void alloc_pair(uint32_t slot, uint32_t cols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
@@ -309,6 +314,10 @@ __device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, ui
     const bool second = BACK && t >= pair.g[0].tiles;
     const GemmArgs& g = pair.g[second];
     const Tile at = tile_at(g, second ? t - pair.g[0].tiles : t);
+    if (g.limit == 0) {   // the wait's self-test: the others find out with copies and products under way
+      *failed = 1;
+      return;
+    }
     const long long m0 = (long long)at.m * 256 + rank * 128 + quad * 32, m = m0 + lane;
     const long long n0 = (long long)at.n * BN + half * (BN / 2);
     const bool alive = m < g.M;
@@ -341,7 +350,7 @@ __device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, ui
       float sums[CHUNKS][32] = {};
       const int k1 = k_begin(g, at.split + 1);
       for (int k = k_begin(g, at.split); k < k1; k = part_end(g, k, k1)) {
-        if (!wait_for(acc_full + buf, phase, g.limit, failed)) return;
+        if (!wait_warp(acc_full + buf, phase, g.limit, failed)) return;
         tc::fence_after_sync();
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
@@ -356,7 +365,7 @@ __device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, ui
 #pragma unroll
       for (int c = 0; c < CHUNKS; ++c) out(sums[c], c);
     } else {
-      if (!wait_for(acc_full + buf, phase, g.limit, failed)) return;
+      if (!wait_warp(acc_full + buf, phase, g.limit, failed)) return;
       tc::fence_after_sync();
 #pragma unroll 1
       for (int c = 0; c < CHUNKS; ++c) {
@@ -380,8 +389,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t *empty = full + C::stages, *acc_full = empty + C::stages, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
   uint32_t* slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile uint32_t* failed = slot + 1;
+  volatile uint32_t* theirs = slot + 2;   // the other CTA's: failed, stages filled
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
+  uint32_t issued = 0;   // stages that the producer has filled
   const int n_tiles = pair.g[0].tiles + (BACK ? pair.g[1].tiles : 0), first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -417,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       if (lane == 0) {
         const uint32_t rank_m = rank * 128, rank_n = rank * (BN / 2);
-        uint32_t stage = 0, phase = 1, issued = 0;
+        uint32_t stage = 0, phase = 1;
         bool ok = !*failed;
         for (int t = first; ok && t < n_tiles; t += step) {
           const bool second = BACK && t >= pair.g[0].tiles;
@@ -455,13 +466,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               it = 0;
               ++pass;
             }
-          }
-        }
-        if (!ok && rank == 0) {   // let what is in flight arrive before the memory is given up
-          const uint32_t n = issued < C::stages ? issued : C::stages;
-          for (uint32_t i = 1; i <= n; ++i) {
-            const uint32_t at = issued - i;
-            mbar_wait_bounded(full + at % C::stages, at / C::stages & 1);
           }
         }
       }
@@ -507,17 +511,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else if (t < pair.g[0].tiles) tile(pair.g[0], t, std::false_type(), std::true_type());
           else tile(pair.g[1], t - pair.g[0].tiles, std::true_type(), std::true_type());
         }
-        if (!ok) {
-          commit_pair(smem_u32(drain), one);
-          mbar_wait_bounded(drain, 0);
-        }
+        // whoever gave up: no product reads either CTA's memory behind this
+        commit_pair(smem_u32(drain), one);
+        mbar_wait_bounded(drain, 0);
       }
     }
   }
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
+  if (threadIdx.x == 0) {
+    if (rank == 1) mbar_wait_bounded(drain, 0);   // the leader signals nothing here behind this
+    const uint32_t to = mapa_shared(smem_u32(slot + 2), rank ^ 1);
+    st_cluster_s32(to, (int)*failed);
+    st_cluster_s32(to + 4, (int)issued);
+  }
+  __syncwarp();
   cluster_sync_all();   // neither CTA leaves while the other can still signal it
+  if (*failed | theirs[0]) {   // the same in both CTAs
+    if (threadIdx.x == 0 && rank == 0) {
+      // Both CTAs' copies complete on this one's barriers, where this one expects those of both: what only one of them
+      // has asked for is counted here, then all of it has to land.  (They are `stages` apart at most.)
+      const uint32_t other = theirs[1];
+#pragma unroll 1
+      for (uint32_t i = other; i < issued; ++i) complete_tx(full + i % C::stages, C::stage);
+#pragma unroll 1
+      for (uint32_t i = issued; i < other; ++i) mbar_arrive_expect_tx(full + i % C::stages, C::stage);
+      drain_ring(full, C::stages, issued > other ? issued : other);
+    }
+    __syncwarp();
+    cluster_sync_all();
+  }
   tc::fence_after_sync();
   if (warp == 1) dealloc_pair(tmem, C::cols);
   if (threadIdx.x == 0 && *failed) atomicOr(&pair.status->flags, kStatusTimeout);
@@ -744,7 +768,7 @@ cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream
     GemmArgs& g = pair.g[at];
     g = args_of(p[i]);
     g.k_iters = q.k_iters[i]; g.passes = q.passes;
-    g.limit = kWaitLimitNs + 4000ull * (unsigned long long)q.k_iters[i] * q.passes;
+    g.limit = p[i].wait_limit ? p[i].wait_limit + 4000ull * (unsigned long long)q.k_iters[i] * q.passes : 0;
     if (q.tokens.rows) return launch_tokens(q.tokens, g, q.a[0], q.b[0], place(q.a[0]), place(q.b[0]), s);
     g.tiles_m = q.tiles_m[i]; g.tiles_n = q.tiles_n[i]; g.splits = q.splits[i];
     const long long tiles = (long long)g.tiles_m * g.tiles_n * g.splits;

@@ -22,7 +22,7 @@ struct GemmArgs {
   Epilogue out;
   bool direct;                    // rows of y, pre, residual on 32-byte boundaries, N in whole pieces of 32 bytes
   bool y_vec, res_vec, pre_vec;   // four values at a time
-  unsigned long long limit;       // of a wait, in ns: 2 s, and 4 us for every stage of a tile
+  unsigned long long limit;       // of a wait, in ns: the handle's and 4 us for every stage of a tile; 0: the epilogue gives up
   DevStatus* status;
 };
 
@@ -67,6 +67,16 @@ __device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, unsign
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
   if (mbar_try_wait(bar, parity)) return true;
   return wait_slow(bar, parity, limit, failed);
+}
+// The same for a warp whose lanes go on together to instructions that a whole warp has to execute (tcgen05.ld): each lane tries for
+// itself, and one that is the last to look can see the phase where the others have given up.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, limit, failed));
+}
+// Waits until the copies of the last fills of a ring have landed: fill i goes to stage i % stages.
+__device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t stages, uint32_t fills) {
+#pragma unroll 1
+  for (uint32_t i = fills > stages ? fills - stages : 0; i < fills; ++i) mbar_wait_bounded(full + i % stages, i / stages & 1);
 }
 
 // Four adjacent values of a row, those from `left` on absent.

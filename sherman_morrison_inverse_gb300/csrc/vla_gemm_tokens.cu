@@ -6,7 +6,8 @@
 // CTAs an SM, keeps what memory's latency needs in flight.  Each CTA leaves its sums in its shared memory, one float32 row a token,
 // and each then adds a share of the tokens from all of them, in order, over distributed shared memory, and takes it
 // through the epilogue: no pass over memory and no second launch.
-// Sums move from tensor memory to float32 registers every 4 stages (see vla_gemm.cu).  Waits are bounded.
+// Sums move from tensor memory to float32 registers every 4 stages (see vla_gemm.cu).  Waits are bounded; a CTA that gives up waits
+// (bounded too) for its products and copies under way.
 // bfloat16, us on the GPU: N 8192, K 8192 with 16 to 128 rows 32 to 38, 4.2 to 3.5 TB/s; N 2048, K 4096 with 128 rows 11.8; N 520, K 264
 // 5.0, which is what a call costs before its size does.
 #include <atomic>
@@ -126,18 +127,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == 0) {
     if (lane == 0 && !*failed) {
-      bool ok = true;
-      while (k < k1) {
-        if (!(ok = wait_for(empty + stage, phase, g.limit, failed))) break;
-        fill();
-      }
-      if (!ok) {   // let what is in flight arrive before the memory is given up
-        const uint32_t n = issued < C::stages ? issued : C::stages;
-        for (uint32_t i = 1; i <= n; ++i) {
-          const uint32_t at = issued - i;
-          mbar_wait_bounded(full + at % C::stages, at / C::stages & 1);
-        }
-      }
+      while (k < k1 && wait_for(empty + stage, phase, g.limit, failed)) fill();
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -169,10 +159,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         buf_phase ^= 1;
       }
     }
-    if (!ok) {
-      commit_one(drain, one);
-      mbar_wait_bounded(drain, 0);
-    }
+    commit_one(drain, one);   // whoever gave up: no product reads the ring behind this
+    mbar_wait_bounded(drain, 0);
   } else {
     // a lane has a row of w (its tensor memory lane) and the sums of half the tokens
     constexpr int HT = BT / 2, W = HT < 32 ? HT : 32;
@@ -180,9 +168,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + half * HT;
     float sums[HT] = {};
     uint32_t buf = 0, buf_phase = 0;
-    bool ok = true;
-    for (int k = k0; k < k1; k = part_end(g, k, k1)) {
-      if (!(ok = wait_for(acc_full + buf, buf_phase, g.limit, failed))) break;
+    bool ok = g.limit > 0;   // 0: the wait's self-test, the others find out with copies and products under way
+    if (!ok) *failed = 1;
+    for (int k = k0; ok && k < k1; k = part_end(g, k, k1)) {
+      if (!(ok = wait_warp(acc_full + buf, buf_phase, g.limit, failed))) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int c = 0; c < HT / W; ++c) {
@@ -214,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
+  if (threadIdx.x == 0 && *failed) drain_ring(full, C::stages, issued);
+  __syncwarp();
   cluster_sync_all();   // every CTA's sums are there
   tc::fence_after_sync();
   if (warp == 1) tc::tmem_dealloc(tmem, C::cols);

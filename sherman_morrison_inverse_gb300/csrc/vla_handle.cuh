@@ -17,6 +17,7 @@ struct vla_handle_s {
   int sm_count = 0;
   vla::DevStatus* status = nullptr;
   std::string last_error;
+  unsigned long long wait_limit = vla::kWaitLimitNs;   // of the products' waits, in ns; 0: their self-test
   // Host-buffer path (vla_scan_fwd_host), made on its first use: a device workspace with
   // the state and kHostSlots staging slots, a copy-in and a copy-out stream, and events.
   bool host_ready = false;

@@ -1,0 +1,80 @@
+"""Products and norms where they end early, at the ends of their ranges, and form by form."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import dense_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+U32, U16 = 2.0 ** -24, 2.0 ** -8
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}
+
+
+@pytest.fixture(scope="module")
+def vla():
+    from _util import ensure_built
+    ensure_built()
+    import sherman_morrison_inverse_gb300 as m
+    return m
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def generator(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rand(gen, *shape, dtype=torch.float32):
+    return torch.randn(*shape, generator=gen, device="cuda").to(dtype)
+
+
+# ---------------------------------------------------------------------------------------------
+# waits that run out
+
+PRODUCTS = [  # M, N, K, dtype, gradient
+    (20, 300, 2048, "bf16", False),       # few weights: CUDA cores, where nothing is waited for
+    (20, 2000, 2048, "bf16", False),      # w's rows in the long dimension, shares over a cluster
+    (128, 8192, 2048, "f32", False),
+    (100, 1000, 4096, "e4m3", False),
+    (1000, 2000, 2048, "bf16", False),    # CTA pairs
+    (700, 130, 4096, "f32", False),       # parts of Kd, joined
+    (2000, 2048, 1024, "e4m3", False),
+    (300, 520, 264, "f32", True),
+    (4096, 1024, 2048, "bf16", True),
+]
+
+
+@pytest.mark.parametrize("M,N,K,dtype,gradient", PRODUCTS)
+def test_a_products_wait_that_runs_out_ends_the_call(vla, M, N, K, dtype, gradient):
+    """Without time to wait every tensor-core product gives up before its sums are there, with copies and products under
+    way: the call ends with its status, and the next ones are right."""
+    gen, h = generator(M), vla.Handle(0)
+    flags = vla.STATUS_TIMEOUT if gradient or N * K > 2 ** 21 // 3 or dtype == "f32" else 0
+    x, w = rand(gen, M, K, dtype=TYPES[dtype]), rand(gen, N, K, dtype=TYPES[dtype])
+    dy = rand(gen, M, N, dtype=TYPES[dtype]) if gradient else None
+
+    def call():
+        return h.linear_backward(dy, x, w) if gradient else [h.linear(x, w)]
+
+    want = call()
+    assert h.status()["flags"] == 0
+    for _ in range(3):
+        h.wait_limit(0)
+        for _ in range(5):
+            call()
+            assert h.status()["flags"] == flags
+        h.wait_limit(2000)
+        for _ in range(5):
+            assert all(torch.equal(a, b) for a, b in zip(call(), want))
+        assert h.status()["flags"] == 0
+    h.close()
+
+
+def test_the_wait_limit_has_a_range(vla):
+    h = vla.Handle(0)
+    with pytest.raises(vla.VlaError, match="0..5000"):
+        h.wait_limit(5001)
+    h.close()
