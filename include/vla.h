@@ -235,11 +235,12 @@ vla_err_t vla_project_u(vla_handle_t h, const void* k_raw, const float* W_u, voi
  * NULL handle or limit_ms outside 1..5000; CUDA if the launch fails. */
 vla_err_t vla_selftest_wait(vla_handle_t h, unsigned int limit_ms, void* stream);
 
-/* How long a wait of vla_linear's and vla_linear_backward's kernels may take on calls of this
- * handle from now on: limit_ms milliseconds (0..5000; 2000 at first), and 4 us for every stage
- * of a tile.  A call whose wait runs out ends what it has under way, sets VLA_STATUS_TIMEOUT and
- * leaves its outputs undefined.  0: a product on the tensor cores gives up without waiting for its
- * sums, copies and products under way: the self-test of that path.  Errors: INVALID_ARG for a NULL
+/* How long a wait in the kernels of vla_linear, vla_linear_backward and vla_layer_norm_backward
+ * may take on calls of this handle from now on: limit_ms milliseconds (0..5000; 2000 at first),
+ * for a product and 4 us for every stage of a tile.  A call whose wait runs out ends what it has
+ * under way, sets VLA_STATUS_TIMEOUT and leaves its outputs undefined.  0: products on the tensor
+ * cores and norms of rows that are copied ahead give up without waiting, with copies and products
+ * under way: the self-test of that path.  Errors: INVALID_ARG for a NULL
  * handle or a limit out of range. */
 vla_err_t vla_wait_limit(vla_handle_t h, unsigned int limit_ms);
 

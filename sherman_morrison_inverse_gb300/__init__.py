@@ -243,8 +243,8 @@ class Handle(_layer.LayerOps):
         _check(self.lib, self._h, self.lib.vla_selftest_wait(self._h, int(limit_ms), _stream_ptr(stream, self.device)))
 
     def wait_limit(self, limit_ms: int = 2000):
-        """How long a wait inside linear and linear_backward may take before the call gives up and sets
-        the timeout flag in status(); 0: it gives up at once (the self-test of that path)."""
+        """How long a wait inside linear, linear_backward and layer_norm_backward may take before the call
+        gives up and sets the timeout flag in status(); 0: it gives up at once (the self-test of that path)."""
         _check(self.lib, self._h, self.lib.vla_wait_limit(self._h, int(limit_ms)))
 
     def host_path_info(self) -> dict:

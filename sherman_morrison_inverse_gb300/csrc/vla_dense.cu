@@ -292,6 +292,7 @@ vla_err_t vla_layer_norm_backward(vla_handle_t h, const void* dy, const void* x,
   a.rows = rows; a.D = D; a.dy_row = strides[0]; a.x_row = strides[1]; a.dres_row = strides[2]; a.dx_row = strides[3];
   a.sm_count = h->sm_count;
   a.status = h->status;
+  a.wait_limit = h->wait_limit;
   cudaError_t e = on_device(h->device, [&]() {
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (rows > 0) return vla::launch_layer_norm_back(a, dy_dtype == VLA_BF16, x_dtype == VLA_BF16, s);

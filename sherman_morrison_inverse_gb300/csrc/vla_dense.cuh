@@ -191,6 +191,7 @@ struct LayerNormBackArgs {
   long long rows, D, dy_row, x_row, dres_row, dx_row;
   int sm_count;
   DevStatus* status;
+  unsigned long long wait_limit;   // of a wait, in ns (0: its self-test)
 };
 cudaError_t launch_layer_norm_back(const LayerNormBackArgs& a, bool dy_bf16, bool x_bf16, cudaStream_t s);
 size_t layer_norm_back_ws(long long rows, long long D, int sm_count);

@@ -73,11 +73,6 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigne
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, unsigned long long limit, volatile uint32_t* failed) {
   return __all_sync(0xffffffffu, wait_for(bar, parity, limit, failed));
 }
-// Waits until the copies of the last fills of a ring have landed: fill i goes to stage i % stages.
-__device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t stages, uint32_t fills) {
-#pragma unroll 1
-  for (uint32_t i = fills > stages ? fills - stages : 0; i < fills; ++i) mbar_wait_bounded(full + i % stages, i / stages & 1);
-}
 
 // Four adjacent values of a row, those from `left` on absent.
 template <typename T>

@@ -128,6 +128,12 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
   }
 }
 
+// Waits until the copies of the last fills of a ring have landed: fill i goes to stage i % stages.
+__device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t stages, uint32_t fills) {
+#pragma unroll 1
+  for (uint32_t i = fills > stages ? fills - stages : 0; i < fills; ++i) mbar_wait_bounded(full + i % stages, i / stages & 1);
+}
+
 // ---- thread-block clusters: distributed shared memory and cluster-scope mbarriers
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {

@@ -209,7 +209,8 @@ cudaError_t forward_of(const LayerNormArgs& a, cudaStream_t s) {
 // with them its sums of dw and db; a row's two sums (of a and of a h) are joined by one barrier.
 // VEC 4: rows on 16-byte boundaries arrive by bulk copies in a ring of stages of rows_per_cta rows, as many as shared
 // memory holds, so that some 200 KB an SM are on their way whatever the registers hold; a stage is filled again
-// behind the barrier of the next one, when nobody reads it any more.  VEC 1: rows anywhere, read directly.
+// behind the barrier of the next one, when nobody reads it any more.  Waits are bounded: a block that gives up waits (bounded too)
+// for its copies under way and leaves the sums that it has.  VEC 1: rows anywhere, read directly.
 // Blocks leave their sums of dw and db as rows of `partial`, which back_sum_kernel adds in their order.
 // 16384 x 4096 bfloat16 with the residual's gradient 103 us, 5.2 TB/s, 78 % of a copy's rate: a row's chain of barriers on the 16 warps
 // that the registers of 16 values a thread allow.  4099 x 1001 float32, value by value, 15 us.
@@ -309,8 +310,9 @@ __global__ void __launch_bounds__(kBackThreads, 1)
   int par = 0, stage = 0, span = 2;   // span: the power of two from wn on
   while (span < wn) span *= 2;
   uint32_t phase = 0;
-  bool ok = true;
-  for (long long first = base; first < a.rows; first += step, row += step, par ^= 1) {
+  bool ok = true, gave_up = false;
+  long long first = base;
+  for (; first < a.rows; first += step, row += step, par ^= 1) {
     const bool live = row < a.rows;
     const TD* dy = static_cast<const TD*>(a.dy) + row * a.dy_row;
     const TX* x = static_cast<const TX*>(a.x) + row * a.x_row;
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       dy = reinterpret_cast<const TD*>(at);
       x = reinterpret_cast<const TX*>(at + dy_bytes);
       dres = reinterpret_cast<const TX*>(at + dy_bytes + x_bytes);
-      ok = mbar_wait_bounded(full + stage, phase);
+      ok = a.wait_limit > 0 && mbar_wait_bounded(full + stage, phase, a.wait_limit);
     }
     uint64_t g[P], h[P], r[P] = {}, t1 = 0, t2 = 0;
     if constexpr (AHEAD) {
@@ -363,8 +365,8 @@ __global__ void __launch_bounds__(kBackThreads, 1)
     if (lane == 0) part[par][warp] = make_float2(s1, s2);
     if (VEC > 1) {
       if (__syncthreads_or(!ok)) {   // a copy that did not arrive: give up, all threads alike
-        if (threadIdx.x == 0) atomicOr(&status->flags, kStatusTimeout);
-        return;
+        gave_up = true;
+        break;
       }
       // behind the barrier nobody reads the stage before this one: the row that is `stages` on goes there
       if (threadIdx.x == 0 && first > base) fill(first + (stages - 1) * step, stage > 0 ? stage - 1 : stages - 1);
@@ -417,6 +419,16 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       stage = 0;
       phase ^= 1;
     }
+  }
+  if (gave_up) {
+    if (threadIdx.x == 0) {
+      // filled so far: the first `stages`, then one an iteration but the first, as long as there are rows
+      const long long passed = (first - base) / step, all = (a.rows - base + step - 1) / step;
+      const long long most = passed > 0 ? passed + stages - 1 : stages;
+      drain_ring(full, stages, (uint32_t)(most < all ? most : all));
+      atomicOr(&status->flags, kStatusTimeout);
+    }
+    __syncthreads();
   }
   // the slots' sums, in their order
   float* sums = reinterpret_cast<float*>(smem);

@@ -73,6 +73,28 @@ def test_a_products_wait_that_runs_out_ends_the_call(vla, M, N, K, dtype, gradie
     h.close()
 
 
+@pytest.mark.parametrize("rows,D,dtype,flagged", [(4096, 4096, "bf16", True), (3000, 128, "f32", True), (330, 8192, "f32", True),
+                                                  (2, 264, "bf16", True), (300, 1001, "f32", False), (5, 8200, "bf16", False)])
+def test_a_norms_wait_that_runs_out_ends_the_call(vla, rows, D, dtype, flagged):
+    """The same for the norm's gradient: rows that are copied ahead are waited for, others are read directly."""
+    gen, h = generator(rows), vla.Handle(0)
+    dy, x, res = (rand(gen, rows, D, dtype=TYPES[dtype]) for _ in range(3))
+    w = rand(gen, D)
+    _, stats = h.layer_norm(x, w, stats=True)
+    want = h.layer_norm_backward(dy, x, w, stats, res)
+    assert h.status()["flags"] == 0
+    for _ in range(3):
+        h.wait_limit(0)
+        for _ in range(5):
+            h.layer_norm_backward(dy, x, w, stats, res)
+            assert h.status()["flags"] == (vla.STATUS_TIMEOUT if flagged else 0)
+        h.wait_limit(2000)
+        for _ in range(5):
+            assert all(torch.equal(a, b) for a, b in zip(h.layer_norm_backward(dy, x, w, stats, res), want))
+        assert h.status()["flags"] == 0
+    h.close()
+
+
 def test_the_wait_limit_has_a_range(vla):
     h = vla.Handle(0)
     with pytest.raises(vla.VlaError, match="0..5000"):
