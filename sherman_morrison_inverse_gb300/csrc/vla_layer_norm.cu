@@ -339,12 +339,12 @@ __global__ void __launch_bounds__(kBackThreads, 1)
       get_row<TX, VEC, NV>(x, live, tpr, tid, D, h);
     }
     const float rs = rstd;
-    const uint64_t scale = pair(rs, rs), shift = pair(-mean * rs, -mean * rs);
+    const uint64_t scale = pair(rs, rs), shift = pair(-mean, -mean);
     stats(row + step);
     if (!KEEP) get_row<float, VEC, NV>(a.w, true, tpr, tid, D, w);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      h[i] = fma2(h[i], scale, shift);
+      h[i] = mul2(add2(h[i], shift), scale);   // x rstd - mean rstd would round off 2^-24 of |mean| rstd
       dw[i] = fma2(g[i], h[i], dw[i]);
       db[i] = add2(g[i], db[i]);
       g[i] = mul2(g[i], w[i]);

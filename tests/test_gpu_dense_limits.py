@@ -100,3 +100,25 @@ def test_the_wait_limit_has_a_range(vla):
     with pytest.raises(vla.VlaError, match="0..5000"):
         h.wait_limit(5001)
     h.close()
+
+
+# ---------------------------------------------------------------------------------------------
+# rows far from zero
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [264, 1001, 4096, 8191, 8200])
+def test_layer_norm_backward_far_from_zero(vla, D, dtype):
+    """A mean of a thousand deviations.  x - mean is exact there (both within a factor of two of one another), so h is off
+    by two roundings of itself, whatever the mean; dy follows h, so that the rows' mean of a h counts."""
+    gen, rows = generator(D), 4
+    x, w = 1000 + rand(gen, rows, D), 1 + 0.2 * rand(gen, D)
+    dy = (x - 1000 + 0.1 * rand(gen, rows, D)).to(TYPES[dtype])
+    _, _, mean, rstd = ref.layer_norm(f64(x), f64(w))
+    stats = torch.tensor(np.stack([mean, rstd], 1), dtype=torch.float32, device="cuda")
+    mean, rstd = f64(stats).T
+    got = vla.layer_norm_backward(dy, x, w, stats)
+    want, mag = ref.layer_norm_backward(f64(dy), f64(x), f64(w), mean, rstd)
+    # sums over a row: chains of at most 140 additions (128 values, or 16 pairs and ten folds); over the rows: four
+    for g, r, m, n, what in zip(got, want, mag, (150, rows + 8, rows + 2), ("dx", "dw", "db")):
+        worst = np.max(np.abs(f64(g) - r) / (n * U32 * m))
+        assert worst <= 1.0, f"{what}: {worst:.3g} times its bound"
