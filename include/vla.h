@@ -447,7 +447,8 @@ typedef enum { VLA_MAT_F32 = 0, VLA_MAT_BF16 = 1, VLA_MAT_E4M3 = 2 } vla_mat_t; 
  *   rows      host array of the row strides {x, w, residual, pre, y}.
  *   workspace device memory of vla_linear_workspace bytes, 16-byte aligned, that nothing else
  *             uses until the call's work is done; NULL where that is 0.
- * Products are exact and sums float32.  Float32 operands: up to 16 rows of x (128 of few weights) the same; else each is
+ * Products are exact and sums float32.  (A tensor core cuts off what an addition shifts out: of bfloat16 results up to 4e-5 of
+ * the sum where all terms have one sign, whatever K is; of float32 results a tenth of that at most.)  Float32 operands: up to 16 rows of x (128 of few weights) the same; else each is
  * taken as three bfloat16 terms, products to about 2^-23 of their magnitude (with fewer bits for values below
  * 2^-110), and a value of 3.39e38 or more, an infinity or a NaN makes the outputs that it enters infinite or NaN.  v is rounded once into pre and not before the activation; y is rounded once.
  * Errors (before any launch): INVALID_ARG for NULL pointers, sizes or strides out of range, unknown types,
@@ -471,7 +472,7 @@ vla_err_t vla_linear_workspace(vla_handle_t h, const void* x, const void* w, lon
  *   pre       [M, N] io dtype, what vla_linear wrote; NULL and unused for VLA_ACT_NONE.
  *   dx, dw    [M, K] and [N, K] io dtype;  db [N] float32.  Each may be NULL: not computed.
  *   rows      host array of the row strides {dy, x, w, pre, dx, dw}.
- * Sums are float32.  With bfloat16 and an activation, g is rounded to bfloat16 for the products (not for db):
+ * Sums are float32, as vla_linear's, whatever M and N are.  With bfloat16 and an activation, g is rounded to bfloat16 for the products (not for db):
  * each term of dx and dw is off by up to 2^-8 of itself.  A gradient without terms (M or N zero) is zero.
  * Workspace and errors: as for vla_linear. */
 vla_err_t vla_linear_backward(vla_handle_t h, const void* dy, const void* x, const void* w, const void* pre, void* dx,

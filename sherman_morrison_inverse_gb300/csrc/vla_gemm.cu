@@ -17,6 +17,9 @@
 // first.  Where the result is float32, sums stay in tensor memory for 4 stages and are then added to float32 registers:
 // a tensor core cuts the bits off that an addition shifts out, always towards zero, and the error of a chain of them
 // grows with its length (float32, K = 1161: 6.8e-7 of the result without, 1.4e-7 with; plain float32 products 3.6e-7).
+// For results rounded to bfloat16 that matters where Kd is long, as a gradient's is by its tokens: terms of one sign come out
+// smaller by 3.4e-5 after 128 stages (8192 of Kd, a hundredth of the rounding), by 3.3e-3 after 8192 (more than it).  A
+// share of Kd of up to 128 stages stays in tensor memory whole; a longer one is added to registers every 64.
 // Kd is split over clusters where there are fewer tiles than clusters; the parts are then added in order.
 // Every wait is bounded: one that runs out sets the handle's timeout flag, and the cluster waits (bounded too) for the products and
 // copies that both CTAs have under way and returns.
@@ -291,6 +294,7 @@ __device__ __forceinline__ void chunk_staged(const GemmArgs& g, const float* v, 
 }
 
 // Warps 4..11: a warp takes 32 rows (those of the tensor memory lanes that it can reach) and half the columns.
+// PROMOTE: sums move to registers every g.part stages.
 template <typename T, int BN, bool PROMOTE, bool BACK>
 __device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, uint32_t chunk, uint64_t* acc_full,
                                          uint64_t* acc_empty, uint32_t rank, int warp, int lane, int first, int step,
@@ -379,7 +383,7 @@ __device__ __forceinline__ void epilogue(const GemmPair& pair, uint32_t tmem, ui
   }
 }
 
-template <int BN, bool E4M3, bool PROMOTE, bool BACK>
+template <typename T, int BN, bool E4M3, bool PROMOTE, bool BACK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ GemmPair pair) {
   using C = Cfg<BN>;
@@ -421,7 +425,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const uint32_t chunk = base + C::o_chunk + (warp - 4) * kChunk;
-    using T = typename std::conditional<PROMOTE, float, __nv_bfloat16>::type;   // y's type
     epilogue<T, BN, PROMOTE, BACK>(pair, tmem, chunk, acc_full, acc_empty, rank, warp, lane, first, step, n_tiles, failed);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
@@ -701,9 +704,9 @@ Plan plan_of(const ProductArgs* p, int count, int mat) {
 }
 
 // follows: the launch before it on the stream is of the same call (see launch_after); others are waited for whole
-template <int BN, bool E4M3, bool PROMOTE, bool BACK>
+template <typename T, int BN, bool E4M3, bool PROMOTE, bool BACK>
 cudaError_t launch(const Maps& maps, const GemmPair& pair, bool follows, cudaStream_t s) {
-  auto kern = gemm_kernel<BN, E4M3, PROMOTE, BACK>;
+  auto kern = gemm_kernel<T, BN, E4M3, PROMOTE, BACK>;
   constexpr int bytes = (int)Cfg<BN>::bytes;
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
@@ -757,7 +760,7 @@ cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream
   auto place = [&](const Operand& o) -> const void* { return o.pack ? ws + q.at[copy_of(q, o)] : o.p; };
   GemmPair pair{};
   Maps maps;
-  bool join = false;
+  bool join = false, whole = true;   // whole: no share of Kd is longer than kWhole stages
   long long pieces = 0;
   const int per = mat == kMatE4m3 ? 128 : 64;
   const bool back = p[0].b_mn;
@@ -771,6 +774,8 @@ cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream
     g.limit = p[i].wait_limit ? p[i].wait_limit + 4000ull * (unsigned long long)q.k_iters[i] * q.passes : 0;
     if (q.tokens.rows) return launch_tokens(q.tokens, g, q.a[0], q.b[0], place(q.a[0]), place(q.b[0]), s);
     g.tiles_m = q.tiles_m[i]; g.tiles_n = q.tiles_n[i]; g.splits = q.splits[i];
+    g.part = p[i].out.y_bf16 ? kLongPart : kPart;
+    if (g.splits > 0 && (q.k_iters[i] * q.passes + g.splits - 1) / g.splits > kWhole) whole = false;
     const long long tiles = (long long)g.tiles_m * g.tiles_n * g.splits;
     if (tiles > 0x1fffffff) return cudaErrorInvalidConfiguration;
     g.tiles = (int)tiles;
@@ -786,16 +791,16 @@ cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream
   }
   if (pair.g[0].tiles + pair.g[1].tiles > 0) {
     const bool wide = q.bn == 256, y16 = p[0].out.y_bf16, follows = p[0].follows || q.copies.count > 0;
-    auto run = [&](auto bn, auto promote) -> cudaError_t {
+    auto run = [&](auto y, auto bn, auto promote) -> cudaError_t {
+      using T = decltype(y);
       constexpr int BN = decltype(bn)::value;
       constexpr bool P = decltype(promote)::value;
-      if (back) return launch<BN, false, P, true>(maps, pair, follows, s);
-      return mat == kMatE4m3 ? launch<BN, true, P, false>(maps, pair, follows, s) : launch<BN, false, P, false>(maps, pair, follows, s);
+      if (back) return launch<T, BN, false, P, true>(maps, pair, follows, s);
+      return mat == kMatE4m3 ? launch<T, BN, true, P, false>(maps, pair, follows, s) : launch<T, BN, false, P, false>(maps, pair, follows, s);
     };
-    using N128 = std::integral_constant<int, 128>;
-    using N256 = std::integral_constant<int, 256>;
-    if (y16) e = wide ? run(N256(), std::false_type()) : run(N128(), std::false_type());
-    else e = wide ? run(N256(), std::true_type()) : run(N128(), std::true_type());
+    auto of = [&](auto y, auto promote) { return wide ? run(y, std::integral_constant<int, 256>(), promote) : run(y, std::integral_constant<int, 128>(), promote); };
+    if (!y16) e = of(float(), std::true_type());
+    else e = whole ? of(__nv_bfloat16(), std::false_type()) : of(__nv_bfloat16(), std::true_type());
     if (e != cudaSuccess) return e;
   }
   if (!join) return e;

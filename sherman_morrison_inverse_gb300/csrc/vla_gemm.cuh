@@ -10,13 +10,16 @@
 namespace vla {
 namespace gemm {
 
-constexpr int kPart = 4;   // stages that add up in tensor memory before float32 registers take the sums over
+// Stages that add up in tensor memory before float32 registers take the sums over: of float32 results, and of others where a
+// share of Kd is longer than kWhole stages.
+constexpr int kPart = 4, kLongPart = 64, kWhole = 128;
 
 // One product of a launch.
 struct GemmArgs {
   long long M, N;
   int tiles_m, tiles_n, splits, tiles;   // tiles: of all splits
   int k_iters, passes;      // stages of one pass over Kd; passes over the terms
+  int part;                 // stages that add up in tensor memory
   float* partial;           // [splits][M][part_row] where splits > 1
   long long part_row;       // N, rounded up to 8
   Epilogue out;
@@ -33,7 +36,7 @@ __device__ __forceinline__ int term_b(int pass) { return (0x021010 >> (4 * (5 - 
 
 // Stages [k, part_end) of a range that ends at k1 add up in tensor memory; parts are added to float32 registers.
 __device__ __forceinline__ int part_end(const GemmArgs& g, int k, int k1) {
-  const int last = (g.passes - 1) * g.k_iters, end = k < last ? last : k + kPart;
+  const int last = (g.passes - 1) * g.k_iters, end = k < last ? last : k + g.part;
   return end < k1 ? end : k1;
 }
 // The first stage of a share of Kd.  (The product is below 2^32: at most 2^24 stages, 6 passes, 32 shares.)

@@ -306,6 +306,7 @@ TokensPlan tokens_plan(long long M, long long N, long long w_values, int all_ite
 cudaError_t launch_tokens(const TokensPlan& t, GemmArgs g, const Operand& x, const Operand& w, const void* x_at, const void* w_at,
                           cudaStream_t s) {
   g.splits = t.splits;
+  g.part = kPart;
   auto run = [&](auto y, auto e4m3) -> cudaError_t {
     using T = decltype(y);
     constexpr bool E = decltype(e4m3)::value;

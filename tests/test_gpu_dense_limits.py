@@ -122,3 +122,63 @@ def test_layer_norm_backward_far_from_zero(vla, D, dtype):
     for g, r, m, n, what in zip(got, want, mag, (150, rows + 8, rows + 2), ("dx", "dw", "db")):
         worst = np.max(np.abs(f64(g) - r) / (n * U32 * m))
         assert worst <= 1.0, f"{what}: {worst:.3g} times its bound"
+
+
+# ---------------------------------------------------------------------------------------------
+# long sums
+
+def same_sign(gen, rows, cols, along, dtype):
+    """[rows, cols] of positive values in `dtype`, every row (along 1) or column (0) with a size of its own; its sums over the other
+    dimension in 64 bits."""
+    size = 1 + torch.rand(rows if along else cols, generator=gen, device="cuda")
+    x, total = torch.empty(rows, cols, dtype=dtype, device="cuda"), []
+    for i in range(0, rows, 4096):
+        part = 0.5 + torch.rand(min(4096, rows - i), cols, generator=gen, device="cuda")
+        x[i:i + 4096] = part * (size[i:i + 4096, None] if along else size)
+        total.append(x[i:i + 4096].double().sum(along))
+    return x, torch.cat(total) if along else sum(total)
+
+
+# Terms of one sign, whose sums a tensor core cuts off towards zero: two units of 2^-23 of the running sum an addition at most, four
+# additions a stage.  A chain of 64 stages, its running sum half of the whole on the mean: 4 x 64 x 2^-23; of up to 128, which is not
+# cut into parts, twice that.  Over the parts float32 additions round to the nearest.  The roundings to bfloat16, 2^-8 / sqrt(3) at most
+# and of either sign, leave four times that over the square root of the number of distinct outputs, of which there are
+# 128 sizes (values of bfloat16 between 1 and 2) times the sums.
+def mean_bound(stages, sums):
+    return 4 * (64 if stages > 128 else stages) * 2.0 ** -23 + 2.0 ** -22 + 4 * U16 / 3 ** 0.5 / (128 * sums) ** 0.5
+
+
+@pytest.mark.parametrize("M", [8192, 16384, 262144 + 40, 524288])
+def test_weight_gradients_of_many_tokens_keep_their_sums(vla, M):
+    """dw sums over the tokens, in one share each of more tiles than there are clusters."""
+    gen, N, K = generator(M), 2048, 2432
+    x, total = same_sign(gen, M, K, 0, torch.bfloat16)
+    dy = (1 + torch.rand(N, generator=gen, device="cuda")).bfloat16()
+    _, dw, _ = vla.linear_backward(dy.expand(M, N), x, torch.zeros(N, K, dtype=torch.bfloat16, device="cuda"), input=False, bias=False)
+    off = dw.double() / (dy.double()[:, None] * total) - 1
+    assert abs(float(off.mean())) <= mean_bound(M / 64, K)
+    assert float(off.abs().max()) <= U16 + 4 * 128 * 2.0 ** -22 + M / 4096 * U32
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("K", [8192, 65536 + 72])
+def test_products_of_long_rows_keep_their_sums(vla, K, dtype):
+    gen, M, N = generator(K), 2048, 2560
+    x, total = same_sign(gen, M, K, 1, TYPES[dtype])
+    w = (1 + torch.rand(N, generator=gen, device="cuda")).to(TYPES[dtype])
+    y = vla.linear(x, w[:, None].expand(N, K).contiguous(), dtype=torch.bfloat16)
+    off = y.double() / (total[:, None] * w.double()) - 1
+    assert abs(float(off.mean())) <= mean_bound(K / (64 if dtype == "bf16" else 128), M / (16 if dtype == "e4m3" else 1))
+
+
+def test_a_long_gradient_beside_a_short_one(vla):
+    """One launch whose products differ in length: dx sums over few columns, dw over many rows."""
+    gen, M, N, K = generator(77), 40000, 1500, 2500
+    dy, x, w = (rand(gen, *s, dtype=torch.bfloat16) for s in ((M, N), (M, K), (N, K)))
+    dx, dw, db = vla.linear_backward(dy, x, w)
+    for got, left, right, stages in ((dw[:100], dy[:, :100].double().t(), x.double(), 64), (dx[-500:], dy[-500:].double(), w.double(), N / 64 + 1)):
+        want, mag = left @ right, left.abs() @ right.abs()
+        # a part's additions are cut off, each by 2^-22 of its sum of magnitudes at most; parts are rounded to the nearest
+        bound = (4 * stages * 2.0 ** -22 + (M / 4096 + 2) * U32) * mag + U16 * want.abs()
+        assert bool(((got.double() - want).abs() <= bound).all())
+        assert float((got.double() - want).norm() / want.norm()) <= U16 / 3 ** 0.5
