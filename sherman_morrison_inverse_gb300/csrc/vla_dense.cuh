@@ -100,9 +100,9 @@ __device__ __forceinline__ float activate(float v, int act) {
 
 // A launch whose CTAs may start before the one before it on the stream is done (see launch_second).  Every thread of them waits for
 // it in wait_for_first before it touches memory, and only a launch of the same call may lie before, of which the same holds:
-// so what is done when it is done includes everything earlier on the stream.
+// so what is done when it is done includes everything earlier on the stream.  follows: false for the first launch of a call.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, A&&... args) {
+cudaError_t launch_after(bool follows, void (*kern)(P...), dim3 grid, int threads, cudaStream_t s, A&&... args) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -111,7 +111,7 @@ cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, cudaStream_
   c.blockDim = dim3((unsigned int)threads);
   c.stream = s;
   c.attrs = &attr;
-  c.numAttrs = 1;
+  c.numAttrs = follows ? 1 : 0;
   return cudaLaunchKernelEx(&c, kern, static_cast<A&&>(args)...);
 }
 

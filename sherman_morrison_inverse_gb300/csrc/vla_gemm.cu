@@ -789,7 +789,8 @@ cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream
          !encode(&maps.b[at], q.b[i], place(q.b[i]), back ? 64 : per, back ? per : q.bn / 2)))
       return cudaErrorInvalidValue;
   }
-  if (pair.g[0].tiles + pair.g[1].tiles > 0) {
+  const bool terms = pair.g[0].tiles + pair.g[1].tiles > 0;
+  if (terms) {
     const bool wide = q.bn == 256, y16 = p[0].out.y_bf16, follows = p[0].follows || q.copies.count > 0;
     auto run = [&](auto y, auto bn, auto promote) -> cudaError_t {
       using T = decltype(y);
@@ -806,7 +807,8 @@ cudaError_t launch_products(const ProductArgs* p, int count, int mat, cudaStream
   if (!join) return e;
   const long long want = (pieces + 255) / 256, most = 16LL * p[0].sm_count;
   const dim3 grid((unsigned int)(want < most ? want : most), back ? 2u : 1u);
-  return p[0].out.y_bf16 ? launch_after(join_kernel<__nv_bfloat16>, grid, 256, s, pair) : launch_after(join_kernel<float>, grid, 256, s, pair);
+  return p[0].out.y_bf16 ? launch_after(terms, join_kernel<__nv_bfloat16>, grid, 256, s, pair)
+                         : launch_after(terms, join_kernel<float>, grid, 256, s, pair);
 }
 
 }  // namespace vla

@@ -608,7 +608,7 @@ cudaError_t backward(const LayerNormBackArgs& a, cudaStream_t s) {
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  return launch_after(back_sum_kernel, dim3((unsigned int)((a.D + 31) / 32), a.db ? 2 : 1), 1024, s, a.partial, a.dw, a.db, a.D, parts);
+  return launch_after(true, back_sum_kernel, dim3((unsigned int)((a.D + 31) / 32), a.db ? 2 : 1), 1024, s, a.partial, a.dw, a.db, a.D, parts);
 }
 
 }  // namespace

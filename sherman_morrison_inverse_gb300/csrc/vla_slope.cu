@@ -107,7 +107,7 @@ cudaError_t launch(const SlopeArgs& a, cudaStream_t s) {
   slope_kernel<T, VEC><<<grid, 256, 0, s>>>(a, stretch);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.db) return e;
-  return launch_after(slope_sum_kernel, dim3((unsigned int)((a.N + 31) / 32)), 256, s, a.partial, a.db, a.N, parts);
+  return launch_after(true, slope_sum_kernel, dim3((unsigned int)((a.N + 31) / 32)), 256, s, a.partial, a.db, a.N, parts);
 }
 
 }  // namespace

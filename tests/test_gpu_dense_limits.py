@@ -1,4 +1,6 @@
 """Products and norms where they end early, at the ends of their ranges, and form by form."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -29,6 +31,52 @@ def generator(seed):
 
 def rand(gen, *shape, dtype=torch.float32):
     return torch.randn(*shape, generator=gen, device="cuda").to(dtype)
+
+
+def launches(call):
+    """What a call launches, from a graph captured of it: the kernels' names in order, and whether each may start before what
+    lies before it on the stream is done."""
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        call()
+    cu, graph = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p(g.raw_cuda_graph())
+
+    class Params(ctypes.Structure):   # CUDA_KERNEL_NODE_PARAMS
+        _fields_ = [("func", ctypes.c_void_p), ("sizes", ctypes.c_uint * 7), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p),
+                    ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+    class Edge(ctypes.Structure):     # CUgraphEdgeData
+        _fields_ = [("from_port", ctypes.c_ubyte), ("to_port", ctypes.c_ubyte), ("type", ctypes.c_ubyte), ("rest", ctypes.c_ubyte * 5)]
+
+    n = ctypes.c_size_t()
+    assert cu.cuGraphGetNodes(graph, None, ctypes.byref(n)) == 0
+    nodes = (ctypes.c_void_p * n.value)()
+    assert cu.cuGraphGetNodes(graph, nodes, ctypes.byref(n)) == 0
+    names = {}
+    for node in nodes:
+        kind, p, text = ctypes.c_int(), Params(), ctypes.c_char_p()
+        assert cu.cuGraphNodeGetType(ctypes.c_void_p(node), ctypes.byref(kind)) == 0
+        if kind.value == 0:
+            assert cu.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+            if p.func:
+                assert cu.cuFuncGetName(ctypes.byref(text), ctypes.c_void_p(p.func)) == 0
+            else:
+                assert cu.cuKernelGetName(ctypes.byref(text), ctypes.c_void_p(p.kern)) == 0
+            names[node] = text.value.decode()
+        else:
+            names[node] = "no kernel"
+    assert cu.cuGraphGetEdges_v2(graph, None, None, None, ctypes.byref(n)) == 0
+    a, b, edges = (ctypes.c_void_p * n.value)(), (ctypes.c_void_p * n.value)(), (Edge * n.value)()
+    assert cu.cuGraphGetEdges_v2(graph, a, b, edges, ctypes.byref(n)) == 0
+    before = {y: (x, e.type) for x, y, e in zip(a, b, edges)}
+    order = [m for m in nodes if m not in before]
+    assert len(order) == (1 if len(nodes) else 0) and len(before) == len(nodes) - len(order)   # one stream: a chain
+    after = {x: y for y, (x, _) in before.items()}
+    while order and order[-1] in after:
+        order.append(after[order[-1]])
+    return [(names[m], m in before and before[m][1] == 1) for m in order]
 
 
 # ---------------------------------------------------------------------------------------------
@@ -182,3 +230,28 @@ def test_a_long_gradient_beside_a_short_one(vla):
         bound = (4 * stages * 2.0 ** -22 + (M / 4096 + 2) * U32) * mag + U16 * want.abs()
         assert bool(((got.double() - want).abs() <= bound).all())
         assert float((got.double() - want).norm() / want.norm()) <= U16 / 3 ** 0.5
+
+
+# ---------------------------------------------------------------------------------------------
+# what a call launches
+
+def test_only_launches_of_one_call_overlap(vla):
+    """A call's first launch waits for all that lies before it on the stream, whatever that is; the later ones may start early."""
+    gen = generator(5)
+    t, e = rand(gen, 100), lambda *s: torch.empty(*s, device="cuda")   # noqa: E731
+    x, w, dy = rand(gen, 700, 77), rand(gen, 130, 77), rand(gen, 700, 130)
+    calls = [
+        (lambda: vla.linear(x, w), True),                                                        # copies, products
+        (lambda: vla.linear_backward(dy, x, w), True),                                           # db, copies, products
+        (lambda: vla.layer_norm_backward(x, x, t[:77].contiguous(), e(700, 2)), True),           # rows, sums
+        (lambda: vla.linear(e(3, 0), e(5, 0)), False),                                           # no terms: nothing but the epilogue
+        (lambda: vla.linear_backward(e(0, 5), e(0, 4), w[:5, :4].contiguous(), bias=False), False),
+        (lambda: vla.linear_backward(e(3, 0), x[:3, :4].contiguous(), e(0, 4), weight=False), False),
+    ]
+    for call, several in calls:
+        def one():
+            t.add_(1)
+            call()
+        got = launches(one)
+        first = [early for name, early in got if "vla" in name or name == "no kernel"][0]
+        assert not first and (several == any(early for _, early in got)), got
