@@ -55,6 +55,7 @@ static lnorm_fn f_lnorm;
 static lnorm_back_fn f_lnorm_back;
 static lnorm_back_ws_fn f_lnorm_back_ws;
 static PyObject *c_new, *t_u8, *s_device, *k_new;                 /* torch.empty; names of its dtype and device */
+static PyObject *c_grad, *s_requires;                             /* torch.is_grad_enabled, and what it is asked for */
 static PyObject *c_strided, *c_at;                                /* see fresh(); None where torch has them not */
 static PyObject *t_f32, *t_bf16, *t_i32, *t_e4m3, *t_i8;          /* torch dtypes */
 static PyObject *c_like, *c_dense, *c_empty, *c_bytes, *c_stream; /* allocators and the current stream */
@@ -588,6 +589,27 @@ static int scratch(PyObject* like, size_t need, long device, PyObject** ws, void
   return -1;
 }
 
+/* The products and norms record no gradient: a tensor that wants one is refused, where gradients are recorded at all.
+ * (0.2 us of a call.) */
+static int no_gradient(PyObject* const* a, const char* const* names, int n) {
+  PyObject* on = PyObject_CallNoArgs(c_grad);
+  if (!on) return -1;
+  Py_DECREF(on);   /* a singleton */
+  for (int i = 0; i < n && on == Py_True; ++i) {
+    if (!names[i] || a[i] == Py_None || PyBool_Check(a[i])) continue;
+    PyObject* r = PyObject_GetAttr(a[i], s_requires);
+    if (!r) return -1;
+    Py_DECREF(r);
+    if (r != Py_True) continue;
+    PyErr_Format(PyExc_ValueError,
+                 "%s requires a gradient, and the call would not record one: make it under torch.no_grad() or in an "
+                 "autograd.Function that calls the gradient's operator",
+                 names[i]);
+    return -1;
+  }
+  return 0;
+}
+
 /* Reads and checks a tensor of evenly spaced rows, [..., width]. */
 static int even_rows(Tensor* t, PyObject* obj, const char* name, const long long* shape, int nd, PyObject* dtype,
                      long device, long long* step) {
@@ -598,7 +620,9 @@ static int even_rows(Tensor* t, PyObject* obj, const char* name, const long long
 /* linear(handle, x, w, bias, residual, y, act, pre, x_scale, w_scale, dtype, stream); act: 0 none, 1 silu, 2 gelu */
 static PyObject* py_linear(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
   (void)mod;
+  static const char* const names[] = {"x", "w", "bias", "residual", "y", NULL, "pre", "x_scale", "w_scale"};
   if (n != 12) return want("linear takes 12 arguments");
+  if (no_gradient(a + 1, names, 9)) return NULL;
   PyObject *self = a[0], *y = NULL, *ws = NULL, *dtype, *odtype;
   Call c;
   Tensor x, w, t;
@@ -663,7 +687,9 @@ bad:
  * computed) */
 static PyObject* py_linear_back(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
   (void)mod;
+  static const char* const names[] = {"dy", "x", "w", "pre", NULL, "dx", "dw", "db"};
   if (n != 10) return want("linear_back takes 10 arguments");
+  if (no_gradient(a + 1, names, 8)) return NULL;
   PyObject *self = a[0], *ws = NULL, *dtype, *got[3] = {NULL, NULL, NULL}, *made;
   Call c;
   Tensor dy, x, w, t;
@@ -738,7 +764,9 @@ bad:
 /* layer_norm(handle, x, w, b, residual, y, eps, stats, stream); stats: a tensor, True (a new one) or False */
 static PyObject* py_layer_norm(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
   (void)mod;
+  static const char* const names[] = {"x", "w", "b", "residual", "y", NULL, "stats"};
   if (n != 9) return want("layer_norm takes 9 arguments");
+  if (no_gradient(a + 1, names, 7)) return NULL;
   PyObject *self = a[0], *y = NULL, *stats = NULL, *dtype, *rdtype, *made;
   Call c;
   Tensor x, r, t;
@@ -797,7 +825,9 @@ bad:
  * computed) */
 static PyObject* py_layer_norm_back(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
   (void)mod;
+  static const char* const names[] = {"dy", "x", "w", "stats", "dresidual", "dx", "dw", "db"};
   if (n != 10) return want("layer_norm_back takes 10 arguments");
+  if (no_gradient(a + 1, names, 8)) return NULL;
   PyObject *self = a[0], *dx = NULL, *dw = NULL, *db = NULL, *ws = NULL, *gtype, *dtype, *made;
   Call c;
   Tensor dy, x, t;
@@ -857,13 +887,13 @@ bad:
   return NULL;
 }
 
-/* setup_dense(addresses of the entry points and workspace queries, torch.empty, torch.uint8, and for fresh() either two
- * callables or None): after setup */
+/* setup_dense(addresses of the entry points and workspace queries, torch.is_grad_enabled, torch.empty, torch.uint8, and for
+ * fresh() either two callables or None): after setup */
 static PyObject* py_setup_dense(PyObject* mod, PyObject* args) {
   (void)mod;
   unsigned long long p[7];
-  PyObject* o[4];
-  if (!PyArg_ParseTuple(args, "KKKKKKKOOOO", p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6, o, o + 1, o + 2, o + 3)) return NULL;
+  PyObject* o[5];
+  if (!PyArg_ParseTuple(args, "KKKKKKKOOOOO", p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6, o, o + 1, o + 2, o + 3, o + 4)) return NULL;
   f_linear = (linear_fn)(uintptr_t)p[0];
   f_linear_ws = (linear_ws_fn)(uintptr_t)p[1];
   f_linear_back = (linear_back_fn)(uintptr_t)p[2];
@@ -871,8 +901,8 @@ static PyObject* py_setup_dense(PyObject* mod, PyObject* args) {
   f_lnorm = (lnorm_fn)(uintptr_t)p[4];
   f_lnorm_back = (lnorm_back_fn)(uintptr_t)p[5];
   f_lnorm_back_ws = (lnorm_back_ws_fn)(uintptr_t)p[6];
-  PyObject** slot[4] = {&c_new, &t_u8, &c_strided, &c_at};
-  for (int i = 0; i < 4; ++i) {
+  PyObject** slot[5] = {&c_grad, &c_new, &t_u8, &c_strided, &c_at};
+  for (int i = 0; i < 5; ++i) {
     Py_INCREF(o[i]);
     Py_XDECREF(*slot[i]);
     *slot[i] = o[i];
@@ -927,5 +957,6 @@ PyMODINIT_FUNC PyInit__layer_binding(void) {
   k_dtype = PyTuple_Pack(1, s_dtype);
   s_device = PyUnicode_InternFromString("device");
   k_new = PyTuple_Pack(2, s_dtype, s_device);
+  s_requires = PyUnicode_InternFromString("requires_grad");
   return PyModule_Create(&module);
 }

@@ -16,6 +16,10 @@ binding they check and marshal arguments, and every step runs in the library's C
 A batch of prompts is dense, [S, T, ...], or packed, [tokens, ...] with ``offsets`` (int32 [S + 1]
 on the device).  States live in pools, [n_slots, ...], and are updated in place; ``slots`` (int32
 [S] on the device) names the slot of each sequence, a negative one skips it.
+
+No operator here records a gradient.  ``linear``, ``layer_norm`` and their gradients refuse a tensor that
+requires one while torch records them: call them under ``torch.no_grad()``, or in the forward and backward
+of a ``torch.autograd.Function``.
 """
 from __future__ import annotations
 
@@ -111,7 +115,8 @@ def declare(lib):
     here = getattr(torch._C, "_cuda_getDevice", None)
     if strided is None or here is None:
         strided = here = None
-    native.setup_dense(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in dense], torch.empty, torch.uint8, strided, here)
+    native.setup_dense(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in dense], torch.is_grad_enabled, torch.empty, torch.uint8,
+                       strided, here)
     _native = native
 
 

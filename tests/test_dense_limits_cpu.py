@@ -1,5 +1,6 @@
 """What the products' and norms' calls refuse and how they end, as far as that goes without a GPU."""
 import pytest
+import torch
 
 from _util import ensure_built
 
@@ -14,3 +15,44 @@ def lib():
 def test_the_wait_limit_needs_a_handle(lib):
     assert lib.vla_wait_limit(None, 100) == 1
     assert b"handle" in lib.vla_last_error(None)
+
+
+@pytest.fixture
+def detached(lib):
+    """A handle's checks without a device behind it."""
+    import sherman_morrison_inverse_gb300 as vla
+
+    class Detached(vla.Handle):
+        def __init__(self):
+            self.lib, self._h, self._ptr_value, self._device_index = lib, None, 0, 0
+
+        def __del__(self):
+            pass
+
+    return Detached()
+
+
+def test_tensors_that_require_a_gradient_are_refused(detached):
+    """The result would silently have none.  Without gradients being recorded the next check speaks."""
+    import sherman_morrison_inverse_gb300 as vla
+    native, h = vla.layer._native, detached
+    z = lambda *s: torch.zeros(*s)   # noqa: E731
+    calls = {   # name -> the call's arguments but the handle and the stream
+        native.linear: dict(x=z(4, 8), w=z(6, 8), bias=z(6), residual=z(4, 6), y=z(4, 6), act=0, pre=z(4, 6), x_scale=z(4), w_scale=z(6),
+                            dtype=None),
+        native.linear_back: dict(dy=z(4, 6), x=z(4, 8), w=z(6, 8), pre=z(4, 6), act=1, dx=z(4, 8), dw=z(6, 8), db=z(6)),
+        native.layer_norm: dict(x=z(4, 8), w=z(8), b=z(8), residual=z(4, 8), y=z(4, 8), eps=1e-5, stats=z(4, 2)),
+        native.layer_norm_back: dict(dy=z(4, 8), x=z(4, 8), w=z(8), stats=z(4, 2), dresidual=z(4, 8), dx=z(4, 8), dw=z(8), db=z(8)),
+    }
+    for call, args in calls.items():
+        for name, value in args.items():
+            if not torch.is_tensor(value):
+                continue
+            value.requires_grad_()
+            with pytest.raises(ValueError, match=f"^{name} requires a gradient"):
+                call(h, *args.values(), 0)
+            with torch.no_grad(), pytest.raises(ValueError, match="not on a CUDA device"):
+                call(h, *args.values(), 0)
+            value.requires_grad_(False)
+        with pytest.raises(ValueError, match="not on a CUDA device"):
+            call(h, *args.values(), 0)

@@ -255,3 +255,39 @@ def test_only_launches_of_one_call_overlap(vla):
         got = launches(one)
         first = [early for name, early in got if "vla" in name or name == "no kernel"][0]
         assert not first and (several == any(early for _, early in got)), got
+
+
+# ---------------------------------------------------------------------------------------------
+# gradients that torch records
+
+def test_products_within_an_autograd_function(vla):
+    """Parameters are taken where gradients are not recorded: under no_grad, and in an autograd.Function, whose gradients
+    are those of torch."""
+    gen = generator(19)
+    x, w, b = (rand(gen, *s).requires_grad_() for s in ((30, 72), (40, 72), (40,)))
+
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, b):
+            pre = torch.empty(x.shape[0], w.shape[0], device="cuda")
+            y = vla.linear(x, w, b, act="silu", pre=pre)
+            ctx.save_for_backward(x, w, pre)
+            return y
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, w, pre = ctx.saved_tensors
+            return vla.linear_backward(dy.contiguous(), x, w, pre, act="silu")
+
+    with pytest.raises(ValueError, match="x requires a gradient"):
+        vla.linear(x, w, b)
+    with torch.no_grad():
+        assert not vla.linear(x, w, b).requires_grad
+    y, dy = Linear.apply(x, w, b), rand(gen, 30, 40)
+    got = torch.autograd.grad(y, (x, w, b), dy)
+    t = [v.detach().double().requires_grad_() for v in (x, w, b)]
+    want = torch.autograd.grad(torch.nn.functional.silu(t[0] @ t[1].t() + t[2]), t, dy.double())
+    for g, r in zip(got, want):
+        # pre is off by 2^-24 of its 72 terms' magnitudes, some 60 for values of its own size, and the slope follows it;
+        # the sums of 30 to 72 terms as much again
+        assert float((g.double() - r).norm() / r.norm()) <= 2 * 72 * U32
