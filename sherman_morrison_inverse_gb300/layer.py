@@ -70,7 +70,7 @@ class _Missing:
         self._why = why
 
     def __getattr__(self, name):
-        raise RuntimeError(f"_layer_binding is not built ({self._why}); run "
+        raise RuntimeError(f"_layer_binding is not built, or not from these sources ({self._why}); run "
                            "`python -m sherman_morrison_inverse_gb300.build`")
 
 
@@ -78,7 +78,8 @@ _native = None
 
 
 def declare(lib):
-    """Declare the layer's C signatures, and hand the entry points to the argument checks in C."""
+    """Declare the layer's C signatures, and hand the entry points to the argument checks in C.  Where those are missing or of
+    other sources, the layer's operators say so when they are called."""
     global _native
     vp, ci, cll, cf = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
     lib.vla_short_conv.argtypes = [vp] * 6 + [cll] * 3 + [vp] * 2 + [cll] * 2 + [ci, vp, ci, ci, vp]
@@ -101,9 +102,14 @@ def declare(lib):
         loader = importlib.machinery.ExtensionFileLoader(f"{__package__}._layer_binding", BINDING)
         native = importlib.util.module_from_spec(importlib.util.spec_from_loader(loader.name, loader))
         loader.exec_module(native)
-    except ImportError as e:
+        _hand_over(native, lib, dense)
+    except (ImportError, AttributeError, TypeError) as e:   # not there; of older sources, without a function or an argument of it
         _native = _Missing(e)
         return
+    _native = native
+
+
+def _hand_over(native, lib, dense):
     at = [ctypes.cast(fn, ctypes.c_void_p).value
           for fn in (lib.vla_short_conv, lib.vla_ssm_scan, lib.vla_ssm_workspace, lib.vla_rms_norm)]
     # the current stream's handle without a Stream object around it, where torch has that
@@ -117,7 +123,6 @@ def declare(lib):
         strided = here = None
     native.setup_dense(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in dense], torch.is_grad_enabled, torch.empty, torch.uint8,
                        strided, here)
-    _native = native
 
 
 _here = contextlib.nullcontext()
