@@ -56,7 +56,7 @@ static lnorm_back_fn f_lnorm_back;
 static lnorm_back_ws_fn f_lnorm_back_ws;
 static PyObject *c_new, *t_u8, *s_device, *k_new;                 /* torch.empty; names of its dtype and device */
 static PyObject *c_grad, *s_requires;                             /* torch.is_grad_enabled, and what it is asked for */
-static PyObject *c_strided, *c_at;                                /* see fresh(); None where torch has them not */
+static PyObject *c_strided, *c_at, *c_modes;                      /* see read_allocator; None where torch has them not */
 static PyObject *t_f32, *t_bf16, *t_i32, *t_e4m3, *t_i8;          /* torch dtypes */
 static PyObject *c_like, *c_dense, *c_empty, *c_bytes, *c_stream; /* allocators and the current stream */
 static PyObject *s_shape, *s_dtype, *s_get_device, *s_stride, *s_data_ptr, *s_ptr, *s_index, *s_fail, *k_dtype;
@@ -193,11 +193,13 @@ typedef struct {
   vla_handle_t h;
   long device;
   void* stream;
+  int direct;   /* see read_allocator; -1: not asked yet */
 } Call;
 
 /* The handle's pointer and device, and the stream (an int; None: torch's current one). */
 static int read_call(Call* c, PyObject* self, PyObject* stream) {
   PyObject *p = PyObject_GetAttr(self, s_ptr), *d = PyObject_GetAttr(self, s_index);
+  c->direct = -1;
   if (p && d) {
     c->h = (vla_handle_t)PyLong_AsVoidPtr(p);
     c->device = PyLong_AsLong(d);
@@ -532,23 +534,25 @@ bad:
   return NULL;
 }
 
-/* A new contiguous tensor on the device of `like`.  Behind a launch torch.empty takes 3.3 us (new_empty 6.3, empty_like 3.2);
- * where torch offers its allocator without the dispatcher (c_strided: sizes, strides, dtype, on the current device, which
- * c_at says), that takes 1.5. */
-static PyObject* fresh(PyObject* like, const long long* shape, int nd, PyObject* dtype, long device) {
-  PyObject *size = shape_tuple(shape, nd), *r = NULL;
-  if (!size) return NULL;
-  long at = -1;
-  if (c_strided != Py_None) {
-    PyObject* d = PyObject_CallNoArgs(c_at);
-    if (d) at = PyLong_AsLong(d);
-    Py_XDECREF(d);
-    if (PyErr_Occurred()) {
-      Py_DECREF(size);
-      return NULL;
-    }
-  }
-  if (at == device) {
+/* Whether the call's outputs can come from torch's allocator without its dispatcher: where torch offers that (c_strided:
+ * sizes, strides, dtype, on the current device, which c_at says), the handle's device is the current one, and no
+ * dispatch mode (c_modes counts them) watches or replaces what is allocated.  Behind a launch torch.empty takes 3.3 us
+ * (new_empty 6.3, empty_like 3.2), that 1.5. */
+static int read_allocator(Call* c) {
+  c->direct = 0;
+  if (c_strided == Py_None) return 0;
+  PyObject *modes = PyObject_CallNoArgs(c_modes), *at = modes ? PyObject_CallNoArgs(c_at) : NULL;
+  if (at) c->direct = PyLong_AsLong(modes) == 0 && PyLong_AsLong(at) == c->device;
+  Py_XDECREF(modes);
+  Py_XDECREF(at);
+  return PyErr_Occurred() ? -1 : 0;
+}
+
+/* A new contiguous tensor on the device of `like`. */
+static PyObject* fresh(Call* c, PyObject* like, const long long* shape, int nd, PyObject* dtype) {
+  PyObject *size, *r = NULL;
+  if ((c->direct < 0 && read_allocator(c)) || !(size = shape_tuple(shape, nd))) return NULL;
+  if (c->direct) {
     long long stride[MAXD], step = 1;
     for (int i = nd - 1; i >= 0; --i) {
       stride[i] = step;
@@ -569,19 +573,19 @@ static PyObject* fresh(PyObject* like, const long long* shape, int nd, PyObject*
 }
 
 /* The tensor given, or a new contiguous one. */
-static PyObject* given_or_new(PyObject* given, PyObject* like, const long long* shape, int nd, PyObject* dtype, long device) {
-  if (given == Py_None) return fresh(like, shape, nd, dtype, device);
+static PyObject* given_or_new(Call* c, PyObject* given, PyObject* like, const long long* shape, int nd, PyObject* dtype) {
+  if (given == Py_None) return fresh(c, like, shape, nd, dtype);
   Py_INCREF(given);
   return given;
 }
 
 /* A workspace of `need` bytes (none for 0). */
-static int scratch(PyObject* like, size_t need, long device, PyObject** ws, void** ptr) {
+static int scratch(Call* c, PyObject* like, size_t need, PyObject** ws, void** ptr) {
   const long long size = (long long)need;
   *ws = NULL;
   *ptr = NULL;
   if (!need) return 0;
-  PyObject* p = (*ws = fresh(like, &size, 1, t_u8, device)) ? call0(*ws, s_data_ptr) : NULL;
+  PyObject* p = (*ws = fresh(c, like, &size, 1, t_u8)) ? call0(*ws, s_data_ptr) : NULL;
   if (p) *ptr = PyLong_AsVoidPtr(p);
   Py_XDECREF(p);
   if (p && !PyErr_Occurred()) return 0;
@@ -663,7 +667,7 @@ static PyObject* py_linear(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
     if (even_rows(&t, a[7], "pre", shape, x.nd, odtype, c.device, &rows[3])) return NULL;
     pre = t.ptr;
   }
-  if (!(y = given_or_new(a[5], a[1], shape, x.nd, odtype, c.device))) return NULL;
+  if (!(y = given_or_new(&c, a[5], a[1], shape, x.nd, odtype))) return NULL;
   if (even_rows(&t, y, "y", shape, x.nd, odtype, c.device, &rows[4])) goto bad;
   yp = t.ptr;
   M = 1;   /* x without columns has its rows all the same */
@@ -671,7 +675,7 @@ static PyObject* py_linear(PyObject* mod, PyObject* const* a, Py_ssize_t n) {
   size_t need = 0;
   vla_err_t code = f_linear_ws(c.h, x.ptr, w.ptr, M, N, K, rows, in, out, &need);
   if (code) return failed(self, code, y);
-  if (scratch(a[1], need, c.device, &ws, &wsp)) goto bad;
+  if (scratch(&c, a[1], need, &ws, &wsp)) goto bad;
   Py_BEGIN_ALLOW_THREADS
   code = f_linear(c.h, x.ptr, w.ptr, (const float*)xs, (const float*)wsc, (const float*)bias, res, pre, yp, M, N, K, rows,
                   (vla_act_t)act, in, out, wsp, need, c.stream);
@@ -727,7 +731,7 @@ static PyObject* py_linear_back(PyObject* mod, PyObject* const* a, Py_ssize_t n)
     const long long* sh = i == 0 ? x.shape : i == 1 ? w.shape : &N;
     const int nd = i == 0 ? x.nd : i == 1 ? 2 : 1;
     PyObject* dt = i == 2 ? t_f32 : dtype;
-    if (!(got[i] = given_or_new(a[6 + i], a[1], sh, nd, dt, c.device))) goto bad;
+    if (!(got[i] = given_or_new(&c, a[6 + i], a[1], sh, nd, dt))) goto bad;
     if (i == 2) {
       if (dense(got[2], name, sh, 1, dt, c.device, &out[2])) goto bad;
     } else {
@@ -740,7 +744,7 @@ static PyObject* py_linear_back(PyObject* mod, PyObject* const* a, Py_ssize_t n)
     vla_err_t code = f_linear_back_ws(c.h, dy.ptr, x.ptr, w.ptr, got[0] != Py_None, got[1] != Py_None, got[2] != Py_None,
                                       M, N, K, rows, (vla_act_t)act, io, &need);
     if (!code) {
-      if (scratch(a[1], need, c.device, &ws, &wsp)) goto bad;
+      if (scratch(&c, a[1], need, &ws, &wsp)) goto bad;
       Py_BEGIN_ALLOW_THREADS
       code = f_linear_back(c.h, dy.ptr, x.ptr, w.ptr, pre, out[0], out[1], (float*)out[2], M, N, K, rows, (vla_act_t)act,
                            io, wsp, need, c.stream);
@@ -787,7 +791,7 @@ static PyObject* py_layer_norm(PyObject* mod, PyObject* const* a, Py_ssize_t n) 
       return NULL;
     rp = r.ptr;
   }
-  if (!(y = given_or_new(a[5], a[1], x.shape, x.nd, dtype, c.device))) return NULL;
+  if (!(y = given_or_new(&c, a[5], a[1], x.shape, x.nd, dtype))) return NULL;
   if (even_rows(&t, y, "y", x.shape, x.nd, dtype, c.device, &y_row)) goto bad;
   if (a[7] != Py_False) {
     if (x.nd >= MAXD) {
@@ -796,7 +800,7 @@ static PyObject* py_layer_norm(PyObject* mod, PyObject* const* a, Py_ssize_t n) 
     }
     for (int i = 0; i < x.nd - 1; ++i) shape[i] = x.shape[i];
     shape[x.nd - 1] = 2;
-    if (!(stats = given_or_new(a[7] == Py_True ? Py_None : a[7], a[1], shape, x.nd, t_f32, c.device))) goto bad;
+    if (!(stats = given_or_new(&c, a[7] == Py_True ? Py_None : a[7], a[1], shape, x.nd, t_f32))) goto bad;
     if (dense(stats, "stats", shape, x.nd, t_f32, c.device, &sp)) goto bad;
   }
   {
@@ -849,20 +853,20 @@ static PyObject* py_layer_norm_back(PyObject* mod, PyObject* const* a, Py_ssize_
     if (even_rows(&t, a[5], "dresidual", x.shape, x.nd, dtype, c.device, &strides[2])) return NULL;
     res = t.ptr;
   }
-  if (!(dx = given_or_new(a[6], a[1], x.shape, x.nd, dtype, c.device)) || even_rows(&t, dx, "dx", x.shape, x.nd, dtype, c.device, &strides[3])) goto bad;
+  if (!(dx = given_or_new(&c, a[6], a[1], x.shape, x.nd, dtype)) || even_rows(&t, dx, "dx", x.shape, x.nd, dtype, c.device, &strides[3])) goto bad;
   dxp = t.ptr;
-  if (!(dw = given_or_new(a[7], a[1], &D, 1, t_f32, c.device)) || dense(dw, "dw", &D, 1, t_f32, c.device, &dwp)) goto bad;
+  if (!(dw = given_or_new(&c, a[7], a[1], &D, 1, t_f32)) || dense(dw, "dw", &D, 1, t_f32, c.device, &dwp)) goto bad;
   if (a[8] == Py_False) {
     Py_INCREF(Py_None);
     db = Py_None;
-  } else if (!(db = given_or_new(a[8], a[1], &D, 1, t_f32, c.device)) || dense(db, "db", &D, 1, t_f32, c.device, &dbp)) {
+  } else if (!(db = given_or_new(&c, a[8], a[1], &D, 1, t_f32)) || dense(db, "db", &D, 1, t_f32, c.device, &dbp)) {
     goto bad;
   }
   {
     size_t need = 0;
     vla_err_t code = f_lnorm_back_ws(c.h, count, D, &need);
     if (!code) {
-      if (scratch(a[1], need, c.device, &ws, &wsp)) goto bad;
+      if (scratch(&c, a[1], need, &ws, &wsp)) goto bad;
       Py_BEGIN_ALLOW_THREADS
       code = f_lnorm_back(c.h, dy.ptr, x.ptr, (const float*)w, (const float*)sp, res, dxp, (float*)dwp, (float*)dbp, count,
                           D, strides, gio, io, wsp, need, c.stream);
@@ -888,12 +892,13 @@ bad:
 }
 
 /* setup_dense(addresses of the entry points and workspace queries, torch.is_grad_enabled, torch.empty, torch.uint8, and for
- * fresh() either two callables or None): after setup */
+ * read_allocator either three callables or None): after setup */
 static PyObject* py_setup_dense(PyObject* mod, PyObject* args) {
   (void)mod;
   unsigned long long p[7];
-  PyObject* o[5];
-  if (!PyArg_ParseTuple(args, "KKKKKKKOOOOO", p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6, o, o + 1, o + 2, o + 3, o + 4)) return NULL;
+  PyObject* o[6];
+  if (!PyArg_ParseTuple(args, "KKKKKKKOOOOOO", p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6, o, o + 1, o + 2, o + 3, o + 4, o + 5))
+    return NULL;
   f_linear = (linear_fn)(uintptr_t)p[0];
   f_linear_ws = (linear_ws_fn)(uintptr_t)p[1];
   f_linear_back = (linear_back_fn)(uintptr_t)p[2];
@@ -901,8 +906,8 @@ static PyObject* py_setup_dense(PyObject* mod, PyObject* args) {
   f_lnorm = (lnorm_fn)(uintptr_t)p[4];
   f_lnorm_back = (lnorm_back_fn)(uintptr_t)p[5];
   f_lnorm_back_ws = (lnorm_back_ws_fn)(uintptr_t)p[6];
-  PyObject** slot[5] = {&c_grad, &c_new, &t_u8, &c_strided, &c_at};
-  for (int i = 0; i < 5; ++i) {
+  PyObject** slot[6] = {&c_grad, &c_new, &t_u8, &c_strided, &c_at, &c_modes};
+  for (int i = 0; i < 6; ++i) {
     Py_INCREF(o[i]);
     Py_XDECREF(*slot[i]);
     *slot[i] = o[i];

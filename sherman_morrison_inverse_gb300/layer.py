@@ -116,13 +116,15 @@ def _hand_over(native, lib, dense):
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
     native.setup(*at, torch.float32, torch.bfloat16, torch.int32, torch.float8_e4m3fn, torch.int8,
                  torch.empty_like, _dense, _empty, _bytes, stream)
-    # the caching allocator without the dispatcher around it, and the current device, where torch has both
+    # the caching allocator without the dispatcher around it, the current device, and the number of modes that watch the
+    # dispatcher, where torch has all three
     strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
     here = getattr(torch._C, "_cuda_getDevice", None)
-    if strided is None or here is None:
-        strided = here = None
+    modes = getattr(torch._C, "_len_torch_dispatch_stack", None)
+    if strided is None or here is None or modes is None:
+        strided = here = modes = None
     native.setup_dense(*[ctypes.cast(fn, ctypes.c_void_p).value for fn in dense], torch.is_grad_enabled, torch.empty, torch.uint8,
-                       strided, here)
+                       strided, here, modes)
 
 
 _here = contextlib.nullcontext()

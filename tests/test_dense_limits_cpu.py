@@ -72,7 +72,7 @@ def test_a_binding_of_older_sources_does_not_keep_the_library_from_loading(lib, 
     if older == "without setup_dense":
         old = text.replace('    {"setup_dense", py_setup_dense, METH_VARARGS, NULL},\n', "")
     else:
-        old = text.replace('"KKKKKKKOOOOO"', '"KKKKKKKOOOO"')
+        old = text.replace('"KKKKKKKOOOOOO"', '"KKKKKKKOOOOO"')
     assert old != text
     source = tmp_path / "layer_binding.c"
     source.write_text(old)

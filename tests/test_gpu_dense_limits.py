@@ -291,3 +291,32 @@ def test_products_within_an_autograd_function(vla):
         # pre is off by 2^-24 of its 72 terms' magnitudes, some 60 for values of its own size, and the slope follows it;
         # the sums of 30 to 72 terms as much again
         assert float((g.double() - r).norm() / r.norm()) <= 2 * 72 * U32
+
+
+# ---------------------------------------------------------------------------------------------
+# where outputs come from
+
+def test_a_dispatch_mode_sees_the_outputs(vla):
+    """A mode that watches torch's dispatcher sees what a call allocates, its workspace among it, as of the other operators."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Watch(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.made = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            out = func(*args, **(kwargs or {}))
+            if "empty" in str(func):
+                self.made.append(out.data_ptr())
+            return out
+
+    gen = generator(3)
+    x, w, nw = rand(gen, 700, 77), rand(gen, 130, 77), rand(gen, 77)
+    want = vla.linear(x, w)
+    with Watch() as watch:
+        y = vla.linear(x, w)
+        h, stats = vla.layer_norm(x, nw, stats=True)
+        grads = [*vla.linear_backward(y, x, w), *vla.layer_norm_backward(x, x, nw, stats)]
+    assert torch.equal(y, want) and {t.data_ptr() for t in (y, h, stats, *grads)} <= set(watch.made)
+    assert len(watch.made) == 9 + 3   # two products' and a norm's workspaces
