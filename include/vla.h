@@ -431,7 +431,7 @@ vla_err_t vla_rms_norm(vla_handle_t h, const void* x, const float* w, void* resi
  * >= 0, the values of a row are adjacent, and no alignment beyond a value's type is
  * required; rows that start on 16-byte boundaries are faster.  Outputs must not overlap
  * any input or each other (y of the product may be its residual, the norm's residual is
- * both).  Bias, norm weights, statistics, scales and their gradients are float32. */
+ * both); one that starts where such another does is refused.  Bias, norm weights, statistics, scales and their gradients are float32. */
 
 typedef enum { VLA_ACT_NONE = 0, VLA_ACT_SILU = 1, VLA_ACT_GELU = 2 } vla_act_t;   /* v; v sigmoid(v); v Phi(v) */
 typedef enum { VLA_MAT_F32 = 0, VLA_MAT_BF16 = 1, VLA_MAT_E4M3 = 2 } vla_mat_t;    /* operands of a product */

@@ -19,6 +19,9 @@ size_t size_of(vla_mat_t t) { return t == VLA_MAT_F32 ? 4 : t == VLA_MAT_BF16 ? 
 bool known(vla_dtype_t t) { return t == VLA_F32 || t == VLA_BF16; }
 bool stride_ok(long long v) { return v >= 0 && v < (1LL << 40); }
 bool rows_apart(long long n, long long row, long long width) { return n <= 1 || row >= width; }
+// Whether an output starts where none of the others does: the overlap that a call is likely to have by mistake.
+template <typename... P>
+bool elsewhere(const void* out, P... p) { return !out || ((out != static_cast<const void*>(p)) && ...); }
 
 vla_err_t check_sizes(vla_handle_t h, const std::string& f, long long M, long long N, long long K) {
   if (M < 0 || N < 0 || K < 0) return fail(h, VLA_ERR_INVALID_ARG, f + ": negative size");
@@ -127,6 +130,8 @@ vla_err_t vla_linear(vla_handle_t h, const void* x, const void* w, const float* 
     return fail(h, VLA_ERR_INVALID_ARG, f + ": misaligned pointer");
   if (!rows_apart(M, rows[4], N) || (pre && !rows_apart(M, rows[3], N)))
     return fail(h, VLA_ERR_INVALID_ARG, f + ": rows of y or pre overlap");
+  if (!elsewhere(y, pre) || !elsewhere(pre, residual) || (K > 0 && (!elsewhere(y, x, w) || !elsewhere(pre, x, w))))
+    return fail(h, VLA_ERR_INVALID_ARG, f + ": y and pre must not be an input (y may be the residual) or each other");
   if (residual == y && M > 1 && rows[2] != rows[4])
     return fail(h, VLA_ERR_INVALID_ARG, f + ": y may be the residual only with the same rows");
   vla::ProductArgs p = linear_product(h, x, w, M, N, K, rows);
@@ -188,6 +193,8 @@ vla_err_t vla_linear_backward(vla_handle_t h, const void* dy, const void* x, con
     return fail(h, VLA_ERR_INVALID_ARG, f + ": misaligned pointer");
   if ((dx && !rows_apart(M, rows[4], K)) || (dw && !rows_apart(N, rows[5], K)))
     return fail(h, VLA_ERR_INVALID_ARG, f + ": rows of dx or dw overlap");
+  if (terms && (!elsewhere(dx, dy, x, w, dw, has_act ? pre : nullptr) || !elsewhere(dw, dy, x, w, has_act ? pre : nullptr)))
+    return fail(h, VLA_ERR_INVALID_ARG, f + ": dx and dw must not be an input or each other");
   BackPlan b = back_plan(h, dy, x, w, dx, dw, db, M, N, K, rows, has_act, io_dtype);
   if ((err = check_ws(h, f, workspace, workspace_bytes, b.ws_bytes)) != VLA_OK) return err;
   char* ws = static_cast<char*>(workspace);
@@ -254,6 +261,7 @@ vla_err_t vla_layer_norm(vla_handle_t h, const void* x, const float* w, const fl
     return fail(h, VLA_ERR_INVALID_ARG, f + ": misaligned pointer");
   if (!rows_apart(rows, y_row, D) || (residual && !rows_apart(rows, res_row, D)))
     return fail(h, VLA_ERR_INVALID_ARG, f + ": rows of y or the residual overlap");
+  if (!elsewhere(y, residual)) return fail(h, VLA_ERR_INVALID_ARG, f + ": y must not be the residual");
   vla::LayerNormArgs a{};
   a.x = x; a.w = w; a.b = b; a.residual = residual; a.y = y; a.stats = stats;
   a.rows = rows; a.D = D; a.x_row = x_row; a.res_row = res_row; a.y_row = y_row;
@@ -285,6 +293,7 @@ vla_err_t vla_layer_norm_backward(vla_handle_t h, const void* dy, const void* x,
   if (!to_values(size_of(dy_dtype), dy) || !to_values(size_of(x_dtype), x, dresidual, dx) || !to_values(4, w, stats, dw, db))
     return fail(h, VLA_ERR_INVALID_ARG, f + ": misaligned pointer");
   if (!rows_apart(rows, strides[3], D)) return fail(h, VLA_ERR_INVALID_ARG, f + ": rows of dx overlap");
+  if (rows > 0 && !elsewhere(dx, dy, x)) return fail(h, VLA_ERR_INVALID_ARG, f + ": dx must not be dy or x");
   if ((err = check_ws(h, f, workspace, workspace_bytes, rows ? vla::layer_norm_back_ws(rows, D, h->sm_count) : 0)) != VLA_OK) return err;
   vla::LayerNormBackArgs a{};
   a.dy = dy; a.x = x; a.w = w; a.stats = stats; a.dres = dresidual; a.dx = dx; a.dw = dw; a.db = db;

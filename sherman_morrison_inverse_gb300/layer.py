@@ -17,6 +17,10 @@ A batch of prompts is dense, [S, T, ...], or packed, [tokens, ...] with ``offset
 on the device).  States live in pools, [n_slots, ...], and are updated in place; ``slots`` (int32
 [S] on the device) names the slot of each sequence, a negative one skips it.
 
+Outputs that the caller gives must not overlap an input or each other (but ``linear``'s y, which may be its residual).
+With ``stream`` a call runs there and allocates from that stream's memory; as of torch's own operators under
+``torch.cuda.stream``, its inputs have to be ready there and to live until the work is done (``Tensor.record_stream``).
+
 No operator here records a gradient.  ``linear``, ``layer_norm`` and their gradients refuse a tensor that
 requires one while torch records them: call them under ``torch.no_grad()``, or in the forward and backward
 of a ``torch.autograd.Function``.

@@ -320,3 +320,27 @@ def test_a_dispatch_mode_sees_the_outputs(vla):
         grads = [*vla.linear_backward(y, x, w), *vla.layer_norm_backward(x, x, nw, stats)]
     assert torch.equal(y, want) and {t.data_ptr() for t in (y, h, stats, *grads)} <= set(watch.made)
     assert len(watch.made) == 9 + 3   # two products' and a norm's workspaces
+
+
+def test_outputs_that_are_an_input_are_refused(vla):
+    """They were read while they were written: with rows wider than 8192 the norm's dw came from dx, a product's y from y."""
+    gen = generator(13)
+    x, w, r, pre = rand(gen, 64, 64), rand(gen, 64, 64), rand(gen, 64, 64), torch.empty(64, 64, device="cuda")
+    wide, nw, stats = rand(gen, 5, 9000), rand(gen, 9000), rand(gen, 5, 2).abs()
+    bad = [
+        lambda: vla.linear(x, w, y=x), lambda: vla.linear(x, w, y=w), lambda: vla.linear(x, w, y=pre, pre=pre, act="silu"),
+        lambda: vla.linear(x, w, pre=x, act="silu"), lambda: vla.linear(x, w, None, r, pre=r, act="silu"),
+        lambda: vla.linear_backward(r, x, w, dx=r), lambda: vla.linear_backward(r, x, w, dx=x), lambda: vla.linear_backward(r, x, w, dw=w),
+        lambda: vla.linear_backward(r, x, w, dw=x), lambda: vla.linear_backward(r, x, w, dx=pre, dw=pre),
+        lambda: vla.linear_backward(r, x, w, pre, act="gelu", dx=pre),
+        lambda: vla.layer_norm(x, nw[:64], None, r, r),
+        lambda: vla.layer_norm_backward(wide, wide.clone(), nw, stats, dx=wide), lambda: vla.layer_norm_backward(wide.clone(), wide, nw, stats, dx=wide),
+    ]
+    kept = [t.clone() for t in (x, w, r, wide)]
+    for call in bad:
+        with pytest.raises(vla.VlaError, match="must not be"):
+            call()
+    assert all(torch.equal(a, b) for a, b in zip(kept, (x, w, r, wide)))
+    vla.linear(x, w, None, r, r)   # the residual as y stays
+    e = torch.empty(0, 64, device="cuda")
+    assert vla.linear(e, w, y=torch.empty(0, 64, device="cuda")).shape == (0, 64)
