@@ -69,7 +69,7 @@ def launches(call):
             names[node] = "no kernel"
     assert cu.cuGraphGetEdges_v2(graph, None, None, None, ctypes.byref(n)) == 0
     a, b, edges = (ctypes.c_void_p * n.value)(), (ctypes.c_void_p * n.value)(), (Edge * n.value)()
-    assert cu.cuGraphGetEdges_v2(graph, a, b, edges, ctypes.byref(n)) == 0
+    assert n.value == 0 or cu.cuGraphGetEdges_v2(graph, a, b, edges, ctypes.byref(n)) == 0
     before = {y: (x, e.type) for x, y, e in zip(a, b, edges)}
     order = [m for m in nodes if m not in before]
     assert len(order) == (1 if len(nodes) else 0) and len(before) == len(nodes) - len(order)   # one stream: a chain
@@ -344,3 +344,92 @@ def test_outputs_that_are_an_input_are_refused(vla):
     vla.linear(x, w, None, r, r)   # the residual as y stays
     e = torch.empty(0, 64, device="cuda")
     assert vla.linear(e, w, y=torch.empty(0, 64, device="cuda")).shape == (0, 64)
+
+
+# ---------------------------------------------------------------------------------------------
+# every form of a product against its reference, float32 above all: which form a call takes is part of the test
+
+FORMS = [  # M, N, K, dtype, out, act, everything (bias, residual, pre in rows with gaps), kernels
+    (16, 1000, 2000, "f32", "f32", "silu", True, ["few_rows"]),
+    (100, 2000, 1100, "f32", "f32", "gelu", True, ["pack", "tokens"]),
+    (30, 8200, 1030, "f32", "f32", "none", False, ["pack", "tokens"]),
+    (300, 777, 1161, "f32", "f32", "silu", True, ["pack", "tokens"]),
+    (300, 3001, 3000, "f32", "f32", "silu", True, ["pack", "gemm", "join"]),       # more weights than that takes
+    (513, 1000, 4000, "f32", "f32", "none", False, ["pack", "gemm", "join"]),      # few tiles, a long Kd
+    (700, 141, 4100, "f32", "f32", "gelu", True, ["pack", "gemm", "join"]),
+    (1001, 777, 1161, "f32", "f32", "silu", True, ["pack", "gemm", "join"]),
+    (6000, 2501, 72, "f32", "f32", "gelu", True, ["pack", "gemm"]),                # rows of y through shared memory
+    (6000, 2504, 200, "f32", "f32", "silu", False, ["pack", "gemm"]),              # and directly
+    (6000, 2504, 200, "bf16", "f32", "silu", True, ["gemm"]),
+    (6000, 2504, 208, "e4m3", "bf16", "gelu", True, ["gemm"]),
+    (513, 1000, 8200, "bf16", "bf16", "gelu", True, ["pack", "gemm", "join"]),
+]
+
+
+def forms_of(call):
+    names = ("few_rows", "tokens", "gemm", "join", "pack", "slope_sum", "slope")
+    return [next(n for n in names if n + "_kernel" in name) for name, _ in launches(call) if "vla" in name]
+
+
+def gaps(gen, rows, width, everything, dtype):
+    return rand(gen, rows, width + 3).to(dtype)[:, 1:1 + width] if everything else rand(gen, rows, width).to(dtype)
+
+
+@pytest.mark.parametrize("M,N,K,dtype,out,act,everything,forms", FORMS)
+def test_products_form_by_form(vla, M, N, K, dtype, out, act, everything, forms):
+    gen = generator(M + N + K)
+    odd = everything and dtype != "e4m3" and (dtype == "f32" or K == 8200)
+    x, w = gaps(gen, M, K, odd, TYPES[dtype]), (gaps(gen, N, K, odd, torch.float32) / K ** 0.5).to(TYPES[dtype])
+    b = rand(gen, N) if everything else None
+    res, pre = (gaps(gen, M, N, True, TYPES[out]) if everything else None for _ in range(2))
+    scales = dict(x_scale=rand(gen, M).abs() + 0.1, w_scale=rand(gen, N).abs() + 0.1) if dtype == "e4m3" else {}
+    call = lambda: vla.linear(x, w, b, res, act=act, pre=pre, dtype=TYPES[out], **scales)   # noqa: E731
+    assert forms_of(call) == forms
+    y = call()
+    f = {k: f64(v) for k, v in scales.items()}
+    want, v, mag = ref.linear(f64(x), f64(w), None if b is None else f64(b), None if res is None else f64(res), act, f.get("x_scale"), f.get("w_scale"))
+    # the sums: K products and their additions, cut off or rounded, and of three terms of bfloat16 what the six products leave
+    # out; the activations' own error (of bfloat16 results 2^-19 of their terms, see the slopes below) and slopes, at most 1.13
+    u, own = (U16, 2.0 ** -18) if out == "bf16" else (U32, 2.0 ** -20)
+    off = (2 * K + 8) * U32 * mag
+    av = np.abs(ref.act(v, act))
+    bound = 1.2 * off + own * (1 + np.abs(v)) ** 2 * (av + 2.0 ** -20) * (act != "none") + 2 * U32 * (av + np.abs(want)) + u * np.abs(want)
+    assert np.max(np.abs(f64(y) - want) / bound) <= 1.0
+    if everything:
+        assert np.max(np.abs(f64(pre) - v) / (off + u * np.abs(v))) <= 1.0
+    if out == "f32" and dtype == "f32":
+        # In the 2-norm the terms' errors are independent.  What six of nine products leave out is 2^-24 of each, and a chain of
+        # 16 additions that are cut off takes 16 x 2^-24 of its sum at most (half of 2^-23 each, the running sum half of the
+        # whole, twice over for terms that are cut off before they are added): 2^-20.  Without one of the six it is 2.4e-6.
+        assert np.linalg.norm((f64(pre) if everything else f64(y)) - (v if everything else want)) <= 2.0 ** -20 * np.linalg.norm(v)
+
+
+@pytest.mark.parametrize("M,N,forms", [(200, 24, ["pack", "tokens"]), (600, 24, ["pack", "gemm"]), (6000, 2504, ["pack", "gemm"])])
+def test_float32_terms_of_every_magnitude(vla, M, N, forms):
+    """One product a sum, of values from 2^-100 to 2^95: three terms of bfloat16 hold them to 2^-24 each, the six products leave
+    3 x 2^-25 out."""
+    x = (torch.diag(2.0 ** torch.arange(-100, 100, 5, device="cuda")) * 1.2345678).repeat(M // 40 + 1, 1)[:M].contiguous()
+    w = torch.full((N, 40), 1.7654321, device="cuda") * (1 + torch.arange(N, device="cuda") / 9999)[:, None]
+    assert forms_of(lambda: vla.linear(x, w)) == forms
+    want = f64(x) @ f64(w).T
+    assert np.max(np.abs(f64(vla.linear(x, w)) / want - 1)) <= 2.0 ** -22
+    # the same values through a gradient: dx = dy w and dw = dy^T x
+    dx = vla.linear_backward(x, w[0, 0].expand(M, N).contiguous(), torch.full((40, N), 1.7654321, device="cuda"), bias=False)[0]
+    assert np.max(np.abs(f64(dx) / (f64(x) @ np.full((40, N), f64(w)[0, 0])) - 1)) <= 2.0 ** -22
+    one = x[:40]
+    dw = vla.linear_backward(one, w[0, 0].expand(40, N).contiguous(), torch.zeros(40, N, device="cuda"), input=False, bias=False)[1]
+    assert np.max(np.abs(f64(dw) / (f64(one).T @ np.full((40, N), f64(w)[0, 0])) - 1)) <= 2.0 ** -22
+
+
+@pytest.mark.parametrize("M,N,K,forms", [(700, 300, 520, ["slope", "slope_sum", "pack", "gemm", "join"]),
+                                         (6000, 1501, 2003, ["slope", "slope_sum", "pack", "gemm", "join"]),
+                                         (7, 300, 200, ["slope", "slope_sum", "pack", "gemm", "join"]),
+                                         (3000, 2500, 2600, ["slope", "slope_sum", "pack", "gemm"])])
+def test_float32_gradients_in_the_2_norm(vla, M, N, K, forms):
+    """The bounds of single values leave room for a whole term; the 2-norm does not (see above)."""
+    gen = generator(M + N)
+    dy, x, w = rand(gen, M, N), rand(gen, M, K), rand(gen, N, K)
+    got = vla.linear_backward(dy, x, w)
+    assert forms_of(lambda: vla.linear_backward(dy, x, w)) == forms
+    for g, r in zip(got, ref.linear_backward(f64(dy), f64(x), f64(w))[0]):
+        assert np.linalg.norm(f64(g) - r) <= 2.0 ** -20 * np.linalg.norm(r)
