@@ -433,3 +433,26 @@ def test_float32_gradients_in_the_2_norm(vla, M, N, K, forms):
     assert forms_of(lambda: vla.linear_backward(dy, x, w)) == forms
     for g, r in zip(got, ref.linear_backward(f64(dy), f64(x), f64(w))[0]):
         assert np.linalg.norm(f64(g) - r) <= 2.0 ** -20 * np.linalg.norm(r)
+
+
+# ---------------------------------------------------------------------------------------------
+# the activations' slopes behind bfloat16, where a bias gradient of one row shows them in float32
+
+@pytest.mark.parametrize("spare", [0, 3])   # eight columns a lane, or one
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_slopes_of_every_bfloat16_value(vla, act, spare):
+    """dy = 1, one row: db is act'(pre) itself.  Relative to the slope's two terms.  gelu: the polynomial and its evaluation 6.4e-7, the
+    approximate exponential and reciprocal 2^-22 each, and v^2 / 2 rounded twice before the exponential, 2^-24 v^2.  silu: the
+    exponential, the reciprocal and the addition between them, 2^-21, and its argument's rounding, |v| 2^-24; 1 - s is off
+    by a rounding of s, which v multiplies."""
+    v = torch.arange(0x4180, dtype=torch.int16, device="cuda")   # 0 to 16
+    v = torch.cat([v, v | -0x8000]).view(torch.bfloat16)
+    v = v[:v.numel() // 8 * 8 - spare]
+    one = torch.ones(1, v.numel(), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(v.numel(), 1, dtype=torch.bfloat16, device="cuda")
+    db = vla.linear_backward(one, one[:, :1], w, v[None], act=act, input=False, weight=False)[2]
+    slope, terms = ref.slope(f64(v), act)
+    size = np.abs(f64(v))
+    bound = (2.0 ** -19 + size ** 2 * U32 if act == "gelu" else 2.0 ** -20 + size * 4 * U32) * terms
+    # where an exponential falls below 2^-126 it is 0
+    assert np.max(np.abs(f64(db) - slope) / (bound + 16 * 2.0 ** -126)) <= 1.0
