@@ -580,7 +580,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Whether CUDA cores take the product (vla_rowvec.cu), eight rows of x at a time: with one or two rows (e4m3), four
 // (bfloat16) or sixteen (float32) the weights' way from memory bounds them; with more, their arithmetic does, and they win only
-// where the tensor cores' fixed cost is the larger part.  Measured (us, CUDA cores against vla_gemm_tokens.cu): bfloat16
+// where the tensor cores' fixed cost is the larger part.  Measured (us, launches by themselves, CUDA cores against vla_gemm_tokens.cu): bfloat16
 // N 8192, K 8192: 24.6 against 32 (1 row), 33.6 against 32 (4), 65 against 33 (8); N 520, K 264, 16 rows: 5.0 against 5.5,
 // 4.8 against 9.7 with rows that a copy has to align; float32 N 8192, K 8192: 208 against 216 (16), 366 against 218 (32);
 // e4m3: 17.4 against 18.8 (1), 22.0 against 18.9 (2), 31.7 against 18.9 (4).

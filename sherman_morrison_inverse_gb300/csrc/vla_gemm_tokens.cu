@@ -8,8 +8,10 @@
 // through the epilogue: no pass over memory and no second launch.
 // Sums move from tensor memory to float32 registers every 4 stages (see vla_gemm.cu).  Waits are bounded; a CTA that gives up waits
 // (bounded too) for its products and copies under way.
-// bfloat16, us on the GPU: N 8192, K 8192 with 16 to 128 rows 32 to 38, 4.2 to 3.5 TB/s; N 2048, K 4096 with 128 rows 11.8; N 520, K 264
-// 5.0, which is what a call costs before its size does.
+// us a launch in a row of them whose weights pass L2 (by itself 1 to 6 more): N 8192, K 8192 with 16 to 128 rows, bfloat16 26.2 to
+// 31.8 (5.1 to 4.2 TB/s), e4m3 16.1 to 20.6 (4.2 to 3.3 TB/s), float32 with 32 to 128 rows 212 to 224, of which the copies of the
+// weights' three terms are the most; bfloat16 N 2048, K 4096 with 128 rows 10.7; N 520, K 264 with 16 rows 4.3, which is what
+// a call costs before its size does.
 #include <atomic>
 
 #include "vla_gemm.cuh"

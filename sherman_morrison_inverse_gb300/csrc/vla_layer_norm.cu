@@ -22,7 +22,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 // and w and b stay in registers.  Each warp takes the mean and the squares around it of its own values, and one
 // exchange joins them: sum of squares around mu = sum over warps of (theirs + n_w (mean_w - mu)^2), with no
 // difference of large sums.  Memory bound: 16384 x 4096 bfloat16 with residual and statistics 91 us, 5.9 TB/s, 88 % of a
-// copy's rate (with 8 values a thread, 512 threads a row, 115 us); 24 x 5120 4.4 us.
+// copy's rate (with 8 values a thread, 512 threads a row, 115 us); 24 x 5120 4.3 us.  Wider than 8192, without the next row ahead:
+// 4096 x 16384 208 us.  VEC 1, for rows off 16-byte boundaries or odd widths, value by value: 16384 x 4095 182 us, 4096 x 16383
+// 869, 4099 x 1001 float32 12.6 (1000 columns: 8.7).
 // RES: 0 none, 1 bfloat16, 2 float32
 template <typename T, int RES, int VEC, int NV>
 __global__ void __launch_bounds__(VEC * NV <= 16 ? 512 : 1024, 1)
@@ -213,7 +215,8 @@ cudaError_t forward_of(const LayerNormArgs& a, cudaStream_t s) {
 // for its copies under way and leaves the sums that it has.  VEC 1: rows anywhere, read directly.
 // Blocks leave their sums of dw and db as rows of `partial`, which back_sum_kernel adds in their order.
 // 16384 x 4096 bfloat16 with the residual's gradient 103 us, 5.2 TB/s, 78 % of a copy's rate: a row's chain of barriers on the 16 warps
-// that the registers of 16 values a thread allow.  4099 x 1001 float32, value by value, 15 us.
+// that the registers of 16 values a thread allow.  Value by value: 4099 x 1001 float32 17.5 us (1000 columns, copied ahead: 17.9),
+// 16384 x 4095 bfloat16 326.
 constexpr int kBackStages = 8;
 constexpr int kBackThreads = 512;
 
@@ -453,7 +456,8 @@ __global__ void __launch_bounds__(kBackThreads, 1)
   }
 }
 
-// Wider rows: dx by a block a row, read twice, and the columns' sums by a kernel of their own.
+// Wider rows: dx by a block a row, read twice, and the columns' sums by a kernel of their own: 4096 x 16384 bfloat16 with the residual's
+// gradient 313 us, a quarter of a copy's rate.
 template <typename TD, typename TX>
 __global__ void __launch_bounds__(256) back_row_kernel(const LayerNormBackArgs a, float inv_d) {
   __shared__ float part[2][2][8];

@@ -6,8 +6,9 @@
 // and sums are float32 in packed pairs.  A warp's sums are folded over the lanes together, so that
 // every lane ends with one of them.
 // Rows off 16-byte boundaries, or Kd in no whole pieces, are read value by value.
-// One row, us on the GPU: N 8192, K 8192 bfloat16 24.6 (5.5 TB/s, 82 % of a copy's rate), e4m3 16, float32 49; N 8512, K 2048 bfloat16
-// 9.2; N 520, K 264 3.1.  Eight rows of float32 N 8192, K 8192: 119, by arithmetic and the first-level cache.
+// One row, us a launch in a row of them whose weights pass L2 (by itself 2 to 3 more): N 8192, K 8192 bfloat16 21.9 (6.1 TB/s,
+// 92 % of a copy's rate), e4m3 14.9 (4.5 TB/s), float32 47.3 (5.7 TB/s); N 8512, K 2048 bfloat16 7.7; N 520, K 264 2.6.  Eight
+// rows of float32 N 8192, K 8192: 81, by arithmetic and the first-level cache.
 #include "vla_dense.cuh"
 
 namespace vla {

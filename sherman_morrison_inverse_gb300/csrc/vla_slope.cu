@@ -4,7 +4,8 @@
 // it), a block's 8 warps every eighth row of a stretch of rows, three rows at a time so that their loads are in flight
 // together.  A column's sum is taken by a thread over its rows, over the block's warps in shared memory, and
 // over the stretches by a second kernel, in a fixed order: float32, chains of M / 8 additions at most (M / 110 at N 8192).
-// 8192 x 8192 bfloat16, gelu: 71 us, 5.7 TB/s, 85 % of a copy's rate (more blocks than one wave 84; value by value 345).
+// 8192 x 8192 bfloat16, gelu: 70 us, 5.7 TB/s, 85 % of a copy's rate (more blocks than one wave 84).  Rows off 16-byte boundaries or
+// of an odd width are read value by value, a column a lane: 8192 x 8191 291 us.
 #include "vla_dense.cuh"
 
 namespace vla {

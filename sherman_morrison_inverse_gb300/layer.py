@@ -212,8 +212,8 @@ class LayerOps:
         """y = act(v) + residual, v = x w^T + bias, the product of a projection with its epilogue.
 
         x [..., K] and w [N, K] in one type, bfloat16, float32 or e4m3 codes, their rows evenly
-        spaced; codes stand for codes * x_scale[..., None] (rms_norm's scales) and codes *
-        w_scale[:, None], [...] and [N] float32 (None: 1).  bias [N] float32.  act "none", "silu"
+        spaced; codes stand for codes * x_scale[..., None] (those of rms_norm with a scale a row) and
+        codes * w_scale[:, None], [...] and [N] float32 (None: 1).  bias [N] float32.  act "none", "silu"
         or "gelu" (v Phi(v)).  Returns y [..., N] in `dtype`: x's type, bfloat16 for codes, or
         float32.  residual and pre have y's shape and type; pre receives v, for the gradient; y may
         be the residual itself."""
