@@ -143,6 +143,41 @@ def test_a_norms_wait_that_runs_out_ends_the_call(vla, rows, D, dtype, flagged):
     h.close()
 
 
+def test_calls_that_give_up_leave_others_alone(vla):
+    """Calls that give up on one stream, with copies under way into shared memory that the next block gets, beside calls on another
+    stream whose results are known."""
+    gen, quick, h = generator(1), vla.Handle(0), vla.Handle(0)
+    quick.wait_limit(0)
+    a, aw = rand(gen, 1000, 2048, dtype=torch.bfloat16), rand(gen, 2000, 2048, dtype=torch.bfloat16)
+    n, nw, stats = rand(gen, 3000, 4096, dtype=torch.bfloat16), rand(gen, 4096), rand(gen, 3000, 2).abs()
+    x, w, dy = rand(gen, 700, 1032, dtype=torch.bfloat16), rand(gen, 1000, 1032, dtype=torch.bfloat16), rand(gen, 700, 1000, dtype=torch.bfloat16)
+    few, codes, wc = x[:40], x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+
+    def right():
+        y, st = h.layer_norm(x, nw[:1032].contiguous(), stats=True)
+        return [h.linear(x, w), h.linear(few, w), h.linear(x.float(), w.float()), h.linear(codes, wc), y, *h.linear_backward(dy, x, w),
+                *h.layer_norm_backward(x, x, nw[:1032].contiguous(), st)]
+
+    want, got = right(), []
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        with torch.cuda.stream(sides[0]):
+            for _ in range(3):
+                quick.linear(a, aw)
+                quick.linear(a[:100], aw)
+                quick.linear_backward(n[:1000, :2000], a, aw)
+                quick.layer_norm_backward(n, n, nw, stats)
+        with torch.cuda.stream(sides[1]):
+            got.append(right())
+    torch.cuda.synchronize()
+    for outs in got:
+        assert all(torch.equal(p, q) for p, q in zip(outs, want))
+    assert quick.status()["flags"] == vla.STATUS_TIMEOUT and h.status()["flags"] == 0
+    quick.close()
+    h.close()
+
+
 def test_the_wait_limit_has_a_range(vla):
     h = vla.Handle(0)
     with pytest.raises(vla.VlaError, match="0..5000"):
